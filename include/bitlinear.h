@@ -458,6 +458,125 @@ bl_status bitlinear_backward_weight(const float *dY, int64_t M, int64_t N, const
                                     const float *d, int64_t K, float *dW, void *ws,
                                     size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit key/value cache and the attention over it -- what stands between a
+ * layer's q, k, v BitLinears and its o BitLinear when a token follows others.
+ * The pages leave attention to the model ([CARD] 模型详情: a Transformer with
+ * grouped key/value heads); the cache's format is this library's:
+ *
+ *   A cache holds n_blocks blocks of T tokens for KVH key/value heads of D
+ *   values:
+ *     K   int8 [n_blocks][KVH][T][D]     sk  fp32 [n_blocks][KVH]
+ *     V   int8 [n_blocks][KVH][D][T]     sv  fp32 [n_blocks][KVH]
+ *   (V transposed inside a block: both products of the attention then read 16
+ *   consecutive bytes per lane).  The key of head h in slot t of block b is
+ *   K[b][h][t][:] * sk[b][h]; V likewise.
+ *   T = 16, 32, 64 or 128; D = 64 or 128; 1 <= KVH <= 65535.
+ *
+ *   A call works on B sequences.  DEVICE arrays (int32, 4-byte aligned):
+ *     q_start [B + 1]  rows q_start[b] .. q_start[b + 1] - 1 of the call's
+ *                      n_tok rows are sequence b's new tokens, n_b of them
+ *                      (0 allowed); non-decreasing, within 0 .. n_tok.
+ *     lengths [B]      its length with the new tokens: row i of them stands
+ *                      at position lengths[b] - n_b + i.
+ *     table [B][max_blocks]  position p is in slot p % T of block
+ *                      table[b][p / T].
+ *   They are read by the kernels only, so a captured graph follows their
+ *   contents from replay to replay.  Values out of range stay harmless: a
+ *   block number outside 0 .. n_blocks - 1 and positions below 0 or at and
+ *   above max_blocks * T hold no token (nothing is written there, no query
+ *   sees them), q_start is taken within 0 .. n_tok.  Rows of no sequence are
+ *   neither read nor written.
+ */
+typedef struct {
+    int8_t *K, *V;             /* 16-byte aligned */
+    float *sk, *sv;            /* 4-byte aligned */
+    int64_t n_blocks, KVH, T, D;
+} bl_kv8;
+
+/* bitlinear_kv8_append -- the new tokens' rows into the cache.
+ *   k, v   in   [n_tok][KVH][D] of `dtype` (BL_F32 / BL_BF16), 16-byte aligned.
+ * Per block and head that gets new tokens, for K and for V: a = max |x| over
+ * the new rows' values there, d = fp32(a / 127).  If the block has earlier
+ * tokens of the sequence and their scale s is larger, d = s; if it is smaller
+ * (s < d), every code of the block becomes rne(fp32(code * fp32(s / d))).
+ * Then the scale is d and the new codes are clamp(rne(fp32(x / d)), -127,
+ * 127), 0 where d = 0.  Bit-exact.  Slots behind the sequence's length hold
+ * codes of no meaning, which are never used.
+ * Two sequences of one call must not get new tokens in the same block, and no
+ * other work may use the blocks that are written.
+ *   n_tok < 2^31, B < 2^24, max_blocks * T < 2^31.  n_tok == 0 or B == 0:
+ *   no-op.
+ */
+bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype dtype, int64_t n_tok,
+                               const int32_t *q_start, const int32_t *lengths,
+                               const int32_t *table, int64_t B, int64_t max_blocks,
+                               const bl_kv8 *cache, void *stream);
+
+/* bitlinear_kv8_attention -- causal attention of the new tokens' queries over
+ * their sequences' cached tokens (the new ones among them: append first).
+ *   q      in   [n_tok][QH][D] of `dtype`, 16-byte aligned; query head h reads
+ *               key/value head h / (QH / KVH); KVH divides QH, QH <= 65535.
+ *   scale       factor of the scores, e.g. 1 / sqrt(D); finite.
+ *   out    out  [n_tok][QH][D] of `dtype`, 16-byte aligned: for the row at
+ *               position p, sum_j softmax_j(scale q . key_j) value_j over the
+ *               tokens at 0 .. p.  A row that sees no token gives zeros.
+ *               May not overlap q.
+ *   ws          >= bitlinear_kv8_attention_ws_bytes(...) bytes, 16-byte
+ *               aligned (NULL allowed when that is 0): partial results of
+ *               sequences that are read in several parts.  Calls that may
+ *               overlap need a workspace each.
+ * The scores, the softmax and all sums are fp32; for fp32 rows every operand
+ * of a product is kept to 22 bits or more, for bf16 rows the softmax weights
+ * are rounded to 11 bits.  Deterministic for given sizes and contents.
+ * Limits as for the append, and n_tok * QH < 2^31.
+ */
+bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64_t n_tok, int64_t QH,
+                                  const int32_t *q_start, const int32_t *lengths,
+                                  const int32_t *table, int64_t B, int64_t max_blocks,
+                                  const bl_kv8 *cache, float scale, void *out, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/* Workspace bytes of bitlinear_kv8_attention; 0 also for sizes it refuses. */
+size_t bitlinear_kv8_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
+                                        int64_t KVH, int64_t T, int64_t D);
+
+/* ------------------------------------------------------------------------
+ * 4-bit weights with group scales -- for the layers that stay out of the
+ * ternary scheme (the output head, embeddings; [CARD] 模型详情 makes only the
+ * Transformer's linear layers BitLinears).  Format (this library's):
+ *   Wq4  uint8 [N][K/2] row-major: byte b of a row holds element 2b in bits
+ *        0..3 and element 2b+1 in bits 4..7, 4-bit two's complement (as Xq4).
+ *   s    bf16 [N][K/group], one scale per `group` consecutive elements of a
+ *        row; the weight is code * s.
+ *   group = 32, 64 or 128; K % group == 0; K <= BL_MAX_K; N < 2^31,
+ *   N * K <= 2^40.
+ *
+ * quant_weight_absmax_i4 -- W [N][K] of `dtype` -> Wq4, s.  Per group:
+ *   a = max |w|, s = bf16(fp32(a / 7)), code = clamp(rne(fp32(w / s)), -7, 7),
+ *   0 where s = 0.  Bit-exact.  (-8 is never produced.)
+ * dequant_weight_i4 -- the weights that the codes stand for, W [N][K] of
+ *   `dtype`: code * s (exact in fp32, one rounding for bf16).  -8 counts -8.
+ * All pointers 16-byte aligned except s, 4-byte aligned.  N * K == 0: no-op.
+ */
+bl_status quant_weight_absmax_i4(const void *W, bl_dtype dtype, int64_t N, int64_t K,
+                                 int64_t group, uint8_t *Wq4, uint16_t *s, void *stream);
+bl_status dequant_weight_i4(const uint8_t *Wq4, const uint16_t *s, int64_t N, int64_t K,
+                            int64_t group, void *W, bl_dtype dtype, void *stream);
+
+/* bitlinear_gemv_w4 -- Y = X W^T for M = 1..16 tokens, W in 4 bits.
+ *   X      in   [M][K] of `dtype`, 16-byte aligned (not quantised).
+ *   Wq4, s in   as above.
+ *   Y      out  fp32 [M][N] = sum over the groups of s * sum_k x code, 4-byte
+ *               aligned.
+ * Sums are fp32; x keeps 22 bits or more (fp32) or all its 8 (bf16) of the
+ * largest |x| of 128 consecutive elements.  M == 0 or N == 0: no-op; K == 0
+ * gives zeros.
+ */
+bl_status bitlinear_gemv_w4(const void *X, bl_dtype dtype, int64_t M, const uint8_t *Wq4,
+                            const uint16_t *s, int64_t N, int64_t K, int64_t group, float *Y,
+                            void *stream);
+
 /* Workspace bytes a call needs for the given sizes (0 for calls that need
  * none; arguments a call does not use are ignored). */
 size_t bl_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t F);

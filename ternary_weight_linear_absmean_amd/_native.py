@@ -7,6 +7,8 @@ pointers and the current HIP stream to the C entry point of the same name.
 Every step of the computation runs in libbitlinear's kernels.  There is no
 fallback: if the library is missing, ``load()`` raises.
 """
+import collections
+import contextlib
 import ctypes
 import os
 
@@ -30,6 +32,8 @@ EXPORTS = ["quant_weight_absmean_pack", "quant_weight_absmean_pack_noalloc", "qu
            "bitlinear_decode_stack", "bitlinear_decode_stack_status",
            "bitlinear_backward_input", "bitlinear_backward_weight",
            "bitlinear_t5_row_bytes", "bitlinear_repack_t5", "bitlinear_gemv_t5",
+           "bitlinear_kv8_append", "bitlinear_kv8_attention", "bitlinear_kv8_attention_ws_bytes",
+           "quant_weight_absmax_i4", "dequant_weight_i4", "bitlinear_gemv_w4",
            "bl_workspace_bytes", "bl_status_string", "bl_last_error", "bl_abi_version"]
 BL_OP_DECODE_STACK = 2
 BL_OP_BACKWARD_INPUT = 3
@@ -62,6 +66,18 @@ class GemvJob(ctypes.Structure):
                 ("Y", ctypes.c_void_p), ("Xq", ctypes.c_void_p), ("d", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class Kv8(ctypes.Structure):
+    """bl_kv8 (include/bitlinear.h)."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("sk", ctypes.c_void_p),
+                ("sv", ctypes.c_void_p), ("n_blocks", ctypes.c_int64), ("KVH", ctypes.c_int64),
+                ("T", ctypes.c_int64), ("D", ctypes.c_int64)]
+
+
+# An 8-bit key/value cache: K int8 [n_blocks, KVH, T, D], V int8 [n_blocks,
+# KVH, D, T], sk and sv fp32 [n_blocks, KVH].  Calls take any such 4-tuple.
+Kv8Cache = collections.namedtuple("Kv8Cache", ("K", "V", "sk", "sv"))
 
 _lib = None
 _p = ctypes.c_void_p
@@ -120,6 +136,21 @@ def load():
     lib.bitlinear_repack_t5.argtypes = [_p, _i64, _i64, _p, _p]
     lib.bitlinear_gemv_t5.restype = st
     lib.bitlinear_gemv_t5.argtypes = [_p, _p, _i64, _p, _p, _i64, _i64, _p, _p, _p]
+    i32 = ctypes.c_int
+    lib.bitlinear_kv8_append.restype = st
+    lib.bitlinear_kv8_append.argtypes = [_p, _p, i32, _i64, _p, _p, _p, _i64, _i64,
+                                         ctypes.POINTER(Kv8), _p]
+    lib.bitlinear_kv8_attention.restype = st
+    lib.bitlinear_kv8_attention.argtypes = [_p, i32, _i64, _i64, _p, _p, _p, _i64, _i64,
+                                            ctypes.POINTER(Kv8), ctypes.c_float, _p, _p, _sz, _p]
+    lib.bitlinear_kv8_attention_ws_bytes.restype = _sz
+    lib.bitlinear_kv8_attention_ws_bytes.argtypes = [_i64] * 7
+    lib.quant_weight_absmax_i4.restype = st
+    lib.quant_weight_absmax_i4.argtypes = [_p, i32, _i64, _i64, _i64, _p, _p, _p]
+    lib.dequant_weight_i4.restype = st
+    lib.dequant_weight_i4.argtypes = [_p, _p, _i64, _i64, _i64, _p, i32, _p]
+    lib.bitlinear_gemv_w4.restype = st
+    lib.bitlinear_gemv_w4.argtypes = [_p, i32, _i64, _p, _p, _i64, _i64, _i64, _p, _p]
     lib.bl_status_string.restype = ctypes.c_char_p
     lib.bl_status_string.argtypes = [ctypes.c_int]
     lib.bl_last_error.restype = ctypes.c_char_p
@@ -486,3 +517,199 @@ def bitlinear_backward_weight(dY, Xq, d, dW=None, ws=None, stream=None):
     _check("bitlinear_backward_weight", load().bitlinear_backward_weight(
         _ptr(dY), M, N, _ptr(Xq), _ptr(d), K, _ptr(dW), _ptr(ws), ws.numel(), _stream(stream)))
     return dW
+
+
+# The calls below run on their tensors' device whichever is current, and their
+# outputs and workspaces are allocated on the stream that the kernels run on.
+
+_DTYPES = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
+
+
+def _at(t, dtype, dev, shape, name):
+    """Address of tensor t, which must be contiguous, of dtype, on dev, of shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, dim, name):
+    """Device and bl_dtype of an fp32 / bf16 tensor with dim dimensions on the GPU."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {list(t.shape)}")
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return t.device, dt
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _where(dev, stream):
+    """The HIP stream to run on, and the context to allocate and launch in."""
+    if stream is None:
+        on = torch.cuda.current_stream(dev)
+        return on.cuda_stream, (_NOTHING if dev.index == torch.cuda.current_device()
+                                else torch.cuda.device(dev))
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def kv8_cache(n_blocks, KVH, T=64, D=128, device="cuda"):
+    """A zeroed Kv8Cache."""
+    def z(*shape, dtype):
+        return torch.zeros(shape, dtype=dtype, device=device)
+    return Kv8Cache(z(n_blocks, KVH, T, D, dtype=torch.int8), z(n_blocks, KVH, D, T, dtype=torch.int8),
+                    z(n_blocks, KVH, dtype=torch.float32), z(n_blocks, KVH, dtype=torch.float32))
+
+
+def _kv8(cache, dev):
+    K, V, sk, sv = cache
+    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise ValueError("the cache's K must be a tensor [n_blocks, KVH, T, D]")
+    nb, KVH, T, D = K.shape
+    return Kv8(_at(K, torch.int8, dev, (nb, KVH, T, D), "cache K"),
+               _at(V, torch.int8, dev, (nb, KVH, D, T), "cache V"),
+               _at(sk, torch.float32, dev, (nb, KVH), "cache sk"),
+               _at(sv, torch.float32, dev, (nb, KVH), "cache sv"), nb, KVH, T, D)
+
+
+def _seqs(q_start, lengths, table, dev):
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be a tensor [B, max_blocks]")
+    B, nb = table.shape
+    return (_at(q_start, torch.int32, dev, (B + 1,), "q_start"),
+            _at(lengths, torch.int32, dev, (B,), "lengths"),
+            _at(table, torch.int32, dev, (B, nb), "table"), B, nb)
+
+
+def bitlinear_kv8_append(k, v, q_start, lengths, table, cache, stream=None):
+    """The new tokens' rows k, v [n_tok, KVH, D] (fp32 or bf16) into the cache
+    (Kv8Cache, updated in place).  int32 on the GPU: q_start [B + 1], lengths
+    [B] (with the new tokens), table [B, max_blocks]."""
+    dev, dt = _rows(k, 3, "k")
+    c = _kv8(cache, dev)
+    n = k.shape[0]
+    shape = (n, c.KVH, c.D)
+    kp, vp = _at(k, k.dtype, dev, shape, "k"), _at(v, k.dtype, dev, shape, "v")
+    meta = _seqs(q_start, lengths, table, dev)
+    handle, context = _where(dev, stream)
+    with context:
+        st = load().bitlinear_kv8_append(kp, vp, dt, n, *meta, c, handle)
+    if st:
+        _check("bitlinear_kv8_append", st)
+
+
+def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
+                            stream=None):
+    """Causal attention of q [n_tok, QH, D] (fp32 or bf16) over the cache:
+    out [n_tok, QH, D].  scale defaults to D ** -0.5; q_start, lengths, table
+    as for bitlinear_kv8_append.  Rows of no sequence are left as they are."""
+    dev, dt = _rows(q, 3, "q")
+    c = _kv8(cache, dev)
+    n, QH, D = q.shape
+    qp = _at(q, q.dtype, dev, (n, QH, c.D), "q")
+    meta = _seqs(q_start, lengths, table, dev)
+    if out is not None:
+        _at(out, q.dtype, dev, (n, QH, D), "out")
+    if ws is not None:
+        _at(ws, torch.uint8, dev, (ws.numel(),), "ws")
+    lib = load()
+    handle, context = _where(dev, stream)
+    with context:
+        if ws is None:
+            need = lib.bitlinear_kv8_attention_ws_bytes(n, QH, meta[3], meta[4], c.KVH, c.T, D)
+            if need:
+                ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+        if out is None:
+            out = torch.empty_like(q)
+        st = lib.bitlinear_kv8_attention(
+            qp, dt, n, QH, *meta, c, D ** -0.5 if scale is None else scale, out.data_ptr(),
+            ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, handle)
+    if st:
+        _check("bitlinear_kv8_attention", st)
+    return out
+
+
+def quant_weight_absmax_i4(W, group=128, Wq4=None, s=None, stream=None):
+    """W [N, K] (fp32 or bf16) -> (Wq4 uint8 [N, K/2] 4-bit codes, s bf16
+    [N, K/group]); group 32, 64 or 128."""
+    dev, dt = _rows(W, 2, "W")
+    N, K = W.shape
+    if group not in (32, 64, 128) or K % group:
+        raise ValueError(f"group must be 32, 64 or 128 and divide K = {K}, got {group}")
+    wp = _at(W, W.dtype, dev, (N, K), "W")
+    handle, context = _where(dev, stream)
+    with context:
+        if Wq4 is None:
+            Wq4 = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
+        if s is None:
+            s = torch.empty((N, K // group), dtype=torch.bfloat16, device=dev)
+        st = load().quant_weight_absmax_i4(
+            wp, dt, N, K, group, _at(Wq4, torch.uint8, dev, (N, K // 2), "Wq4"),
+            _at(s, torch.bfloat16, dev, (N, K // group), "s"), handle)
+    if st:
+        _check("quant_weight_absmax_i4", st)
+    return Wq4, s
+
+
+def _w4(Wq4, s):
+    """(device, N, K, group, addresses) of 4-bit weights."""
+    if not isinstance(Wq4, torch.Tensor) or not Wq4.is_cuda:
+        raise TypeError("Wq4 must be a CUDA (HIP) tensor")
+    if Wq4.dim() != 2 or not isinstance(s, torch.Tensor) or s.dim() != 2:
+        raise ValueError("Wq4 must be [N, K/2] and s [N, K/group]")
+    (N, K2), groups, dev = Wq4.shape, s.shape[1], Wq4.device
+    group = 2 * K2 // groups if groups else 128
+    if 2 * K2 != group * groups or group not in (32, 64, 128):
+        raise ValueError(f"Wq4 {list(Wq4.shape)} and s {list(s.shape)} do not make groups of 32, "
+                         "64 or 128")
+    return (dev, N, 2 * K2, group, _at(Wq4, torch.uint8, dev, (N, K2), "Wq4"),
+            _at(s, torch.bfloat16, dev, (N, groups), "s"))
+
+
+def dequant_weight_i4(Wq4, s, dtype=torch.float32, W=None, stream=None):
+    """The weights [N, K] of dtype (fp32 or bf16) that 4-bit codes stand for."""
+    dev, N, K, group, wp, sp = _w4(Wq4, s)
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be float32 or bfloat16")
+    handle, context = _where(dev, stream)
+    with context:
+        if W is None:
+            W = torch.empty((N, K), dtype=dtype, device=dev)
+        st = load().dequant_weight_i4(wp, sp, N, K, group, _at(W, dtype, dev, (N, K), "W"),
+                                      _DTYPES[dtype], handle)
+    if st:
+        _check("dequant_weight_i4", st)
+    return W
+
+
+def bitlinear_gemv_w4(X, Wq4, s, Y=None, stream=None):
+    """Y [M, N] fp32 = X W^T for X [M, K] (fp32 or bf16), 1 <= M <= 16, and
+    4-bit weights (Wq4 [N, K/2], s [N, K/group])."""
+    dev, dt = _rows(X, 2, "X")
+    wdev, N, K, group, wp, sp = _w4(Wq4, s)
+    M = X.shape[0]
+    if wdev != dev:
+        raise ValueError(f"Wq4 is on {wdev}, not on {dev}")
+    xp = _at(X, X.dtype, dev, (M, K), "X")
+    handle, context = _where(dev, stream)
+    with context:
+        if Y is None:
+            Y = torch.empty((M, N), dtype=torch.float32, device=dev)
+        st = load().bitlinear_gemv_w4(xp, dt, M, wp, sp, N, K, group,
+                                      _at(Y, torch.float32, dev, (M, N), "Y"), handle)
+    if st:
+        _check("bitlinear_gemv_w4", st)
+    return Y

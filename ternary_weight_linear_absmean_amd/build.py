@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libbitlinear.so")
 
 SOURCES = ["api.cpp", "quant.hip", "gemv.hip", "gemm.hip", "gemm_skinny.hip", "ffn.hip",
-           "stack.hip", "stack_persistent.hip", "backward.hip", "t5.hip"]
+           "stack.hip", "stack_persistent.hip", "backward.hip", "t5.hip",
+           "kv8.hip", "kv8_attention.hip", "w4.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

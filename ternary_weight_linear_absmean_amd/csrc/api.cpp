@@ -654,3 +654,194 @@ BL_EXPORT bl_status bitlinear_gemv_t5(const int8_t *Xq, const float *d, int64_t 
                                        static_cast<hipStream_t>(stream)),
                     name);
 }
+
+// Shared checks of the two calls on the 8-bit cache (rows: k or q; rows2: v or
+// out); *noop is set when there is no row.
+static bl_status check_kv8(const char *name, const void *rows, const void *rows2, bl_dtype dtype,
+                           int64_t n_tok, const int32_t *q_start, const int32_t *lengths,
+                           const int32_t *table, int64_t B, int64_t max_blocks,
+                           const bl_kv8 *c, bool *noop) {
+    *noop = false;
+    if (!c)
+        return fail(BL_ERR_NULL, "%s: cache is NULL", name);
+    if ((c->T != 16 && c->T != 32 && c->T != 64 && c->T != 128) || (c->D != 64 && c->D != 128))
+        return fail(BL_ERR_SHAPE, "%s: need T = 16, 32, 64 or 128 and D = 64 or 128 (T=%lld D=%lld)",
+                    name, (long long)c->T, (long long)c->D);
+    if (c->KVH < 1 || c->KVH > 65535 || c->n_blocks < 0 || c->n_blocks > kI32Max)
+        return fail(BL_ERR_SHAPE, "%s: need KVH in [1, 65535], n_blocks in [0, 2^31) (KVH=%lld "
+                    "n_blocks=%lld)", name, (long long)c->KVH, (long long)c->n_blocks);
+    if (n_tok < 0 || n_tok > kI32Max || B < 0 || B >= (1 << 24) || max_blocks < 0 ||
+        max_blocks > kI32Max / c->T)
+        return fail(BL_ERR_SHAPE, "%s: need n_tok in [0, 2^31), B in [0, 2^24), max_blocks * T in "
+                    "[0, 2^31) (n_tok=%lld B=%lld max_blocks=%lld)", name, (long long)n_tok,
+                    (long long)B, (long long)max_blocks);
+    if (dtype != BL_F32 && dtype != BL_BF16)
+        return fail(BL_ERR_DTYPE, "%s: unknown dtype %d", name, (int)dtype);
+    if (n_tok == 0 || B == 0) {
+        *noop = true;
+        return ok();
+    }
+    if (!rows || !rows2 || !q_start || !lengths || (max_blocks > 0 && !table) ||
+        (c->n_blocks > 0 && (!c->K || !c->V || !c->sk || !c->sv)))
+        return fail(BL_ERR_NULL, "%s: NULL pointer (rows=%p %p q_start=%p lengths=%p table=%p K=%p "
+                    "V=%p sk=%p sv=%p)", name, rows, rows2, (const void *)q_start,
+                    (const void *)lengths, (const void *)table, (void *)c->K, (void *)c->V,
+                    (void *)c->sk, (void *)c->sv);
+    if (!aligned(rows, 16) || !aligned(rows2, 16) || !aligned(c->K, 16) || !aligned(c->V, 16))
+        return fail(BL_ERR_ALIGN, "%s: rows, K and V must be 16-byte aligned", name);
+    if (!aligned(q_start, 4) || !aligned(lengths, 4) || !aligned(table, 4) ||
+        !aligned(c->sk, 4) || !aligned(c->sv, 4))
+        return fail(BL_ERR_ALIGN, "%s: q_start, lengths, table, sk and sv must be 4-byte aligned",
+                    name);
+    return BL_OK;
+}
+
+BL_EXPORT bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype dtype,
+                                         int64_t n_tok, const int32_t *q_start,
+                                         const int32_t *lengths, const int32_t *table, int64_t B,
+                                         int64_t max_blocks, const bl_kv8 *cache, void *stream) {
+    const char *name = "bitlinear_kv8_append";
+    bool noop = false;
+    bl_status st = check_kv8(name, k, v, dtype, n_tok, q_start, lengths, table, B, max_blocks,
+                             cache, &noop);
+    if (st != BL_OK || noop)
+        return st;
+    st = check_arch();
+    if (st != BL_OK)
+        return st;
+    const bl::Kv8Seqs seqs = {q_start, lengths, table, (int)n_tok, (int)B, (int)max_blocks};
+    return launched(bl::launch_kv8_append(k, v, dtype == BL_BF16 ? 1 : 0, seqs, *cache,
+                                          static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+BL_EXPORT size_t bitlinear_kv8_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B,
+                                                  int64_t max_blocks, int64_t KVH, int64_t T,
+                                                  int64_t D) {
+    if (n_tok <= 0 || B <= 0 || B >= (1 << 24) || QH < 1 || QH > 65535 || KVH < 1 || QH % KVH != 0 ||
+        n_tok > kI32Max / QH || (T != 16 && T != 32 && T != 64 && T != 128) ||
+        (D != 64 && D != 128) || max_blocks < 0 || max_blocks > kI32Max / T)
+        return 0;
+    return round_up(bl::kv8_attention_ws_floats(n_tok, QH, B, max_blocks, KVH, T, D) * sizeof(float),
+                    256);
+}
+
+BL_EXPORT bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64_t n_tok,
+                                            int64_t QH, const int32_t *q_start,
+                                            const int32_t *lengths, const int32_t *table,
+                                            int64_t B, int64_t max_blocks, const bl_kv8 *cache,
+                                            float scale, void *out, void *ws, size_t ws_bytes,
+                                            void *stream) {
+    const char *name = "bitlinear_kv8_attention";
+    bool noop = false;
+    bl_status st = check_kv8(name, q, out, dtype, n_tok, q_start, lengths, table, B, max_blocks,
+                             cache, &noop);
+    if (st != BL_OK)
+        return st;
+    if (QH < 1 || QH > 65535 || QH % cache->KVH != 0 || n_tok > kI32Max / QH)
+        return fail(BL_ERR_SHAPE, "%s: need QH in [1, 65535], a multiple of KVH, n_tok * QH < 2^31 "
+                    "(QH=%lld KVH=%lld n_tok=%lld)", name, (long long)QH, (long long)cache->KVH,
+                    (long long)n_tok);
+    if (!(scale - scale == 0.0f))
+        return fail(BL_ERR_SHAPE, "%s: scale must be finite", name);
+    if (noop)
+        return ok();
+    const size_t need = bitlinear_kv8_attention_ws_bytes(n_tok, QH, B, max_blocks, cache->KVH,
+                                                         cache->T, cache->D);
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(BL_ERR_WORKSPACE, "%s: workspace %zu bytes at %p, need %zu", name, ws_bytes, ws,
+                    need);
+    if (!aligned(ws, 16))
+        return fail(BL_ERR_ALIGN, "%s: ws must be 16-byte aligned", name);
+    st = check_arch();
+    if (st != BL_OK)
+        return st;
+    const bl::Kv8Seqs seqs = {q_start, lengths, table, (int)n_tok, (int)B, (int)max_blocks};
+    return launched(bl::launch_kv8_attention(q, dtype == BL_BF16 ? 1 : 0, (int)QH, seqs, *cache,
+                                             scale, out, static_cast<float *>(ws),
+                                             static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+// Shared checks of the calls on 4-bit weights (K == 0 and empty N pass).
+static bl_status check_w4(const char *name, bl_dtype dtype, int64_t N, int64_t K, int64_t group) {
+    if (group != 32 && group != 64 && group != 128)
+        return fail(BL_ERR_SHAPE, "%s: group=%lld must be 32, 64 or 128", name, (long long)group);
+    if (N < 0 || N > kI32Max || K < 0 || K > BL_MAX_K || K % group != 0 ||
+        N * K > ((int64_t)1 << 40))
+        return fail(BL_ERR_SHAPE, "%s: need N in [0, 2^31), K in [0, %d], K %% group == 0, "
+                    "N*K <= 2^40 (N=%lld K=%lld group=%lld)", name, BL_MAX_K, (long long)N,
+                    (long long)K, (long long)group);
+    if (dtype != BL_F32 && dtype != BL_BF16)
+        return fail(BL_ERR_DTYPE, "%s: unknown dtype %d", name, (int)dtype);
+    return BL_OK;
+}
+
+static bl_status check_w4_ptrs(const char *name, const void *W, const uint8_t *Wq4,
+                               const uint16_t *s) {
+    if (!W || !Wq4 || !s)
+        return fail(BL_ERR_NULL, "%s: NULL pointer (W=%p Wq4=%p s=%p)", name, W, (const void *)Wq4,
+                    (const void *)s);
+    if (!aligned(W, 16) || !aligned(Wq4, 16) || !aligned(s, 4))
+        return fail(BL_ERR_ALIGN, "%s: W and Wq4 must be 16-byte aligned, s 4-byte", name);
+    return check_arch();
+}
+
+BL_EXPORT bl_status quant_weight_absmax_i4(const void *W, bl_dtype dtype, int64_t N, int64_t K,
+                                           int64_t group, uint8_t *Wq4, uint16_t *s,
+                                           void *stream) {
+    const char *name = "quant_weight_absmax_i4";
+    bl_status st = check_w4(name, dtype, N, K, group);
+    if (st != BL_OK)
+        return st;
+    if (N == 0 || K == 0)
+        return ok();
+    st = check_w4_ptrs(name, W, Wq4, s);
+    if (st != BL_OK)
+        return st;
+    return launched(bl::launch_quant_weight_i4(W, dtype == BL_BF16 ? 1 : 0, N, K, (int)group, Wq4,
+                                               s, static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+BL_EXPORT bl_status dequant_weight_i4(const uint8_t *Wq4, const uint16_t *s, int64_t N, int64_t K,
+                                      int64_t group, void *W, bl_dtype dtype, void *stream) {
+    const char *name = "dequant_weight_i4";
+    bl_status st = check_w4(name, dtype, N, K, group);
+    if (st != BL_OK)
+        return st;
+    if (N == 0 || K == 0)
+        return ok();
+    st = check_w4_ptrs(name, W, Wq4, s);
+    if (st != BL_OK)
+        return st;
+    return launched(bl::launch_dequant_weight_i4(Wq4, s, N, K, (int)group, W,
+                                                 dtype == BL_BF16 ? 1 : 0,
+                                                 static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+BL_EXPORT bl_status bitlinear_gemv_w4(const void *X, bl_dtype dtype, int64_t M,
+                                      const uint8_t *Wq4, const uint16_t *s, int64_t N, int64_t K,
+                                      int64_t group, float *Y, void *stream) {
+    const char *name = "bitlinear_gemv_w4";
+    bl_status st = check_w4(name, dtype, N, K, group);
+    if (st != BL_OK)
+        return st;
+    if (M < 0 || M > bl::kW4MaxTokens)
+        return fail(BL_ERR_SHAPE, "%s: M=%lld must be in [0, %d]", name, (long long)M,
+                    bl::kW4MaxTokens);
+    if (M == 0 || N == 0)
+        return ok();
+    if (!Y || (K > 0 && (!X || !Wq4 || !s)))
+        return fail(BL_ERR_NULL, "%s: NULL pointer (X=%p Wq4=%p s=%p Y=%p)", name, X,
+                    (const void *)Wq4, (const void *)s, (void *)Y);
+    if ((K > 0 && (!aligned(X, 16) || !aligned(Wq4, 16) || !aligned(s, 4))) || !aligned(Y, 4))
+        return fail(BL_ERR_ALIGN, "%s: X and Wq4 must be 16-byte aligned, s and Y 4-byte", name);
+    st = check_arch();
+    if (st != BL_OK)
+        return st;
+    return launched(bl::launch_gemv_w4(X, dtype == BL_BF16 ? 1 : 0, (int)M, Wq4, s, (int)N, (int)K,
+                                       (int)group, Y, static_cast<hipStream_t>(stream)),
+                    name);
+}

@@ -173,4 +173,29 @@ hipError_t launch_ffn_tail(const float *G, const float *U, const float *norm_w,
                            float eps, int M, int F, int8_t *Hq, float *dh, float *dz,
                            hipStream_t s);
 
+// 8-bit key/value cache (kv8.hip).  The metadata arrays of a call; every
+// pointer is a device pointer, every value in them may be anything.
+struct Kv8Seqs {
+    const int32_t *q_start, *lengths, *table;
+    int n_tok, B, max_blocks;
+};
+hipError_t launch_kv8_append(const void *k, const void *v, int dtype, const Kv8Seqs &seqs,
+                             const bl_kv8 &cache, hipStream_t s);
+// Attention over the cache (kv8_attention.hip); ws holds
+// kv8_attention_ws_floats() floats.
+size_t kv8_attention_ws_floats(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
+                               int64_t KVH, int64_t T, int64_t D);
+hipError_t launch_kv8_attention(const void *q, int dtype, int QH, const Kv8Seqs &seqs,
+                                const bl_kv8 &cache, float scale, void *out, float *ws,
+                                hipStream_t s);
+
+// 4-bit weights with group scales (w4.hip); group = 32, 64 or 128.
+hipError_t launch_quant_weight_i4(const void *W, int dtype, int64_t N, int64_t K, int group,
+                                  uint8_t *Wq4, uint16_t *s4, hipStream_t s);
+hipError_t launch_dequant_weight_i4(const uint8_t *Wq4, const uint16_t *s4, int64_t N, int64_t K,
+                                    int group, void *W, int dtype, hipStream_t s);
+constexpr int kW4MaxTokens = 16;
+hipError_t launch_gemv_w4(const void *X, int dtype, int M, const uint8_t *Wq4, const uint16_t *s4,
+                          int N, int K, int group, float *Y, hipStream_t s);
+
 }  // namespace bl

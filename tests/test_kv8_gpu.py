@@ -1,0 +1,374 @@
+"""The 8-bit key/value cache and the attention over it against the 64-bit
+oracle: the cache's bytes and scales exactly, the attention within a bound
+from its arithmetic."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv8 as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def make(seed, n, lens, T, D, KVH, dtype, G=1, spare=3, behind=0, before=0):
+    """A filled cache, the new rows and the arrays of a call: sequence b has
+    lens[b] tokens, n[b] of them new; `before` / `behind` rows of no sequence."""
+    g = torch.Generator().manual_seed(seed)
+    need = [max(0, -(-x // T)) for x in lens]
+    nb = sum(need) + spare
+    order = torch.randperm(nb, generator=g).tolist()
+    table = torch.full((len(n), max(need + [1]) + 1), -1, dtype=torch.int32)
+    for b, m in enumerate(need):
+        for j in range(m):
+            table[b, j] = order.pop()
+    rows = before + sum(n) + behind
+    q_start = torch.tensor([before] + [before + sum(n[:b + 1]) for b in range(len(n))], dtype=torch.int32)
+
+    def codes(*shape):
+        return torch.randint(-127, 128, shape, generator=g).to(torch.int8)
+
+    def scales():
+        return (0.5 + torch.rand(nb, KVH, generator=g)) / 40
+    s = dict(K=codes(nb, KVH, T, D), V=codes(nb, KVH, D, T), sk=scales(), sv=scales(), table=table,
+             q_start=q_start, lengths=torch.tensor(lens, dtype=torch.int32),
+             k=torch.randn(rows, KVH, D, generator=g).to(dtype),
+             v=torch.randn(rows, KVH, D, generator=g).to(dtype),
+             q=torch.randn(rows, KVH * G, D, generator=g).to(dtype))
+    return s
+
+
+def cuda(s):
+    return {k: v.cuda() for k, v in s.items()}
+
+
+def cache(bl, s):
+    return bl.Kv8Cache(s["K"], s["V"], s["sk"], s["sv"])
+
+
+def append(bl, s, **kw):
+    bl.bitlinear_kv8_append(s["k"], s["v"], s["q_start"], s["lengths"], s["table"], cache(bl, s), **kw)
+
+
+def attend(bl, s, **kw):
+    return bl.bitlinear_kv8_attention(s["q"], s["q_start"], s["lengths"], s["table"], cache(bl, s), **kw)
+
+
+def n64(t):
+    return t.double().cpu().numpy()
+
+
+def check_append(bl, s):
+    d = cuda(s)
+    append(bl, d)
+    K, V = s["K"].numpy().copy(), s["V"].numpy().transpose(0, 1, 3, 2).copy()
+    sk, sv = s["sk"].numpy().copy(), s["sv"].numpy().copy()
+    meta = s["q_start"].numpy(), s["lengths"].numpy(), s["table"].numpy()
+    ref.append(n64(s["k"]), K, sk, *meta)
+    ref.append(n64(s["v"]), V, sv, *meta)
+    assert np.array_equal(d["sk"].cpu().numpy(), sk, equal_nan=True)
+    assert np.array_equal(d["sv"].cpu().numpy(), sv, equal_nan=True)
+    assert np.array_equal(d["K"].cpu().numpy(), K)
+    assert np.array_equal(d["V"].cpu().numpy(), V.transpose(0, 1, 3, 2))
+    return d
+
+
+def check_attention(s, got, scale=None):
+    """A score is off by at most reach * (2^-21 for the operands' 22 bits + (D +
+    8) 2^-24 for the sum), which moves every weight by twice that; weights and
+    sums add (keys + 64) 2^-24 of sum p |v|; bf16 rows' weights are rounded to
+    11 bits (2^-11) and the result to bf16 (2^-8 of it).  What is held in 16
+    bits has a smallest step too: 2^-38 of a row's largest |q| (a score moves
+    by `far` of it), and 2^-38 of the largest weight times value scale, each
+    code at most 128: keys 2^-31 max sv."""
+    D = s["q"].shape[2]
+    scale = D ** -0.5 if scale is None else scale
+    out, wide, reach, far = ref.attention(n64(s["q"]), s["K"].cpu().numpy(), s["V"].cpu().numpy(),
+                                     s["sk"].cpu().numpy(), s["sv"].cpu().numpy(),
+                                     s["q_start"].cpu().numpy(), s["lengths"].cpu().numpy(),
+                                     s["table"].cpu().numpy(), scale)
+    keys = min(max(int(x) for x in s["lengths"]), s["table"].shape[1] * s["K"].shape[2])
+    ds = reach * (2.0 ** -21 + (D + 8) * 2.0 ** -24) + far * 2.0 ** -38
+    sv = s["sv"].cpu()
+    sv = float(sv[torch.isfinite(sv)].max())
+    tol = wide * (2 * ds[..., None] + (keys + 64) * 2.0 ** -24) + keys * 2.0 ** -31 * sv
+    if s["q"].dtype == BF16:
+        tol = tol + wide * 2.0 ** -11
+        tol = tol + (np.abs(out) + tol) * 2.0 ** -8
+    got = n64(got)
+    used = ~np.isnan(out)
+    assert np.isfinite(got[used]).all()
+    worst = np.max((np.abs(got - out) - tol)[used], initial=-1.0)
+    assert worst <= 0, worst
+    return used
+
+
+CASES = [
+    # n, lens, T, D, KVH, G
+    ([1], [1], 64, 128, 5, 4),
+    ([1], [2], 16, 64, 1, 1),
+    ([1], [200], 64, 128, 5, 4),
+    ([1, 1, 1], [64, 65, 63], 64, 128, 2, 4),
+    ([1] * 7, [1, 17, 16, 15, 128, 129, 300], 16, 64, 3, 7),
+    ([1] * 70, [3 + 5 * i for i in range(70)], 32, 128, 1, 2),
+    ([5, 3, 1, 0, 2], [5, 130, 77, 20, 2], 32, 64, 2, 4),
+    ([40, 1, 90], [100, 31, 90], 16, 128, 2, 3),
+    ([130], [259], 128, 64, 2, 1),
+    ([129, 7], [300, 7], 128, 128, 1, 8),
+    ([0, 0, 1, 0], [0, 9, 33, 0], 64, 64, 2, 16),
+    ([2], [50], 64, 128, 1, 40),
+    ([300], [300], 64, 128, 1, 4),
+    ([33], [600], 64, 64, 3, 4),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_append_is_exact(gpu, case, dtype):
+    n, lens, T, D, KVH, G = CASES[case]
+    check_append(gpu, make(case, n, lens, T, D, KVH, dtype, before=case % 3, behind=(case + 1) % 3))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention(gpu, case, dtype):
+    n, lens, T, D, KVH, G = CASES[case]
+    s = make(case, n, lens, T, D, KVH, dtype, G, before=case % 3, behind=(case + 1) % 3)
+    d = cuda(s)
+    out = torch.full_like(d["q"], 77.0)
+    assert attend(gpu, d, out=out) is out
+    used = check_attention(s, out)
+    # rows of no sequence stay
+    assert (out.cpu().float().numpy()[~used] == 77.0).all()
+    again = attend(gpu, d)
+    assert np.array_equal(again.cpu().float().numpy()[used], out.cpu().float().numpy()[used])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_long_sequence_in_parts(gpu, dtype):
+    s = make(5, [1, 1, 6], [9000, 4097, 8191], 64, 128, 2, dtype, 4)
+    check_attention(s, attend(gpu, cuda(s)))
+
+
+@pytest.mark.parametrize("n,lens", [([1] * 3, [500, 1, 90]), ([70, 20, 30], [300, 20, 31])])
+def test_what_is_masked_never_shows(gpu, n, lens):
+    """NaN and infinite scales and any codes in blocks and slots behind a
+    length, in spare blocks and in blocks that no valid entry names."""
+    s = make(9, n, lens, 32, 64, 2, F32, 4, spare=8)
+    want = attend(gpu, cuda(s))
+    used = {int(s["table"][b, j]) for b in range(len(n)) for j in range(-(-lens[b] // 32))}
+    free = [i for i in range(len(s["sk"])) if i not in used]
+    s["sk"][free] = float("nan")
+    s["sv"][free] = float("inf")
+    s["table"][s["table"] < 0] = free[0]
+    for b in range(len(n)):
+        if lens[b] % 32:
+            i = int(s["table"][b, lens[b] // 32])
+            s["K"][i, :, lens[b] % 32:] = -128
+            s["V"][i, :, :, lens[b] % 32:] = -128
+    got = attend(gpu, cuda(s))
+    assert torch.equal(want, got)
+
+
+@pytest.mark.parametrize("n", [[1, 1, 1], [40, 2, 3]])
+def test_blocks_out_of_range_hold_nothing(gpu, n):
+    lens = [200, 40, 90]
+    s = make(11, n, lens, 16, 64, 2, F32, 2)
+    s["table"][0, 2] = -5
+    s["table"][0, 5] = len(s["K"])
+    s["table"][0, 12] = 2 ** 31 - 1            # the block of the newest tokens
+    s["table"][2, :] = -2 ** 31                # a sequence without any token
+    check_append(gpu, s)
+    out = attend(gpu, cuda(s))
+    check_attention(s, out)
+    assert (out[-n[2]:] == 0).all()
+
+
+@pytest.mark.parametrize("n", [[3, 1, 2], [50, 2, 30]])
+def test_odd_lengths_and_starts(gpu, n):
+    """Lengths below the new tokens' number, zero, negative, beyond the table;
+    starts beyond the rows."""
+    s = make(12, n, [max(3, x - 2) for x in n], 16, 64, 1, F32, 2)
+    s["lengths"] = torch.tensor([n[0] - 2, 0, s["table"].shape[1] * 16 + 5], dtype=torch.int32)
+    s["table"] = torch.arange(s["table"].numel(), dtype=torch.int32).view(s["table"].shape) % len(s["K"])
+    s["table"][2] = s["table"][0]
+    d = cuda(s)
+    check_attention(s, attend(gpu, d))
+    s["lengths"][2] = 0
+    check_append(gpu, s)
+    s["lengths"] = torch.tensor([-7, -2 ** 31, 2 ** 31 - 1], dtype=torch.int32)
+    check_attention(s, attend(gpu, cuda(s)))
+    s["q_start"][3] = 2 ** 31 - 1
+    s["q_start"][0] = -9
+    s["lengths"] = torch.tensor([n[0] - 2, 0, 17], dtype=torch.int32)
+    check_attention(s, attend(gpu, cuda(s)))
+
+
+def test_extreme_scales_and_scores(gpu):
+    """Zero and very different scales from block to block, scores far apart."""
+    s = make(13, [1, 60], [400, 60], 16, 64, 2, F32, 4)
+    s["sv"][::3] = 0
+    s["sv"][1::3] *= 1e-7
+    s["sk"][::4] = 0
+    s["sk"][1::4] *= 30
+    check_attention(s, attend(gpu, cuda(s)))
+    s["q"][0] *= 1e-30
+    s["q"][1:] *= 1e3
+    check_attention(s, attend(gpu, cuda(s)))
+    s["q"][0] = 0
+    check_attention(s, attend(gpu, cuda(s), scale=-0.7), scale=-0.7)
+    check_attention(s, attend(gpu, cuda(s), scale=0.0), scale=0.0)
+
+
+def test_append_zero_tiny_and_growing(gpu):
+    s = make(14, [3, 20], [9, 40], 16, 64, 2, F32)
+    s["k"][:] = 0                              # nothing new above the old scale
+    s["v"][:3] = 1e-42                         # a / 127 underflows
+    d = check_append(gpu, s)
+    s = {k: v.cpu() for k, v in d.items()}
+    s["v"] *= 1e3
+    s["k"][:] = torch.linspace(-200, 200, s["k"].numel()).view(s["k"].shape)
+    check_append(gpu, s)
+
+
+def test_append_twice_is_append_once(gpu):
+    s = cuda(make(15, [1] * 9 + [100], [5 * i + 1 for i in range(9)] + [150], 64, 128, 3, BF16))
+    append(gpu, s)
+    once = {k: v.clone() for k, v in s.items()}
+    append(gpu, s)
+    assert all(torch.equal(s[k], once[k]) for k in ("K", "V", "sk", "sv"))
+
+
+def test_offsets_past_32_bits(gpu):
+    """Blocks whose bytes start behind 2^32."""
+    T, D, KVH = 128, 128, 8
+    nb = 2 ** 32 // (T * D * KVH) + 40
+    s = make(16, [1, 20], [260, 300], T, D, KVH, F32, 4)
+    small = {k: v.clone() for k, v in s.items()}
+    s = cuda(s)
+    ids = torch.randperm(40, generator=torch.Generator().manual_seed(1))[:len(s["sk"])].cuda() + nb - 40
+    for name in ("K", "V", "sk", "sv"):
+        big = torch.empty((nb,) + s[name].shape[1:], dtype=s[name].dtype, device="cuda")
+        big[ids] = s[name]
+        s[name] = big
+    s["table"] = torch.where(s["table"] >= 0, ids[s["table"].clamp(min=0)].int(), s["table"])
+    append(gpu, s)
+    want = check_append(gpu, small)
+    for name in ("K", "V", "sk", "sv"):
+        assert torch.equal(s[name][ids], want[name])
+    assert torch.equal(attend(gpu, s), attend(gpu, want))
+
+
+def test_a_step_after_another(gpu):
+    """Prompt, then single tokens: append and attend, as a decode loop does,
+    the cache against the oracle's after every step."""
+    bl, T, D, KVH, G = gpu, 16, 64, 2, 4
+    g = torch.Generator().manual_seed(3)
+    c = bl.kv8_cache(12, KVH, T, D)
+    K, V = np.zeros((12, KVH, T, D), np.int8), np.zeros((12, KVH, T, D), np.int8)
+    sk, sv = np.zeros((12, KVH), np.float32), np.zeros((12, KVH), np.float32)
+    table = torch.randperm(12, generator=g).int().view(2, 6)
+    lens = [0, 0]
+    for n in [[21, 5]] + [[1, 1]] * 14 + [[3, 0], [0, 4]]:
+        lens = [a + b for a, b in zip(lens, n)]
+        s = dict(q_start=torch.tensor([0, n[0], sum(n)], dtype=torch.int32),
+                 lengths=torch.tensor(lens, dtype=torch.int32), table=table)
+        for x, heads in (("q", KVH * G), ("k", KVH), ("v", KVH)):
+            s[x] = torch.randn(sum(n), heads, D, generator=g) * (1 + lens[0] / 20)
+        d = dict(cuda(s), K=c.K, V=c.V, sk=c.sk, sv=c.sv)
+        append(bl, d)
+        out = attend(bl, d)
+        meta = s["q_start"].numpy(), s["lengths"].numpy(), s["table"].numpy()
+        ref.append(n64(s["k"]), K, sk, *meta)
+        ref.append(n64(s["v"]), V, sv, *meta)
+        assert np.array_equal(c.K.cpu().numpy(), K)
+        assert np.array_equal(c.V.cpu().numpy().transpose(0, 1, 3, 2), V)
+        assert np.array_equal(c.sk.cpu().numpy(), sk) and np.array_equal(c.sv.cpu().numpy(), sv)
+        check_attention({k: v.cpu() for k, v in d.items()}, out)
+
+
+def test_graph_follows_its_arrays(gpu):
+    """One captured step, replayed as the sequences grow, with eager work
+    between the replays."""
+    bl = gpu
+    first = make(17, [1, 1], [40, 700], 64, 128, 2, BF16, 4)
+    s = cuda(first)
+    eager = {k: v.clone() for k, v in s.items()}
+    out = torch.zeros_like(s["q"])
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    append(bl, s), attend(bl, s, out=out, ws=ws)
+    for k in s:
+        s[k].copy_(eager[k])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        append(bl, s)
+        attend(bl, s, out=out, ws=ws)
+    for step in range(5):
+        for k in ("q", "k", "v"):
+            x = torch.randn(s[k].shape, generator=torch.Generator().manual_seed(step)).to(BF16).cuda()
+            s[k].copy_(x), eager[k].copy_(x)
+        graph.replay()
+        append(bl, eager)
+        want = attend(bl, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert all(torch.equal(s[k], eager[k]) for k in ("K", "V", "sk", "sv"))
+        s["lengths"] += 1
+        eager["lengths"] += 1
+
+
+def test_two_streams(gpu):
+    """Calls on streams of their own, outputs and workspaces allocated by the calls."""
+    jobs = [cuda(make(20 + i, [1, 1], [3000 + i, 2500], 64, 128, 2, F32, 4)) for i in range(2)]
+    want = [attend(gpu, s) for s in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = []
+    for _ in range(4):
+        for s, st in zip(jobs, streams):
+            got.append(attend(gpu, s, stream=st))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 2])
+
+
+def test_refusals(gpu):
+    bl = gpu
+    s = cuda(make(18, [2, 1], [40, 30], 16, 64, 2, F32, 4))
+    c = cache(bl, s)
+    meta = s["q_start"], s["lengths"], s["table"]
+    ok = s["q"]
+    for bad, err in ((ok.half(), TypeError), (ok.cpu(), TypeError), (ok[:, :, :32], ValueError),
+                     (ok.transpose(0, 1), ValueError), (ok[0], ValueError)):
+        with pytest.raises(err):
+            bl.bitlinear_kv8_attention(bad, *meta, c)
+    for i, bad in ((0, s["q_start"].long()), (0, s["q_start"][1:]), (1, s["lengths"].cpu()),
+                   (1, s["lengths"][:1]), (2, s["table"][0]), (2, s["table"].t())):
+        m = list(meta)
+        m[i] = bad
+        with pytest.raises((TypeError, ValueError)):
+            bl.bitlinear_kv8_attention(ok, *m, c)
+        with pytest.raises((TypeError, ValueError)):
+            bl.bitlinear_kv8_append(s["k"], s["v"], *m, c)
+    with pytest.raises(ValueError):                                   # V as K is laid out
+        bl.bitlinear_kv8_attention(ok, *meta, c._replace(V=c.V.transpose(2, 3).contiguous()))
+    with pytest.raises(TypeError):
+        bl.bitlinear_kv8_append(s["k"], s["v"].to(BF16), *meta, c)
+    with pytest.raises(ValueError):
+        bl.bitlinear_kv8_attention(ok, *meta, c, out=torch.empty_like(ok)[:1])
+    with pytest.raises(bl.BitLinearError) as e:                       # QH not a multiple of KVH
+        bl.bitlinear_kv8_attention(ok[:, :7].contiguous(), *meta, c)
+    assert e.value.status == 2
+    with pytest.raises(bl.BitLinearError) as e:
+        bl.bitlinear_kv8_attention(ok, *meta, c, scale=float("nan"))
+    assert e.value.status == 2
+    with pytest.raises(bl.BitLinearError) as e:                       # T = 8
+        bl.bitlinear_kv8_append(s["k"], s["v"], *meta, bl.kv8_cache(4, 2, 8, 64))
+    assert e.value.status == 2
+    # nothing to do
+    empty = torch.zeros(1, dtype=torch.int32, device="cuda")
+    none = empty[:0]
+    bl.bitlinear_kv8_append(s["k"][:0], s["v"][:0], s["q_start"], s["lengths"], s["table"], c)
+    assert bl.bitlinear_kv8_attention(ok[:0], empty, none, none.view(0, 3), c).shape == ok[:0].shape
