@@ -1,79 +1,508 @@
 // kv8_attention.hip -- causal attention over the 8-bit key/value cache.
 //
-// out = sum_j p_j v_j / sum_j p_j, p_j = exp(s_j - max s), s_j = scale q.k_j,
-// in one pass over the keys with a running maximum.  One wave per (row, query
-// head), a lane holding D / 64 of the values.
+// out = sum_j p_j v_j / sum_j p_j, p_j = 2^(s_j - m), s_j = scale log2(e)
+// q.k_j, m the running maximum: one pass over the keys, the sums rescaled by
+// 2^(m_old - m) when the maximum grows.
+//
+// Both products run on fp16 matrix instructions (16x16x32) with fp32 sums.
+// An int8 code is exact in fp16: the byte with its sign bit flipped, put
+// below the byte 0x64, reads as 1024 + (code + 128), and one packed add of
+// -1152 leaves the code (v_xor per 4 codes, v_perm and v_pk_add_f16 per 2).
+// The other operand is scaled by a power of two into fp16's range and, for
+// fp32 rows, split into two halves of 11 bits each (two matrix instructions):
+//   q      by row, its largest |q| to [2^13, 2^14);
+//   p sv   the value scale goes with the weight, by u, a power of two >= every
+//          value scale seen so far: p sv / u * 2^14 <= 2^14.
+// bf16 rows keep q exactly and round p sv to 11 bits once: their result is
+// rounded to 8.
+//
+// Rows of a tile: the query heads of one key/value head are neighbouring rows
+// of one product, so a cached byte is read once for all of them: row r of
+// sequence b is token r / G, head r % G (G query heads to a key head).
+//
+// Operand layouts (lane = 16 quad + low): S^T = K Q^T puts key 4 quad + i, row
+// low into accumulator i.  Which key a row of the K operand is, is free: row 4
+// g + i of the operand for keys tt holds key 16 g + 4 tt + i of the tile, so
+// that lane quad g ends up with keys 16 g .. 16 g + 15 of its row -- exactly the
+// P^T operand of O^T = V^T P^T, whose V^T operand is then 16 consecutive bytes
+// of a row of the transposed V.  No value crosses lanes between the products.
+// A quad's 16 tokens lie in one block of the cache whatever T is.
 #include "kv8_common.h"
 
 namespace bl {
 namespace {
 
-constexpr int kThreads = 256;
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+typedef float float4v __attribute__((ext_vector_type(4)));
 
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kTile = 64;                   // keys per wave and step
+constexpr int kRows = 16;                   // rows of a tile
+constexpr int kBusyGroups = 1536;           // workgroups that the parts are to make
+
+__device__ __forceinline__ float4v mfma(half8 a, half8 b, float4v c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Four int8 codes -> four fp16.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t v = w ^ 0x80808080u;
+    const half2 bias = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+    lo = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, perm(0x64646464u, v, 0x04010400u)) + bias);
+    hi = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, perm(0x64646464u, v, 0x04030402u)) + bias);
+}
+__device__ __forceinline__ half8 codes8(uint32_t w0, uint32_t w1) {
+    uint4 o;
+    codes_to_f16(w0, o.x, o.y);
+    codes_to_f16(w1, o.z, o.w);
+    return __builtin_bit_cast(half8, o);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const half2 h = {(_Float16)a, (_Float16)b};
+    uint32_t w = __builtin_bit_cast(uint32_t, h);
+    // One rounding for every reader: where a is itself a product the compiler
+    // otherwise forms it twice, in fp32 then fp16 here and in one step there,
+    // and a value near a tie then differs by a whole step from its rest.
+    asm("" : "+v"(w));
+    return w;
+}
+// What fp16 leaves of a pair that was rounded to `h`.
+__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t h) {
+    const half2 v = __builtin_bit_cast(half2, h);
+    return pack2(a - (float)v[0], b - (float)v[1]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ uint32_t bf16_round(float x) {
+    const uint32_t w = __float_as_uint(x);
+    return (w + 0x7FFFu + (w >> 16 & 1u)) >> 16;
+}
+
+// The largest / the sum over the four lanes that share a row (quads).
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// Four consecutive values of a row.
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void kv8_attention_kernel(const void *__restrict__ q, int QH,
-                                                                 Kv8Seqs seqs, Kv8Cache c,
-                                                                 float scale, void *out) {
-    const int lane = threadIdx.x & 63;
-    const int64_t i = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-    if (i >= (int64_t)seqs.n_tok * QH) return;
-    const int t = (int)(i / QH), hq = (int)(i % QH), h = hq / (QH / c.KVH);
-    const int b = find_seq(seqs.B, t, [&](int x) { return (int64_t)q_at(seqs, x); });
-    const int q0 = q_at(seqs, b), q1 = q_at(seqs, b + 1);
-    if (t < q0 || t >= q1) return;
-    const int64_t pos = (int64_t)seqs.lengths[b] - (q1 - t);
-    const int per = c.D / 64;
-    float x[2], o[2] = {0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
-    for (int e = 0; e < per; ++e) {
-        const int64_t at = i * c.D + e * 64 + lane;
-        x[e] = BF16 ? bf16_lo(static_cast<const uint16_t *>(q)[at]) : static_cast<const float *>(q)[at];
+__device__ __forceinline__ float4 load4(const void *p, int64_t at) {
+    if (BF16) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at);
+        return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
     }
-    const int64_t end = min(pos + 1, (int64_t)seqs.max_blocks << c.t_shift);
-    for (int64_t j = 0; j < end; ++j) {
-        const int id = seqs.table[(int64_t)b * seqs.max_blocks + (j >> c.t_shift)];
-        if (id < 0 || id >= c.n_blocks) continue;
-        const int64_t hb = (int64_t)id * c.KVH + h;
-        const int slot = (int)j & (c.T - 1);
-        float s = 0.0f;
-        for (int e = 0; e < per; ++e)
-            s += x[e] * (float)c.K[hb * c.T * c.D + slot * c.D + e * 64 + lane];
-        for (int w = 1; w < 64; w <<= 1) s += __shfl_xor(s, w);
-        s = s * c.sk[hb] * scale;
-        const float mn = fmaxf(m, s), f = expf(m - mn), p = expf(s - mn);
-        m = mn;
-        l = l * f + p;
-        for (int e = 0; e < per; ++e)
-            o[e] = o[e] * f +
-                   p * ((float)c.V[hb * c.T * c.D + (e * 64 + lane) * c.T + slot] * c.sv[hb]);
+    return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+}
+template <bool BF16>
+__device__ __forceinline__ void store4(void *p, int64_t at, float4 v) {
+    if (BF16) {
+        uint2 w;
+        w.x = bf16_round(v.x) | bf16_round(v.y) << 16;
+        w.y = bf16_round(v.z) | bf16_round(v.w) << 16;
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + at) = w;
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = v;
     }
-    for (int e = 0; e < per; ++e) {
-        const int64_t at = i * c.D + e * 64 + lane;
-        const float y = l > 0.0f ? o[e] / l : 0.0f;
-        if (BF16) {
-            const uint32_t w = __float_as_uint(y);
-            static_cast<uint16_t *>(out)[at] = (uint16_t)((w + 0x7FFF + (w >> 16 & 1)) >> 16);
+}
+
+// A power of two >= |x| (for |x| in [2^-100, 2^127)); 2^14 over it stays finite.
+__device__ __forceinline__ float pow2_above(float x) {
+    const uint32_t e = min(max((__float_as_uint(x) >> 23) & 255u, 27u), 253u);
+    return __uint_as_float((e + 1) << 23);
+}
+
+struct Args {
+    const void *q;
+    void *out;
+    float *part;              // [S][n_tok * QH][D], then [S][n_tok * QH][2]
+    Kv8Seqs seqs;
+    Kv8Cache c;
+    int QH, G, S;
+    int64_t chunk;            // keys of a part
+    float scale2;             // scale * log2(e)
+};
+
+__device__ __forceinline__ int64_t key_capacity(const Args &a) {
+    return a.c.n_blocks > 0 ? (int64_t)a.seqs.max_blocks << a.c.t_shift : 0;
+}
+
+// Few rows: one workgroup per (16 rows, key head, part of the keys), its waves
+// taking 64-key tiles in turn, each with sums of its own, joined in LDS.
+template <bool BF16, int D>
+__global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
+    constexpr int ND = D / 64;              // 64-value pieces of a row
+    constexpr int NO = D / 16;              // 16-value tiles of the output
+    constexpr int NS = BF16 ? 1 : 2;        // fp16 parts of q and of p sv
+    __shared__ float join[kWaves][kRows][D + 4];
+    __shared__ float join_m[kWaves][kRows], join_l[kWaves][kRows];
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int low = lane & 15, quad = lane >> 4;
+    const int h = blockIdx.y, split = blockIdx.z;
+    const Kv8Seqs &sq = a.seqs;
+    const Kv8Cache &c = a.c;
+    const int64_t slot = blockIdx.x;
+    const int G = a.G;
+
+    // tiles of sequence b: slots from floor(q_start[b] G / 16) + b on
+    const int b = find_seq(sq.B, slot, [&](int i) {
+        return (int64_t)q_at(sq, i) * G / kRows + i;
+    });
+    const int q0 = q_at(sq, b), n = q_at(sq, b + 1) - q0;
+    const int64_t nth = slot - ((int64_t)q0 * G / kRows + b);
+    if (nth < 0 || n <= 0 || nth * kRows >= (int64_t)n * G) return;
+    const int64_t r0 = nth * kRows;
+    const int rows = (int)min((int64_t)kRows, (int64_t)n * G - r0);
+    const int64_t start = (int64_t)sq.lengths[b] - n;             // position of the first new token
+    const int64_t cap = key_capacity(a);
+    const int64_t last_pos = start + (r0 + rows - 1) / G;
+    const int64_t end = min(last_pos + 1, cap);                   // keys the tile sees
+    const int64_t k0 = (int64_t)split * a.chunk;
+    if (split > 0 && k0 >= end) return;
+    const int64_t k1 = min(end, k0 + a.chunk);
+
+    // this lane's row (rows past the last repeat it; they are not written)
+    const int64_t r = r0 + min(low, rows - 1);
+    const int tok = (int)(r / G);
+    const int hq = h * G + (int)(r - (int64_t)tok * G);
+    const int64_t row = (int64_t)(q0 + tok) * a.QH + hq;
+    const int64_t pos = start + tok;
+
+    // q of the row: values 64 dc + 16 quad + 8 half + 0..7 per matrix step
+    half8 qh[NS][ND][2];
+    float c_row;
+    {
+        float4 v[ND][4];
+        float top = 0.0f;
+#pragma unroll
+        for (int dc = 0; dc < ND; ++dc)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[dc][e] = load4<BF16>(a.q, row * D + 64 * dc + 16 * quad + 4 * e);
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(v[dc][e].x), fabsf(v[dc][e].y)),
+                                       fmaxf(fabsf(v[dc][e].z), fabsf(v[dc][e].w))));
+            }
+        top = quad_max(top);
+        // top in [2^(e-127), 2^(e-126)): times 2^(140 - e) it is in [2^13, 2^14);
+        // in two factors, as 2^(140 - e) may pass fp32's range
+        const int e = max((int)(__float_as_uint(top) >> 23), 1);
+        const float f1 = __uint_as_float((uint32_t)(127 + (140 - e) / 2) << 23);
+        const float f2 = __uint_as_float((uint32_t)(127 + (140 - e) - (140 - e) / 2) << 23);
+        c_row = a.scale2 / f1 / f2;
+#pragma unroll
+        for (int dc = 0; dc < ND; ++dc)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t w[4], z[4];
+#pragma unroll
+                for (int e2 = 0; e2 < 2; ++e2) {
+                    const float4 x = v[dc][2 * hf + e2];
+                    const float x0 = x.x * f1 * f2, x1 = x.y * f1 * f2;
+                    const float x2 = x.z * f1 * f2, x3 = x.w * f1 * f2;
+                    w[2 * e2] = pack2(x0, x1);
+                    w[2 * e2 + 1] = pack2(x2, x3);
+                    z[2 * e2] = rest2(x0, x1, w[2 * e2]);
+                    z[2 * e2 + 1] = rest2(x2, x3, w[2 * e2 + 1]);
+                }
+                qh[0][dc][hf] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
+                if (NS == 2)
+                    qh[NS - 1][dc][hf] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
+            }
+    }
+
+    float m = -INFINITY, l = 0.0f, u = 0.0f;
+    float4v o[NO];
+#pragma unroll
+    for (int i = 0; i < NO; ++i) o[i] = float4v{0.f, 0.f, 0.f, 0.f};
+
+    const int64_t first_tile = k0 + (int64_t)wave * kTile;
+    constexpr int64_t kStep = (int64_t)kWaves * kTile;
+    const int32_t *table = sq.table + (int64_t)b * sq.max_blocks;
+    // block of this lane's quad of a tile; -1 where it holds no token
+    auto block_at = [&](int64_t tile) {
+        const int64_t t = tile + 16 * quad;
+        const int id = t < k1 ? table[t >> c.t_shift] : -1;
+        return id >= 0 && id < c.n_blocks ? id : -1;
+    };
+    uint4 kb[4][ND], vb[NO];
+    float sk = 0.0f, sv = 0.0f;
+    auto load_k = [&](int64_t tile, int id) {
+        // this lane's operand row: key 16 g + 4 tt + i of the tile, 4 g + i = low
+        const int g = low >> 2;
+        const int idk = max(__shfl(id, 16 * g), 0);
+        const int s0 = (int)((tile + 16 * g) & (c.T - 1)) + (low & 3);
+        const int8_t *p = c.K + (((int64_t)idk * c.KVH + h) * c.T + s0) * D + 16 * quad;
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int dc = 0; dc < ND; ++dc)
+                kb[tt][dc] = *reinterpret_cast<const uint4 *>(p + 4 * tt * D + 64 * dc);
+    };
+    auto load_v = [&](int64_t tile, int id) {
+        const int64_t hb = (int64_t)max(id, 0) * c.KVH + h;
+        sk = c.sk[hb];
+        sv = c.sv[hb];
+        const int8_t *p = c.V + (hb * D + low) * c.T + (int)((tile + 16 * quad) & (c.T - 1));
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+            vb[i] = *reinterpret_cast<const uint4 *>(p + 16 * i * c.T);
+    };
+
+    if (first_tile < k1) {
+        int id = block_at(first_tile);
+        load_k(first_tile, id);
+        load_v(first_tile, id);
+        int id_next = block_at(first_tile + kStep);
+        for (int64_t tile = first_tile; tile < k1; tile += kStep) {
+            float4v s[4];
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) {
+                s[tt] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int dc = 0; dc < ND; ++dc) {
+                    const half8 k_lo = codes8(kb[tt][dc].x, kb[tt][dc].y);
+                    const half8 k_hi = codes8(kb[tt][dc].z, kb[tt][dc].w);
+#pragma unroll
+                    for (int x = 0; x < NS; ++x) {
+                        s[tt] = mfma(k_lo, qh[x][dc][0], s[tt]);
+                        s[tt] = mfma(k_hi, qh[x][dc][1], s[tt]);
+                    }
+                }
+            }
+            const int64_t next = tile + kStep;
+            const bool more = next < k1;
+            if (more) load_k(next, id_next);
+
+            const float cs = c_row * sk;
+            const int64_t key0 = tile + 16 * quad;
+            const bool whole = id >= 0 && key0 + 15 <= pos && key0 + 16 <= k1;
+            float top = -INFINITY;
+            if (__ballot(!whole) == 0) {
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s[tt][i] *= cs;
+                        top = fmaxf(top, s[tt][i]);
+                    }
+            } else {
+                const int lim = id >= 0 ? (int)min(min(pos + 1, k1) - key0, (int64_t)16) : 0;
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = s[tt][i] * cs;
+                        s[tt][i] = 4 * tt + i < lim ? x : -INFINITY;
+                        top = fmaxf(top, s[tt][i]);
+                    }
+            }
+            const float m_new = fmaxf(m, quad_max(top));
+            const float base = m_new == -INFINITY ? 0.0f : m_new;
+            const float u_new = fmaxf(u, pow2_above(quad_max(id >= 0 ? fabsf(sv) : 0.0f)));
+            float fix = exp2_fast(m - base);               // 0 while nothing was seen
+            l *= fix;
+            if (u_new != u) fix *= u / u_new;              // u = 0 at first
+            if (__ballot(fix != 1.0f)) {
+#pragma unroll
+                for (int i = 0; i < NO; ++i) o[i] *= fix;
+            }
+            m = m_new;
+            u = u_new;
+            const float w_sv = id >= 0 ? sv * (16384.0f / u) : 0.0f;
+            half8 ph[NS][2];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                uint32_t w[4], z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tt = 2 * ks + (e >> 1), i = 2 * (e & 1);
+                    const float p0 = exp2_fast(s[tt][i] - base), p1 = exp2_fast(s[tt][i + 1] - base);
+                    l += p0 + p1;
+                    const float y0 = p0 * w_sv, y1 = p1 * w_sv;
+                    w[e] = pack2(y0, y1);
+                    if (NS == 2) z[e] = rest2(y0, y1, w[e]);
+                }
+                ph[0][ks] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
+                if (NS == 2)
+                    ph[NS - 1][ks] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
+            }
+#pragma unroll
+            for (int i = 0; i < NO; ++i) {
+                const half8 v_lo = codes8(vb[i].x, vb[i].y), v_hi = codes8(vb[i].z, vb[i].w);
+#pragma unroll
+                for (int x = 0; x < NS; ++x) {
+                    o[i] = mfma(v_lo, ph[x][0], o[i]);
+                    o[i] = mfma(v_hi, ph[x][1], o[i]);
+                }
+            }
+            if (more) {
+                id = id_next;
+                load_v(next, id);
+                id_next = block_at(next + kStep);
+            }
+        }
+    }
+    l = quad_sum(l);
+
+    // join the waves: thread (row, values) sums what each brings
+    const float unit = u / 16384.0f;
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) join[wave][low][16 * i + 4 * quad + e] = o[i][e] * unit;
+    if (quad == 0) {
+        join_m[wave][low] = m;
+        join_l[wave][low] = l;
+    }
+    __syncthreads();
+    constexpr int kPieces = kRows * D / 4 / kThreads;
+#pragma unroll
+    for (int pc = 0; pc < kPieces; ++pc) {
+        const int at = (pc * kThreads + (int)threadIdx.x) * 4;
+        const int rr = at / D, d = at % D;
+        if (rr >= rows) continue;
+        float mm = join_m[0][rr];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, join_m[w][rr]);
+        const float base = mm == -INFINITY ? 0.0f : mm;
+        float ll = 0.0f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float f = exp2_fast(join_m[w][rr] - base);
+            const float4 x = *reinterpret_cast<const float4 *>(&join[w][rr][d]);
+            ll += join_l[w][rr] * f;
+            y.x += x.x * f; y.y += x.y * f; y.z += x.z * f; y.w += x.w * f;
+        }
+        const int64_t rj = r0 + rr;
+        const int tj = (int)(rj / G);
+        const int64_t row_j = (int64_t)(q0 + tj) * a.QH + h * G + (rj - (int64_t)tj * G);
+        if (min(start + tj + 1, cap) <= a.chunk) {
+            // every key the row sees is in part 0
+            if (split > 0) continue;
+            const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+            store4<BF16>(a.out, row_j * D + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
         } else {
-            static_cast<float *>(out)[at] = y;
+            const int64_t all = (int64_t)sq.n_tok * a.QH;
+            *reinterpret_cast<float4 *>(a.part + ((int64_t)split * all + row_j) * D + d) = y;
+            if (d == 0) {
+                float *ml = a.part + (int64_t)a.S * all * D + ((int64_t)split * all + row_j) * 2;
+                ml[0] = mm;
+                ml[1] = ll;
+            }
         }
     }
 }
 
+// Joins the parts of the rows whose keys were read in more than one: one
+// workgroup per (row, head); wave w sums the parts w, w + 4, ...
+template <bool BF16, int D>
+__global__ __launch_bounds__(kThreads) void kv8_join_kernel(Args a) {
+    constexpr int E = D / 64;
+    __shared__ float sum[kWaves][D], sum_l[kWaves], top[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t row = blockIdx.x;
+    const Kv8Seqs &sq = a.seqs;
+    const int t = (int)(row / a.QH);
+    const int b = find_seq(sq.B, t, [&](int i) { return (int64_t)q_at(sq, i); });
+    const int q1 = q_at(sq, b + 1);
+    if (t < q_at(sq, b) || t >= q1) return;
+    const int64_t keys = min((int64_t)sq.lengths[b] - (q1 - t) + 1, key_capacity(a));
+    if (keys <= a.chunk) return;                                // written directly
+    const int parts = (int)((keys + a.chunk - 1) / a.chunk);    // <= S
+    const int64_t all = (int64_t)sq.n_tok * a.QH;
+    const float *ml = a.part + (int64_t)a.S * all * D;
+    float mm = -INFINITY;
+    for (int s = lane; s < parts; s += 64) mm = fmaxf(mm, ml[(s * all + row) * 2]);
+    mm = group_max(mm, 64);
+    const float base = mm == -INFINITY ? 0.0f : mm;
+    float y[E] = {}, ll = 0.0f;
+    for (int s = wave; s < parts; s += kWaves) {
+        const float f = exp2_fast(ml[(s * all + row) * 2] - base);
+        ll += ml[(s * all + row) * 2 + 1] * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] += a.part[(s * all + row) * D + 64 * e + lane] * f;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[wave][64 * e + lane] = y[e];
+    if (lane == 0) sum_l[wave] = ll;
+    __syncthreads();
+    if (threadIdx.x < D / 4) {
+        const int d = 4 * threadIdx.x;
+        ll = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            ll += sum_l[w];
+            o.x += sum[w][d]; o.y += sum[w][d + 1]; o.z += sum[w][d + 2]; o.w += sum[w][d + 3];
+        }
+        const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+        store4<BF16>(a.out, row * D + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+}
+
+// Parts the keys are read in.  The lengths are on the device, so the bound
+// max_blocks * T takes their place: parts behind a sequence's end exit at once.
+struct Plan {
+    int64_t slots, chunk;
+    int S;
+};
+Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH, int64_t T) {
+    const int64_t G = QH / KVH, keys = max_blocks * T, unit = kTile * kWaves;
+    const int64_t seqs = n_tok < B ? n_tok : B;
+    const double busy = (double)KVH * (seqs + (n_tok - seqs) * (double)G / kRows);
+    const double want = keys * busy / kBusyGroups;
+    Plan p = {n_tok * G / kRows + B, keys > unit ? keys : unit, 1};
+    if (want < p.chunk) p.chunk = want > unit ? (int64_t)want : unit;
+    p.chunk = (p.chunk + unit - 1) / unit * unit;
+    if (keys > p.chunk) p.S = (int)((keys + p.chunk - 1) / p.chunk);
+    return p;
+}
+
+template <bool BF16, int D>
+hipError_t attend(const Args &a, const Plan &p, hipStream_t s) {
+    hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>),
+                       dim3((unsigned)p.slots, (unsigned)a.c.KVH, (unsigned)p.S), dim3(kThreads), 0, s,
+                       a);
+    if (p.S > 1)
+        hipLaunchKernelGGL((kv8_join_kernel<BF16, D>), dim3((unsigned)(a.seqs.n_tok * a.QH)),
+                           dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
-size_t kv8_attention_ws_floats(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) {
-    return 0;
+size_t kv8_attention_ws_floats(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
+                               int64_t KVH, int64_t T, int64_t D) {
+    const Plan p = plan_for(n_tok, QH, B, max_blocks, KVH, T);
+    return p.S > 1 ? (size_t)p.S * n_tok * QH * (D + 2) : 0;
 }
 
 hipError_t launch_kv8_attention(const void *q, int dtype, int QH, const Kv8Seqs &seqs,
                                 const bl_kv8 &cache, float scale, void *out, float *ws,
                                 hipStream_t s) {
-    const Kv8Cache c = kv8_device(cache);
-    const dim3 grid((unsigned)(((int64_t)seqs.n_tok * QH + 3) / 4)), block(kThreads);
-    if (dtype)
-        hipLaunchKernelGGL(kv8_attention_kernel<true>, grid, block, 0, s, q, QH, seqs, c, scale, out);
-    else
-        hipLaunchKernelGGL(kv8_attention_kernel<false>, grid, block, 0, s, q, QH, seqs, c, scale, out);
-    return hipGetLastError();
+    const Plan p = plan_for(seqs.n_tok, QH, seqs.B, seqs.max_blocks, cache.KVH, cache.T);
+    Args a = {};
+    a.q = q;
+    a.out = out;
+    a.part = ws;
+    a.seqs = seqs;
+    a.c = kv8_device(cache);
+    a.QH = QH;
+    a.G = QH / a.c.KVH;
+    a.chunk = p.chunk;
+    a.S = p.S;
+    a.scale2 = (float)((double)scale * 1.4426950408889634);
+    if (cache.D == 64) return dtype ? attend<true, 64>(a, p, s) : attend<false, 64>(a, p, s);
+    return dtype ? attend<true, 128>(a, p, s) : attend<false, 128>(a, p, s);
 }
 
 }  // namespace bl
