@@ -98,6 +98,10 @@ template <int CTRL>
 __device__ __forceinline__ int dpp_i32(int v) {
     return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, false);
 }
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+    return __int_as_float(dpp_i32<CTRL>(__float_as_int(v)));
+}
 __device__ __forceinline__ int group_sum(int v, int G) {
     if (G >= 2) v += dpp_i32<kDppXor1>(v);
     if (G >= 4) v += dpp_i32<kDppXor2>(v);
@@ -115,6 +119,23 @@ __device__ __forceinline__ float group_max(float v, int G) {
     if (G >= 32) v = fmaxf(v, __shfl_xor(v, 16));
     if (G >= 64) v = fmaxf(v, __shfl_xor(v, 32));
     return v;
+}
+
+// Lanes 16 q + i of a wave, q the quad: results that every quad of an i gets,
+// by swaps of 16-lane rows between two registers (no LDS round trip).
+__device__ __forceinline__ float quad_max(float v) {
+    uint32_t a = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    a = __float_as_uint(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+    r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    uint32_t a = __float_as_uint(v);
+    auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    a = __float_as_uint(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 __device__ __forceinline__ int dot4(uint32_t a, uint32_t b, int c) {
@@ -166,6 +187,33 @@ __device__ __forceinline__ float scalar_load(const float *p) {
 }
 __device__ __forceinline__ double scalar_load(const double *p) {
     return *(const __attribute__((address_space(4))) double *)p;
+}
+
+// fp16 operands of the matrix instructions.
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ float4v mfma_16x16x32(half8 a, half8 b, float4v c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+    const half2 h = {(_Float16)a, (_Float16)b};
+    uint32_t w = __builtin_bit_cast(uint32_t, h);
+    // One rounding for every reader: where a is itself a product the compiler
+    // otherwise forms it twice, in fp32 then fp16 here and in one step there,
+    // and a value near a tie then differs by a whole step from its rest.
+    asm("" : "+v"(w));
+    return w;
+}
+// What fp16 leaves of a pair that was rounded to `h`.
+__device__ __forceinline__ uint32_t f16_rest(float a, float b, uint32_t h) {
+    const half2 v = __builtin_bit_cast(half2, h);
+    return f16_pair(a - (float)v[0], b - (float)v[1]);
+}
+// fp32 -> bf16 bits, ties to even.
+__device__ __forceinline__ uint32_t bf16_round(float x) {
+    const uint32_t w = __float_as_uint(x);
+    return (w + 0x7FFFu + (w >> 16 & 1u)) >> 16;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -32,19 +32,11 @@
 namespace bl {
 namespace {
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half2 __attribute__((ext_vector_type(2)));
-typedef float float4v __attribute__((ext_vector_type(4)));
-
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 64;                   // keys per wave and step
 constexpr int kRows = 16;                   // rows of a tile
 constexpr int kBusyGroups = 1536;           // workgroups that the parts are to make
-
-__device__ __forceinline__ float4v mfma(half8 a, half8 b, float4v c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
 
 // Four int8 codes -> four fp16.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -60,37 +52,7 @@ __device__ __forceinline__ half8 codes8(uint32_t w0, uint32_t w1) {
     return __builtin_bit_cast(half8, o);
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const half2 h = {(_Float16)a, (_Float16)b};
-    uint32_t w = __builtin_bit_cast(uint32_t, h);
-    // One rounding for every reader: where a is itself a product the compiler
-    // otherwise forms it twice, in fp32 then fp16 here and in one step there,
-    // and a value near a tie then differs by a whole step from its rest.
-    asm("" : "+v"(w));
-    return w;
-}
-// What fp16 leaves of a pair that was rounded to `h`.
-__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t h) {
-    const half2 v = __builtin_bit_cast(half2, h);
-    return pack2(a - (float)v[0], b - (float)v[1]);
-}
-
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-__device__ __forceinline__ uint32_t bf16_round(float x) {
-    const uint32_t w = __float_as_uint(x);
-    return (w + 0x7FFFu + (w >> 16 & 1u)) >> 16;
-}
-
-// The largest / the sum over the four lanes that share a row (quads).
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
-}
-__device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
-}
 
 // Four consecutive values of a row.
 template <bool BF16>
@@ -207,10 +169,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
                     const float4 x = v[dc][2 * hf + e2];
                     const float x0 = x.x * f1 * f2, x1 = x.y * f1 * f2;
                     const float x2 = x.z * f1 * f2, x3 = x.w * f1 * f2;
-                    w[2 * e2] = pack2(x0, x1);
-                    w[2 * e2 + 1] = pack2(x2, x3);
-                    z[2 * e2] = rest2(x0, x1, w[2 * e2]);
-                    z[2 * e2 + 1] = rest2(x2, x3, w[2 * e2 + 1]);
+                    w[2 * e2] = f16_pair(x0, x1);
+                    w[2 * e2 + 1] = f16_pair(x2, x3);
+                    z[2 * e2] = f16_rest(x0, x1, w[2 * e2]);
+                    z[2 * e2 + 1] = f16_rest(x2, x3, w[2 * e2 + 1]);
                 }
                 qh[0][dc][hf] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
                 if (NS == 2)
@@ -272,8 +234,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
                     const half8 k_hi = codes8(kb[tt][dc].z, kb[tt][dc].w);
 #pragma unroll
                     for (int x = 0; x < NS; ++x) {
-                        s[tt] = mfma(k_lo, qh[x][dc][0], s[tt]);
-                        s[tt] = mfma(k_hi, qh[x][dc][1], s[tt]);
+                        s[tt] = mfma_16x16x32(k_lo, qh[x][dc][0], s[tt]);
+                        s[tt] = mfma_16x16x32(k_hi, qh[x][dc][1], s[tt]);
                     }
                 }
             }
@@ -327,8 +289,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
                     const float p0 = exp2_fast(s[tt][i] - base), p1 = exp2_fast(s[tt][i + 1] - base);
                     l += p0 + p1;
                     const float y0 = p0 * w_sv, y1 = p1 * w_sv;
-                    w[e] = pack2(y0, y1);
-                    if (NS == 2) z[e] = rest2(y0, y1, w[e]);
+                    w[e] = f16_pair(y0, y1);
+                    if (NS == 2) z[e] = f16_rest(y0, y1, w[e]);
                 }
                 ph[0][ks] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
                 if (NS == 2)
@@ -339,8 +301,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
                 const half8 v_lo = codes8(vb[i].x, vb[i].y), v_hi = codes8(vb[i].z, vb[i].w);
 #pragma unroll
                 for (int x = 0; x < NS; ++x) {
-                    o[i] = mfma(v_lo, ph[x][0], o[i]);
-                    o[i] = mfma(v_hi, ph[x][1], o[i]);
+                    o[i] = mfma_16x16x32(v_lo, ph[x][0], o[i]);
+                    o[i] = mfma_16x16x32(v_hi, ph[x][1], o[i]);
                 }
             }
             if (more) {
