@@ -125,6 +125,7 @@ struct ProdArgs {
     int M, N, K;
 };
 
+constexpr int kCUs = 256;
 constexpr int kMaxWaves = 8;
 
 // One or two tokens.  A wave takes slices of 512 values of K: 16 lanes hold 32
@@ -209,10 +210,123 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_w4_few_kernel(ProdArgs a,
     }
 }
 
+// One or two tokens and many rows: X in LDS (fp32), every wave for itself.  A
+// wave takes 4 R rows at a time through all of K, one slice's X in registers
+// for its R loads, the next slice's loads in flight.
+constexpr int kStreamThreads = 256;
+constexpr int kStreamGroups = 1024;
+constexpr size_t kStreamLds = 64 * 1024;
+constexpr int kStreamRows = 32768;
+size_t stream_lds(int M, int K) {
+    return (size_t)M * ((K + kSlice - 1) / kSlice) * kSlice * sizeof(float);
+}
+template <bool BF16, int M, int R>
+__global__ __launch_bounds__(kStreamThreads, 4) void gemv_w4_stream_kernel(ProdArgs a, int g_shift) {
+    extern __shared__ float xs[];               // [M][slices][8][16][4]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int kl = lane & 15, rg = lane >> 4;
+    const int units = a.K / 32, groups = units >> g_shift;
+    const int slices = (units + 15) / 16;
+    // 16 bytes e of the 128 of lane kl stand at [slice][e][kl]: a read of one
+    // e by 16 lanes is 256 consecutive bytes
+    for (int i = threadIdx.x; i < M * slices * 64; i += kStreamThreads) {
+        const int m = i / (slices * 64), k = (i - m * slices * 64) * 8;
+        float x[8];
+        load8<BF16>(a.X, (int64_t)m * a.K + min(k, a.K - 8), x);
+        if (k >= a.K) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+        }
+        const int sl = k / kSlice, l = k / 32 % 16, e = k / 8 % 4;
+        float *d = xs + (((m * slices + sl) * 8 + 2 * e) * 16 + l) * 4;
+        *reinterpret_cast<float4 *>(d) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(d + 64) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    __syncthreads();
+    const int tiles = (a.N + 4 * R - 1) / (4 * R);
+    const int step = gridDim.x * (kStreamThreads / 64);
+    int tile = blockIdx.x * (kStreamThreads / 64) + wave;
+    uint4 w[R];
+    uint32_t sb[R];
+    auto load_w = [&](int t, int sl) {
+        const int u = min(sl * 16 + kl, units - 1);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t n = min((int64_t)t * (4 * R) + 4 * r + rg, (int64_t)a.N - 1);
+            w[r] = reinterpret_cast<const uint4 *>(a.Wq4)[n * units + u];
+            sb[r] = a.s4[n * groups + (u >> g_shift)];
+        }
+    };
+    if (tile < tiles) load_w(tile, 0);
+    for (; tile < tiles; tile += step) {
+        float acc[M][R];
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[m][r] = 0.0f;
+        for (int sl = 0; sl < slices; ++sl) {
+            uint4 wc[R];
+            float d[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                wc[r] = w[r];
+                d[r] = __uint_as_float(sb[r] << 16);
+            }
+            const bool end = sl + 1 == slices;
+            load_w(end ? min(tile + step, tiles - 1) : tile, end ? 0 : sl + 1);
+            float4 x[M][8];
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[m][e] = *reinterpret_cast<const float4 *>(xs + (((m * slices + sl) * 8 + e) * 16 + kl) * 4);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t ww[4] = {wc[r].x, wc[r].y, wc[r].z, wc[r].w};
+                float s0[M], s1[M];
+#pragma unroll
+                for (int m = 0; m < M; ++m) s0[m] = s1[m] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const Codes c = codes_to_f16(ww[j]);
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        const float4 lo = x[m][2 * j], hi = x[m][2 * j + 1];
+                        s0[m] = __builtin_fmaf((float)c.p[0][0], lo.x, s0[m]);
+                        s1[m] = __builtin_fmaf((float)c.p[0][1], hi.x, s1[m]);
+                        s0[m] = __builtin_fmaf((float)c.p[1][0], lo.y, s0[m]);
+                        s1[m] = __builtin_fmaf((float)c.p[1][1], hi.y, s1[m]);
+                        s0[m] = __builtin_fmaf((float)c.p[2][0], lo.z, s0[m]);
+                        s1[m] = __builtin_fmaf((float)c.p[2][1], hi.z, s1[m]);
+                        s0[m] = __builtin_fmaf((float)c.p[3][0], lo.w, s0[m]);
+                        s1[m] = __builtin_fmaf((float)c.p[3][1], hi.w, s1[m]);
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    acc[m][r] = __builtin_fmaf(s0[m] + s1[m], d[r], acc[m][r]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float v = acc[m][r];
+                v += dpp_f32<kDppXor1>(v);
+                v += dpp_f32<kDppXor2>(v);
+                v += dpp_f32<kDppHalfMirror>(v);
+                v += dpp_f32<kDppMirror>(v);
+                const int64_t n = (int64_t)tile * (4 * R) + 4 * r + rg;
+                if (kl == 0 && n < a.N) a.Y[m * (int64_t)a.N + n] = v;
+            }
+    }
+}
+
 // Three tokens and more: 16x16x32 products, A = 16 tokens x 32 values of X, B =
-// 32 values x 16 rows of W.  A wave takes chunks of 128 values; lane 16 quad +
-// low holds 32 values of token `low`, and 16 bytes of row `low` per 16 rows of
-// W, R times.
+// 32 values x 16 rows of W.  A wave takes chunks of 128 values: 16 bytes of row
+// `low` per 16 rows of W, R times, and the tokens' values, loaded in whole
+// lines (16 lanes a token), made fp16 and passed through LDS of the wave's own
+// into the operand's order.
 //
 // X is scaled by a power of two per token and chunk, the largest to [2^13,
 // 2^14), and rounded to fp16: bf16 values are exact (down to 2^-31 of the
@@ -223,10 +337,19 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_w4_few_kernel(ProdArgs a,
 // lie in one scale group.  With groups of 128 any dword of each quad's 16 bytes
 // will do; with 32 the quads have to bring the four dwords of one lane, which
 // is a transpose of the 4 x 4 dwords between registers and quads (4 row swaps
-// per 16 bytes); with 64 half of it.  X is loaded in the order this makes.  The
-// sum of a group leaves the matrix accumulators once, times X's factor and the
-// scale, into fp32 totals.
+// per 16 bytes); with 64 half of it.  place() is where 8 values of X belong
+// then.  The sum of a group leaves the matrix accumulators once, times X's
+// factor and the scale, into fp32 totals.
 constexpr int kChunk = 128;
+
+// Matrix instruction (dword) and quad that the 8 values of dword j of quad sq's
+// 16 bytes go to: 4 instruction + quad.
+template <int GROUP>
+__device__ __forceinline__ int place(int sq, int j) {
+    if (GROUP == 128) return j << 2 | sq;
+    if (GROUP == 64) return ((j & 1) | (sq & 2)) << 2 | ((sq & 1) | (j & 2));
+    return sq << 2 | j;
+}
 
 __device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -239,75 +362,103 @@ __device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {
     b = r[1];
 }
 
-template <bool BF16, int GROUP, int R>
-__global__ __launch_bounds__(64 * kMaxWaves) void gemv_w4_mfma_kernel(ProdArgs a) {
+// Between a wave's writes and reads of LDS by different lanes (the hardware
+// keeps their order; the compiler has to).
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// LDS of a wave: [part of X][instruction, quad][16 tokens + 1 of padding] units
+// of 16 bytes, then 16 factors; the final sums take its place.
+template <bool BF16>
+constexpr int wave_lds() { return (BF16 ? 1 : 2) * 16 * 17 * 16 + 64; }
+
+// WHOLE: K % 128 == 0 and s aligned to the scales of a chunk.
+template <bool BF16, int GROUP, int R, bool WHOLE, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void gemv_w4_mfma_kernel(ProdArgs a) {
     constexpr int NS = BF16 ? 1 : 2;
     constexpr int NG = kChunk / GROUP;          // groups of a chunk
-    __shared__ float red[kMaxWaves][R][4][64];
+    extern __shared__ uint4 lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int low = lane & 15, quad = lane >> 4;
+    uint4 *xs = lds + wave * (wave_lds<BF16>() / 16);
+    float *xf = reinterpret_cast<float *>(xs + NS * 16 * 17);
     const int64_t n0 = (int64_t)blockIdx.x * (16 * R);
-    const int units = a.K / 32, groups = a.K / GROUP;
-    const int64_t xrow = (int64_t)min(low, a.M - 1) * a.K;
+    const int units = a.K / 32, groups = a.K / GROUP, chunks = (units + 3) / 4;
     float4v tot[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) tot[r] = float4v{0.f, 0.f, 0.f, 0.f};
 
-    for (int c = wave; c * kChunk < a.K; c += waves) {
-        // K is a multiple of 32, so a chunk's end falls between units
+    for (int c = wave; c < chunks; c += waves) {
+        // K is a multiple of 32, so its end falls between units; codes behind
+        // it count 0, whatever X they meet (the row's last)
         uint4 w[R];
-        uint16_t sb[R][NG];
+        float sc[R][NG];
         const int u = c * 4 + quad;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t n = min(n0 + 16 * r + low, (int64_t)a.N - 1);
-            w[r] = reinterpret_cast<const uint4 *>(a.Wq4)[n * units + min(u, units - 1)];
+            w[r] = reinterpret_cast<const uint4 *>(a.Wq4)[n * units + (WHOLE ? u : min(u, units - 1))];
+            const uint16_t *sp = a.s4 + n * groups + c * NG;
+            if (WHOLE && NG == 4) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(sp);
+                sc[r][0] = bf16_lo(v.x);
+                sc[r][1 % NG] = bf16_hi(v.x);
+                sc[r][2 % NG] = bf16_lo(v.y);
+                sc[r][3 % NG] = bf16_hi(v.y);
+            } else if (WHOLE && NG == 2) {
+                const uint32_t v = *reinterpret_cast<const uint32_t *>(sp);
+                sc[r][0] = bf16_lo(v);
+                sc[r][1 % NG] = bf16_hi(v);
+            } else {
 #pragma unroll
-            for (int g = 0; g < NG; ++g) sb[r][g] = a.s4[n * groups + min(c * NG + g, groups - 1)];
-        }
-        float x[4][8];
-        float top = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            // the 8 values that matrix instruction j takes from this quad:
-            // dword dj of quad dq's 16 bytes
-            const int dq = GROUP == 128 ? quad : GROUP == 64 ? (quad & 1) | (j & 2) : j;
-            const int dj = GROUP == 128 ? j : GROUP == 64 ? (j & 1) | (quad & 2) : quad;
-            const int uu = c * 4 + dq;
-            load8<BF16>(a.X, xrow + 32 * (int64_t)min(uu, units - 1) + 8 * dj, x[j]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (uu >= units) x[j][e] = 0.0f;
-                top = fmaxf(top, fabsf(x[j][e]));
+                for (int g = 0; g < NG; ++g)
+                    sc[r][g] = __uint_as_float((uint32_t)sp[min(g, groups - 1 - c * NG)] << 16);
             }
         }
-        top = quad_max(top);
-        // top in [2^(e-127), 2^(e-126)) -> [2^13, 2^14), in two factors as
-        // their product may pass fp32's range
-        const int ex = max((int)(__float_as_uint(top) >> 23), 1);
-        const int e1 = (140 - ex) / 2, e2 = 140 - ex - e1;
-        const float f1 = __uint_as_float((uint32_t)(127 + e1) << 23);
-        const float f2 = __uint_as_float((uint32_t)(127 + e2) << 23);
-        // 2^(ex - 140), exact (as a subnormal where ex < 14)
-        const float back = __uint_as_float((uint32_t)(127 - e1) << 23) *
-                           __uint_as_float((uint32_t)(127 - e2) << 23);
-        half8 xh[NS][4];
+        // four tokens at a time: this lane has values 8 low .. of token 4 i + quad
+        const int at = WHOLE ? 8 * low : min(8 * low, a.K - 8 - c * kChunk);
+        float x[4][8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int i = 0; i < 4; ++i)
+            load8<BF16>(a.X, (int64_t)min(4 * i + quad, a.M - 1) * a.K + c * kChunk + at, x[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (4 * i >= a.M) break;            // uniform: their rows of the operand are not used
+            float top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) top = fmaxf(top, fmaxf(fabsf(x[i][e]), fabsf(x[i][e + 1])));
+            top = group_max(top, 16);
+            // top in [2^(e-127), 2^(e-126)): to [2^13, 2^14), or by 2^127 where
+            // it is below 2^-114
+            const int ex = max((int)(__float_as_uint(top) >> 23), 13);
+            const float f1 = __uint_as_float((uint32_t)(267 - ex) << 23);
             uint32_t h[4], z[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {                  // in the codes' order
-                const float v0 = x[j][e] * f1 * f2, v1 = x[j][e + 4] * f1 * f2;
+                const float v0 = x[i][e] * f1, v1 = x[i][e + 4] * f1;
                 h[e] = f16_pair(v0, v1);
                 if (NS == 2) z[e] = f16_rest(v0, v1, h[e]);
             }
-            xh[0][j] = __builtin_bit_cast(half8, make_uint4(h[0], h[1], h[2], h[3]));
-            if (NS == 2) xh[NS - 1][j] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
+            uint4 *dst = xs + place<GROUP>(low >> 2, low & 3) * 17 + 4 * i + quad;
+            dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            if (NS == 2) dst[16 * 17] = make_uint4(z[0], z[1], z[2], z[3]);
+            if (low == 0) xf[4 * i + quad] = __uint_as_float((uint32_t)(ex - 12) << 23) * 0.5f;   // 2^(ex - 140)
         }
-        // the factors of the tokens whose sums this lane gets
-        float f[4];
+        wave_fence();
+        half8 xh[NS][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = __shfl(back, 4 * quad + e);
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                xh[s][j] = __builtin_bit_cast(half8, xs[(s * 16 + j * 4 + quad) * 17 + low]);
+        const float4v f = *reinterpret_cast<const float4v *>(xf + 4 * quad);
+        wave_fence();
+        if (!WHOLE && u >= units) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) w[r] = make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             uint32_t d[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
@@ -328,69 +479,89 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_w4_mfma_kernel(ProdArgs a
 #pragma unroll
                     for (int s = 0; s < NS; ++s) acc = mfma_16x16x32(xh[s][j], b, acc);
                 }
-                const float sc = __uint_as_float((uint32_t)sb[r][g] << 16);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tot[r][e] = __builtin_fmaf(acc[e] * f[e], sc, tot[r][e]);
+                for (int e = 0; e < 4; ++e) tot[r][e] = __builtin_fmaf(acc[e] * f[e], sc[r][g], tot[r][e]);
             }
         }
     }
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(lds);            // [wave][R][4][64]
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) red[wave][r][e][lane] = tot[r][e];
+        for (int e = 0; e < 4; ++e) red[((wave * R + r) * 4 + e) * 64 + lane] = tot[r][e];
     __syncthreads();
     for (int i = threadIdx.x; i < R * 256; i += blockDim.x) {
         const int r = i >> 8, e = i >> 6 & 3, l = i & 63;
         const int m = 4 * (l >> 4) + e;
         const int64_t n = n0 + 16 * r + (l & 15);
         if (m >= a.M || n >= a.N) continue;
-        float y = red[0][r][e][l];
-        for (int v = 1; v < waves; ++v) y += red[v][r][e][l];
+        float y = red[i];
+        for (int v = 1; v < waves; ++v) y += red[v * R * 256 + i];
         a.Y[m * (int64_t)a.N + n] = y;
     }
 }
 
 // Waves for `parts` of K: as few as keep the longest share of a wave.
-int waves_for(int parts) {
-    if (parts <= kMaxWaves) return parts > 0 ? parts : 1;
-    const int share = (parts + kMaxWaves - 1) / kMaxWaves;
+int waves_for(int parts, int most) {
+    if (parts <= most) return parts > 0 ? parts : 1;
+    const int share = (parts + most - 1) / most;
     return (parts + share - 1) / share;
 }
 
 template <bool BF16, int M, int R>
 void few(const ProdArgs &a, int group, hipStream_t s) {
     const unsigned grid = (unsigned)((a.N + 4 * R - 1) / (4 * R));
-    const int waves = waves_for((a.K + kSlice - 1) / kSlice);
+    const int waves = waves_for((a.K + kSlice - 1) / kSlice, kMaxWaves);
     hipLaunchKernelGGL((gemv_w4_few_kernel<BF16, M, R>), dim3(grid), dim3(64 * waves), 0, s, a,
                        group == 32 ? 0 : group == 64 ? 1 : 2);
 }
-template <bool BF16, int GROUP, int R>
+template <bool BF16, int M, int R>
+void stream(const ProdArgs &a, int group, hipStream_t s) {
+    const int tiles = (a.N + 4 * R - 1) / (4 * R), per = kStreamThreads / 64;
+    const int groups = (tiles + per - 1) / per;
+    hipLaunchKernelGGL((gemv_w4_stream_kernel<BF16, M, R>),
+                       dim3(groups < kStreamGroups ? groups : kStreamGroups), dim3(kStreamThreads),
+                       stream_lds(M, a.K), s, a, group == 32 ? 0 : group == 64 ? 1 : 2);
+}
+template <bool BF16, int GROUP, int R, bool WHOLE, int WAVES>
 void many(const ProdArgs &a, hipStream_t s) {
+    static_assert(R * 1024 <= wave_lds<BF16>(), "the final sums fit X's place");
     const unsigned grid = (unsigned)((a.N + 16 * R - 1) / (16 * R));
-    const int waves = waves_for((a.K + kChunk - 1) / kChunk);
-    hipLaunchKernelGGL((gemv_w4_mfma_kernel<BF16, GROUP, R>), dim3(grid), dim3(64 * waves), 0, s, a);
+    const int waves = waves_for((a.K + kChunk - 1) / kChunk, WAVES);
+    hipLaunchKernelGGL((gemv_w4_mfma_kernel<BF16, GROUP, R, WHOLE, WAVES>), dim3(grid), dim3(64 * waves),
+                       waves * wave_lds<BF16>(), s, a);
+}
+template <bool BF16, int GROUP, bool WHOLE>
+void many(const ProdArgs &a, hipStream_t s) {
+    // the widest workgroups that still give every CU one
+    if (a.N <= 16 * kCUs) many<BF16, GROUP, 1, WHOLE, 16>(a, s);
+    else if (a.N <= 32 * kCUs) many<BF16, GROUP, 2, WHOLE, 16>(a, s);
+    else many<BF16, GROUP, 4, WHOLE, 8>(a, s);
 }
 template <bool BF16, int GROUP>
 void many(const ProdArgs &a, hipStream_t s) {
-    if (a.N >= 16384) many<BF16, GROUP, 4>(a, s);
-    else many<BF16, GROUP, 1>(a, s);
+    if (a.K % kChunk == 0 && reinterpret_cast<uintptr_t>(a.s4) % (2 * kChunk / GROUP) == 0)
+        many<BF16, GROUP, true>(a, s);
+    else
+        many<BF16, GROUP, false>(a, s);
+}
+
+template <bool BF16, int M>
+void one_or_two(const ProdArgs &a, int group, hipStream_t s) {
+    if (a.N >= kStreamRows && stream_lds(M, a.K) <= kStreamLds)
+        stream<BF16, M, 4>(a, group, s);
+    else
+        few<BF16, M, 4>(a, group, s);
 }
 
 template <bool BF16>
 void product(const ProdArgs &a, int group, hipStream_t s) {
-    if (a.M == 1) {
-        if (a.N >= 8192) few<BF16, 1, 8>(a, group, s);
-        else few<BF16, 1, 2>(a, group, s);
-    } else if (a.M == 2) {
-        if (a.N >= 8192) few<BF16, 2, 8>(a, group, s);
-        else few<BF16, 2, 2>(a, group, s);
-    } else if (group == 32) {
-        many<BF16, 32>(a, s);
-    } else if (group == 64) {
-        many<BF16, 64>(a, s);
-    } else {
-        many<BF16, 128>(a, s);
-    }
+    if (a.M == 1) one_or_two<BF16, 1>(a, group, s);
+    else if (a.M == 2) one_or_two<BF16, 2>(a, group, s);
+    else if (group == 32) many<BF16, 32>(a, s);
+    else if (group == 64) many<BF16, 64>(a, s);
+    else many<BF16, 128>(a, s);
 }
 
 int dword_shift(int group) { return group == 32 ? 2 : group == 64 ? 3 : 4; }
