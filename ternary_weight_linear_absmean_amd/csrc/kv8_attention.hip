@@ -36,7 +36,10 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 64;                   // keys per wave and step
 constexpr int kRows = 16;                   // rows of a tile
-constexpr int kBusyGroups = 1536;           // workgroups that the parts are to make
+#ifndef BG
+#define BG 1536
+#endif
+constexpr int kBusyGroups = BG;           // workgroups that the parts are to make
 
 // Four int8 codes -> four fp16.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -365,11 +368,18 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
 }
 
 // Joins the parts of the rows whose keys were read in more than one: one
-// workgroup per (row, head); wave w sums the parts w, w + 4, ...
-template <bool BF16, int D>
-__global__ __launch_bounds__(kThreads) void kv8_join_kernel(Args a) {
-    constexpr int E = D / 64;
-    __shared__ float sum[kWaves][D], sum_l[kWaves], top[kWaves];
+// workgroup per (row, head).  The parts' weights 2^(m_s - m) go to LDS first;
+// then D / 4 threads read a part, 16 bytes each, so that the workgroup has 4
+// THREADS / D parts in flight: 256 threads for up to 64 parts, 1024 for more
+// (128 parts of 20 rows: 11.4 us with 256 threads, 4.7 with 1024; 4 parts of
+// 1280 rows: 4.9 and 10.3).
+constexpr int kMaxParts = 2048;
+template <bool BF16, int D, int THREADS, int PARTS>
+__global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
+    constexpr int kWide = D / 4, kLines = THREADS / kWide, kJoinWaves = THREADS / 64;
+    __shared__ float weight[PARTS > THREADS ? PARTS : THREADS];
+    __shared__ float red[2][kJoinWaves];
+    __shared__ float4 sum[kJoinWaves][kWide];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row = blockIdx.x;
     const Kv8Seqs &sq = a.seqs;
@@ -379,35 +389,69 @@ __global__ __launch_bounds__(kThreads) void kv8_join_kernel(Args a) {
     if (t < q_at(sq, b) || t >= q1) return;
     const int64_t keys = min((int64_t)sq.lengths[b] - (q1 - t) + 1, key_capacity(a));
     if (keys <= a.chunk) return;                                // written directly
-    const int parts = (int)((keys + a.chunk - 1) / a.chunk);    // <= S
+    const int parts = (int)((keys + a.chunk - 1) / a.chunk);    // <= S <= PARTS
     const int64_t all = (int64_t)sq.n_tok * a.QH;
-    const float *ml = a.part + (int64_t)a.S * all * D;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.S * all * D);
+    // the first lines are under way while the weights are formed
+    const int d = threadIdx.x % kWide, line = threadIdx.x / kWide;
+    const float4 *src = reinterpret_cast<const float4 *>(a.part) + row * kWide + d;
+    const int64_t pitch = all * kWide;
+    const float4 first = src[min(line, parts - 1) * pitch];
+    constexpr int kEach = (PARTS + THREADS - 1) / THREADS;
+    float2 v[kEach];
     float mm = -INFINITY;
-    for (int s = lane; s < parts; s += 64) mm = fmaxf(mm, ml[(s * all + row) * 2]);
-    mm = group_max(mm, 64);
-    const float base = mm == -INFINITY ? 0.0f : mm;
-    float y[E] = {}, ll = 0.0f;
-    for (int s = wave; s < parts; s += kWaves) {
-        const float f = exp2_fast(ml[(s * all + row) * 2] - base);
-        ll += ml[(s * all + row) * 2 + 1] * f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] += a.part[(s * all + row) * D + 64 * e + lane] * f;
+    for (int i = 0; i < kEach; ++i) {
+        const int s = threadIdx.x + i * THREADS;
+        v[i] = s < parts ? ml[s * all + row] : make_float2(-INFINITY, 0.0f);
+        mm = fmaxf(mm, v[i].x);
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sum[wave][64 * e + lane] = y[e];
-    if (lane == 0) sum_l[wave] = ll;
+    mm = group_max(mm, 64);
+    if (lane == 0) red[0][wave] = mm;
     __syncthreads();
-    if (threadIdx.x < D / 4) {
-        const int d = 4 * threadIdx.x;
-        ll = 0.0f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    mm = group_max(red[0][lane % kJoinWaves], kJoinWaves);
+    const float base = mm == -INFINITY ? 0.0f : mm;
+    float ll = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            ll += sum_l[w];
-            o.x += sum[w][d]; o.y += sum[w][d + 1]; o.z += sum[w][d + 2]; o.w += sum[w][d + 3];
+    for (int i = 0; i < kEach; ++i) {
+        const float f = exp2_fast(v[i].x - base);
+        weight[threadIdx.x + i * THREADS] = f;
+        ll += v[i].y * f;
+    }
+    ll = quad_sum(ll);
+    ll += dpp_f32<kDppXor1>(ll);
+    ll += dpp_f32<kDppXor2>(ll);
+    ll += dpp_f32<kDppHalfMirror>(ll);
+    ll += dpp_f32<kDppMirror>(ll);
+    if (lane == 0) red[1][wave] = ll;
+    __syncthreads();
+    float f = weight[line];
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (line < parts) y = make_float4(first.x * f, first.y * f, first.z * f, first.w * f);
+#pragma unroll 4
+    for (int s = line + kLines; s < parts; s += kLines) {
+        const float4 x = src[s * pitch];
+        f = weight[s];
+        y.x += x.x * f; y.y += x.y * f; y.z += x.z * f; y.w += x.w * f;
+    }
+    // lanes kWide apart have the same values
+    for (int o = kWide; o < 64; o *= 2) {
+        y.x += __shfl_xor(y.x, o); y.y += __shfl_xor(y.y, o);
+        y.z += __shfl_xor(y.z, o); y.w += __shfl_xor(y.w, o);
+    }
+    if (lane < kWide) sum[wave][lane] = y;
+    __syncthreads();
+    if (threadIdx.x < kWide) {
+        ll = 0.0f;
+        y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kJoinWaves; ++w) {
+            ll += red[1][w];
+            const float4 x = sum[w][threadIdx.x];
+            y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
         }
         const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-        store4<BF16>(a.out, row * D + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        store4<BF16>(a.out, row * D + 4 * threadIdx.x, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
     }
 }
 
@@ -434,9 +478,11 @@ hipError_t attend(const Args &a, const Plan &p, hipStream_t s) {
     hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>),
                        dim3((unsigned)p.slots, (unsigned)a.c.KVH, (unsigned)p.S), dim3(kThreads), 0, s,
                        a);
-    if (p.S > 1)
-        hipLaunchKernelGGL((kv8_join_kernel<BF16, D>), dim3((unsigned)(a.seqs.n_tok * a.QH)),
-                           dim3(kThreads), 0, s, a);
+    const dim3 rows((unsigned)(a.seqs.n_tok * a.QH));
+    if (p.S > 64)
+        hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 1024, kMaxParts>), rows, dim3(1024), 0, s, a);
+    else if (p.S > 1)
+        hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 256, 64>), rows, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
