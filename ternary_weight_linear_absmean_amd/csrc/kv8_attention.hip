@@ -36,10 +36,11 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 64;                   // keys per wave and step
 constexpr int kRows = 16;                   // rows of a tile
-#ifndef BG
-#define BG 1536
+#ifndef FEWR
+#define FEWR 32
 #endif
-constexpr int kBusyGroups = BG;           // workgroups that the parts are to make
+constexpr int kFewRows = FEWR;                // rows of a sequence from which many is many
+constexpr int kBusyGroups = 1536;           // workgroups that the parts are to make
 
 // Four int8 codes -> four fp16.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -84,6 +85,13 @@ __device__ __forceinline__ float pow2_above(float x) {
     return __uint_as_float((e + 1) << 23);
 }
 
+// The power of two that takes |x| <= top to [2^13, 2^14), or 2^127 where top is
+// below 2^-114.
+__device__ __forceinline__ float to_f16_range(float top) {
+    const int e = max((int)(__float_as_uint(top) >> 23), 13);
+    return __uint_as_float((uint32_t)(267 - e) << 23);
+}
+
 struct Args {
     const void *q;
     void *out;
@@ -91,6 +99,7 @@ struct Args {
     Kv8Seqs seqs;
     Kv8Cache c;
     int QH, G, S;
+    int64_t min_rows, max_rows;   // rows of the sequences that a kernel takes
     int64_t chunk;            // keys of a part
     float scale2;             // scale * log2(e)
 };
@@ -123,7 +132,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     });
     const int q0 = q_at(sq, b), n = q_at(sq, b + 1) - q0;
     const int64_t nth = slot - ((int64_t)q0 * G / kRows + b);
-    if (nth < 0 || n <= 0 || nth * kRows >= (int64_t)n * G) return;
+    if (nth < 0 || n <= 0 || nth * kRows >= (int64_t)n * G || (int64_t)n * G > a.max_rows) return;
     const int64_t r0 = nth * kRows;
     const int rows = (int)min((int64_t)kRows, (int64_t)n * G - r0);
     const int64_t start = (int64_t)sq.lengths[b] - n;             // position of the first new token
@@ -156,12 +165,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
                                        fmaxf(fabsf(v[dc][e].z), fabsf(v[dc][e].w))));
             }
         top = quad_max(top);
-        // top in [2^(e-127), 2^(e-126)): times 2^(140 - e) it is in [2^13, 2^14);
-        // in two factors, as 2^(140 - e) may pass fp32's range
-        const int e = max((int)(__float_as_uint(top) >> 23), 1);
-        const float f1 = __uint_as_float((uint32_t)(127 + (140 - e) / 2) << 23);
-        const float f2 = __uint_as_float((uint32_t)(127 + (140 - e) - (140 - e) / 2) << 23);
-        c_row = a.scale2 / f1 / f2;
+        const float f = to_f16_range(top);
+        c_row = a.scale2 / f;
 #pragma unroll
         for (int dc = 0; dc < ND; ++dc)
 #pragma unroll
@@ -170,8 +175,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
 #pragma unroll
                 for (int e2 = 0; e2 < 2; ++e2) {
                     const float4 x = v[dc][2 * hf + e2];
-                    const float x0 = x.x * f1 * f2, x1 = x.y * f1 * f2;
-                    const float x2 = x.z * f1 * f2, x3 = x.w * f1 * f2;
+                    const float x0 = x.x * f, x1 = x.y * f, x2 = x.z * f, x3 = x.w * f;
                     w[2 * e2] = f16_pair(x0, x1);
                     w[2 * e2 + 1] = f16_pair(x2, x3);
                     z[2 * e2] = f16_rest(x0, x1, w[2 * e2]);
@@ -367,6 +371,292 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     }
 }
 
+// Many rows: one workgroup per (128 rows, key head, part of the keys), 32 rows
+// a wave, 64 keys at a time.  The workgroup turns the codes of a tile into fp16
+// once, in LDS, for all its rows (16 rows a workgroup did it for each: four
+// conversions per matrix step), the next tile's codes in flight meanwhile;
+// 32x32x16 products take 1 KB of LDS per 32 cycles, which four SIMDs just get.
+//
+// Layouts (lane = 32 half + low): S^T = K Q^T puts key 8 (i / 4) + 4 half + i
+// % 4 of the operand's rows, row low, into accumulator i.  Operand row r holds
+// key r with its bits 2 and 3 swapped, so accumulators 8 s .. 8 s + 7 are keys
+// 16 s + 8 half .. + 7: the P^T operand of step s.
+//
+// LDS: K [64][D] and V^T [D][64] in 16-byte pieces, piece p of line y at p ^ y
+// (K, D = 128) or p ^ (y / 2) (lines of 128 bytes), so that 16 lanes reading
+// one piece of 16 lines touch every bank once.
+constexpr int kManyRows = 128;
+typedef float float16v __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ float16v mfma_32x32x16(half8 a, half8 b, float16v c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+template <bool BF16, int D>
+__global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
+    constexpr int NS = BF16 ? 1 : 2;
+    constexpr int NQ = D / 16;              // steps of K Q^T
+    constexpr int NO = D / 32;              // tiles of the output
+    constexpr int kPieces = kTile * D / 16 / kThreads;      // 16-byte pieces of K and of V per thread
+    __shared__ uint4 kl[2][kTile * D / 8], vl[2][kTile * D / 8];
+    __shared__ float4 granules[2][4];       // sk, sv and 1 where valid, of 16 tokens each
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int low = lane & 31, half = lane >> 5;
+    const int h = blockIdx.y, split = blockIdx.z;
+    const Kv8Seqs &sq = a.seqs;
+    const Kv8Cache &c = a.c;
+    const int64_t slot = blockIdx.x;
+    const int G = a.G;
+    const int b = find_seq(sq.B, slot, [&](int i) {
+        return (int64_t)q_at(sq, i) * G / kManyRows + i;
+    });
+    const int q0 = q_at(sq, b), n = q_at(sq, b + 1) - q0;
+    int64_t nth = slot - ((int64_t)q0 * G / kManyRows + b);
+    const int64_t tiles = ((int64_t)n * G + kManyRows - 1) / kManyRows;
+    if (nth < 0 || n <= 0 || nth >= tiles || (int64_t)n * G <= a.min_rows) return;
+    nth = tiles - 1 - nth;                  // the rows that see most first
+    const int64_t all_rows = (int64_t)n * G;
+    const int64_t r0 = nth * kManyRows;
+    const int64_t start = (int64_t)sq.lengths[b] - n;
+    const int64_t cap = key_capacity(a);
+    const int64_t end = min(start + (min(r0 + kManyRows, all_rows) - 1) / G + 1, cap);
+    const int64_t k0 = (int64_t)split * a.chunk;
+    if (split > 0 && k0 >= end) return;
+    const int64_t k1 = min(end, k0 + a.chunk);
+
+    const int64_t rw = r0 + 32 * wave;      // the wave's first row
+    const bool rows_here = rw < all_rows;
+    const int64_t r = min(rw + low, all_rows - 1);
+    const int tok = (int)(r / G);
+    const int64_t row = (int64_t)(q0 + tok) * a.QH + h * G + (int)(r - (int64_t)tok * G);
+    const int64_t pos = start + tok;
+    // the keys that the wave's first and last row see
+    const int64_t pos_lo = start + min(rw, all_rows - 1) / G;
+    const int64_t pos_hi = start + min(rw + 31, all_rows - 1) / G;
+
+    half8 qh[NS][NQ];
+    float c_row;
+    {
+        float4 v[NQ][2];
+        float top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < NQ; ++s)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                v[s][e] = load4<BF16>(a.q, row * D + 16 * s + 8 * half + 4 * e);
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(v[s][e].x), fabsf(v[s][e].y)),
+                                       fmaxf(fabsf(v[s][e].z), fabsf(v[s][e].w))));
+            }
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float f = to_f16_range(top);
+        c_row = a.scale2 / f;
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) {
+            uint32_t w[4], z[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x0 = v[s][e].x * f, x1 = v[s][e].y * f, x2 = v[s][e].z * f, x3 = v[s][e].w * f;
+                w[2 * e] = f16_pair(x0, x1);
+                w[2 * e + 1] = f16_pair(x2, x3);
+                if (NS == 2) {
+                    z[2 * e] = f16_rest(x0, x1, w[2 * e]);
+                    z[2 * e + 1] = f16_rest(x2, x3, w[2 * e + 1]);
+                }
+            }
+            qh[0][s] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
+            if (NS == 2) qh[NS - 1][s] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
+        }
+    }
+
+    // piece i of this thread: of K key kp / (D / 16), values 16 (kp % (D / 16))
+    // ..; of V value vp / 4, tokens 16 (vp % 4) ..
+    const int32_t *table = sq.table + (int64_t)b * sq.max_blocks;
+    auto block_at = [&](int64_t t) {
+        const int id = t < k1 ? table[t >> c.t_shift] : -1;
+        return id >= 0 && id < c.n_blocks ? id : -1;
+    };
+    uint4 kr[kPieces], vr[kPieces];
+    float4 gr = make_float4(0.f, 0.f, 0.f, 0.f);
+    int kid[kPieces], vid[kPieces], gid = -1;
+    auto load_ids = [&](int64_t tile) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = threadIdx.x + i * kThreads;
+            kid[i] = block_at(tile + p / (D / 16));
+            vid[i] = block_at(tile + 16 * (p & 3));
+        }
+        if (threadIdx.x < 4) gid = block_at(tile + 16 * threadIdx.x);
+    };
+    auto load_tile = [&](int64_t tile) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = threadIdx.x + i * kThreads;
+            const int key = p / (D / 16), kd = p % (D / 16), vd = p >> 2;
+            const int64_t kb = (int64_t)max(kid[i], 0) * c.KVH + h, vb = (int64_t)max(vid[i], 0) * c.KVH + h;
+            kr[i] = *reinterpret_cast<const uint4 *>(c.K + (kb * c.T + ((tile + key) & (c.T - 1))) * D + 16 * kd);
+            vr[i] = *reinterpret_cast<const uint4 *>(c.V + (vb * D + vd) * c.T +
+                                                     ((tile + 16 * (p & 3)) & (c.T - 1)));
+        }
+        if (threadIdx.x < 4) {
+            const int64_t gb = (int64_t)max(gid, 0) * c.KVH + h;
+            gr = make_float4(c.sk[gb], c.sv[gb], gid >= 0 ? 1.0f : 0.0f, 0.0f);
+        }
+    };
+    auto k_at = [](int key, int piece) {
+        return D == 128 ? key * 16 + (piece ^ (key & 15)) : key * 8 + (piece ^ ((key >> 1) & 7));
+    };
+    auto v_at = [](int d, int piece) { return d * 8 + (piece ^ ((d >> 1) & 7)); };
+    auto to_lds = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = threadIdx.x + i * kThreads;
+            const int key = p / (D / 16), kd = p % (D / 16), vd = p >> 2, vt = p & 3;
+            kl[buf][k_at(key, 2 * kd)] = __builtin_bit_cast(uint4, codes8(kr[i].x, kr[i].y));
+            kl[buf][k_at(key, 2 * kd + 1)] = __builtin_bit_cast(uint4, codes8(kr[i].z, kr[i].w));
+            vl[buf][v_at(vd, 2 * vt)] = __builtin_bit_cast(uint4, codes8(vr[i].x, vr[i].y));
+            vl[buf][v_at(vd, 2 * vt + 1)] = __builtin_bit_cast(uint4, codes8(vr[i].z, vr[i].w));
+        }
+        if (threadIdx.x < 4) granules[buf][threadIdx.x] = gr;
+    };
+
+    float m = -INFINITY, l = 0.0f, u = 0.0f;
+    float16v o[NO];
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+    // operand row low holds this key of 32
+    const int key_low = (low & 0x13) | (low & 4) << 1 | (low & 8) >> 1;
+
+    if (k0 < k1) {
+        load_ids(k0);
+        load_tile(k0);
+        load_ids(k0 + kTile);
+        to_lds(0);
+        __syncthreads();
+        int buf = 0;
+        for (int64_t tile = k0; tile < k1; tile += kTile, buf ^= 1) {
+            const bool more = tile + kTile < k1;
+            if (more) {
+                load_tile(tile + kTile);
+                load_ids(tile + 2 * kTile);
+            }
+            if (rows_here && tile <= pos_hi) {
+                float16v s[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+#pragma unroll
+                    for (int st = 0; st < NQ; ++st) {
+                        const half8 k = __builtin_bit_cast(half8, kl[buf][k_at(32 * t + key_low, 2 * st + half)]);
+#pragma unroll
+                        for (int x = 0; x < NS; ++x) s[t] = mfma_32x32x16(k, qh[x][st], s[t]);
+                    }
+                }
+                float4 gn[4];
+                float top = -INFINITY, sv_top = 0.0f;
+                bool valid = true;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    gn[g] = granules[buf][g];
+                    valid = valid && gn[g].z != 0.0f;
+                    sv_top = fmaxf(sv_top, gn[g].z != 0.0f ? fabsf(gn[g].y) : 0.0f);
+                }
+                if (valid && tile + kTile <= k1 && tile + kTile - 1 <= pos_lo) {     // uniform
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float cs = c_row * gn[g].x;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float x = s[g >> 1][8 * (g & 1) + e] * cs;
+                            s[g >> 1][8 * (g & 1) + e] = x;
+                            top = fmaxf(top, x);
+                        }
+                    }
+                } else {
+                    const int lim = (int)min(min(pos + 1, k1) - tile, (int64_t)kTile);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float cs = c_row * gn[g].x;
+                        const int lim_g = gn[g].z != 0.0f ? lim - 16 * g - 8 * half : 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float x = e < lim_g ? s[g >> 1][8 * (g & 1) + e] * cs : -INFINITY;
+                            s[g >> 1][8 * (g & 1) + e] = x;
+                            top = fmaxf(top, x);
+                        }
+                    }
+                }
+                const float m_new = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+                const float base = m_new == -INFINITY ? 0.0f : m_new;
+                const float u_new = fmaxf(u, pow2_above(sv_top));
+                float fix = exp2_fast(m - base);
+                l *= fix;
+                if (u_new != u) fix *= u / u_new;
+                if (__ballot(fix != 1.0f)) {
+#pragma unroll
+                    for (int i = 0; i < NO; ++i) o[i] *= fix;
+                }
+                m = m_new;
+                u = u_new;
+                const float inv_u = 16384.0f / u;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {          // 16 keys
+                    const float w_sv = gn[g].z != 0.0f ? gn[g].y * inv_u : 0.0f;
+                    uint32_t w[4], z[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p0 = exp2_fast(s[g >> 1][8 * (g & 1) + 2 * e] - base);
+                        const float p1 = exp2_fast(s[g >> 1][8 * (g & 1) + 2 * e + 1] - base);
+                        l += p0 + p1;
+                        const float y0 = p0 * w_sv, y1 = p1 * w_sv;
+                        w[e] = f16_pair(y0, y1);
+                        if (NS == 2) z[e] = f16_rest(y0, y1, w[e]);
+                    }
+                    const half8 p_hi = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
+                    const half8 p_lo = NS == 2 ? __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3])) : p_hi;
+#pragma unroll
+                    for (int i = 0; i < NO; ++i) {
+                        const half8 v = __builtin_bit_cast(half8, vl[buf][v_at(32 * i + low, 2 * g + half)]);
+                        o[i] = mfma_32x32x16(v, p_hi, o[i]);
+                        if (NS == 2) o[i] = mfma_32x32x16(v, p_lo, o[i]);
+                    }
+                }
+            }
+            if (more) to_lds(buf ^ 1);
+            __syncthreads();
+        }
+    }
+    if (rw + low >= all_rows) return;
+    l += __shfl_xor(l, 32);
+    const float unit = u / 16384.0f;
+    if (min(pos + 1, cap) <= a.chunk) {
+        if (split > 0) return;
+        const float inv = l > 0.0f ? unit / l : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                store4<BF16>(a.out, row * D + 32 * i + 2 * e + 4 * half,
+                             make_float4(o[i][e] * inv, o[i][e + 1] * inv, o[i][e + 2] * inv, o[i][e + 3] * inv));
+    } else {
+        const int64_t all = (int64_t)sq.n_tok * a.QH;
+        float *dst = a.part + ((int64_t)split * all + row) * D;
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                store4<false>(dst, 32 * i + 2 * e + 4 * half,
+                              make_float4(o[i][e] * unit, o[i][e + 1] * unit, o[i][e + 2] * unit, o[i][e + 3] * unit));
+        if (half == 0) {
+            float *ml = a.part + (int64_t)a.S * all * D + ((int64_t)split * all + row) * 2;
+            ml[0] = m;
+            ml[1] = l;
+        }
+    }
+}
+
 // Joins the parts of the rows whose keys were read in more than one: one
 // workgroup per (row, head).  The parts' weights 2^(m_s - m) go to LDS first;
 // then D / 4 threads read a part, 16 bytes each, so that the workgroup has 4
@@ -474,10 +764,20 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
 }
 
 template <bool BF16, int D>
-hipError_t attend(const Args &a, const Plan &p, hipStream_t s) {
-    hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>),
-                       dim3((unsigned)p.slots, (unsigned)a.c.KVH, (unsigned)p.S), dim3(kThreads), 0, s,
-                       a);
+hipError_t attend(Args a, const Plan &p, hipStream_t s) {
+    // Where the sequences bring many rows on average, those that do go to the
+    // kernel for many; the other kernel takes the rest (all of them otherwise).
+    const int64_t rows_all = a.seqs.n_tok * (int64_t)a.G;
+    a.max_rows = rows_all;
+    if (rows_all > kFewRows * (int64_t)a.seqs.B) {
+        a.min_rows = a.max_rows = a.seqs.B > 1 ? kFewRows : 0;
+        hipLaunchKernelGGL((kv8_rows128_kernel<BF16, D>),
+                           dim3((unsigned)(rows_all / kManyRows + a.seqs.B), (unsigned)a.c.KVH, (unsigned)p.S),
+                           dim3(kThreads), 0, s, a);
+    }
+    if (a.max_rows > 0)
+        hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>),
+                           dim3((unsigned)p.slots, (unsigned)a.c.KVH, (unsigned)p.S), dim3(kThreads), 0, s, a);
     const dim3 rows((unsigned)(a.seqs.n_tok * a.QH));
     if (p.S > 64)
         hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 1024, kMaxParts>), rows, dim3(1024), 0, s, a);
