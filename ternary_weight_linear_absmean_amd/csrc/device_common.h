@@ -130,6 +130,12 @@ __device__ __forceinline__ float quad_max(float v) {
     r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+// The larger of lanes l and l ^ 32.
+__device__ __forceinline__ float half_max(float v) {
+    const uint32_t a = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 __device__ __forceinline__ float quad_sum(float v) {
     uint32_t a = __float_as_uint(v);
     auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);

@@ -79,10 +79,15 @@ __device__ __forceinline__ void store4(void *p, int64_t at, float4 v) {
     }
 }
 
-// A power of two >= |x| (for |x| in [2^-100, 2^127)); 2^14 over it stays finite.
+// A power of two >= |x| (for |x| in [2^-100, 2^126)); 2^14 over it stays finite.
 __device__ __forceinline__ float pow2_above(float x) {
-    const uint32_t e = min(max((__float_as_uint(x) >> 23) & 255u, 27u), 253u);
+    const uint32_t e = min(max((__float_as_uint(x) >> 23) & 255u, 27u), 252u);
     return __uint_as_float((e + 1) << 23);
+}
+
+// 1 / x for a power of two in [2^-126, 2^126].
+__device__ __forceinline__ float pow2_inverse(float x) {
+    return __uint_as_float(0x7F000000u - __float_as_uint(x));
 }
 
 // The power of two that takes |x| <= top to [2^13, 2^14), or 2^127 where top is
@@ -90,6 +95,41 @@ __device__ __forceinline__ float pow2_above(float x) {
 __device__ __forceinline__ float to_f16_range(float top) {
     const int e = max((int)(__float_as_uint(top) >> 23), 13);
     return __uint_as_float((uint32_t)(267 - e) << 23);
+}
+
+constexpr float kUnit = 16384.0f;           // p sv / u is held as fp16 times this
+// A row's reference m follows its maximum only when that is kSlack above it:
+// 2^kSlack kUnit still is in fp16's range, and with scores of one spread the
+// sums are rescaled once or twice a sequence and not at every step.
+constexpr float kSlack = 1.9f;
+constexpr float kTiny = 1.17549435e-38f;    // a score factor of 0 (or none) without 0 * inf
+
+// Scores s (16 keys of a granule in 8 n accumulators: N = 2 of rows16, 1 of 8)
+// to fp16 weights times w_sv: hi, and lo for fp32 rows; their sum into l.  For
+// bf16 rows w_sv goes into the exponent (to 2^-20, against the 2^-12 of the
+// rounding): one multiply-add and one exponential a score.
+template <bool BF16, int N, typename S>
+__device__ __forceinline__ void weights(const S &s, float cs, float base, float w_sv, float &l, half8 *hi,
+                                        half8 *lo) {
+    const float w = fmaxf(w_sv, 1.4551915e-11f);          // 2^-36: below fp16's smallest step of kUnit
+    const float shift = BF16 ? __builtin_amdgcn_logf(w) - base : -base;
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        uint32_t h[4], z[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float p0 = exp2_fast(__builtin_fmaf(s(8 * k + 2 * e), cs, shift));
+            const float p1 = exp2_fast(__builtin_fmaf(s(8 * k + 2 * e + 1), cs, shift));
+            sum += p0 + p1;
+            const float y0 = BF16 ? p0 : p0 * w_sv, y1 = BF16 ? p1 : p1 * w_sv;
+            h[e] = f16_pair(y0, y1);
+            if (!BF16) z[e] = f16_rest(y0, y1, h[e]);
+        }
+        hi[k] = __builtin_bit_cast(half8, make_uint4(h[0], h[1], h[2], h[3]));
+        if (!BF16) lo[k] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
+    }
+    l = BF16 ? __builtin_fmaf(sum, __builtin_amdgcn_rcpf(w), l) : l + sum;
 }
 
 struct Args {
@@ -165,7 +205,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
                                        fmaxf(fabsf(v[dc][e].z), fabsf(v[dc][e].w))));
             }
         top = quad_max(top);
-        const float f = to_f16_range(top);
+        const float f = a.scale2 < 0.0f ? -to_f16_range(top) : to_f16_range(top);
         c_row = a.scale2 / f;
 #pragma unroll
         for (int dc = 0; dc < ND; ++dc)
@@ -187,7 +227,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
             }
     }
 
-    float m = -INFINITY, l = 0.0f, u = 0.0f;
+    float m = -INFINITY, l = 0.0f, u = 0.0f, unit_u = 0.0f;     // unit_u = kUnit / u
     float4v o[NO];
 #pragma unroll
     for (int i = 0; i < NO; ++i) o[i] = float4v{0.f, 0.f, 0.f, 0.f};
@@ -250,59 +290,36 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
             const bool more = next < k1;
             if (more) load_k(next, id_next);
 
-            const float cs = c_row * sk;
+            const float cs = fmaxf(c_row * sk, kTiny);
             const int64_t key0 = tile + 16 * quad;
             const bool whole = id >= 0 && key0 + 15 <= pos && key0 + 16 <= k1;
-            float top = -INFINITY;
-            if (__ballot(!whole) == 0) {
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        s[tt][i] *= cs;
-                        top = fmaxf(top, s[tt][i]);
-                    }
-            } else {
+            if (__ballot(!whole) != 0) {
                 const int lim = id >= 0 ? (int)min(min(pos + 1, k1) - key0, (int64_t)16) : 0;
 #pragma unroll
                 for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = s[tt][i] * cs;
-                        s[tt][i] = 4 * tt + i < lim ? x : -INFINITY;
-                        top = fmaxf(top, s[tt][i]);
-                    }
+                    for (int i = 0; i < 4; ++i) s[tt][i] = 4 * tt + i < lim ? s[tt][i] : -INFINITY;
             }
-            const float m_new = fmaxf(m, quad_max(top));
-            const float base = m_new == -INFINITY ? 0.0f : m_new;
+            float top = s[0][0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e >> 2][e & 3]);
+            top = quad_max(top * cs);
             const float u_new = fmaxf(u, pow2_above(quad_max(id >= 0 ? fabsf(sv) : 0.0f)));
-            float fix = exp2_fast(m - base);               // 0 while nothing was seen
-            l *= fix;
-            if (u_new != u) fix *= u / u_new;              // u = 0 at first
-            if (__ballot(fix != 1.0f)) {
+            if (__builtin_expect(__ballot(top > m + kSlack || u_new != u) != 0, 0)) {
+                const float m_new = fmaxf(m, top);
+                float fix = m == -INFINITY ? 0.0f : exp2_fast(m - m_new);
+                l *= fix;
+                const float inverse = pow2_inverse(u_new);
+                fix *= u * inverse;                        // u = 0 at first
+                unit_u = kUnit * inverse;
 #pragma unroll
                 for (int i = 0; i < NO; ++i) o[i] *= fix;
+                m = m_new;
+                u = u_new;
             }
-            m = m_new;
-            u = u_new;
-            const float w_sv = id >= 0 ? sv * (16384.0f / u) : 0.0f;
             half8 ph[NS][2];
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                uint32_t w[4], z[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int tt = 2 * ks + (e >> 1), i = 2 * (e & 1);
-                    const float p0 = exp2_fast(s[tt][i] - base), p1 = exp2_fast(s[tt][i + 1] - base);
-                    l += p0 + p1;
-                    const float y0 = p0 * w_sv, y1 = p1 * w_sv;
-                    w[e] = f16_pair(y0, y1);
-                    if (NS == 2) z[e] = f16_rest(y0, y1, w[e]);
-                }
-                ph[0][ks] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
-                if (NS == 2)
-                    ph[NS - 1][ks] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
-            }
+            weights<BF16, 2>([&](int e) { return s[e >> 2][e & 3]; }, cs, m == -INFINITY ? 0.0f : m, id >= 0 ? sv * unit_u : 0.0f, l,
+                             ph[0], ph[NS - 1]);
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
                 const half8 v_lo = codes8(vb[i].x, vb[i].y), v_hi = codes8(vb[i].z, vb[i].w);
@@ -322,7 +339,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     l = quad_sum(l);
 
     // join the waves: thread (row, values) sums what each brings
-    const float unit = u / 16384.0f;
+    const float unit = u / kUnit;
 #pragma unroll
     for (int i = 0; i < NO; ++i)
 #pragma unroll
@@ -371,11 +388,13 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     }
 }
 
-// Many rows: one workgroup per (128 rows, key head, part of the keys), 32 rows
-// a wave, 64 keys at a time.  The workgroup turns the codes of a tile into fp16
-// once, in LDS, for all its rows (16 rows a workgroup did it for each: four
-// conversions per matrix step), the next tile's codes in flight meanwhile;
-// 32x32x16 products take 1 KB of LDS per 32 cycles, which four SIMDs just get.
+// Many rows: one workgroup per (128 rows, key head, part of the keys), in two
+// groups of four waves that take 64-key tiles in turn; a wave has 32 rows.  A
+// group turns the codes of a tile into fp16 once, in LDS, for all rows (16-row
+// workgroups did it for each: four conversions per matrix step), the next
+// tile's codes in flight meanwhile.  The groups have sums of their own, joined
+// at the end: a workgroup fills a CU alone, so that a prompt's tiles, which see
+// few keys or many, pack better than two workgroups a CU.
 //
 // Layouts (lane = 32 half + low): S^T = K Q^T puts key 8 (i / 4) + 4 half + i
 // % 4 of the operand's rows, row low, into accumulator i.  Operand row r holds
@@ -386,21 +405,31 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
 // (K, D = 128) or p ^ (y / 2) (lines of 128 bytes), so that 16 lanes reading
 // one piece of 16 lines touch every bank once.
 constexpr int kManyRows = 128;
+constexpr int kManyThreads = 2 * kThreads;
 typedef float float16v __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ float16v mfma_32x32x16(half8 a, half8 b, float16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+template <int D>
+struct ManyLds {
+    // of each group, twice: the tile being used and the next
+    uint4 k[2][2][kTile * D / 8], v[2][2][kTile * D / 8];
+    float4 granules[2][2][4];               // sk, sv and 1 where valid, of 16 tokens each
+};
+
 template <bool BF16, int D>
-__global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
+__global__ __launch_bounds__(kManyThreads, 2) void kv8_rows128_kernel(Args a) {
     constexpr int NS = BF16 ? 1 : 2;
     constexpr int NQ = D / 16;              // steps of K Q^T
     constexpr int NO = D / 32;              // tiles of the output
     constexpr int kPieces = kTile * D / 16 / kThreads;      // 16-byte pieces of K and of V per thread
-    __shared__ uint4 kl[2][kTile * D / 8], vl[2][kTile * D / 8];
-    __shared__ float4 granules[2][4];       // sk, sv and 1 where valid, of 16 tokens each
+    extern __shared__ uint4 lds_raw[];
+    ManyLds<D> &lds = *reinterpret_cast<ManyLds<D> *>(lds_raw);
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6 & 3;
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    const int gt = threadIdx.x & (kThreads - 1);            // thread of the group
     const int low = lane & 31, half = lane >> 5;
     const int h = blockIdx.y, split = blockIdx.z;
     const Kv8Seqs &sq = a.seqs;
@@ -412,10 +441,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     });
     const int q0 = q_at(sq, b), n = q_at(sq, b + 1) - q0;
     int64_t nth = slot - ((int64_t)q0 * G / kManyRows + b);
-    const int64_t tiles = ((int64_t)n * G + kManyRows - 1) / kManyRows;
-    if (nth < 0 || n <= 0 || nth >= tiles || (int64_t)n * G <= a.min_rows) return;
-    nth = tiles - 1 - nth;                  // the rows that see most first
     const int64_t all_rows = (int64_t)n * G;
+    const int64_t tiles = (all_rows + kManyRows - 1) / kManyRows;
+    if (nth < 0 || n <= 0 || nth >= tiles || all_rows <= a.min_rows) return;
+    nth = tiles - 1 - nth;                  // the rows that see most first
     const int64_t r0 = nth * kManyRows;
     const int64_t start = (int64_t)sq.lengths[b] - n;
     const int64_t cap = key_capacity(a);
@@ -430,7 +459,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     const int tok = (int)(r / G);
     const int64_t row = (int64_t)(q0 + tok) * a.QH + h * G + (int)(r - (int64_t)tok * G);
     const int64_t pos = start + tok;
-    // the keys that the wave's first and last row see
+    // the positions of the wave's first and last row
     const int64_t pos_lo = start + min(rw, all_rows - 1) / G;
     const int64_t pos_hi = start + min(rw + 31, all_rows - 1) / G;
 
@@ -448,7 +477,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
                                        fmaxf(fabsf(v[s][e].z), fabsf(v[s][e].w))));
             }
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float f = to_f16_range(top);
+        const float f = a.scale2 < 0.0f ? -to_f16_range(top) : to_f16_range(top);
         c_row = a.scale2 / f;
 #pragma unroll
         for (int s = 0; s < NQ; ++s) {
@@ -468,192 +497,209 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
         }
     }
 
-    // piece i of this thread: of K key kp / (D / 16), values 16 (kp % (D / 16))
-    // ..; of V value vp / 4, tokens 16 (vp % 4) ..
+    // A tile starts at a multiple of 64, so a key's slot is its own low bits,
+    // and the tile's in blocks of 128.
     const int32_t *table = sq.table + (int64_t)b * sq.max_blocks;
     auto block_at = [&](int64_t t) {
         const int id = t < k1 ? table[t >> c.t_shift] : -1;
         return id >= 0 && id < c.n_blocks ? id : -1;
     };
+    const uint32_t block_bytes = (uint32_t)(c.KVH * c.T) * D;              // < 2^31
+    const int pk = gt / (D / 16), pv = gt >> 2;             // key and value of piece 0; + 32, + 64 of piece 1
+    const int8_t *kp = c.K + ((int64_t)h * c.T + (pk & (c.T - 1))) * D + 16 * (gt % (D / 16));
+    const int8_t *vp = c.V + ((int64_t)h * D + pv) * c.T + (16 * gt & 48 & (c.T - 1));
+    const int k_next = c.T > 32 ? 32 * D : 0, v_next = 64 * c.T;
     uint4 kr[kPieces], vr[kPieces];
     float4 gr = make_float4(0.f, 0.f, 0.f, 0.f);
-    int kid[kPieces], vid[kPieces], gid = -1;
+    int kid[kPieces], vid;
     auto load_ids = [&](int64_t tile) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int p = threadIdx.x + i * kThreads;
-            kid[i] = block_at(tile + p / (D / 16));
-            vid[i] = block_at(tile + 16 * (p & 3));
-        }
-        if (threadIdx.x < 4) gid = block_at(tile + 16 * threadIdx.x);
+        for (int i = 0; i < kPieces; ++i) kid[i] = block_at(tile + pk + 32 * i);
+        vid = block_at(tile + 16 * (gt & 3));
     };
     auto load_tile = [&](int64_t tile) {
+        const int in = (int)tile & (c.T - 1);
+        const int8_t *vb = vp + (uint64_t)(uint32_t)max(vid, 0) * block_bytes + in;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int p = threadIdx.x + i * kThreads;
-            const int key = p / (D / 16), kd = p % (D / 16), vd = p >> 2;
-            const int64_t kb = (int64_t)max(kid[i], 0) * c.KVH + h, vb = (int64_t)max(vid[i], 0) * c.KVH + h;
-            kr[i] = *reinterpret_cast<const uint4 *>(c.K + (kb * c.T + ((tile + key) & (c.T - 1))) * D + 16 * kd);
-            vr[i] = *reinterpret_cast<const uint4 *>(c.V + (vb * D + vd) * c.T +
-                                                     ((tile + 16 * (p & 3)) & (c.T - 1)));
+            kr[i] = *reinterpret_cast<const uint4 *>(kp + (uint64_t)(uint32_t)max(kid[i], 0) * block_bytes +
+                                                     (in * D + i * k_next));
+            vr[i] = *reinterpret_cast<const uint4 *>(vb + i * v_next);
         }
-        if (threadIdx.x < 4) {
-            const int64_t gb = (int64_t)max(gid, 0) * c.KVH + h;
-            gr = make_float4(c.sk[gb], c.sv[gb], gid >= 0 ? 1.0f : 0.0f, 0.0f);
+        if (gt < 4) {
+            const int64_t gb = (int64_t)max(vid, 0) * c.KVH + h;
+            gr = make_float4(c.sk[gb], c.sv[gb], vid >= 0 ? 1.0f : 0.0f, 0.0f);
         }
     };
+    // LDS bytes: K line of 2 D bytes, V^T line of 128; a piece's place is its
+    // number's 16 bytes XOR the line's, so that pieces of one line are reached
+    // by an XOR of the thread's address, and lines 32 apart by an offset
     auto k_at = [](int key, int piece) {
-        return D == 128 ? key * 16 + (piece ^ (key & 15)) : key * 8 + (piece ^ ((key >> 1) & 7));
+        return D == 128 ? key * 256 + ((piece ^ (key & 15)) << 4) : key * 128 + ((piece ^ ((key >> 1) & 7)) << 4);
     };
-    auto v_at = [](int d, int piece) { return d * 8 + (piece ^ ((d >> 1) & 7)); };
+    auto v_at = [](int d, int piece) { return d * 128 + ((piece ^ ((d >> 1) & 7)) << 4); };
+    char *const lds_k = reinterpret_cast<char *>(lds.k[group][0]), *const lds_v = reinterpret_cast<char *>(lds.v[group][0]);
+    constexpr int kBuf = kTile * D * 2;                     // bytes of a tile of K or V
+    const int k_put = k_at(pk, 2 * (gt % (D / 16))), v_put = v_at(pv, 2 * (gt & 3));
     auto to_lds = [&](int buf) {
+        int ka = k_put + buf * kBuf, va = v_put + buf * kBuf;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int p = threadIdx.x + i * kThreads;
-            const int key = p / (D / 16), kd = p % (D / 16), vd = p >> 2, vt = p & 3;
-            kl[buf][k_at(key, 2 * kd)] = __builtin_bit_cast(uint4, codes8(kr[i].x, kr[i].y));
-            kl[buf][k_at(key, 2 * kd + 1)] = __builtin_bit_cast(uint4, codes8(kr[i].z, kr[i].w));
-            vl[buf][v_at(vd, 2 * vt)] = __builtin_bit_cast(uint4, codes8(vr[i].x, vr[i].y));
-            vl[buf][v_at(vd, 2 * vt + 1)] = __builtin_bit_cast(uint4, codes8(vr[i].z, vr[i].w));
+            *reinterpret_cast<uint4 *>(lds_k + ka + i * 64 * D) = __builtin_bit_cast(uint4, codes8(kr[i].x, kr[i].y));
+            *reinterpret_cast<uint4 *>(lds_k + (ka ^ 16) + i * 64 * D) = __builtin_bit_cast(uint4, codes8(kr[i].z, kr[i].w));
+            *reinterpret_cast<uint4 *>(lds_v + va + i * 64 * 128) = __builtin_bit_cast(uint4, codes8(vr[i].x, vr[i].y));
+            *reinterpret_cast<uint4 *>(lds_v + (va ^ 16) + i * 64 * 128) = __builtin_bit_cast(uint4, codes8(vr[i].z, vr[i].w));
         }
-        if (threadIdx.x < 4) granules[buf][threadIdx.x] = gr;
+        if (gt < 4) lds.granules[group][buf][gt] = gr;
     };
 
-    float m = -INFINITY, l = 0.0f, u = 0.0f;
+    float m = -INFINITY, l = 0.0f, u = 0.0f, unit_u = 0.0f;     // unit_u = kUnit / u
     float16v o[NO];
 #pragma unroll
     for (int i = 0; i < NO; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
-    // operand row low holds this key of 32
-    const int key_low = (low & 0x13) | (low & 4) << 1 | (low & 8) >> 1;
+    // operand row low holds key low, bits 2 and 3 swapped, of 32
+    const int k_get = k_at((low & 0x13) | (low & 4) << 1 | (low & 8) >> 1, half), v_get = v_at(low, half);
 
-    if (k0 < k1) {
-        load_ids(k0);
-        load_tile(k0);
-        load_ids(k0 + kTile);
+    constexpr int kStep = 2 * kTile;
+    int64_t tile = k0 + kTile * group;
+    if (tile < k1) {
+        load_ids(tile);
+        load_tile(tile);
+        load_ids(tile + kStep);
         to_lds(0);
-        __syncthreads();
-        int buf = 0;
-        for (int64_t tile = k0; tile < k1; tile += kTile, buf ^= 1) {
-            const bool more = tile + kTile < k1;
-            if (more) {
-                load_tile(tile + kTile);
-                load_ids(tile + 2 * kTile);
-            }
-            if (rows_here && tile <= pos_hi) {
-                float16v s[2];
+    }
+    __syncthreads();
+    int buf = 0;
+    // both groups make the first one's steps, for the barrier's sake
+    for (int64_t at = k0; at < k1; at += kStep, tile += kStep, buf ^= 1) {
+        const bool more = tile + kStep < k1;
+        if (more) {
+            load_tile(tile + kStep);
+            load_ids(tile + 2 * kStep);
+        }
+        if (rows_here && tile <= pos_hi && tile < k1) {
+            // opaque, or the loop would hold an address for each piece
+            int ka = k_get + buf * kBuf, va = v_get + buf * kBuf;
+            asm("" : "+v"(ka), "+v"(va));
+            float16v s[2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+                for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
 #pragma unroll
-                    for (int st = 0; st < NQ; ++st) {
-                        const half8 k = __builtin_bit_cast(half8, kl[buf][k_at(32 * t + key_low, 2 * st + half)]);
+                for (int st = 0; st < NQ; ++st) {
+                    const half8 k = *reinterpret_cast<const half8 *>(lds_k + (ka ^ 32 * st) + t * 64 * D);
 #pragma unroll
-                        for (int x = 0; x < NS; ++x) s[t] = mfma_32x32x16(k, qh[x][st], s[t]);
-                    }
+                    for (int x = 0; x < NS; ++x) s[t] = mfma_32x32x16(k, qh[x][st], s[t]);
                 }
-                float4 gn[4];
-                float top = -INFINITY, sv_top = 0.0f;
-                bool valid = true;
+            }
+            float cs[4], w_sv[4], sv_top = 0.0f;
+            bool valid = true;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float4 gn = lds.granules[group][buf][g];
+                cs[g] = fmaxf(c_row * gn.x, kTiny);
+                w_sv[g] = gn.z != 0.0f ? gn.y : 0.0f;
+                valid = valid && gn.z != 0.0f;
+                sv_top = fmaxf(sv_top, fabsf(w_sv[g]));
+            }
+            if (!(valid && tile + kTile <= k1 && tile + kTile - 1 <= pos_lo)) {       // uniform
+                const int lim = (int)min(min(pos + 1, k1) - tile, (int64_t)kTile);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    gn[g] = granules[buf][g];
-                    valid = valid && gn[g].z != 0.0f;
-                    sv_top = fmaxf(sv_top, gn[g].z != 0.0f ? fabsf(gn[g].y) : 0.0f);
-                }
-                if (valid && tile + kTile <= k1 && tile + kTile - 1 <= pos_lo) {     // uniform
+                    const int lim_g = lds.granules[group][buf][g].z != 0.0f ? lim - 16 * g - 8 * half : 0;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const float cs = c_row * gn[g].x;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float x = s[g >> 1][8 * (g & 1) + e] * cs;
-                            s[g >> 1][8 * (g & 1) + e] = x;
-                            top = fmaxf(top, x);
-                        }
-                    }
-                } else {
-                    const int lim = (int)min(min(pos + 1, k1) - tile, (int64_t)kTile);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const float cs = c_row * gn[g].x;
-                        const int lim_g = gn[g].z != 0.0f ? lim - 16 * g - 8 * half : 0;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float x = e < lim_g ? s[g >> 1][8 * (g & 1) + e] * cs : -INFINITY;
-                            s[g >> 1][8 * (g & 1) + e] = x;
-                            top = fmaxf(top, x);
-                        }
-                    }
-                }
-                const float m_new = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
-                const float base = m_new == -INFINITY ? 0.0f : m_new;
-                const float u_new = fmaxf(u, pow2_above(sv_top));
-                float fix = exp2_fast(m - base);
-                l *= fix;
-                if (u_new != u) fix *= u / u_new;
-                if (__ballot(fix != 1.0f)) {
-#pragma unroll
-                    for (int i = 0; i < NO; ++i) o[i] *= fix;
-                }
-                m = m_new;
-                u = u_new;
-                const float inv_u = 16384.0f / u;
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {          // 16 keys
-                    const float w_sv = gn[g].z != 0.0f ? gn[g].y * inv_u : 0.0f;
-                    uint32_t w[4], z[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float p0 = exp2_fast(s[g >> 1][8 * (g & 1) + 2 * e] - base);
-                        const float p1 = exp2_fast(s[g >> 1][8 * (g & 1) + 2 * e + 1] - base);
-                        l += p0 + p1;
-                        const float y0 = p0 * w_sv, y1 = p1 * w_sv;
-                        w[e] = f16_pair(y0, y1);
-                        if (NS == 2) z[e] = f16_rest(y0, y1, w[e]);
-                    }
-                    const half8 p_hi = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
-                    const half8 p_lo = NS == 2 ? __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3])) : p_hi;
-#pragma unroll
-                    for (int i = 0; i < NO; ++i) {
-                        const half8 v = __builtin_bit_cast(half8, vl[buf][v_at(32 * i + low, 2 * g + half)]);
-                        o[i] = mfma_32x32x16(v, p_hi, o[i]);
-                        if (NS == 2) o[i] = mfma_32x32x16(v, p_lo, o[i]);
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        s[g >> 1][8 * (g & 1) + e] = e < lim_g ? s[g >> 1][8 * (g & 1) + e] : -INFINITY;
                 }
             }
-            if (more) to_lds(buf ^ 1);
-            __syncthreads();
+            float top = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float t8 = s[g >> 1][8 * (g & 1)];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) t8 = fmaxf(t8, s[g >> 1][8 * (g & 1) + e]);
+                top = fmaxf(top, t8 * cs[g]);
+            }
+            top = half_max(top);
+            const float u_new = fmaxf(u, pow2_above(sv_top));
+            if (__builtin_expect(__ballot(top > m + kSlack || u_new != u) != 0, 0)) {
+                const float m_new = fmaxf(m, top);
+                float fix = m == -INFINITY ? 0.0f : exp2_fast(m - m_new);
+                l *= fix;
+                const float inverse = pow2_inverse(u_new);
+                fix *= u * inverse;                        // u = 0 at first
+                unit_u = kUnit * inverse;
+#pragma unroll
+                for (int i = 0; i < NO; ++i) o[i] *= fix;
+                m = m_new;
+                u = u_new;
+            }
+            const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {                  // 16 keys
+                half8 p_hi, p_lo;
+                weights<BF16, 1>([&](int e) { return s[g >> 1][8 * (g & 1) + e]; }, cs[g], base,
+                                 w_sv[g] * unit_u, l, &p_hi, &p_lo);
+#pragma unroll
+                for (int i = 0; i < NO; ++i) {
+                    const half8 v = *reinterpret_cast<const half8 *>(lds_v + (va ^ 32 * g) + i * 32 * 128);
+                    o[i] = mfma_32x32x16(v, p_hi, o[i]);
+                    if (NS == 2) o[i] = mfma_32x32x16(v, p_lo, o[i]);
+                }
+            }
         }
+        if (more) to_lds(buf ^ 1);
+        __syncthreads();
     }
-    if (rw + low >= all_rows) return;
-    l += __shfl_xor(l, 32);
-    const float unit = u / 16384.0f;
-    if (min(pos + 1, cap) <= a.chunk) {
+
+    // join the groups: the second leaves its sums in LDS, [wave][value][lane]
+    l = l + __shfl_xor(l, 32);
+    float *join = reinterpret_cast<float *>(lds_raw) + wave * (16 * NO + 3) * 64 + lane;
+    static_assert(4 * (16 * NO + 3) * 64 * sizeof(float) <= sizeof(ManyLds<D>), "the join fits");
+    const float unit = u / kUnit;
+    if (group == 1) {
+        join[0] = m;
+        join[64] = l;
+        join[128] = unit;
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) join[(3 + 16 * i + e) * 64] = o[i][e];
+    }
+    __syncthreads();
+    if (group == 1 || rw + low >= all_rows) return;
+    const float m1 = join[0], mm = fmaxf(m, m1), base = mm == -INFINITY ? 0.0f : mm;
+    float f0 = exp2_fast(m - base), f1 = exp2_fast(m1 - base);
+    l = l * f0 + join[64] * f1;
+    f0 *= unit;
+    f1 *= join[128];
+    const bool direct = min(pos + 1, cap) <= a.chunk;
+    if (direct) {
         if (split > 0) return;
-        const float inv = l > 0.0f ? unit / l : 0.0f;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        f0 *= inv;
+        f1 *= inv;
+    }
+    const int64_t all = (int64_t)sq.n_tok * a.QH;
+    float *dst = a.part + ((int64_t)split * all + row) * D;
 #pragma unroll
-        for (int i = 0; i < NO; ++i)
+    for (int i = 0; i < NO; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                store4<BF16>(a.out, row * D + 32 * i + 2 * e + 4 * half,
-                             make_float4(o[i][e] * inv, o[i][e + 1] * inv, o[i][e + 2] * inv, o[i][e + 3] * inv));
-    } else {
-        const int64_t all = (int64_t)sq.n_tok * a.QH;
-        float *dst = a.part + ((int64_t)split * all + row) * D;
+        for (int e = 0; e < 16; e += 4) {
+            float y[4];
 #pragma unroll
-        for (int i = 0; i < NO; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                store4<false>(dst, 32 * i + 2 * e + 4 * half,
-                              make_float4(o[i][e] * unit, o[i][e + 1] * unit, o[i][e + 2] * unit, o[i][e + 3] * unit));
-        if (half == 0) {
-            float *ml = a.part + (int64_t)a.S * all * D + ((int64_t)split * all + row) * 2;
-            ml[0] = m;
-            ml[1] = l;
+            for (int x = 0; x < 4; ++x) y[x] = o[i][e + x] * f0 + join[(3 + 16 * i + e + x) * 64] * f1;
+            const int d = 32 * i + 2 * e + 4 * half;
+            if (direct) store4<BF16>(a.out, row * D + d, make_float4(y[0], y[1], y[2], y[3]));
+            else store4<false>(dst, d, make_float4(y[0], y[1], y[2], y[3]));
         }
+    if (!direct && half == 0) {
+        float *ml = a.part + (int64_t)a.S * all * D + ((int64_t)split * all + row) * 2;
+        ml[0] = mm;
+        ml[1] = l;
     }
 }
 
@@ -773,7 +819,7 @@ hipError_t attend(Args a, const Plan &p, hipStream_t s) {
         a.min_rows = a.max_rows = a.seqs.B > 1 ? kFewRows : 0;
         hipLaunchKernelGGL((kv8_rows128_kernel<BF16, D>),
                            dim3((unsigned)(rows_all / kManyRows + a.seqs.B), (unsigned)a.c.KVH, (unsigned)p.S),
-                           dim3(kThreads), 0, s, a);
+                           dim3(kManyThreads), sizeof(ManyLds<D>), s, a);
     }
     if (a.max_rows > 0)
         hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>),
