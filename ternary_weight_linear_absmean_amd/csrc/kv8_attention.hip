@@ -34,12 +34,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+constexpr int kCUs = 256;
 constexpr int kTile = 64;                   // keys per wave and step
 constexpr int kRows = 16;                   // rows of a tile
-#ifndef FEWR
-#define FEWR 32
-#endif
-constexpr int kFewRows = FEWR;                // rows of a sequence from which many is many
+constexpr int kFewRows = 32;                // rows of a sequence above which they are many
+constexpr int kFewTiles = kFewRows / kRows;
 constexpr int kBusyGroups = 1536;           // workgroups that the parts are to make
 
 // Four int8 codes -> four fp16.
@@ -166,12 +165,15 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     const int64_t slot = blockIdx.x;
     const int G = a.G;
 
-    // tiles of sequence b: slots from floor(q_start[b] G / 16) + b on
-    const int b = find_seq(sq.B, slot, [&](int i) {
+    // tiles of sequence b: slots from floor(q_start[b] G / 16) + b on, or,
+    // where sequences of more than kFewRows go to the other kernel, the two
+    // that kFewRows make
+    const bool two = a.max_rows == kFewRows;
+    const int b = two ? (int)(slot / kFewTiles) : find_seq(sq.B, slot, [&](int i) {
         return (int64_t)q_at(sq, i) * G / kRows + i;
     });
     const int q0 = q_at(sq, b), n = q_at(sq, b + 1) - q0;
-    const int64_t nth = slot - ((int64_t)q0 * G / kRows + b);
+    const int64_t nth = two ? slot % kFewTiles : slot - ((int64_t)q0 * G / kRows + b);
     if (nth < 0 || n <= 0 || nth * kRows >= (int64_t)n * G || (int64_t)n * G > a.max_rows) return;
     const int64_t r0 = nth * kRows;
     const int rows = (int)min((int64_t)kRows, (int64_t)n * G - r0);
@@ -388,13 +390,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     }
 }
 
-// Many rows: one workgroup per (128 rows, key head, part of the keys), in two
-// groups of four waves that take 64-key tiles in turn; a wave has 32 rows.  A
-// group turns the codes of a tile into fp16 once, in LDS, for all rows (16-row
-// workgroups did it for each: four conversions per matrix step), the next
-// tile's codes in flight meanwhile.  The groups have sums of their own, joined
-// at the end: a workgroup fills a CU alone, so that a prompt's tiles, which see
-// few keys or many, pack better than two workgroups a CU.
+// Many rows: one workgroup per (128 rows, key head, part of the keys), 32 rows
+// a wave, 64 keys at a time.  The workgroup turns the codes of a tile into fp16
+// once, in LDS, for all rows (16-row workgroups did it for each: four
+// conversions per matrix step).  While tile t is used, t + 1 is turned into
+// the other buffer and the codes of t + 2 are on their way.
 //
 // Layouts (lane = 32 half + low): S^T = K Q^T puts key 8 (i / 4) + 4 half + i
 // % 4 of the operand's rows, row low, into accumulator i.  Operand row r holds
@@ -405,36 +405,34 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
 // (K, D = 128) or p ^ (y / 2) (lines of 128 bytes), so that 16 lanes reading
 // one piece of 16 lines touch every bank once.
 constexpr int kManyRows = 128;
-constexpr int kManyThreads = 2 * kThreads;
 typedef float float16v __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ float16v mfma_32x32x16(half8 a, half8 b, float16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
-
-template <int D>
-struct ManyLds {
-    // of each group, twice: the tile being used and the next
-    uint4 k[2][2][kTile * D / 8], v[2][2][kTile * D / 8];
-    float4 granules[2][2][4];               // sk, sv and 1 where valid, of 16 tokens each
-};
-
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
 template <bool BF16, int D>
-__global__ __launch_bounds__(kManyThreads, 2) void kv8_rows128_kernel(Args a) {
+__global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     constexpr int NS = BF16 ? 1 : 2;
     constexpr int NQ = D / 16;              // steps of K Q^T
     constexpr int NO = D / 32;              // tiles of the output
     constexpr int kPieces = kTile * D / 16 / kThreads;      // 16-byte pieces of K and of V per thread
-    extern __shared__ uint4 lds_raw[];
-    ManyLds<D> &lds = *reinterpret_cast<ManyLds<D> *>(lds_raw);
+    __shared__ uint4 buf_k[2 * kTile * D / 8], buf_v[2 * kTile * D / 8];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6 & 3;
-    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
-    const int gt = threadIdx.x & (kThreads - 1);            // thread of the group
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, gt = threadIdx.x;
     const int low = lane & 31, half = lane >> 5;
-    const int h = blockIdx.y, split = blockIdx.z;
+    const int split = blockIdx.z;
+    // Heads of one tile side by side, tiles that see most first.  Two
+    // workgroups share a CU: where all start at once, the second of each is to
+    // be the first's complement, so the order turns round after the first 256.
+    const int64_t groups = (int64_t)gridDim.x;
+    int64_t at = blockIdx.x;
+    if (at >= kCUs && groups <= 2 * kCUs) at = groups - 1 - (at - kCUs);
+    const int h = (int)(at % a.c.KVH);
+    const int64_t slot = at / a.c.KVH;
     const Kv8Seqs &sq = a.seqs;
     const Kv8Cache &c = a.c;
-    const int64_t slot = blockIdx.x;
     const int G = a.G;
     const int b = find_seq(sq.B, slot, [&](int i) {
         return (int64_t)q_at(sq, i) * G / kManyRows + i;
@@ -510,13 +508,15 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv8_rows128_kernel(Args a) {
     const int8_t *vp = c.V + ((int64_t)h * D + pv) * c.T + (16 * gt & 48 & (c.T - 1));
     const int k_next = c.T > 32 ? 32 * D : 0, v_next = 64 * c.T;
     uint4 kr[kPieces], vr[kPieces];
-    float4 gr = make_float4(0.f, 0.f, 0.f, 0.f);
     int kid[kPieces], vid;
+    float sk = 0.0f, sv = 0.0f, sk_next, sv_next;           // of granule lane % 4: 16 tokens of a tile
+    bool in_use = false, in_use_next;
     auto load_ids = [&](int64_t tile) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) kid[i] = block_at(tile + pk + 32 * i);
         vid = block_at(tile + 16 * (gt & 3));
     };
+    // what lies behind k1 is read from block 0
     auto load_tile = [&](int64_t tile) {
         const int in = (int)tile & (c.T - 1);
         const int8_t *vb = vp + (uint64_t)(uint32_t)max(vid, 0) * block_bytes + in;
@@ -526,10 +526,10 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv8_rows128_kernel(Args a) {
                                                      (in * D + i * k_next));
             vr[i] = *reinterpret_cast<const uint4 *>(vb + i * v_next);
         }
-        if (gt < 4) {
-            const int64_t gb = (int64_t)max(vid, 0) * c.KVH + h;
-            gr = make_float4(c.sk[gb], c.sv[gb], vid >= 0 ? 1.0f : 0.0f, 0.0f);
-        }
+        const int64_t gb = (int64_t)max(vid, 0) * c.KVH + h;
+        sk_next = c.sk[gb];
+        sv_next = c.sv[gb];
+        in_use_next = vid >= 0;
     };
     // LDS bytes: K line of 2 D bytes, V^T line of 128; a piece's place is its
     // number's 16 bytes XOR the line's, so that pieces of one line are reached
@@ -538,11 +538,11 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv8_rows128_kernel(Args a) {
         return D == 128 ? key * 256 + ((piece ^ (key & 15)) << 4) : key * 128 + ((piece ^ ((key >> 1) & 7)) << 4);
     };
     auto v_at = [](int d, int piece) { return d * 128 + ((piece ^ ((d >> 1) & 7)) << 4); };
-    char *const lds_k = reinterpret_cast<char *>(lds.k[group][0]), *const lds_v = reinterpret_cast<char *>(lds.v[group][0]);
+    char *const lds_k = reinterpret_cast<char *>(buf_k), *const lds_v = reinterpret_cast<char *>(buf_v);
     constexpr int kBuf = kTile * D * 2;                     // bytes of a tile of K or V
     const int k_put = k_at(pk, 2 * (gt % (D / 16))), v_put = v_at(pv, 2 * (gt & 3));
     auto to_lds = [&](int buf) {
-        int ka = k_put + buf * kBuf, va = v_put + buf * kBuf;
+        const int ka = k_put + buf * kBuf, va = v_put + buf * kBuf;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             *reinterpret_cast<uint4 *>(lds_k + ka + i * 64 * D) = __builtin_bit_cast(uint4, codes8(kr[i].x, kr[i].y));
@@ -550,7 +550,6 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv8_rows128_kernel(Args a) {
             *reinterpret_cast<uint4 *>(lds_v + va + i * 64 * 128) = __builtin_bit_cast(uint4, codes8(vr[i].x, vr[i].y));
             *reinterpret_cast<uint4 *>(lds_v + (va ^ 16) + i * 64 * 128) = __builtin_bit_cast(uint4, codes8(vr[i].z, vr[i].w));
         }
-        if (gt < 4) lds.granules[group][buf][gt] = gr;
     };
 
     float m = -INFINITY, l = 0.0f, u = 0.0f, unit_u = 0.0f;     // unit_u = kUnit / u
@@ -562,54 +561,62 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv8_rows128_kernel(Args a) {
     // operand row low holds key low, bits 2 and 3 swapped, of 32
     const int k_get = k_at((low & 0x13) | (low & 4) << 1 | (low & 8) >> 1, half), v_get = v_at(low, half);
 
-    constexpr int kStep = 2 * kTile;
-    int64_t tile = k0 + kTile * group;
-    if (tile < k1) {
-        load_ids(tile);
-        load_tile(tile);
-        load_ids(tile + kStep);
+    if (k0 < k1) {
+        load_ids(k0);
+        load_tile(k0);
+        sk = sk_next;
+        sv = sv_next;
+        in_use = in_use_next;
+        load_ids(k0 + kTile);
         to_lds(0);
+        load_tile(k0 + kTile);
+        load_ids(k0 + 2 * kTile);
+        __syncthreads();
     }
-    __syncthreads();
     int buf = 0;
-    // both groups make the first one's steps, for the barrier's sake
-    for (int64_t at = k0; at < k1; at += kStep, tile += kStep, buf ^= 1) {
-        const bool more = tile + kStep < k1;
-        if (more) {
-            load_tile(tile + kStep);
-            load_ids(tile + 2 * kStep);
+    for (int64_t tile = k0; tile < k1; tile += kTile, buf ^= 1) {
+        const bool here = rows_here && tile <= pos_hi;
+        // opaque, or the loop would hold an address for each piece
+        int ka = k_get + buf * kBuf, va = v_get + buf * kBuf;
+        asm("" : "+v"(ka), "+v"(va));
+        __builtin_amdgcn_s_setprio(1);            // the CU's other workgroup fills what this leaves
+        // also where the wave's rows do not see the tile: one block to schedule
+        float16v s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < NQ; ++st) {
+                const half8 k = *reinterpret_cast<const half8 *>(lds_k + (ka ^ 32 * st) + t * 64 * D);
+#pragma unroll
+                for (int x = 0; x < NS; ++x) s[t] = mfma_32x32x16(k, qh[x][st], s[t]);
+            }
         }
-        if (rows_here && tile <= pos_hi && tile < k1) {
-            // opaque, or the loop would hold an address for each piece
-            int ka = k_get + buf * kBuf, va = v_get + buf * kBuf;
-            asm("" : "+v"(ka), "+v"(va));
-            float16v s[2];
+        to_lds(buf ^ 1);
+        __builtin_amdgcn_s_setprio(0);
+        float cs[4], w_sv[4], sv_top = 0.0f;
+        bool valid = true;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
-#pragma unroll
-                for (int st = 0; st < NQ; ++st) {
-                    const half8 k = *reinterpret_cast<const half8 *>(lds_k + (ka ^ 32 * st) + t * 64 * D);
-#pragma unroll
-                    for (int x = 0; x < NS; ++x) s[t] = mfma_32x32x16(k, qh[x][st], s[t]);
-                }
-            }
-            float cs[4], w_sv[4], sv_top = 0.0f;
-            bool valid = true;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float4 gn = lds.granules[group][buf][g];
-                cs[g] = fmaxf(c_row * gn.x, kTiny);
-                w_sv[g] = gn.z != 0.0f ? gn.y : 0.0f;
-                valid = valid && gn.z != 0.0f;
-                sv_top = fmaxf(sv_top, fabsf(w_sv[g]));
-            }
+        for (int g = 0; g < 4; ++g) {
+            const bool ok = lane_value(in_use ? 1.0f : 0.0f, g) != 0.0f;
+            cs[g] = fmaxf(c_row * lane_value(sk, g), kTiny);
+            w_sv[g] = ok ? lane_value(sv, g) : 0.0f;
+            valid = valid && ok;
+            sv_top = fmaxf(sv_top, fabsf(w_sv[g]));
+        }
+        const bool used = in_use;
+        sk = sk_next;
+        sv = sv_next;
+        in_use = in_use_next;
+        load_tile(tile + 2 * kTile);
+        load_ids(tile + 3 * kTile);
+        if (here) {
             if (!(valid && tile + kTile <= k1 && tile + kTile - 1 <= pos_lo)) {       // uniform
                 const int lim = (int)min(min(pos + 1, k1) - tile, (int64_t)kTile);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int lim_g = lds.granules[group][buf][g].z != 0.0f ? lim - 16 * g - 8 * half : 0;
+                    const int lim_g = lane_value(used ? 1.0f : 0.0f, g) != 0.0f ? lim - 16 * g - 8 * half : 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         s[g >> 1][8 * (g & 1) + e] = e < lim_g ? s[g >> 1][8 * (g & 1) + e] : -INFINITY;
@@ -651,37 +658,16 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv8_rows128_kernel(Args a) {
                 }
             }
         }
-        if (more) to_lds(buf ^ 1);
         __syncthreads();
     }
 
-    // join the groups: the second leaves its sums in LDS, [wave][value][lane]
+    if (rw + low >= all_rows) return;
     l = l + __shfl_xor(l, 32);
-    float *join = reinterpret_cast<float *>(lds_raw) + wave * (16 * NO + 3) * 64 + lane;
-    static_assert(4 * (16 * NO + 3) * 64 * sizeof(float) <= sizeof(ManyLds<D>), "the join fits");
-    const float unit = u / kUnit;
-    if (group == 1) {
-        join[0] = m;
-        join[64] = l;
-        join[128] = unit;
-#pragma unroll
-        for (int i = 0; i < NO; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) join[(3 + 16 * i + e) * 64] = o[i][e];
-    }
-    __syncthreads();
-    if (group == 1 || rw + low >= all_rows) return;
-    const float m1 = join[0], mm = fmaxf(m, m1), base = mm == -INFINITY ? 0.0f : mm;
-    float f0 = exp2_fast(m - base), f1 = exp2_fast(m1 - base);
-    l = l * f0 + join[64] * f1;
-    f0 *= unit;
-    f1 *= join[128];
+    float f0 = u / kUnit;
     const bool direct = min(pos + 1, cap) <= a.chunk;
     if (direct) {
         if (split > 0) return;
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        f0 *= inv;
-        f1 *= inv;
+        f0 = l > 0.0f ? f0 / l : 0.0f;
     }
     const int64_t all = (int64_t)sq.n_tok * a.QH;
     float *dst = a.part + ((int64_t)split * all + row) * D;
@@ -691,14 +677,14 @@ __global__ __launch_bounds__(kManyThreads, 2) void kv8_rows128_kernel(Args a) {
         for (int e = 0; e < 16; e += 4) {
             float y[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) y[x] = o[i][e + x] * f0 + join[(3 + 16 * i + e + x) * 64] * f1;
+            for (int x = 0; x < 4; ++x) y[x] = o[i][e + x] * f0;
             const int d = 32 * i + 2 * e + 4 * half;
             if (direct) store4<BF16>(a.out, row * D + d, make_float4(y[0], y[1], y[2], y[3]));
             else store4<false>(dst, d, make_float4(y[0], y[1], y[2], y[3]));
         }
     if (!direct && half == 0) {
         float *ml = a.part + (int64_t)a.S * all * D + ((int64_t)split * all + row) * 2;
-        ml[0] = mm;
+        ml[0] = m;
         ml[1] = l;
     }
 }
@@ -817,13 +803,15 @@ hipError_t attend(Args a, const Plan &p, hipStream_t s) {
     a.max_rows = rows_all;
     if (rows_all > kFewRows * (int64_t)a.seqs.B) {
         a.min_rows = a.max_rows = a.seqs.B > 1 ? kFewRows : 0;
-        hipLaunchKernelGGL((kv8_rows128_kernel<BF16, D>),
-                           dim3((unsigned)(rows_all / kManyRows + a.seqs.B), (unsigned)a.c.KVH, (unsigned)p.S),
-                           dim3(kManyThreads), sizeof(ManyLds<D>), s, a);
+        const int64_t groups = (rows_all / kManyRows + a.seqs.B) * a.c.KVH;
+        hipLaunchKernelGGL((kv8_rows128_kernel<BF16, D>), dim3((unsigned)groups, 1, (unsigned)p.S),
+                           dim3(kThreads), 0, s, a);
     }
-    if (a.max_rows > 0)
+    if (a.max_rows > 0) {
+        const int64_t slots = a.max_rows == kFewRows ? (int64_t)a.seqs.B * kFewTiles : p.slots;
         hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>),
-                           dim3((unsigned)p.slots, (unsigned)a.c.KVH, (unsigned)p.S), dim3(kThreads), 0, s, a);
+                           dim3((unsigned)slots, (unsigned)a.c.KVH, (unsigned)p.S), dim3(kThreads), 0, s, a);
+    }
     const dim3 rows((unsigned)(a.seqs.n_tok * a.QH));
     if (p.S > 64)
         hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 1024, kMaxParts>), rows, dim3(1024), 0, s, a);
