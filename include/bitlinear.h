@@ -541,6 +541,30 @@ bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64_t n_tok, 
 size_t bitlinear_kv8_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
                                         int64_t KVH, int64_t T, int64_t D);
 
+/* bitlinear_decode_stack_kv -- bitlinear_decode_stack with an attention in the
+ * place of its one-key stand-in: in each layer k and v (fp32) are appended to
+ * the layer's cache and a = bitlinear_kv8_attention of q over it.
+ *   layers, n_layers, dims, x, trace   as bitlinear_decode_stack; D = 64 or
+ *                 128; path BL_STACK_AUTO or BL_STACK_LAUNCHES (it runs as
+ *                 launches either way; wait_us is not used).
+ *   caches   in   HOST array of n_layers caches (device pointers inside),
+ *                 KVH = KV / D heads of D, the same T in all.
+ *   q_start       DEVICE int32 [2] holding {0, 1}: one new token.
+ *   length, table DEVICE int32 [1] and [max_blocks], as for the append.
+ *   scale         as for the attention.
+ *   ws            >= bitlinear_decode_stack_kv_ws_bytes(dims, T, max_blocks)
+ *                 bytes, 16-byte aligned.
+ */
+bl_status bitlinear_decode_stack_kv(const bl_layer *layers, const bl_kv8 *caches, int n_layers,
+                                    const bl_stack_dims *dims, const int32_t *q_start,
+                                    const int32_t *length, const int32_t *table,
+                                    int64_t max_blocks, float scale, float *x, float *trace,
+                                    void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of bitlinear_decode_stack_kv; 0 also for sizes it refuses. */
+size_t bitlinear_decode_stack_kv_ws_bytes(const bl_stack_dims *dims, int64_t T,
+                                          int64_t max_blocks);
+
 /* ------------------------------------------------------------------------
  * 4-bit weights with group scales -- for the layers that stay out of the
  * ternary scheme (the output head, embeddings; [CARD] 模型详情 makes only the

@@ -33,6 +33,7 @@ EXPORTS = ["quant_weight_absmean_pack", "quant_weight_absmean_pack_noalloc", "qu
            "bitlinear_backward_input", "bitlinear_backward_weight",
            "bitlinear_t5_row_bytes", "bitlinear_repack_t5", "bitlinear_gemv_t5",
            "bitlinear_kv8_append", "bitlinear_kv8_attention", "bitlinear_kv8_attention_ws_bytes",
+           "bitlinear_decode_stack_kv", "bitlinear_decode_stack_kv_ws_bytes",
            "quant_weight_absmax_i4", "dequant_weight_i4", "bitlinear_gemv_w4",
            "bl_workspace_bytes", "bl_status_string", "bl_last_error", "bl_abi_version"]
 BL_OP_DECODE_STACK = 2
@@ -145,6 +146,12 @@ def load():
                                             ctypes.POINTER(Kv8), ctypes.c_float, _p, _p, _sz, _p]
     lib.bitlinear_kv8_attention_ws_bytes.restype = _sz
     lib.bitlinear_kv8_attention_ws_bytes.argtypes = [_i64] * 7
+    lib.bitlinear_decode_stack_kv.restype = st
+    lib.bitlinear_decode_stack_kv.argtypes = [
+        ctypes.POINTER(Layer), ctypes.POINTER(Kv8), i32, ctypes.POINTER(StackDims), _p, _p, _p, _i64,
+        ctypes.c_float, _p, _p, _p, _sz, _p]
+    lib.bitlinear_decode_stack_kv_ws_bytes.restype = _sz
+    lib.bitlinear_decode_stack_kv_ws_bytes.argtypes = [ctypes.POINTER(StackDims), _i64, _i64]
     lib.quant_weight_absmax_i4.restype = st
     lib.quant_weight_absmax_i4.argtypes = [_p, i32, _i64, _i64, _i64, _p, _p, _p]
     lib.dequant_weight_i4.restype = st
@@ -641,6 +648,48 @@ def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=N
     if st:
         _check("bitlinear_kv8_attention", st)
     return out
+
+
+def bitlinear_decode_stack_kv(layers, caches, x, q_start, lengths, table, H, KV, F, D, eps=1e-5,
+                              scale=None, trace=False, ws=None, stream=None):
+    """bitlinear_decode_stack with the attention over 8-bit caches: one token of
+    one sequence through len(layers) layers, each appending to its Kv8Cache and
+    attending over it.  q_start int32 [2] = [0, 1], lengths int32 [1] (with the
+    new token) and table int32 [1, max_blocks] on the GPU.  x fp32 [H] is
+    updated in place; scale defaults to D ** -0.5."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA (HIP) tensor")
+    dev, n = x.device, len(layers)
+    if len(caches) != n:
+        raise ValueError(f"{n} layers and {len(caches)} caches")
+    xp = _at(x, torch.float32, dev, (H,), "x")
+    arr, kvs = (Layer * max(1, n))(), (Kv8 * max(1, n))()
+    wide = {"Wd": F}
+    rows = {"Wq": H, "Wk": KV, "Wv": KV, "Wo": H, "Wg": F, "Wu": F, "Wd": H}
+    for i, L in enumerate(layers):
+        vals = [_at(L[k], torch.uint8, dev, (rows[k], wide.get(k, H) // 4), k) for k in LAYER_WEIGHTS]
+        vals += [_at(L[k], torch.float32, dev, (1,), k) for k in LAYER_GAMMAS]
+        nw = L.get("ffn_norm")
+        arr[i] = Layer(*vals, None if nw is None else _at(nw, torch.float32, dev, (F,), "ffn_norm"))
+        kvs[i] = _kv8(caches[i], dev)
+    qp, lp, tp, B, nb = _seqs(q_start, lengths, table, dev)
+    if B != 1:
+        raise ValueError(f"one sequence, got {B}")
+    dims = StackDims(H, KV, F, D, float(eps), BL_STACK_AUTO, 0, 0)
+    lib = load()
+    handle, context = _where(dev, stream)
+    with context:
+        tr = torch.empty((n, 5 * H + 2 * KV), dtype=torch.float32, device=dev) if trace else None
+        if ws is None:
+            need = lib.bitlinear_decode_stack_kv_ws_bytes(ctypes.byref(dims), kvs[0].T if n else 64, nb)
+            ws = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+        st = lib.bitlinear_decode_stack_kv(
+            arr, kvs, n, ctypes.byref(dims), qp, lp, tp, nb, D ** -0.5 if scale is None else scale, xp,
+            None if tr is None else tr.data_ptr(), _at(ws, torch.uint8, dev, (ws.numel(),), "ws"),
+            ws.numel(), handle)
+    if st:
+        _check("bitlinear_decode_stack_kv", st)
+    return tr
 
 
 def quant_weight_absmax_i4(W, group=128, Wq4=None, s=None, stream=None):

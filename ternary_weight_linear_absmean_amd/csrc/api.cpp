@@ -509,18 +509,9 @@ static bl_status check_stack_dims(const char *name, const bl_stack_dims *dims) {
     return BL_OK;
 }
 
-BL_EXPORT bl_status bitlinear_decode_stack(const bl_layer *layers, int n_layers,
-                                           const bl_stack_dims *dims, float *x, float *trace,
-                                           void *ws, size_t ws_bytes, void *stream) {
-    const char *name = "bitlinear_decode_stack";
-    bl_status st0 = check_stack_dims(name, dims);
-    if (st0 != BL_OK)
-        return st0;
-    const int64_t H = dims->H, KV = dims->KV, F = dims->F, D = dims->D;
-    if (n_layers < 0)
-        return fail(BL_ERR_SHAPE, "%s: n_layers=%d must be >= 0", name, n_layers);
-    if (n_layers == 0)
-        return ok();
+// Shared checks of the layers and vectors of a stack call (n_layers > 0).
+static bl_status check_stack_layers(const char *name, const bl_layer *layers, int n_layers,
+                                    const float *x, const float *trace) {
     if (!layers || !x)
         return fail(BL_ERR_NULL, "%s: NULL layers or x", name);
     if (!aligned(x, 16) || (trace && !aligned(trace, 16)))
@@ -539,6 +530,24 @@ BL_EXPORT bl_status bitlinear_decode_stack(const bl_layer *layers, int n_layers,
         if (L.ffn_norm && !aligned(L.ffn_norm, 16))
             return fail(BL_ERR_ALIGN, "%s: layer %d: ffn_norm must be 16-byte aligned", name, l);
     }
+    return BL_OK;
+}
+
+BL_EXPORT bl_status bitlinear_decode_stack(const bl_layer *layers, int n_layers,
+                                           const bl_stack_dims *dims, float *x, float *trace,
+                                           void *ws, size_t ws_bytes, void *stream) {
+    const char *name = "bitlinear_decode_stack";
+    bl_status st0 = check_stack_dims(name, dims);
+    if (st0 != BL_OK)
+        return st0;
+    const int64_t H = dims->H, KV = dims->KV, F = dims->F, D = dims->D;
+    if (n_layers < 0)
+        return fail(BL_ERR_SHAPE, "%s: n_layers=%d must be >= 0", name, n_layers);
+    if (n_layers == 0)
+        return ok();
+    st0 = check_stack_layers(name, layers, n_layers, x, trace);
+    if (st0 != BL_OK)
+        return st0;
     const size_t need = bl_workspace_bytes(BL_OP_DECODE_STACK, 1, H, KV, F);
     if (!ws || ws_bytes < need)
         return fail(BL_ERR_WORKSPACE, "%s: workspace %zu bytes at %p, need %zu", name, ws_bytes,
@@ -554,7 +563,7 @@ BL_EXPORT bl_status bitlinear_decode_stack(const bl_layer *layers, int n_layers,
                     (long long)F);
     return launched(bl::launch_decode_stack(layers, n_layers, (int)H, (int)KV, (int)F, (int)D,
                                             dims->eps, dims->wait_us, x, trace,
-                                            static_cast<float *>(ws), dims->path,
+                                            static_cast<float *>(ws), dims->path, nullptr,
                                             static_cast<hipStream_t>(stream)),
                     name);
 }
@@ -843,5 +852,84 @@ BL_EXPORT bl_status bitlinear_gemv_w4(const void *X, bl_dtype dtype, int64_t M,
         return st;
     return launched(bl::launch_gemv_w4(X, dtype == BL_BF16 ? 1 : 0, (int)M, Wq4, s, (int)N, (int)K,
                                        (int)group, Y, static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+// The sizes of a stack over caches: those of the stack, and the heads that the
+// cache takes.
+static bl_status check_stack_kv_dims(const char *name, const bl_stack_dims *dims, int64_t T,
+                                     int64_t max_blocks) {
+    bl_status st = check_stack_dims(name, dims);
+    if (st != BL_OK)
+        return st;
+    if (dims->path == BL_STACK_PERSISTENT)
+        return fail(BL_ERR_SHAPE, "%s: the persistent path has no attention", name);
+    if ((dims->D != 64 && dims->D != 128) || (T != 16 && T != 32 && T != 64 && T != 128) ||
+        max_blocks < 0 || max_blocks > kI32Max / T)
+        return fail(BL_ERR_SHAPE, "%s: need D = 64 or 128, T = 16, 32, 64 or 128, max_blocks * T in "
+                    "[0, 2^31) (D=%lld T=%lld max_blocks=%lld)", name, (long long)dims->D,
+                    (long long)T, (long long)max_blocks);
+    return BL_OK;
+}
+
+BL_EXPORT size_t bitlinear_decode_stack_kv_ws_bytes(const bl_stack_dims *dims, int64_t T,
+                                                    int64_t max_blocks) {
+    if (check_stack_kv_dims("bitlinear_decode_stack_kv_ws_bytes", dims, T, max_blocks) != BL_OK)
+        return 0;
+    return bl_workspace_bytes(BL_OP_DECODE_STACK, 1, dims->H, dims->KV, dims->F) +
+           bitlinear_kv8_attention_ws_bytes(1, dims->H / dims->D, 1, max_blocks,
+                                            dims->KV / dims->D, T, dims->D);
+}
+
+BL_EXPORT bl_status bitlinear_decode_stack_kv(const bl_layer *layers, const bl_kv8 *caches,
+                                              int n_layers, const bl_stack_dims *dims,
+                                              const int32_t *q_start, const int32_t *length,
+                                              const int32_t *table, int64_t max_blocks,
+                                              float scale, float *x, float *trace, void *ws,
+                                              size_t ws_bytes, void *stream) {
+    const char *name = "bitlinear_decode_stack_kv";
+    if (n_layers < 0)
+        return fail(BL_ERR_SHAPE, "%s: n_layers=%d must be >= 0", name, n_layers);
+    if (n_layers > 0 && !caches)
+        return fail(BL_ERR_NULL, "%s: caches is NULL", name);
+    bl_status st = check_stack_kv_dims(name, dims, n_layers > 0 ? caches[0].T : 64, max_blocks);
+    if (st != BL_OK)
+        return st;
+    if (!(scale - scale == 0.0f))
+        return fail(BL_ERR_SHAPE, "%s: scale must be finite", name);
+    if (n_layers == 0)
+        return ok();
+    st = check_stack_layers(name, layers, n_layers, x, trace);
+    if (st != BL_OK)
+        return st;
+    for (int l = 0; l < n_layers; ++l) {
+        const bl_kv8 &c = caches[l];
+        if (c.D != dims->D || c.KVH != dims->KV / dims->D || c.T != caches[0].T)
+            return fail(BL_ERR_SHAPE, "%s: layer %d: need a cache of %lld heads of %lld, T as in the "
+                        "first layer (KVH=%lld D=%lld T=%lld)", name, l,
+                        (long long)(dims->KV / dims->D), (long long)dims->D, (long long)c.KVH,
+                        (long long)c.D, (long long)c.T);
+        bool noop = false;
+        st = check_kv8(name, x, x, BL_F32, 1, q_start, length, table, 1, max_blocks, &c, &noop);
+        if (st != BL_OK)
+            return st;
+    }
+    const size_t own = bl_workspace_bytes(BL_OP_DECODE_STACK, 1, dims->H, dims->KV, dims->F);
+    const size_t need = bitlinear_decode_stack_kv_ws_bytes(dims, caches[0].T, max_blocks);
+    if (!ws || ws_bytes < need)
+        return fail(BL_ERR_WORKSPACE, "%s: workspace %zu bytes at %p, need %zu", name, ws_bytes,
+                    ws, need);
+    if (!aligned(ws, 16))
+        return fail(BL_ERR_ALIGN, "%s: ws must be 16-byte aligned", name);
+    st = check_arch();
+    if (st != BL_OK)
+        return st;
+    const bl::StackKv kv = {caches, {q_start, length, table, 1, 1, (int)max_blocks}, scale,
+                            reinterpret_cast<float *>(static_cast<char *>(ws) + own)};
+    return launched(bl::launch_decode_stack(layers, n_layers, (int)dims->H, (int)dims->KV,
+                                            (int)dims->F, (int)dims->D, dims->eps, dims->wait_us,
+                                            x, trace, static_cast<float *>(ws),
+                                            BL_STACK_LAUNCHES, &kv,
+                                            static_cast<hipStream_t>(stream)),
                     name);
 }

@@ -39,7 +39,7 @@ constexpr int kTile = 64;                   // keys per wave and step
 constexpr int kRows = 16;                   // rows of a tile
 constexpr int kFewRows = 32;                // rows of a sequence above which they are many
 constexpr int kFewTiles = kFewRows / kRows;
-constexpr int kBusyGroups = 1536;           // workgroups that the parts are to make
+constexpr int kBusyGroups = 512;           // workgroups that the parts are to make
 
 // Four int8 codes -> four fp16.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -695,7 +695,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
 // THREADS / D parts in flight: 256 threads for up to 64 parts, 1024 for more
 // (128 parts of 20 rows: 11.4 us with 256 threads, 4.7 with 1024; 4 parts of
 // 1280 rows: 4.9 and 10.3).
-constexpr int kMaxParts = 2048;
+constexpr int kMaxParts = kBusyGroups;
 template <bool BF16, int D, int THREADS, int PARTS>
 __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
     constexpr int kWide = D / 4, kLines = THREADS / kWide, kJoinWaves = THREADS / 64;
@@ -777,22 +777,29 @@ __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
     }
 }
 
-// Parts the keys are read in.  The lengths are on the device, so the bound
-// max_blocks * T takes their place: parts behind a sequence's end exit at once.
+// Parts the keys are read in: as many as keep kBusyGroups workgroups going, of
+// whole steps (64 keys of each wave), and none where that saves a workgroup
+// fewer than three steps (1.7 us each when they wait for memory), as the join
+// is a launch and 2 to 3 us.  In us, one part and with parts: 5 heads x 512
+// keys 8.0 and 9.0, 1024 keys 11.4 and 9.0, 32768 keys 26.5 (2048 a part) and
+// 20.0; 160 heads x 1024 keys 15.2 and 19.3; with kBusyGroups 1536 instead of
+// 512, 160 x 4096 took 46.7 instead of 42.8, 64 (ragged) x 8192 28.5 instead
+// of 24.6.  The lengths are on the device, so the bound max_blocks * T takes
+// their place: parts behind a sequence's end exit at once.
 struct Plan {
     int64_t slots, chunk;
     int S;
 };
 Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH, int64_t T) {
     const int64_t G = QH / KVH, keys = max_blocks * T, unit = kTile * kWaves;
+    const int64_t steps = keys > 0 ? (keys + unit - 1) / unit : 1;
     const int64_t seqs = n_tok < B ? n_tok : B;
     const double busy = (double)KVH * (seqs + (n_tok - seqs) * (double)G / kRows);
-    const double want = keys * busy / kBusyGroups;
-    Plan p = {n_tok * G / kRows + B, keys > unit ? keys : unit, 1};
-    if (want < p.chunk) p.chunk = want > unit ? (int64_t)want : unit;
-    p.chunk = (p.chunk + unit - 1) / unit * unit;
-    if (keys > p.chunk) p.S = (int)((keys + p.chunk - 1) / p.chunk);
-    return p;
+    int64_t parts = (int64_t)(kBusyGroups / busy);
+    parts = parts < 1 ? 1 : parts < steps ? parts : steps;
+    int64_t each = (steps + parts - 1) / parts;
+    if (steps - each < 3) each = steps;
+    return {n_tok * G / kRows + B, each * unit, (int)((steps + each - 1) / each)};
 }
 
 template <bool BF16, int D>

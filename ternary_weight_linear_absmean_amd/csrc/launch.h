@@ -148,11 +148,29 @@ StackWs stack_ws(float *ws, int H, int KV, int F);
 // Decode-stack paths (bl_stack_dims.path).
 enum StackPath { kStackAuto = 0, kStackLaunches = 1, kStackPersistent = 2 };
 
+// 8-bit key/value cache (kv8.hip).  The metadata arrays of a call; every
+// pointer is a device pointer, every value in them may be anything.
+struct Kv8Seqs {
+    const int32_t *q_start, *lengths, *table;
+    int n_tok, B, max_blocks;
+};
+hipError_t launch_kv8_append(const void *k, const void *v, int dtype, const Kv8Seqs &seqs,
+                             const bl_kv8 &cache, hipStream_t s);
+// The caches of a stack whose attention is over cached tokens: one per layer,
+// the arrays of one sequence with one new token, and the attention's workspace.
+struct StackKv {
+    const bl_kv8 *caches;
+    Kv8Seqs seqs;
+    float scale;
+    float *ws;
+};
+
 // One token (M = 1) through n_layers layers; x [H] fp32 is updated in place.
-// trace: NULL or [n_layers][5 H + 2 KV] = x_in, q, k, v, o, x_mid, y.
+// trace: NULL or [n_layers][5 H + 2 KV] = x_in, q, k, v, o, x_mid, y.  kv:
+// NULL for the one-key stand-in; else the path of launches.
 hipError_t launch_decode_stack(const StackLayer *layers, int n_layers, int H, int KV, int F,
                                int D, float eps, int wait_us, float *x, float *trace, float *ws,
-                               int path, hipStream_t s);
+                               int path, const StackKv *kv, hipStream_t s);
 
 // The persistent path: one launch per 16 layers, one workgroup per compute
 // unit of the current device.  fits() says whether these sizes fit its
@@ -173,14 +191,6 @@ hipError_t launch_ffn_tail(const float *G, const float *U, const float *norm_w,
                            float eps, int M, int F, int8_t *Hq, float *dh, float *dz,
                            hipStream_t s);
 
-// 8-bit key/value cache (kv8.hip).  The metadata arrays of a call; every
-// pointer is a device pointer, every value in them may be anything.
-struct Kv8Seqs {
-    const int32_t *q_start, *lengths, *table;
-    int n_tok, B, max_blocks;
-};
-hipError_t launch_kv8_append(const void *k, const void *v, int dtype, const Kv8Seqs &seqs,
-                             const bl_kv8 &cache, hipStream_t s);
 // Attention over the cache (kv8_attention.hip); ws holds
 // kv8_attention_ws_floats() floats.
 size_t kv8_attention_ws_floats(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,

@@ -11,7 +11,9 @@
 //   G, U    = BitLinear(x)                 (one fused launch)
 //   y       = down(requant(subln(relu(G)^2 * U)));   x = x + y
 // q and k are computed (their weights are streamed like every other
-// projection) but, with one key, do not change a.
+// projection) but, with one key, do not change a.  With caches, k and v are
+// appended to the layer's and a is the attention over its tokens (two launches
+// in the place of one, three where the tokens are read in parts).
 #include "device_common.h"
 #include "launch.h"
 
@@ -72,9 +74,9 @@ StackWs stack_ws(float *ws, int H, int KV, int F) {
 
 hipError_t launch_decode_stack(const StackLayer *layers, int n_layers, int H, int KV, int F,
                                int D, float eps, int wait_us, float *x, float *trace, float *ws,
-                               int path, hipStream_t s) {
+                               int path, const StackKv *kv, hipStream_t s) {
     const StackWs w = stack_ws(ws, H, KV, F);
-    if (path == kStackPersistent || (path == kStackAuto && stack_persistent_fits(H, KV, F, D)))
+    if (!kv && (path == kStackPersistent || (path == kStackAuto && stack_persistent_fits(H, KV, F, D))))
         return launch_decode_stack_persistent(layers, n_layers, H, KV, F, D, eps, wait_us, x,
                                               trace, w, s);
     // this path has no bounded waits: its status is always 0
@@ -101,8 +103,15 @@ hipError_t launch_decode_stack(const StackLayer *layers, int n_layers, int H, in
         };
         hipError_t e = launch_gemv_fused(qkv, 3, 1, s);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(expand_heads_kernel, eb, dim3(kThreads), 0, s, (const float *)tv, a, H,
-                           D, group);
+        if (kv) {
+            e = launch_kv8_append(tk, tv, 0, kv->seqs, kv->caches[l], s);
+            if (e != hipSuccess) return e;
+            e = launch_kv8_attention(tq, 0, H / D, kv->seqs, kv->caches[l], kv->scale, a, kv->ws, s);
+            if (e != hipSuccess) return e;
+        } else {
+            hipLaunchKernelGGL(expand_heads_kernel, eb, dim3(kThreads), 0, s, (const float *)tv, a,
+                               H, D, group);
+        }
         GemvJob oj[1] = {{a, L.Wo, L.go, to, nullptr, nullptr, H, H, 0}};
         e = launch_gemv_fused(oj, 1, 1, s);
         if (e != hipSuccess) return e;

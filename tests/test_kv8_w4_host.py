@@ -139,3 +139,32 @@ def test_oracle_w4_by_hand():
     assert q[0, :4].tolist() == [7, -4, 0, 2] and q[0, 33] == 7 and s.tolist() == [[1, 2]]
     assert ref.unpack_w4(np.array([[0xF8, 0x71]], np.uint8)).tolist() == [[-8, -1, 1, 7]]
     assert ref.bf16(np.array([1 + 2.0 ** -8, 1 + 3 * 2.0 ** -8])).tolist() == [1, 1 + 2.0 ** -6]
+
+
+def test_stack_kv_refusals(lib):
+    from ternary_weight_linear_absmean_amd._native import Layer, StackDims
+    f, need = lib.bitlinear_decode_stack_kv, lib.bitlinear_decode_stack_kv_ws_bytes
+
+    def dims(H=512, KV=128, F=640, D=64, eps=1e-5, path=0):
+        return StackDims(H, KV, F, D, eps, path, 0, 0)
+
+    def call(d=None, L=None, n=1, c=None, x=A16, ws=A16, size=1 << 40, nb=4, qs=A4, ln=A4, tb=A4, scale=1.0):
+        L = L or Layer(*[A16] * 14, None)
+        c = cache(D=64) if c is None else c
+        return f(L, c, n, d or dims(), qs, ln, tb, nb, scale, x, None, ws, size, None)
+    for d in (dims(H=500), dims(D=32), dims(D=256), dims(path=2), dims(path=-1), dims(eps=-1.0), dims(KV=192)):
+        assert call(d) == SHAPE
+        assert need(d, 64, 4) == 0
+    for c in (cache(D=128), cache(D=64, KVH=1), cache(D=64, T=8), cache(D=64, n_blocks=-1)):
+        assert call(c=c) == SHAPE
+    assert call(nb=-1) == SHAPE and call(nb=2 ** 31) == SHAPE and call(n=-1) == SHAPE
+    assert call(scale=float("nan")) == SHAPE
+    assert call(n=0, x=None, ws=None) == OK
+    for kw in (dict(x=None), dict(qs=None), dict(ln=None), dict(tb=None), dict(c=cache(D=64, K=None)),
+               dict(L=Layer(*[A16] * 13, None, None))):
+        assert call(**kw) == NULL
+    for kw in (dict(x=A4), dict(ws=A4), dict(qs=A1), dict(c=cache(D=64, V=A4))):
+        assert call(**kw) == ALIGN
+    size = need(dims(), 64, 4)
+    assert size >= lib.bl_workspace_bytes(bl.BL_OP_DECODE_STACK, 1, 512, 128, 640)
+    assert call(ws=None) == WS and call(size=size - 1) == WS
