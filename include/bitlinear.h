@@ -528,7 +528,10 @@ bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype dtype, int
  *               overlap need a workspace each.
  * The scores, the softmax and all sums are fp32; for fp32 rows every operand
  * of a product is kept to 22 bits or more, for bf16 rows the softmax weights
- * are rounded to 11 bits.  Deterministic for given sizes and contents.
+ * are rounded to 11 bits.  An operand's smallest step is 2^-38 of the row's
+ * largest |q|, and 2^-38 of the largest weight times the largest sv of the
+ * sequence.  sk and sv are >= 0, as the append writes them.  Deterministic for
+ * given sizes and contents.
  * Limits as for the append, and n_tok * QH < 2^31.
  */
 bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64_t n_tok, int64_t QH,
@@ -593,9 +596,10 @@ bl_status dequant_weight_i4(const uint8_t *Wq4, const uint16_t *s, int64_t N, in
  *   Wq4, s in   as above.
  *   Y      out  fp32 [M][N] = sum over the groups of s * sum_k x code, 4-byte
  *               aligned.
- * Sums are fp32; x keeps 22 bits or more (fp32) or all its 8 (bf16) of the
- * largest |x| of 128 consecutive elements.  M == 0 or N == 0: no-op; K == 0
- * gives zeros.
+ * Sums are fp32.  M <= 2 multiplies fp32 x as it is; above, fp32 x is held to
+ * 22 bits or more of the largest |x| of 128 consecutive elements, bf16 x
+ * exactly.  |x| is to stay below 2^117 (sums of codes come before their scale).
+ * Deterministic for given sizes.  M == 0 or N == 0: no-op; K == 0 gives zeros.
  */
 bl_status bitlinear_gemv_w4(const void *X, bl_dtype dtype, int64_t M, const uint8_t *Wq4,
                             const uint16_t *s, int64_t N, int64_t K, int64_t group, float *Y,

@@ -328,10 +328,12 @@ __global__ __launch_bounds__(kStreamThreads, 4) void gemv_w4_stream_kernel(ProdA
 // lines (16 lanes a token), made fp16 and passed through LDS of the wave's own
 // into the operand's order.
 //
-// X is scaled by a power of two per token and chunk, the largest to [2^13,
-// 2^14), and rounded to fp16: bf16 values are exact (down to 2^-31 of the
-// largest), fp32 values are split in two halves of 11 bits, each with its
-// matrix instructions.
+// bf16 tokens go into bf16 products as they are, with the codes + 8 (exact in
+// bf16); one more product with ones sums X, and 8 times that is taken off a
+// group's sum.  The numbers grow by a factor of about 3 for it, against the
+// 2^-24 of the fp32 sums.  fp32 tokens are scaled by a power of two per token
+// and chunk, the largest to [2^13, 2^14), and split in two fp16 halves of 11
+// bits, each with its matrix instructions.
 //
 // A matrix instruction sums over the four quads, and all that it sums has to
 // lie in one scale group.  With groups of 128 any dword of each quad's 16 bytes
@@ -371,6 +373,27 @@ __device__ __forceinline__ void wave_fence() {
 
 // LDS of a wave: [part of X][instruction, quad][16 tokens + 1 of padding] units
 // of 16 bytes, then 16 factors; the final sums take its place.
+typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
+typedef float float2v __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ float4v mfma_bf16(bf8v a, bf8v b, float4v c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// The 8 codes of a dword, + 8, as bf16 in their order.
+__device__ __forceinline__ bf8v codes_to_bf16(uint32_t w) {
+    const uint32_t x = w ^ 0x88888888u;
+    uint32_t even = x & 0x0F0F0F0Fu, odd = (x >> 4) & 0x0F0F0F0Fu, o[4];
+    // opaque: as bytes, which convert in one instruction each, and not as bit
+    // fields of x, which take two
+    asm("" : "+v"(even), "+v"(odd));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2v f = {(float)((even >> (8 * i)) & 255u), (float)((odd >> (8 * i)) & 255u)};
+        o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf2v));
+    }
+    return __builtin_bit_cast(bf8v, make_uint4(o[0], o[1], o[2], o[3]));
+}
+
 template <bool BF16>
 constexpr int wave_lds() { return (BF16 ? 1 : 2) * 16 * 17 * 16 + 64; }
 
@@ -419,45 +442,66 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_w4_mfma_kernel(ProdArgs a) {
         }
         // four tokens at a time: this lane has values 8 low .. of token 4 i + quad
         const int at = WHOLE ? 8 * low : min(8 * low, a.K - 8 - c * kChunk);
-        float x[4][8];
+        uint4 *dst = xs + place<GROUP>(low >> 2, low & 3) * 17 + quad;
+        if (BF16) {
+            uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            load8<BF16>(a.X, (int64_t)min(4 * i + quad, a.M - 1) * a.K + c * kChunk + at, x[i]);
+            for (int i = 0; i < 4; ++i)
+                x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.X) +
+                                                        (int64_t)min(4 * i + quad, a.M - 1) * a.K + c * kChunk + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (4 * i >= a.M) break;            // uniform: their rows of the operand are not used
-            float top = 0.0f;
+            for (int i = 0; i < 4; ++i)
+                if (4 * i < a.M) dst[4 * i] = x[i];        // the other rows of the operand are not used
+        } else {
+            float x[4][8];
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) top = fmaxf(top, fmaxf(fabsf(x[i][e]), fabsf(x[i][e + 1])));
-            top = group_max(top, 16);
-            // top in [2^(e-127), 2^(e-126)): to [2^13, 2^14), or by 2^127 where
-            // it is below 2^-114
-            const int ex = max((int)(__float_as_uint(top) >> 23), 13);
-            const float f1 = __uint_as_float((uint32_t)(267 - ex) << 23);
-            uint32_t h[4], z[4];
+            for (int i = 0; i < 4; ++i)
+                load8<false>(a.X, (int64_t)min(4 * i + quad, a.M - 1) * a.K + c * kChunk + at, x[i]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {                  // in the codes' order
-                const float v0 = x[i][e] * f1, v1 = x[i][e + 4] * f1;
-                h[e] = f16_pair(v0, v1);
-                if (NS == 2) z[e] = f16_rest(v0, v1, h[e]);
+            for (int i = 0; i < 4; ++i) {
+                if (4 * i >= a.M) break;                   // uniform
+                float top = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) top = fmaxf(top, fmaxf(fabsf(x[i][e]), fabsf(x[i][e + 1])));
+                top = group_max(top, 16);
+                // top in [2^(e-127), 2^(e-126)): to [2^13, 2^14), or by 2^127
+                // where it is below 2^-114
+                const int ex = max((int)(__float_as_uint(top) >> 23), 13);
+                const float f1 = __uint_as_float((uint32_t)(267 - ex) << 23);
+                uint32_t h[4], z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {              // in the codes' order
+                    const float v0 = x[i][e] * f1, v1 = x[i][e + 4] * f1;
+                    h[e] = f16_pair(v0, v1);
+                    z[e] = f16_rest(v0, v1, h[e]);
+                }
+                dst[4 * i] = make_uint4(h[0], h[1], h[2], h[3]);
+                dst[4 * i + 16 * 17] = make_uint4(z[0], z[1], z[2], z[3]);
+                if (low == 0) xf[4 * i + quad] = __uint_as_float((uint32_t)(ex - 12) << 23) * 0.5f;   // 2^(ex - 140)
             }
-            uint4 *dst = xs + place<GROUP>(low >> 2, low & 3) * 17 + 4 * i + quad;
-            dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-            if (NS == 2) dst[16 * 17] = make_uint4(z[0], z[1], z[2], z[3]);
-            if (low == 0) xf[4 * i + quad] = __uint_as_float((uint32_t)(ex - 12) << 23) * 0.5f;   // 2^(ex - 140)
         }
         wave_fence();
-        half8 xh[NS][4];
+        uint4 xr[NS][4];
 #pragma unroll
         for (int s = 0; s < NS; ++s)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                xh[s][j] = __builtin_bit_cast(half8, xs[(s * 16 + j * 4 + quad) * 17 + low]);
+            for (int j = 0; j < 4; ++j) xr[s][j] = xs[(s * 16 + j * 4 + quad) * 17 + low];
         const float4v f = *reinterpret_cast<const float4v *>(xf + 4 * quad);
         wave_fence();
         if (!WHOLE && u >= units) {
 #pragma unroll
             for (int r = 0; r < R; ++r) w[r] = make_uint4(0, 0, 0, 0);
+        }
+        float4v x_sum[NG];                      // of each group's X, in every column
+        if (BF16) {
+            const bf8v ones = __builtin_bit_cast(bf8v, make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u));
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                x_sum[g] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = g * (4 / NG); j < (g + 1) * (4 / NG); ++j)
+                    x_sum[g] = mfma_bf16(__builtin_bit_cast(bf8v, xr[0][j]), ones, x_sum[g]);
+            }
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -475,12 +519,18 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_w4_mfma_kernel(ProdArgs a) {
                 float4v acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = g * (4 / NG); j < (g + 1) * (4 / NG); ++j) {
-                    const half8 b = __builtin_bit_cast(half8, codes_to_f16(d[j]));
+                    if (BF16) {
+                        acc = mfma_bf16(__builtin_bit_cast(bf8v, xr[0][j]), codes_to_bf16(d[j]), acc);
+                    } else {
+                        const half8 b = __builtin_bit_cast(half8, codes_to_f16(d[j]));
 #pragma unroll
-                    for (int s = 0; s < NS; ++s) acc = mfma_16x16x32(xh[s][j], b, acc);
+                        for (int s = 0; s < NS; ++s) acc = mfma_16x16x32(__builtin_bit_cast(half8, xr[s][j]), b, acc);
+                    }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tot[r][e] = __builtin_fmaf(acc[e] * f[e], sc[r][g], tot[r][e]);
+                for (int e = 0; e < 4; ++e)
+                    tot[r][e] = __builtin_fmaf(BF16 ? __builtin_fmaf(-8.0f, x_sum[g][e], acc[e]) : acc[e] * f[e],
+                                               sc[r][g], tot[r][e]);
             }
         }
     }
