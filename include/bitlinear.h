@@ -505,8 +505,8 @@ typedef struct {
  * codes of no meaning, which are never used.
  * Two sequences of one call must not get new tokens in the same block, and no
  * other work may use the blocks that are written.
- *   n_tok < 2^31, B < 2^24, max_blocks * T < 2^31.  n_tok == 0 or B == 0:
- *   no-op.
+ *   n_tok < 2^31, B < 2^24, max_blocks * T < 2^31 (BL_ERR_HIP if a grid
+ *   passes the runtime's 2^32 threads).  n_tok == 0 or B == 0: no-op.
  */
 bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype dtype, int64_t n_tok,
                                const int32_t *q_start, const int32_t *lengths,
@@ -577,7 +577,7 @@ size_t bitlinear_decode_stack_kv_ws_bytes(const bl_stack_dims *dims, int64_t T,
  *   s    bf16 [N][K/group], one scale per `group` consecutive elements of a
  *        row; the weight is code * s.
  *   group = 32, 64 or 128; K % group == 0; K <= BL_MAX_K; N < 2^31,
- *   N * K <= 2^40.
+ *   N * K <= 2^40 (BL_ERR_HIP if a grid passes the runtime's 2^32 threads).
  *
  * quant_weight_absmax_i4 -- W [N][K] of `dtype` -> Wq4, s.  Per group:
  *   a = max |w|, s = bf16(fp32(a / 7)), code = clamp(rne(fp32(w / s)), -7, 7),

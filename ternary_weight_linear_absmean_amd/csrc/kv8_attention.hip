@@ -237,11 +237,13 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     const int64_t first_tile = k0 + (int64_t)wave * kTile;
     constexpr int64_t kStep = (int64_t)kWaves * kTile;
     const int32_t *table = sq.table + (int64_t)b * sq.max_blocks;
-    // block of this lane's quad of a tile; -1 where it holds no token
-    auto block_at = [&](int64_t tile) {
-        const int64_t t = tile + 16 * quad;
-        const int id = t < k1 ? table[t >> c.t_shift] : -1;
-        return id >= 0 && id < c.n_blocks ? id : -1;
+    // Block of this lane's quad of a tile: the table's entry is loaded a step
+    // ahead, at a clamped place, and looked at only when it is used (a look at
+    // once would wait for it, and for all loads before it, in every step); -1
+    // where it holds no token.
+    auto entry_at = [&](int64_t tile) { return table[min(tile + 16 * quad, k1 - 1) >> c.t_shift]; };
+    auto block_of = [&](int64_t tile, int entry) {
+        return tile + 16 * quad < k1 && entry >= 0 && entry < c.n_blocks ? entry : -1;
     };
     uint4 kb[4][ND], vb[NO];
     float sk = 0.0f, sv = 0.0f;
@@ -268,10 +270,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     };
 
     if (first_tile < k1) {
-        int id = block_at(first_tile);
+        int id = block_of(first_tile, entry_at(first_tile));
         load_k(first_tile, id);
         load_v(first_tile, id);
-        int id_next = block_at(first_tile + kStep);
+        int entry = entry_at(first_tile + kStep), id_next = -1;
         for (int64_t tile = first_tile; tile < k1; tile += kStep) {
             float4v s[4];
 #pragma unroll
@@ -290,7 +292,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
             }
             const int64_t next = tile + kStep;
             const bool more = next < k1;
-            if (more) load_k(next, id_next);
+            if (more) {
+                id_next = block_of(next, entry);
+                load_k(next, id_next);
+            }
 
             const float cs = fmaxf(c_row * sk, kTiny);
             const int64_t key0 = tile + 16 * quad;
@@ -334,7 +339,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
             if (more) {
                 id = id_next;
                 load_v(next, id);
-                id_next = block_at(next + kStep);
+                entry = entry_at(next + kStep);
             }
         }
     }
@@ -498,9 +503,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     // A tile starts at a multiple of 64, so a key's slot is its own low bits,
     // and the tile's in blocks of 128.
     const int32_t *table = sq.table + (int64_t)b * sq.max_blocks;
-    auto block_at = [&](int64_t t) {
-        const int id = t < k1 ? table[t >> c.t_shift] : -1;
-        return id >= 0 && id < c.n_blocks ? id : -1;
+    auto entry_at = [&](int64_t t) { return table[min(t, k1 - 1) >> c.t_shift]; };     // as above
+    auto block_of = [&](int64_t t, int entry) {
+        return t < k1 && entry >= 0 && entry < c.n_blocks ? entry : -1;
     };
     const uint32_t block_bytes = (uint32_t)(c.KVH * c.T) * D;              // < 2^31
     const int pk = gt / (D / 16), pv = gt >> 2;             // key and value of piece 0; + 32, + 64 of piece 1
@@ -508,21 +513,22 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     const int8_t *vp = c.V + ((int64_t)h * D + pv) * c.T + (16 * gt & 48 & (c.T - 1));
     const int k_next = c.T > 32 ? 32 * D : 0, v_next = 64 * c.T;
     uint4 kr[kPieces], vr[kPieces];
-    int kid[kPieces], vid;
+    int k_entry[kPieces], v_entry;
     float sk = 0.0f, sv = 0.0f, sk_next, sv_next;           // of granule lane % 4: 16 tokens of a tile
     bool in_use = false, in_use_next;
     auto load_ids = [&](int64_t tile) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) kid[i] = block_at(tile + pk + 32 * i);
-        vid = block_at(tile + 16 * (gt & 3));
+        for (int i = 0; i < kPieces; ++i) k_entry[i] = entry_at(tile + pk + 32 * i);
+        v_entry = entry_at(tile + 16 * (gt & 3));
     };
     // what lies behind k1 is read from block 0
     auto load_tile = [&](int64_t tile) {
-        const int in = (int)tile & (c.T - 1);
+        const int in = (int)tile & (c.T - 1), vid = block_of(tile + 16 * (gt & 3), v_entry);
         const int8_t *vb = vp + (uint64_t)(uint32_t)max(vid, 0) * block_bytes + in;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            kr[i] = *reinterpret_cast<const uint4 *>(kp + (uint64_t)(uint32_t)max(kid[i], 0) * block_bytes +
+            const int kid = block_of(tile + pk + 32 * i, k_entry[i]);
+            kr[i] = *reinterpret_cast<const uint4 *>(kp + (uint64_t)(uint32_t)max(kid, 0) * block_bytes +
                                                      (in * D + i * k_next));
             vr[i] = *reinterpret_cast<const uint4 *>(vb + i * v_next);
         }
@@ -692,7 +698,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
 // Joins the parts of the rows whose keys were read in more than one: one
 // workgroup per (row, head).  The parts' weights 2^(m_s - m) go to LDS first;
 // then D / 4 threads read a part, 16 bytes each, so that the workgroup has 4
-// THREADS / D parts in flight: 256 threads for up to 64 parts, 1024 for more
+// THREADS / D parts in flight: 256 threads for up to 16 parts, 1024 for more
 // (128 parts of 20 rows: 11.4 us with 256 threads, 4.7 with 1024; 4 parts of
 // 1280 rows: 4.9 and 10.3).
 constexpr int kMaxParts = kBusyGroups;
@@ -794,8 +800,10 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
     const int64_t G = QH / KVH, keys = max_blocks * T, unit = kTile * kWaves;
     const int64_t steps = keys > 0 ? (keys + unit - 1) / unit : 1;
     const int64_t seqs = n_tok < B ? n_tok : B;
-    const double busy = (double)KVH * (seqs + (n_tok - seqs) * (double)G / kRows);
-    int64_t parts = (int64_t)(kBusyGroups / busy);
+    const bool many = n_tok * G > kFewRows * B;
+    const double tiles = n_tok * (double)G / (many ? kManyRows : kRows);
+    const double busy = KVH * (tiles > seqs ? tiles : seqs);
+    int64_t parts = (int64_t)((many || seqs == 1 ? kCUs : kBusyGroups) / busy);
     parts = parts < 1 ? 1 : parts < steps ? parts : steps;
     int64_t each = (steps + parts - 1) / parts;
     if (steps - each < 3) each = steps;
@@ -811,6 +819,7 @@ hipError_t attend(Args a, const Plan &p, hipStream_t s) {
     if (rows_all > kFewRows * (int64_t)a.seqs.B) {
         a.min_rows = a.max_rows = a.seqs.B > 1 ? kFewRows : 0;
         const int64_t groups = (rows_all / kManyRows + a.seqs.B) * a.c.KVH;
+        if (groups >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((kv8_rows128_kernel<BF16, D>), dim3((unsigned)groups, 1, (unsigned)p.S),
                            dim3(kThreads), 0, s, a);
     }
@@ -820,10 +829,10 @@ hipError_t attend(Args a, const Plan &p, hipStream_t s) {
                            dim3((unsigned)slots, (unsigned)a.c.KVH, (unsigned)p.S), dim3(kThreads), 0, s, a);
     }
     const dim3 rows((unsigned)(a.seqs.n_tok * a.QH));
-    if (p.S > 64)
+    if (p.S > 16)
         hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 1024, kMaxParts>), rows, dim3(1024), 0, s, a);
     else if (p.S > 1)
-        hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 256, 64>), rows, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 256, 16>), rows, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
