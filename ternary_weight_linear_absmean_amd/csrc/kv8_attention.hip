@@ -272,8 +272,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     if (first_tile < k1) {
         int id = block_of(first_tile, entry_at(first_tile));
         load_k(first_tile, id);
-        load_v(first_tile, id);
         int entry = entry_at(first_tile + kStep), id_next = -1;
+        load_v(first_tile, id);
         for (int64_t tile = first_tile; tile < k1; tile += kStep) {
             float4v s[4];
 #pragma unroll
@@ -338,8 +338,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
             }
             if (more) {
                 id = id_next;
+                entry = entry_at(next + kStep);            // before V: loads come back in order
                 load_v(next, id);
-                entry = entry_at(next + kStep);
             }
         }
     }
@@ -589,16 +589,17 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
         // also where the wave's rows do not see the tile: one block to schedule
         float16v s[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
 #pragma unroll
-            for (int st = 0; st < NQ; ++st) {
+        for (int st = 0; st < NQ; ++st)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
                 const half8 k = *reinterpret_cast<const half8 *>(lds_k + (ka ^ 32 * st) + t * 64 * D);
 #pragma unroll
                 for (int x = 0; x < NS; ++x) s[t] = mfma_32x32x16(k, qh[x][st], s[t]);
             }
-        }
         to_lds(buf ^ 1);
         __builtin_amdgcn_s_setprio(0);
         float cs[4], w_sv[4], sv_top = 0.0f;
