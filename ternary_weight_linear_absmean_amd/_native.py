@@ -8,7 +8,6 @@ Every step of the computation runs in libbitlinear's kernels.  There is no
 fallback: if the library is missing, ``load()`` raises.
 """
 import collections
-import contextlib
 import ctypes
 import os
 
@@ -549,18 +548,33 @@ def _at(t, dtype, dev, shape, name):
 
 
 def _rows(t, dim, name):
-    """Device and bl_dtype of an fp32 / bf16 tensor with dim dimensions on the GPU."""
+    """Device, bl_dtype, address and shape of a contiguous fp32 / bf16 tensor
+    with dim dimensions on the GPU."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions, got {list(t.shape)}")
+    shape = t.shape
+    if len(shape) != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {list(shape)}")
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise TypeError(f"{name} must be float32 or bfloat16")
-    return t.device, dt
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.device, dt, t.data_ptr(), shape
 
 
-_NOTHING = contextlib.nullcontext()
+class _Nowhere:
+    """A context that changes nothing (contextlib's costs 0.2 us a call)."""
+    __slots__ = ()
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Nowhere()
 
 
 def _where(dev, stream):
@@ -568,7 +582,7 @@ def _where(dev, stream):
     if stream is None:
         # the handle alone: a Stream object costs 1.8 us, as much as a small launch
         return (torch._C._cuda_getCurrentRawStream(dev.index),
-                _NOTHING if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev))
+                _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev))
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
     return stream.cuda_stream, torch.cuda.stream(stream)
@@ -606,11 +620,12 @@ def bitlinear_kv8_append(k, v, q_start, lengths, table, cache, stream=None):
     """The new tokens' rows k, v [n_tok, KVH, D] (fp32 or bf16) into the cache
     (Kv8Cache, updated in place).  int32 on the GPU: q_start [B + 1], lengths
     [B] (with the new tokens), table [B, max_blocks]."""
-    dev, dt = _rows(k, 3, "k")
+    dev, dt, kp, shape = _rows(k, 3, "k")
     c = _kv8(cache, dev)
-    n = k.shape[0]
-    shape = (n, c.KVH, c.D)
-    kp, vp = _at(k, k.dtype, dev, shape, "k"), _at(v, k.dtype, dev, shape, "v")
+    n = shape[0]
+    if shape[1] != c.KVH or shape[2] != c.D:
+        raise ValueError(f"k must be [n_tok, {c.KVH}, {c.D}], got {list(shape)}")
+    vp = _at(v, k.dtype, dev, shape, "v")
     meta = _seqs(q_start, lengths, table, dev)
     handle, context = _where(dev, stream)
     with context:
@@ -624,27 +639,30 @@ def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=N
     """Causal attention of q [n_tok, QH, D] (fp32 or bf16) over the cache:
     out [n_tok, QH, D].  scale defaults to D ** -0.5; q_start, lengths, table
     as for bitlinear_kv8_append.  Rows of no sequence are left as they are."""
-    dev, dt = _rows(q, 3, "q")
+    dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
     c = _kv8(cache, dev)
-    n, QH, D = q.shape
-    qp = _at(q, q.dtype, dev, (n, QH, c.D), "q")
+    if D != c.D:
+        raise ValueError(f"q must be [n_tok, QH, {c.D}], got {list(q.shape)}")
     meta = _seqs(q_start, lengths, table, dev)
     if out is not None:
         _at(out, q.dtype, dev, (n, QH, D), "out")
+    wp = size = 0
     if ws is not None:
-        _at(ws, torch.uint8, dev, (ws.numel(),), "ws")
+        size = ws.numel()
+        wp = _at(ws, torch.uint8, dev, (size,), "ws")
     lib = load()
     handle, context = _where(dev, stream)
     with context:
         if ws is None:
-            need = lib.bitlinear_kv8_attention_ws_bytes(n, QH, meta[3], meta[4], c.KVH, c.T, D)
-            if need:
-                ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+            size = lib.bitlinear_kv8_attention_ws_bytes(n, QH, meta[3], meta[4], c.KVH, c.T, D)
+            if size:
+                ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+                wp = ws.data_ptr()
         if out is None:
             out = torch.empty_like(q)
         st = lib.bitlinear_kv8_attention(
-            qp, dt, n, QH, *meta, c, D ** -0.5 if scale is None else scale, out.data_ptr(),
-            ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, handle)
+            qp, dt, n, QH, *meta, c, D ** -0.5 if scale is None else scale, out.data_ptr(), wp, size,
+            handle)
     if st:
         _check("bitlinear_kv8_attention", st)
     return out
@@ -695,20 +713,20 @@ def bitlinear_decode_stack_kv(layers, caches, x, q_start, lengths, table, H, KV,
 def quant_weight_absmax_i4(W, group=128, Wq4=None, s=None, stream=None):
     """W [N, K] (fp32 or bf16) -> (Wq4 uint8 [N, K/2] 4-bit codes, s bf16
     [N, K/group]); group 32, 64 or 128."""
-    dev, dt = _rows(W, 2, "W")
-    N, K = W.shape
+    dev, dt, wp, (N, K) = _rows(W, 2, "W")
     if group not in (32, 64, 128) or K % group:
         raise ValueError(f"group must be 32, 64 or 128 and divide K = {K}, got {group}")
-    wp = _at(W, W.dtype, dev, (N, K), "W")
+    if Wq4 is not None:
+        _at(Wq4, torch.uint8, dev, (N, K // 2), "Wq4")
+    if s is not None:
+        _at(s, torch.bfloat16, dev, (N, K // group), "s")
     handle, context = _where(dev, stream)
     with context:
         if Wq4 is None:
             Wq4 = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
         if s is None:
             s = torch.empty((N, K // group), dtype=torch.bfloat16, device=dev)
-        st = load().quant_weight_absmax_i4(
-            wp, dt, N, K, group, _at(Wq4, torch.uint8, dev, (N, K // 2), "Wq4"),
-            _at(s, torch.bfloat16, dev, (N, K // group), "s"), handle)
+        st = load().quant_weight_absmax_i4(wp, dt, N, K, group, Wq4.data_ptr(), s.data_ptr(), handle)
     if st:
         _check("quant_weight_absmax_i4", st)
     return Wq4, s
@@ -718,15 +736,16 @@ def _w4(Wq4, s):
     """(device, N, K, group, addresses) of 4-bit weights."""
     if not isinstance(Wq4, torch.Tensor) or not Wq4.is_cuda:
         raise TypeError("Wq4 must be a CUDA (HIP) tensor")
-    if Wq4.dim() != 2 or not isinstance(s, torch.Tensor) or s.dim() != 2:
+    packed = Wq4.shape
+    if len(packed) != 2 or not isinstance(s, torch.Tensor) or s.dim() != 2:
         raise ValueError("Wq4 must be [N, K/2] and s [N, K/group]")
-    N, K2 = Wq4.shape
+    N, K2 = packed
     groups, dev = s.shape[1], Wq4.device
     group = 2 * K2 // groups if groups else 128
     if 2 * K2 != group * groups or group not in (32, 64, 128):
-        raise ValueError(f"Wq4 {list(Wq4.shape)} and s {list(s.shape)} do not make groups of 32, "
-                         "64 or 128")
-    return (dev, N, 2 * K2, group, _at(Wq4, torch.uint8, dev, (N, K2), "Wq4"),
+        raise ValueError(f"Wq4 {list(packed)} and s {list(s.shape)} do not make groups of 32, 64 or "
+                         "128")
+    return (dev, N, 2 * K2, group, _at(Wq4, torch.uint8, dev, packed, "Wq4"),
             _at(s, torch.bfloat16, dev, (N, groups), "s"))
 
 
@@ -735,12 +754,13 @@ def dequant_weight_i4(Wq4, s, dtype=torch.float32, W=None, stream=None):
     dev, N, K, group, wp, sp = _w4(Wq4, s)
     if dtype not in _DTYPES:
         raise TypeError("dtype must be float32 or bfloat16")
+    if W is not None:
+        _at(W, dtype, dev, (N, K), "W")
     handle, context = _where(dev, stream)
     with context:
         if W is None:
             W = torch.empty((N, K), dtype=dtype, device=dev)
-        st = load().dequant_weight_i4(wp, sp, N, K, group, _at(W, dtype, dev, (N, K), "W"),
-                                      _DTYPES[dtype], handle)
+        st = load().dequant_weight_i4(wp, sp, N, K, group, W.data_ptr(), _DTYPES[dtype], handle)
     if st:
         _check("dequant_weight_i4", st)
     return W
@@ -749,18 +769,19 @@ def dequant_weight_i4(Wq4, s, dtype=torch.float32, W=None, stream=None):
 def bitlinear_gemv_w4(X, Wq4, s, Y=None, stream=None):
     """Y [M, N] fp32 = X W^T for X [M, K] (fp32 or bf16), 1 <= M <= 16, and
     4-bit weights (Wq4 [N, K/2], s [N, K/group])."""
-    dev, dt = _rows(X, 2, "X")
+    dev, dt, xp, (M, cols) = _rows(X, 2, "X")
     wdev, N, K, group, wp, sp = _w4(Wq4, s)
-    M = X.shape[0]
     if wdev != dev:
         raise ValueError(f"Wq4 is on {wdev}, not on {dev}")
-    xp = _at(X, X.dtype, dev, (M, K), "X")
+    if cols != K:
+        raise ValueError(f"X must be [M, {K}], got {[M, cols]}")
+    if Y is not None:
+        _at(Y, torch.float32, dev, (M, N), "Y")
     handle, context = _where(dev, stream)
     with context:
         if Y is None:
             Y = torch.empty((M, N), dtype=torch.float32, device=dev)
-        st = load().bitlinear_gemv_w4(xp, dt, M, wp, sp, N, K, group,
-                                      _at(Y, torch.float32, dev, (M, N), "Y"), handle)
+        st = load().bitlinear_gemv_w4(xp, dt, M, wp, sp, N, K, group, Y.data_ptr(), handle)
     if st:
         _check("bitlinear_gemv_w4", st)
     return Y
