@@ -39,7 +39,10 @@ constexpr int kTile = 64;                   // keys per wave and step
 constexpr int kRows = 16;                   // rows of a tile
 constexpr int kFewRows = 32;                // rows of a sequence above which they are many
 constexpr int kFewTiles = kFewRows / kRows;
-constexpr int kBusyGroups = 512;           // workgroups that the parts are to make
+constexpr int kGroups = 512;               // workgroups of 256 that run at once: two to a CU
+constexpr int kStepShift = 8;               // log2 of the keys that a workgroup's waves take in a step
+constexpr int kLongSteps = 32;              // see Plan
+constexpr int kCutSeqs = 256;               // sequences of calls that cut, four to a lane
 
 // Four int8 codes -> four fp16.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -134,21 +137,197 @@ __device__ __forceinline__ void weights(const S &s, float cs, float base, float 
 struct Args {
     const void *q;
     void *out;
-    float *part;              // [S][n_tok * QH][D], then [S][n_tok * QH][2]
     Kv8Seqs seqs;
     Kv8Cache c;
-    int QH, G, S;
-    int64_t min_rows, max_rows;   // rows of the sequences that a kernel takes
-    int64_t chunk;            // keys of a part
+    int QH, G;
     float scale2;             // scale * log2(e)
+    // rows of the sequences that a kernel takes: more than, at most
+    int64_t min_rows, max_rows;
+    bool mixed;               // both kernels run
+    // many rows: S parts of `chunk` keys; [S][n_tok * QH][D], then [S][n_tok *
+    // QH][2]
+    float *part;
+    int64_t chunk;
+    int S;
+    // few rows: pieces for about `most` workgroups; cuts: whether a unit may be
+    // cut, `slots` pieces of such at most; [slots][16][D], then [slots][16][2],
+    // then (slot and row of the first, pieces) by row of q
+    float *cut;
+    int most, slots, step_shift;
+    bool cuts;
 };
 
 __device__ __forceinline__ int64_t key_capacity(const Args &a) {
     return a.c.n_blocks > 0 ? (int64_t)a.seqs.max_blocks << a.c.t_shift : 0;
 }
 
-// Few rows: one workgroup per (16 rows, key head, part of the keys), its waves
-// taking 64-key tiles in turn, each with sums of its own, joined in LDS.
+// Who reads which keys, for few rows.  A unit is (16 rows of a sequence, key
+// head) over the sequence's keys, in steps of 256 keys (64 of each wave).  The
+// lengths are on the device, so every workgroup works the division out from
+// them, the same for all: U units of W steps in all are cut into pieces of c =
+// ceil(W / max(most - U, most / 2)) steps, or not at all where that saves the
+// longest less than three steps (1.7 us each when they wait for memory), as
+// the join is a launch and 2 to 3 us.  That makes W / c + U pieces at most, 2 W
+// / c of them of units that are cut.  Workgroup i takes piece i of the line of
+// all.  (From max_blocks instead of the lengths: FIGURES.)
+//
+// Where the host rules cuts out, a unit's place follows from q_start alone:
+// tile slots of sequence b from floor(q_start[b] G / 16) + b on, or, where
+// sequences of more than kFewRows go to the other kernel, the two that kFewRows
+// make; KVH units each.
+__device__ __forceinline__ int2 *cut_info(const Args &a, int D) {
+    return reinterpret_cast<int2 *>(a.cut + (int64_t)a.slots * kRows * (D + 2));
+}
+struct SeqWork {
+    int q0, n, length;
+    uint32_t tiles, steps;
+};
+__device__ __forceinline__ SeqWork work_of(const Args &a, int q0, int q1, int length) {
+    SeqWork w;
+    w.q0 = min(max(q0, 0), a.seqs.n_tok);
+    w.n = min(max(q1, 0), a.seqs.n_tok) - w.q0;
+    w.length = length;
+    const int64_t rows = (int64_t)w.n * a.G;
+    const int64_t keys = min(max((int64_t)length, (int64_t)1), max(key_capacity(a), (int64_t)1));
+    w.tiles = rows > 0 && rows <= a.max_rows ? (uint32_t)(rows + kRows - 1) / kRows : 0u;
+    w.steps = (uint32_t)((keys - 1) >> a.step_shift) + 1;
+    return w;
+}
+__device__ __forceinline__ SeqWork work_of(const Args &a, int b) {
+    return work_of(a, a.seqs.q_start[b], a.seqs.q_start[b + 1], a.seqs.lengths[b]);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or_0(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+// Running sum / maximum over the lanes: row_shr 1, 2, 4, 8, then the last lane
+// of each 16 to the next, of the first 32 to the others.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    v += dpp_or_0<0x111, 0xF>(v);
+    v += dpp_or_0<0x112, 0xF>(v);
+    v += dpp_or_0<0x114, 0xF>(v);
+    v += dpp_or_0<0x118, 0xF>(v);
+    v += dpp_or_0<0x142, 0xA>(v);
+    v += dpp_or_0<0x143, 0xC>(v);
+    return v;
+}
+__device__ __forceinline__ uint32_t wave_scan_max(uint32_t v) {
+    v = max(v, dpp_or_0<0x111, 0xF>(v));
+    v = max(v, dpp_or_0<0x112, 0xF>(v));
+    v = max(v, dpp_or_0<0x114, 0xF>(v));
+    v = max(v, dpp_or_0<0x118, 0xF>(v));
+    v = max(v, dpp_or_0<0x142, 0xA>(v));
+    return max(v, dpp_or_0<0x143, 0xC>(v));
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+__device__ __forceinline__ uint32_t steps_of_piece(const Args &a, uint32_t units, uint32_t steps, uint32_t top) {
+    const uint32_t most = (uint32_t)a.most;
+    const uint32_t share = units < most / 2 ? most - units : most / 2;
+    const uint32_t c = max((steps + share - 1) / share, 1u);
+    return top < c + 3 ? top : c;
+}
+
+// Piece `pos` of the line: which of its unit, and where among the pieces of
+// units that are cut the unit's begin (-1: not cut).
+struct Piece {
+    SeqWork work;
+    int b, slot;
+    uint32_t h, tile, nth, pieces, c;       // head and 16 rows; of the unit's pieces, of c steps
+};
+__device__ __forceinline__ bool find_unit(const Args &a, uint32_t pos, Piece &p) {
+    const int64_t slot = pos / (uint32_t)a.c.KVH;
+    p.h = pos - (uint32_t)slot * a.c.KVH;
+    int64_t nth;
+    if (a.mixed) {
+        p.b = (int)(slot / kFewTiles);
+        nth = slot % kFewTiles;
+    } else {
+        p.b = find_seq(a.seqs.B, slot, [&](int i) { return (int64_t)q_at(a.seqs, i) * a.G / kRows + i; });
+        nth = slot - ((int64_t)q_at(a.seqs, p.b) * a.G / kRows + p.b);
+    }
+    p.work = work_of(a, p.b);
+    p.tile = (uint32_t)nth;
+    p.nth = 0;
+    p.pieces = 1;
+    p.slot = -1;
+    return nth >= 0 && nth < p.work.tiles;
+}
+__device__ __forceinline__ bool find_piece(const Args &a, uint32_t pos, Piece &p) {
+    const int lane = threadIdx.x & 63, B = a.seqs.B;
+    const uint32_t heads = (uint32_t)a.c.KVH;
+    uint32_t cut_before = 0;
+    if (B == 1) {
+        p.b = 0;
+        p.work = work_of(a, 0);
+        const uint32_t units = heads * p.work.tiles;
+        p.c = steps_of_piece(a, units, units * p.work.steps, p.work.steps);
+        p.pieces = (p.work.steps + p.c - 1) / p.c;
+        if (pos >= units * p.pieces) return false;
+    } else {
+        constexpr int kPer = kCutSeqs / 64;     // sequence 64 j + lane
+        int q0[kPer], q1[kPer], length[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            q0[j] = q1[j] = length[j] = 0;
+            if (64 * j < B) {
+                const int b = min(64 * j + lane, B - 1);
+                q0[j] = a.seqs.q_start[b];
+                q1[j] = a.seqs.q_start[b + 1];
+                length[j] = a.seqs.lengths[b];
+            }
+        }
+        SeqWork w[kPer];
+        uint32_t units = 0, steps = 0, top = 1;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            w[j] = work_of(a, q0[j], q1[j], length[j]);
+            if (64 * j + lane >= B) w[j].tiles = 0;
+            const uint32_t u = heads * w[j].tiles;
+            units += u;
+            steps += u * w[j].steps;
+            top = max(top, u > 0 ? w[j].steps : 1u);
+        }
+        p.c = steps_of_piece(a, lane_of(wave_scan(units), 63), lane_of(wave_scan(steps), 63),
+                             lane_of(wave_scan_max(top), 63));
+        bool found = false;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            if (64 * j >= B || found) continue;             // uniform
+            const uint32_t pieces = w[j].steps <= p.c ? 1u : (w[j].steps + p.c - 1) / p.c;
+            const uint32_t mine = heads * w[j].tiles * pieces, cut = pieces > 1 ? mine : 0u;
+            const uint32_t upto = wave_scan(mine), cut_upto = wave_scan(cut);
+            const uint64_t in = __ballot(pos < upto);
+            if (in != 0) {
+                const int i = __builtin_ctzll(in);
+                found = true;
+                pos -= lane_of(upto - mine, i);
+                cut_before += lane_of(cut_upto - cut, i);
+                p.b = 64 * j + i;
+                p.pieces = lane_of(pieces, i);
+                p.work = SeqWork{(int)lane_of((uint32_t)w[j].q0, i), (int)lane_of((uint32_t)w[j].n, i),
+                                 (int)lane_of((uint32_t)w[j].length, i), lane_of(w[j].tiles, i),
+                                 lane_of(w[j].steps, i)};
+            } else {
+                pos -= lane_of(upto, 63);
+                cut_before += lane_of(cut_upto, 63);
+            }
+        }
+        if (!found) return false;
+    }
+    const uint32_t unit = p.pieces == 1 ? pos : pos / p.pieces;
+    p.nth = pos - unit * p.pieces;
+    p.h = p.work.tiles == 1 ? unit : unit / p.work.tiles;
+    p.tile = unit - p.h * p.work.tiles;
+    p.slot = p.pieces == 1 ? -1 : (int)(cut_before + unit * p.pieces);
+    return true;
+}
+
+// Few rows: one workgroup to a piece; its waves take 64-key tiles in turn, each
+// with sums of its own, joined in LDS.
 template <bool BF16, int D>
 __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     constexpr int ND = D / 64;              // 64-value pieces of a row
@@ -159,37 +338,31 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int low = lane & 15, quad = lane >> 4;
-    const int h = blockIdx.y, split = blockIdx.z;
     const Kv8Seqs &sq = a.seqs;
     const Kv8Cache &c = a.c;
-    const int64_t slot = blockIdx.x;
-    const int G = a.G;
+    const uint32_t G = (uint32_t)a.G;
 
-    // tiles of sequence b: slots from floor(q_start[b] G / 16) + b on, or,
-    // where sequences of more than kFewRows go to the other kernel, the two
-    // that kFewRows make
-    const bool two = a.max_rows == kFewRows;
-    const int b = two ? (int)(slot / kFewTiles) : find_seq(sq.B, slot, [&](int i) {
-        return (int64_t)q_at(sq, i) * G / kRows + i;
-    });
-    const int q0 = q_at(sq, b), n = q_at(sq, b + 1) - q0;
-    const int64_t nth = two ? slot % kFewTiles : slot - ((int64_t)q0 * G / kRows + b);
-    if (nth < 0 || n <= 0 || nth * kRows >= (int64_t)n * G || (int64_t)n * G > a.max_rows) return;
-    const int64_t r0 = nth * kRows;
-    const int rows = (int)min((int64_t)kRows, (int64_t)n * G - r0);
-    const int64_t start = (int64_t)sq.lengths[b] - n;             // position of the first new token
-    const int64_t cap = key_capacity(a);
-    const int64_t last_pos = start + (r0 + rows - 1) / G;
-    const int64_t end = min(last_pos + 1, cap);                   // keys the tile sees
-    const int64_t k0 = (int64_t)split * a.chunk;
-    if (split > 0 && k0 >= end) return;
-    const int64_t k1 = min(end, k0 + a.chunk);
+    Piece piece;
+    if (!(a.cuts ? find_piece(a, blockIdx.x, piece) : find_unit(a, blockIdx.x, piece))) return;
+    const int b = piece.b, q0 = piece.work.q0, n = piece.work.n;
+    const int h = (int)piece.h;
+    const uint32_t r0 = piece.tile * kRows;                       // of the sequence's n G < 2^31
+    const int rows = (int)min((uint32_t)kRows, (uint32_t)n * G - r0);
+    const int64_t start = (int64_t)piece.work.length - n;         // position of the first new token
+    const int64_t end = min(start + (r0 + rows - 1) / G + 1, key_capacity(a));     // keys the tile sees
+    const bool uncut = piece.pieces == 1;
+    const int64_t k0 = uncut ? 0 : (int64_t)(piece.nth * piece.c) << a.step_shift;
+    const int64_t k1 = uncut ? end : min(end, (int64_t)((piece.nth + 1) * piece.c) << a.step_shift);
+    const int64_t slot = piece.slot + (int64_t)piece.nth;         // of what is cut
+    if (!uncut && slot >= a.slots) return;
 
     // this lane's row (rows past the last repeat it; they are not written)
-    const int64_t r = r0 + min(low, rows - 1);
+    const uint32_t r = r0 + min(low, rows - 1);
     const int tok = (int)(r / G);
-    const int hq = h * G + (int)(r - (int64_t)tok * G);
+    const int hq = h * G + (int)(r - tok * G);
     const int64_t row = (int64_t)(q0 + tok) * a.QH + hq;
+    if (a.cuts && piece.nth == 0 && (int)threadIdx.x < rows)
+        cut_info(a, D)[row] = make_int2(uncut ? -1 : piece.slot * kRows + low, (int)piece.pieces);
     const int64_t pos = start + tok;
 
     // q of the row: values 64 dc + 16 quad + 8 half + 0..7 per matrix step
@@ -375,19 +548,15 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
             ll += join_l[w][rr] * f;
             y.x += x.x * f; y.y += x.y * f; y.z += x.z * f; y.w += x.w * f;
         }
-        const int64_t rj = r0 + rr;
-        const int tj = (int)(rj / G);
-        const int64_t row_j = (int64_t)(q0 + tj) * a.QH + h * G + (rj - (int64_t)tj * G);
-        if (min(start + tj + 1, cap) <= a.chunk) {
-            // every key the row sees is in part 0
-            if (split > 0) continue;
+        const uint32_t rj = r0 + rr, tj = rj / G;
+        const int64_t row_j = (int64_t)(q0 + (int)tj) * a.QH + h * G + (rj - tj * G);
+        if (uncut) {
             const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
             store4<BF16>(a.out, row_j * D + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
         } else {
-            const int64_t all = (int64_t)sq.n_tok * a.QH;
-            *reinterpret_cast<float4 *>(a.part + ((int64_t)split * all + row_j) * D + d) = y;
+            *reinterpret_cast<float4 *>(a.cut + (slot * kRows + rr) * D + d) = y;
             if (d == 0) {
-                float *ml = a.part + (int64_t)a.S * all * D + ((int64_t)split * all + row_j) * 2;
+                float *ml = a.cut + (int64_t)a.slots * kRows * D + (slot * kRows + rr) * 2;
                 ml[0] = mm;
                 ml[1] = ll;
             }
@@ -699,40 +868,73 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
 // Joins the parts of the rows whose keys were read in more than one: one
 // workgroup per (row, head).  The parts' weights 2^(m_s - m) go to LDS first;
 // then D / 4 threads read a part, 16 bytes each, so that the workgroup has 4
-// THREADS / D parts in flight: 256 threads for up to 16 parts, 1024 for more
-// (128 parts of 20 rows: 11.4 us with 256 threads, 4.7 with 1024; 4 parts of
-// 1280 rows: 4.9 and 10.3).
-constexpr int kMaxParts = kBusyGroups;
-template <bool BF16, int D, int THREADS, int PARTS>
+// THREADS / D parts in flight: 1024 threads for up to kJoinRows rows, 256 for
+// more (128 parts of 20 rows: 11.4 us with 256 threads, 4.7 with 1024; 4 parts
+// of 1280 rows: 4.9 and 10.3).
+//
+// Rows of sequences that the few-rows kernel takes (FEW): row r of a call of
+// which it takes all, or else row r % (kFewRows KVH) of sequence r / (kFewRows
+// KVH), of which it has kFewRows rows a head at most.
+constexpr int kMaxParts = kGroups;
+constexpr int kJoinRows = 512;
+template <bool BF16, int D, int THREADS, bool FEW>
 __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
     constexpr int kWide = D / 4, kLines = THREADS / kWide, kJoinWaves = THREADS / 64;
-    __shared__ float weight[PARTS > THREADS ? PARTS : THREADS];
+    __shared__ float weight[kMaxParts > THREADS ? kMaxParts : THREADS];
     __shared__ float red[2][kJoinWaves];
     __shared__ float4 sum[kJoinWaves][kWide];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t row = blockIdx.x;
     const Kv8Seqs &sq = a.seqs;
-    const int t = (int)(row / a.QH);
-    const int b = find_seq(sq.B, t, [&](int i) { return (int64_t)q_at(sq, i); });
-    const int q1 = q_at(sq, b + 1);
-    if (t < q_at(sq, b) || t >= q1) return;
-    const int64_t keys = min((int64_t)sq.lengths[b] - (q1 - t) + 1, key_capacity(a));
-    if (keys <= a.chunk) return;                                // written directly
-    const int parts = (int)((keys + a.chunk - 1) / a.chunk);    // <= S <= PARTS
-    const int64_t all = (int64_t)sq.n_tok * a.QH;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.S * all * D);
+    int64_t row = blockIdx.x;
+    int parts;
+    // lines and (m, l) of part s, `pitch` rows apart
+    const float4 *lines;
+    const float2 *ml;
+    int64_t pitch;
+    if (FEW) {
+        int b, t;
+        if (a.mixed) {
+            const int each = kFewRows * a.c.KVH;
+            b = (int)(row / each);
+            const int r = (int)(row - (int64_t)b * each), h = r / kFewRows;
+            t = q_at(sq, b) + r % kFewRows / a.G;
+            row = (int64_t)t * a.QH + h * a.G + r % kFewRows % a.G;
+        } else {
+            t = (int)(row / a.QH);
+            b = find_seq(sq.B, t, [&](int i) { return (int64_t)q_at(sq, i); });
+        }
+        const int q0 = q_at(sq, b), q1 = q_at(sq, b + 1);
+        if (t < q0 || t >= q1 || (int64_t)(q1 - q0) * a.G > a.max_rows) return;
+        const int2 info = cut_info(a, D)[row];
+        parts = info.y;
+        if (parts < 2 || parts > kMaxParts || info.x < 0 || info.x / kRows > a.slots - parts) return;  // written directly
+        const int64_t first_row = info.x;
+        pitch = kRows;
+        lines = reinterpret_cast<const float4 *>(a.cut) + first_row * kWide;
+        ml = reinterpret_cast<const float2 *>(a.cut + (int64_t)a.slots * kRows * D) + first_row;
+    } else {
+        const int t = (int)(row / a.QH);
+        const int b = find_seq(sq.B, t, [&](int i) { return (int64_t)q_at(sq, i); });
+        const int q0 = q_at(sq, b), q1 = q_at(sq, b + 1);
+        if (t < q0 || t >= q1 || (int64_t)(q1 - q0) * a.G <= a.min_rows) return;
+        const int64_t keys = min((int64_t)sq.lengths[b] - (q1 - t) + 1, key_capacity(a));
+        if (keys <= a.chunk) return;                            // written directly
+        parts = (int)((keys + a.chunk - 1) / a.chunk);          // <= S <= kMaxParts
+        const int64_t all = (int64_t)sq.n_tok * a.QH;
+        pitch = all;
+        lines = reinterpret_cast<const float4 *>(a.part) + row * kWide;
+        ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.S * all * D) + row;
+    }
     // the first lines are under way while the weights are formed
     const int d = threadIdx.x % kWide, line = threadIdx.x / kWide;
-    const float4 *src = reinterpret_cast<const float4 *>(a.part) + row * kWide + d;
-    const int64_t pitch = all * kWide;
-    const float4 first = src[min(line, parts - 1) * pitch];
-    constexpr int kEach = (PARTS + THREADS - 1) / THREADS;
+    const float4 first = lines[min(line, parts - 1) * pitch * kWide + d];
+    constexpr int kEach = (kMaxParts + THREADS - 1) / THREADS;
     float2 v[kEach];
     float mm = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int s = threadIdx.x + i * THREADS;
-        v[i] = s < parts ? ml[s * all + row] : make_float2(-INFINITY, 0.0f);
+        v[i] = s < parts ? ml[s * pitch] : make_float2(-INFINITY, 0.0f);
         mm = fmaxf(mm, v[i].x);
     }
     mm = group_max(mm, 64);
@@ -759,7 +961,7 @@ __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
     if (line < parts) y = make_float4(first.x * f, first.y * f, first.z * f, first.w * f);
 #pragma unroll 4
     for (int s = line + kLines; s < parts; s += kLines) {
-        const float4 x = src[s * pitch];
+        const float4 x = lines[s * pitch * kWide + d];
         f = weight[s];
         y.x += x.x * f; y.y += x.y * f; y.z += x.z * f; y.w += x.w * f;
     }
@@ -784,56 +986,89 @@ __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
     }
 }
 
-// Parts the keys are read in: as many as keep kBusyGroups workgroups going, of
-// whole steps (64 keys of each wave), and none where that saves a workgroup
-// fewer than three steps (1.7 us each when they wait for memory), as the join
-// is a launch and 2 to 3 us.  In us, one part and with parts: 5 heads x 512
-// keys 8.0 and 9.0, 1024 keys 11.4 and 9.0, 32768 keys 26.5 (2048 a part) and
-// 20.0; 160 heads x 1024 keys 15.2 and 19.3; with kBusyGroups 1536 instead of
-// 512, 160 x 4096 took 46.7 instead of 42.8, 64 (ragged) x 8192 28.5 instead
-// of 24.6.  The lengths are on the device, so the bound max_blocks * T takes
-// their place: parts behind a sequence's end exit at once.
+template <bool BF16, int D, bool FEW>
+void join(const Args &a, int64_t rows, hipStream_t s) {
+    if (rows <= kJoinRows)
+        hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 1024, FEW>), dim3((unsigned)rows), dim3(1024), 0, s, a);
+    else
+        hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 256, FEW>), dim3((unsigned)rows), dim3(256), 0, s, a);
+}
+
+// What a call launches, from its sizes alone.  Where the sequences bring many
+// rows on average, those that do go to the kernel for many rows; the other
+// takes the rest, or else all.
+//
+// Many rows: as many parts of the keys as keep a workgroup on every CU, none
+// where that saves fewer than three steps.  The lengths are on the device, so
+// max_blocks * T takes their place: parts behind a sequence's end exit at once.
 struct Plan {
-    int64_t slots, chunk;
+    bool many, few, cuts;
     int S;
+    int64_t chunk;
+    int64_t groups;           // of the few-rows kernel
+    int most, slots, step_shift;
+    int64_t part, cut;        // floats of the workspace
 };
-Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH, int64_t T) {
+Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH, int64_t T, int64_t D) {
     const int64_t G = QH / KVH, keys = max_blocks * T, unit = kTile * kWaves;
     const int64_t steps = keys > 0 ? (keys + unit - 1) / unit : 1;
     const int64_t seqs = n_tok < B ? n_tok : B;
-    const bool many = n_tok * G > kFewRows * B;
-    const double tiles = n_tok * (double)G / (many ? kManyRows : kRows);
-    const double busy = KVH * (tiles > seqs ? tiles : seqs);
-    int64_t parts = (int64_t)((many || seqs == 1 ? kCUs : kBusyGroups) / busy);
-    parts = parts < 1 ? 1 : parts < steps ? parts : steps;
-    int64_t each = (steps + parts - 1) / parts;
-    if (steps - each < 3) each = steps;
-    return {n_tok * G / kRows + B, each * unit, (int)((steps + each - 1) / each)};
+    Plan p = {};
+    p.S = 1;
+    p.chunk = steps * unit;
+    p.many = n_tok * G > kFewRows * B;
+    p.few = !p.many || B > 1;
+    if (p.many) {
+        const double tiles = n_tok * (double)G / kManyRows;
+        int64_t parts = (int64_t)(kCUs / (KVH * (tiles > seqs ? tiles : seqs)));
+        parts = parts < 1 ? 1 : parts < steps ? parts : steps;
+        int64_t each = (steps + parts - 1) / parts;
+        if (steps - each < 3) each = steps;
+        p.chunk = each * unit;
+        p.S = (int)((steps + each - 1) / each);
+        if (p.S > 1) p.part = (p.S * n_tok * QH * (D + 2) + 3) / 4 * 4;
+    }
+    if (p.few) {
+        // one sequence: 32768 keys of 5 heads 19.6 us with 512, 16.5 with 256
+        p.most = seqs == 1 ? kCUs : kGroups;
+        int64_t tiles = n_tok * G / kRows + seqs;
+        if (p.many && tiles > seqs * kFewTiles) tiles = seqs * kFewTiles;
+        const int64_t units = tiles * KVH;
+        // longer steps where their number would pass 32 bits
+        p.step_shift = kStepShift;
+        auto line = [&] { return units * (((steps - 1) >> (p.step_shift - kStepShift)) + 1); };
+        while (line() >= (int64_t)1 << 30) ++p.step_shift;
+        p.cuts = steps > 3 && B <= kCutSeqs &&
+                 ((KVH * seqs < p.most / 2 && (!p.many || p.S > 1)) || steps >= kLongSteps);
+        p.groups = (p.many ? B * kFewTiles : n_tok * G / kRows + B) * KVH;
+        if (p.cuts) {
+            p.groups = units < p.most / 2 ? p.most : units + p.most / 2;
+            if (p.groups > line()) p.groups = line();
+            p.slots = (int)(line() < 2 * p.most ? line() : 2 * p.most);
+            p.cut = (int64_t)p.slots * kRows * (D + 2) + 2 * n_tok * QH;
+        }
+    }
+    return p;
 }
 
 template <bool BF16, int D>
 hipError_t attend(Args a, const Plan &p, hipStream_t s) {
-    // Where the sequences bring many rows on average, those that do go to the
-    // kernel for many; the other kernel takes the rest (all of them otherwise).
-    const int64_t rows_all = a.seqs.n_tok * (int64_t)a.G;
-    a.max_rows = rows_all;
-    if (rows_all > kFewRows * (int64_t)a.seqs.B) {
-        a.min_rows = a.max_rows = a.seqs.B > 1 ? kFewRows : 0;
-        const int64_t groups = (rows_all / kManyRows + a.seqs.B) * a.c.KVH;
+    const int64_t rows = (int64_t)a.seqs.n_tok * a.QH;
+    if (p.many) {
+        a.min_rows = p.few ? kFewRows : 0;
+        const int64_t groups = ((int64_t)a.seqs.n_tok * a.G / kManyRows + a.seqs.B) * a.c.KVH;
         if (groups >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((kv8_rows128_kernel<BF16, D>), dim3((unsigned)groups, 1, (unsigned)p.S),
                            dim3(kThreads), 0, s, a);
+        if (p.S > 1) join<BF16, D, false>(a, rows, s);
     }
-    if (a.max_rows > 0) {
-        const int64_t slots = a.max_rows == kFewRows ? (int64_t)a.seqs.B * kFewTiles : p.slots;
-        hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>),
-                           dim3((unsigned)slots, (unsigned)a.c.KVH, (unsigned)p.S), dim3(kThreads), 0, s, a);
+    if (p.few) {
+        a.mixed = p.many;
+        a.max_rows = p.many ? kFewRows : rows;
+        if (p.groups >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidConfiguration;
+        hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>), dim3((unsigned)p.groups), dim3(kThreads), 0, s, a);
+        if (p.cuts) join<BF16, D, true>(a, p.many ? (int64_t)a.seqs.B * kFewRows * a.c.KVH : rows, s);
     }
-    const dim3 rows((unsigned)(a.seqs.n_tok * a.QH));
-    if (p.S > 16)
-        hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 1024, kMaxParts>), rows, dim3(1024), 0, s, a);
-    else if (p.S > 1)
-        hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 256, 16>), rows, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -841,25 +1076,30 @@ hipError_t attend(Args a, const Plan &p, hipStream_t s) {
 
 size_t kv8_attention_ws_floats(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
                                int64_t KVH, int64_t T, int64_t D) {
-    const Plan p = plan_for(n_tok, QH, B, max_blocks, KVH, T);
-    return p.S > 1 ? (size_t)p.S * n_tok * QH * (D + 2) : 0;
+    const Plan p = plan_for(n_tok, QH, B, max_blocks, KVH, T, D);
+    return (size_t)(p.part + p.cut);
 }
 
 hipError_t launch_kv8_attention(const void *q, int dtype, int QH, const Kv8Seqs &seqs,
                                 const bl_kv8 &cache, float scale, void *out, float *ws,
                                 hipStream_t s) {
-    const Plan p = plan_for(seqs.n_tok, QH, seqs.B, seqs.max_blocks, cache.KVH, cache.T);
+    const Plan p = plan_for(seqs.n_tok, QH, seqs.B, seqs.max_blocks, cache.KVH, cache.T, cache.D);
     Args a = {};
     a.q = q;
     a.out = out;
-    a.part = ws;
     a.seqs = seqs;
     a.c = kv8_device(cache);
     a.QH = QH;
     a.G = QH / a.c.KVH;
+    a.scale2 = (float)((double)scale * 1.4426950408889634);
+    a.part = ws;
     a.chunk = p.chunk;
     a.S = p.S;
-    a.scale2 = (float)((double)scale * 1.4426950408889634);
+    a.cut = ws + p.part;
+    a.cuts = p.cuts;
+    a.most = p.most;
+    a.slots = p.slots;
+    a.step_shift = p.step_shift;
     if (cache.D == 64) return dtype ? attend<true, 64>(a, p, s) : attend<false, 64>(a, p, s);
     return dtype ? attend<true, 128>(a, p, s) : attend<false, 128>(a, p, s);
 }

@@ -146,6 +146,15 @@ def test_attention(gpu, case, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_row_counts_around_the_bounds(gpu, dtype):
+    """Calls and sequences of 31 to 33 rows a head, and just below and above."""
+    for G, n in ((4, [1] * 8), (1, [32]), (1, [16, 16]), (1, [31, 33]), (1, [33, 32, 1]), (2, [16]), (8, [4, 1]),
+                 (8, [2, 2]), (32, [1, 2])):
+        s = make(31, n, [40 + 3 * i + x for i, x in enumerate(n)], 16, 64, 1, dtype, G)
+        check_attention(s, attend(gpu, cuda(s)))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_long_sequence_in_parts(gpu, dtype):
     s = make(5, [1, 1, 6], [9000, 4097, 8191], 64, 128, 2, dtype, 4)
     check_attention(s, attend(gpu, cuda(s)))
