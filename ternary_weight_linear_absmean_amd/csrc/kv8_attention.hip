@@ -42,7 +42,7 @@ constexpr int kFewTiles = kFewRows / kRows;
 constexpr int kGroups = 512;               // workgroups of 256 that run at once: two to a CU
 constexpr int kStepShift = 8;               // log2 of the keys that a workgroup's waves take in a step
 constexpr int kLongSteps = 32;              // see Plan
-constexpr int kCutSeqs = 256;               // sequences of calls that cut, four to a lane
+constexpr int kLineSeqs = 256;              // sequences that a wave lines up, four to a lane
 
 // Four int8 codes -> four fp16.
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -144,10 +144,9 @@ struct Args {
     // rows of the sequences that a kernel takes: more than, at most
     int64_t min_rows, max_rows;
     bool mixed;               // both kernels run
-    // many rows: S parts of `chunk` keys; [S][n_tok * QH][D], then [S][n_tok *
-    // QH][2]
+    // many rows: up to S parts of a sequence's keys; [S][n_tok * QH][D], then
+    // [S][n_tok * QH][2]
     float *part;
-    int64_t chunk;
     int S;
     // few rows: pieces for about `most` workgroups; cuts: whether a unit may be
     // cut, `slots` pieces of such at most; [slots][16][D], then [slots][16][2],
@@ -169,14 +168,24 @@ __device__ __forceinline__ int64_t key_capacity(const Args &a) {
 // longest less than three steps (1.7 us each when they wait for memory), as
 // the join is a launch and 2 to 3 us.  That makes W / c + U pieces at most, 2 W
 // / c of them of units that are cut.  Workgroup i takes piece i of the line of
-// all.  (From max_blocks instead of the lengths: FIGURES.)
+// all.  (From max_blocks in
+// the lengths' place: 2000 keys with room for 32768 12.3 us and not 9.3, 16 x
+// 4000 with room for 131072 37 and not 22, 63 x 500 beside 20000 150 and not
+// 22.)
 //
-// Where the host rules cuts out, a unit's place follows from q_start alone:
-// tile slots of sequence b from floor(q_start[b] G / 16) + b on, or, where
-// sequences of more than kFewRows go to the other kernel, the two that kFewRows
-// make; KVH units each.
+// With more than kLineSeqs sequences nothing is cut and a unit's place follows
+// from q_start alone: tile slots of sequence b from floor(q_start[b] G / 16) + b
+// on, or, where sequences of more than kFewRows go to the other kernel, the two
+// that kFewRows make; KVH units each.  (Slots leave some workgroups idle, a
+// fifth with 4 rows a sequence: 64 ragged sequences of up to 4096 keys 54.4 us,
+// in a line 47.9; in a line of 1000 sequences every workgroup would look at all
+// of them: 250 keys each 73.8 and 128 us.)
 __device__ __forceinline__ int2 *cut_info(const Args &a, int D) {
     return reinterpret_cast<int2 *>(a.cut + (int64_t)a.slots * kRows * (D + 2));
+}
+__device__ __forceinline__ uint32_t steps_of(const Args &a, int length, int shift) {
+    const int64_t keys = min(max((int64_t)length, (int64_t)1), max(key_capacity(a), (int64_t)1));
+    return (uint32_t)((keys - 1) >> shift) + 1;
 }
 struct SeqWork {
     int q0, n, length;
@@ -188,9 +197,8 @@ __device__ __forceinline__ SeqWork work_of(const Args &a, int q0, int q1, int le
     w.n = min(max(q1, 0), a.seqs.n_tok) - w.q0;
     w.length = length;
     const int64_t rows = (int64_t)w.n * a.G;
-    const int64_t keys = min(max((int64_t)length, (int64_t)1), max(key_capacity(a), (int64_t)1));
     w.tiles = rows > 0 && rows <= a.max_rows ? (uint32_t)(rows + kRows - 1) / kRows : 0u;
-    w.steps = (uint32_t)((keys - 1) >> a.step_shift) + 1;
+    w.steps = steps_of(a, length, a.step_shift);
     return w;
 }
 __device__ __forceinline__ SeqWork work_of(const Args &a, int b) {
@@ -264,11 +272,14 @@ __device__ __forceinline__ bool find_piece(const Args &a, uint32_t pos, Piece &p
         p.b = 0;
         p.work = work_of(a, 0);
         const uint32_t units = heads * p.work.tiles;
-        p.c = steps_of_piece(a, units, units * p.work.steps, p.work.steps);
-        p.pieces = (p.work.steps + p.c - 1) / p.c;
+        p.pieces = 1;
+        if (a.cuts) {
+            p.c = steps_of_piece(a, units, units * p.work.steps, p.work.steps);
+            p.pieces = (p.work.steps + p.c - 1) / p.c;
+        }
         if (pos >= units * p.pieces) return false;
     } else {
-        constexpr int kPer = kCutSeqs / 64;     // sequence 64 j + lane
+        constexpr int kPer = kLineSeqs / 64;     // sequence 64 j + lane
         int q0[kPer], q1[kPer], length[kPer];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -282,6 +293,7 @@ __device__ __forceinline__ bool find_piece(const Args &a, uint32_t pos, Piece &p
         }
         SeqWork w[kPer];
         uint32_t units = 0, steps = 0, top = 1;
+        p.c = 0xFFFFFFFFu;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             w[j] = work_of(a, q0[j], q1[j], length[j]);
@@ -291,15 +303,16 @@ __device__ __forceinline__ bool find_piece(const Args &a, uint32_t pos, Piece &p
             steps += u * w[j].steps;
             top = max(top, u > 0 ? w[j].steps : 1u);
         }
-        p.c = steps_of_piece(a, lane_of(wave_scan(units), 63), lane_of(wave_scan(steps), 63),
-                             lane_of(wave_scan_max(top), 63));
+        if (a.cuts)
+            p.c = steps_of_piece(a, lane_of(wave_scan(units), 63), lane_of(wave_scan(steps), 63),
+                                 lane_of(wave_scan_max(top), 63));
         bool found = false;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             if (64 * j >= B || found) continue;             // uniform
             const uint32_t pieces = w[j].steps <= p.c ? 1u : (w[j].steps + p.c - 1) / p.c;
             const uint32_t mine = heads * w[j].tiles * pieces, cut = pieces > 1 ? mine : 0u;
-            const uint32_t upto = wave_scan(mine), cut_upto = wave_scan(cut);
+            const uint32_t upto = wave_scan(mine), cut_upto = a.cuts ? wave_scan(cut) : 0u;
             const uint64_t in = __ballot(pos < upto);
             if (in != 0) {
                 const int i = __builtin_ctzll(in);
@@ -343,7 +356,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     const uint32_t G = (uint32_t)a.G;
 
     Piece piece;
-    if (!(a.cuts ? find_piece(a, blockIdx.x, piece) : find_unit(a, blockIdx.x, piece))) return;
+    if (!(a.seqs.B <= kLineSeqs ? find_piece(a, blockIdx.x, piece) : find_unit(a, blockIdx.x, piece))) return;
     const int b = piece.b, q0 = piece.work.q0, n = piece.work.n;
     const int h = (int)piece.h;
     const uint32_t r0 = piece.tile * kRows;                       // of the sequence's n G < 2^31
@@ -586,6 +599,12 @@ __device__ __forceinline__ float16v mfma_32x32x16(half8 a, half8 b, float16v c) 
 __device__ __forceinline__ float lane_value(float v, int lane) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
+// Keys of a part of a sequence: a S-th of them in whole steps, or all where
+// that saves fewer than three.
+__device__ __forceinline__ int64_t keys_of_part(const Args &a, int length) {
+    const uint32_t steps = steps_of(a, length, kStepShift), each = (steps + a.S - 1) / (uint32_t)a.S;
+    return (int64_t)(steps - each < 3 ? steps : each) << kStepShift;
+}
 template <bool BF16, int D>
 __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     constexpr int NS = BF16 ? 1 : 2;
@@ -621,9 +640,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     const int64_t start = (int64_t)sq.lengths[b] - n;
     const int64_t cap = key_capacity(a);
     const int64_t end = min(start + (min(r0 + kManyRows, all_rows) - 1) / G + 1, cap);
-    const int64_t k0 = (int64_t)split * a.chunk;
+    const int64_t chunk = keys_of_part(a, sq.lengths[b]);
+    const int64_t k0 = split * chunk;
     if (split > 0 && k0 >= end) return;
-    const int64_t k1 = min(end, k0 + a.chunk);
+    const int64_t k1 = min(end, k0 + chunk);
 
     const int64_t rw = r0 + 32 * wave;      // the wave's first row
     const bool rows_here = rw < all_rows;
@@ -840,7 +860,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     if (rw + low >= all_rows) return;
     l = l + __shfl_xor(l, 32);
     float f0 = u / kUnit;
-    const bool direct = min(pos + 1, cap) <= a.chunk;
+    const bool direct = min(pos + 1, cap) <= chunk;
     if (direct) {
         if (split > 0) return;
         f0 = l > 0.0f ? f0 / l : 0.0f;
@@ -868,15 +888,16 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
 // Joins the parts of the rows whose keys were read in more than one: one
 // workgroup per (row, head).  The parts' weights 2^(m_s - m) go to LDS first;
 // then D / 4 threads read a part, 16 bytes each, so that the workgroup has 4
-// THREADS / D parts in flight: 1024 threads for up to kJoinRows rows, 256 for
-// more (128 parts of 20 rows: 11.4 us with 256 threads, 4.7 with 1024; 4 parts
-// of 1280 rows: 4.9 and 10.3).
+// THREADS / D parts in flight: 1024 threads for up to kJoinRows rows of what may
+// be more than kJoinParts parts, or else 256 (128 parts of 20 rows: 11.4 us
+// with 256 threads, 4.7 with 1024; 4 parts of 1280 rows: 4.9 and 10.3; the
+// whole call with 4 parts of 20 rows 8.6 and 9.2).
 //
 // Rows of sequences that the few-rows kernel takes (FEW): row r of a call of
 // which it takes all, or else row r % (kFewRows KVH) of sequence r / (kFewRows
 // KVH), of which it has kFewRows rows a head at most.
 constexpr int kMaxParts = kGroups;
-constexpr int kJoinRows = 512;
+constexpr int kJoinRows = 512, kJoinParts = 16;
 template <bool BF16, int D, int THREADS, bool FEW>
 __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
     constexpr int kWide = D / 4, kLines = THREADS / kWide, kJoinWaves = THREADS / 64;
@@ -918,8 +939,9 @@ __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
         const int q0 = q_at(sq, b), q1 = q_at(sq, b + 1);
         if (t < q0 || t >= q1 || (int64_t)(q1 - q0) * a.G <= a.min_rows) return;
         const int64_t keys = min((int64_t)sq.lengths[b] - (q1 - t) + 1, key_capacity(a));
-        if (keys <= a.chunk) return;                            // written directly
-        parts = (int)((keys + a.chunk - 1) / a.chunk);          // <= S <= kMaxParts
+        const int64_t chunk = keys_of_part(a, sq.lengths[b]);
+        if (keys <= chunk) return;                              // written directly
+        parts = (int)((keys + chunk - 1) / chunk);              // <= S <= kMaxParts
         const int64_t all = (int64_t)sq.n_tok * a.QH;
         pitch = all;
         lines = reinterpret_cast<const float4 *>(a.part) + row * kWide;
@@ -987,8 +1009,8 @@ __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
 }
 
 template <bool BF16, int D, bool FEW>
-void join(const Args &a, int64_t rows, hipStream_t s) {
-    if (rows <= kJoinRows)
+void join(const Args &a, int64_t rows, int64_t parts, hipStream_t s) {
+    if (rows <= kJoinRows && parts > kJoinParts)
         hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 1024, FEW>), dim3((unsigned)rows), dim3(1024), 0, s, a);
     else
         hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 256, FEW>), dim3((unsigned)rows), dim3(256), 0, s, a);
@@ -998,13 +1020,17 @@ void join(const Args &a, int64_t rows, hipStream_t s) {
 // rows on average, those that do go to the kernel for many rows; the other
 // takes the rest, or else all.
 //
-// Many rows: as many parts of the keys as keep a workgroup on every CU, none
-// where that saves fewer than three steps.  The lengths are on the device, so
-// max_blocks * T takes their place: parts behind a sequence's end exit at once.
+// Many rows: as many parts of the keys as keep a workgroup on every CU, if that
+// can save three steps; how many a sequence has, and of what keys, its length
+// says on the device (parts behind its end exit at once).
+//
+// Few rows: units are cut where one sequence may be longer than three steps and
+// they are few, or where the longest could hold up the others or a prompt for
+// long (kLongSteps: 54 us); otherwise the join would cost more than it saves.
 struct Plan {
     bool many, few, cuts;
+    int64_t steps;            // of the longest sequence that max_blocks allows
     int S;
-    int64_t chunk;
     int64_t groups;           // of the few-rows kernel
     int most, slots, step_shift;
     int64_t part, cut;        // floats of the workspace
@@ -1014,18 +1040,15 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
     const int64_t steps = keys > 0 ? (keys + unit - 1) / unit : 1;
     const int64_t seqs = n_tok < B ? n_tok : B;
     Plan p = {};
+    p.steps = steps;
     p.S = 1;
-    p.chunk = steps * unit;
     p.many = n_tok * G > kFewRows * B;
     p.few = !p.many || B > 1;
     if (p.many) {
         const double tiles = n_tok * (double)G / kManyRows;
         int64_t parts = (int64_t)(kCUs / (KVH * (tiles > seqs ? tiles : seqs)));
         parts = parts < 1 ? 1 : parts < steps ? parts : steps;
-        int64_t each = (steps + parts - 1) / parts;
-        if (steps - each < 3) each = steps;
-        p.chunk = each * unit;
-        p.S = (int)((steps + each - 1) / each);
+        if (steps - (steps + parts - 1) / parts >= 3) p.S = (int)parts;
         if (p.S > 1) p.part = (p.S * n_tok * QH * (D + 2) + 3) / 4 * 4;
     }
     if (p.few) {
@@ -1038,9 +1061,10 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
         p.step_shift = kStepShift;
         auto line = [&] { return units * (((steps - 1) >> (p.step_shift - kStepShift)) + 1); };
         while (line() >= (int64_t)1 << 30) ++p.step_shift;
-        p.cuts = steps > 3 && B <= kCutSeqs &&
+        p.cuts = steps > 3 && B <= kLineSeqs &&
                  ((KVH * seqs < p.most / 2 && (!p.many || p.S > 1)) || steps >= kLongSteps);
-        p.groups = (p.many ? B * kFewTiles : n_tok * G / kRows + B) * KVH;
+        p.groups = units;
+        if (B > kLineSeqs) p.groups = (p.many ? B * kFewTiles : n_tok * G / kRows + B) * KVH;
         if (p.cuts) {
             p.groups = units < p.most / 2 ? p.most : units + p.most / 2;
             if (p.groups > line()) p.groups = line();
@@ -1060,14 +1084,15 @@ hipError_t attend(Args a, const Plan &p, hipStream_t s) {
         if (groups >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((kv8_rows128_kernel<BF16, D>), dim3((unsigned)groups, 1, (unsigned)p.S),
                            dim3(kThreads), 0, s, a);
-        if (p.S > 1) join<BF16, D, false>(a, rows, s);
+        if (p.S > 1) join<BF16, D, false>(a, rows, p.S, s);
     }
     if (p.few) {
         a.mixed = p.many;
         a.max_rows = p.many ? kFewRows : rows;
         if (p.groups >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>), dim3((unsigned)p.groups), dim3(kThreads), 0, s, a);
-        if (p.cuts) join<BF16, D, true>(a, p.many ? (int64_t)a.seqs.B * kFewRows * a.c.KVH : rows, s);
+        if (p.cuts)
+            join<BF16, D, true>(a, p.many ? (int64_t)a.seqs.B * kFewRows * a.c.KVH : rows, p.steps, s);
     }
     return hipGetLastError();
 }
@@ -1093,7 +1118,6 @@ hipError_t launch_kv8_attention(const void *q, int dtype, int QH, const Kv8Seqs 
     a.G = QH / a.c.KVH;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     a.part = ws;
-    a.chunk = p.chunk;
     a.S = p.S;
     a.cut = ws + p.part;
     a.cuts = p.cuts;

@@ -12,14 +12,15 @@ pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
 
 
-def make(seed, n, lens, T, D, KVH, dtype, G=1, spare=3, behind=0, before=0):
+def make(seed, n, lens, T, D, KVH, dtype, G=1, spare=3, behind=0, before=0, width=0):
     """A filled cache, the new rows and the arrays of a call: sequence b has
-    lens[b] tokens, n[b] of them new; `before` / `behind` rows of no sequence."""
+    lens[b] tokens, n[b] of them new; `before` / `behind` rows of no sequence; a
+    table of `width` entries a sequence at least."""
     g = torch.Generator().manual_seed(seed)
     need = [max(0, -(-x // T)) for x in lens]
     nb = sum(need) + spare
     order = torch.randperm(nb, generator=g).tolist()
-    table = torch.full((len(n), max(need + [1]) + 1), -1, dtype=torch.int32)
+    table = torch.full((len(n), max(need + [1, width - 1]) + 1), -1, dtype=torch.int32)
     for b, m in enumerate(need):
         for j in range(m):
             table[b, j] = order.pop()
@@ -158,6 +159,40 @@ def test_row_counts_around_the_bounds(gpu, dtype):
 def test_long_sequence_in_parts(gpu, dtype):
     s = make(5, [1, 1, 6], [9000, 4097, 8191], 64, 128, 2, dtype, 4)
     check_attention(s, attend(gpu, cuda(s)))
+
+
+LINES = [
+    # n, lens, T, KVH, G: few rows, cut by the lengths that stand in the table's width
+    ([1], [3000], 64, 2, 4),
+    ([1, 1, 1], [1200, 4100, 0], 64, 2, 4),
+    ([1, 0, 3, 1], [1300, 9, 5000, 1], 32, 5, 4),
+    ([1] * 5, [700, 20, 1500, 2, 1025], 16, 3, 7),
+    ([1] * 64, [1 + 37 * i % 1000 for i in range(63)] + [9000], 128, 5, 1),
+    ([1] * 65 + [2], [1 + 37 * i % 1000 for i in range(65)] + [9000], 128, 4, 2),
+    ([i % 3 for i in range(256)], [2 + 37 * i % 500 for i in range(256)], 128, 1, 4),
+    ([1] * 257, [1 + 37 * i % 500 for i in range(257)], 128, 1, 4),
+    ([9] * 30, [9 + 37 * i % 500 for i in range(29)] + [6000], 64, 2, 3),
+    # with sequences of many rows
+    ([1, 100, 2, 1], [5000, 300, 700, 2600], 64, 2, 4),
+    ([0, 400, 1, 1], [0, 1000, 3000, 1], 64, 1, 8),
+    ([1] * 20 + [300], [1 + 37 * i % 1000 for i in range(20)] + [9000], 64, 2, 4),
+    ([70], [3000], 64, 2, 4),
+    ([40, 50], [4000, 300], 32, 2, 4),
+    ([3, 1] * 70 + [1500], [3 + 37 * i % 700 for i in range(140)] + [1500], 128, 1, 2),
+]
+
+
+@pytest.mark.parametrize("width", [0, 9000])
+@pytest.mark.parametrize("case", range(len(LINES)))
+def test_cut_by_the_lengths(gpu, case, width):
+    n, lens, T, KVH, G = LINES[case]
+    dtype, D = (F32, BF16)[case % 2], (128, 64)[case // 2 % 2]
+    s = make(40 + case, n, lens, T, D, KVH, dtype, G, before=case % 2, behind=2, width=-(-width // T))
+    d = cuda(s)
+    out = torch.full_like(d["q"], 77.0)
+    attend(gpu, d, out=out)
+    used = check_attention(s, out)
+    assert (out.cpu().float().numpy()[~used] == 77.0).all()
 
 
 @pytest.mark.parametrize("n,lens", [([1] * 3, [500, 1, 90]), ([70, 20, 30], [300, 20, 31])])
