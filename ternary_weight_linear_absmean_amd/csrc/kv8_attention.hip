@@ -134,6 +134,11 @@ __device__ __forceinline__ void weights(const S &s, float cs, float base, float 
     l = BF16 ? __builtin_fmaf(sum, __builtin_amdgcn_rcpf(w), l) : l + sum;
 }
 
+// A count of keys taken into [0, most].
+__device__ __forceinline__ uint32_t keys_within(int64_t keys, uint32_t most) {
+    return (uint32_t)min(max(keys, (int64_t)0), (int64_t)most);
+}
+
 struct Args {
     const void *q;
     void *out;
@@ -364,8 +369,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     const int64_t start = (int64_t)piece.work.length - n;         // position of the first new token
     const int64_t end = min(start + (r0 + rows - 1) / G + 1, key_capacity(a));     // keys the tile sees
     const bool uncut = piece.pieces == 1;
-    const int64_t k0 = uncut ? 0 : (int64_t)(piece.nth * piece.c) << a.step_shift;
-    const int64_t k1 = uncut ? end : min(end, (int64_t)((piece.nth + 1) * piece.c) << a.step_shift);
+    // key positions: below 2^31, and so are they with a few tiles more in 32 bits
+    const uint32_t k0 = uncut ? 0 : piece.nth * piece.c << a.step_shift;
+    const uint32_t k1 = keys_within(end, uncut ? 0x7FFFFFFFu : k0 + (piece.c << a.step_shift));
     const int64_t slot = piece.slot + (int64_t)piece.nth;         // of what is cut
     if (!uncut && slot >= a.slots) return;
 
@@ -376,7 +382,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     const int64_t row = (int64_t)(q0 + tok) * a.QH + hq;
     if (a.cuts && piece.nth == 0 && (int)threadIdx.x < rows)
         cut_info(a, D)[row] = make_int2(uncut ? -1 : piece.slot * kRows + low, (int)piece.pieces);
-    const int64_t pos = start + tok;
+    const uint32_t sees = keys_within(start + tok + 1, k1);       // keys before this one
 
     // q of the row: values 64 dc + 16 quad + 8 half + 0..7 per matrix step
     half8 qh[NS][ND][2];
@@ -420,20 +426,20 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
 #pragma unroll
     for (int i = 0; i < NO; ++i) o[i] = float4v{0.f, 0.f, 0.f, 0.f};
 
-    const int64_t first_tile = k0 + (int64_t)wave * kTile;
-    constexpr int64_t kStep = (int64_t)kWaves * kTile;
+    const uint32_t first_tile = k0 + wave * kTile;
+    constexpr uint32_t kStep = kWaves * kTile;
     const int32_t *table = sq.table + (int64_t)b * sq.max_blocks;
     // Block of this lane's quad of a tile: the table's entry is loaded a step
     // ahead, at a clamped place, and looked at only when it is used (a look at
     // once would wait for it, and for all loads before it, in every step); -1
     // where it holds no token.
-    auto entry_at = [&](int64_t tile) { return table[min(tile + 16 * quad, k1 - 1) >> c.t_shift]; };
-    auto block_of = [&](int64_t tile, int entry) {
+    auto entry_at = [&](uint32_t tile) { return table[min(tile + 16 * quad, k1 - 1) >> c.t_shift]; };
+    auto block_of = [&](uint32_t tile, int entry) {
         return tile + 16 * quad < k1 && entry >= 0 && entry < c.n_blocks ? entry : -1;
     };
     uint4 kb[4][ND], vb[NO];
     float sk = 0.0f, sv = 0.0f;
-    auto load_k = [&](int64_t tile, int id) {
+    auto load_k = [&](uint32_t tile, int id) {
         // this lane's operand row: key 16 g + 4 tt + i of the tile, 4 g + i = low
         const int g = low >> 2;
         const int idk = max(__shfl(id, 16 * g), 0);
@@ -445,7 +451,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
             for (int dc = 0; dc < ND; ++dc)
                 kb[tt][dc] = *reinterpret_cast<const uint4 *>(p + 4 * tt * D + 64 * dc);
     };
-    auto load_v = [&](int64_t tile, int id) {
+    auto load_v = [&](uint32_t tile, int id) {
         const int64_t hb = (int64_t)max(id, 0) * c.KVH + h;
         sk = c.sk[hb];
         sv = c.sv[hb];
@@ -460,7 +466,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
         load_k(first_tile, id);
         int entry = entry_at(first_tile + kStep), id_next = -1;
         load_v(first_tile, id);
-        for (int64_t tile = first_tile; tile < k1; tile += kStep) {
+        for (uint32_t tile = first_tile; tile < k1; tile += kStep) {
             float4v s[4];
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt) {
@@ -476,7 +482,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
                     }
                 }
             }
-            const int64_t next = tile + kStep;
+            const uint32_t next = tile + kStep;
             const bool more = next < k1;
             if (more) {
                 id_next = block_of(next, entry);
@@ -484,10 +490,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
             }
 
             const float cs = fmaxf(c_row * sk, kTiny);
-            const int64_t key0 = tile + 16 * quad;
-            const bool whole = id >= 0 && key0 + 15 <= pos && key0 + 16 <= k1;
+            const uint32_t key0 = tile + 16 * quad;
+            const bool whole = id >= 0 && key0 + 16 <= sees;
             if (__ballot(!whole) != 0) {
-                const int lim = id >= 0 ? (int)min(min(pos + 1, k1) - key0, (int64_t)16) : 0;
+                const int lim = id >= 0 && key0 < sees ? (int)min(sees - key0, 16u) : 0;
 #pragma unroll
                 for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
@@ -641,9 +647,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     const int64_t cap = key_capacity(a);
     const int64_t end = min(start + (min(r0 + kManyRows, all_rows) - 1) / G + 1, cap);
     const int64_t chunk = keys_of_part(a, sq.lengths[b]);
-    const int64_t k0 = split * chunk;
-    if (split > 0 && k0 >= end) return;
-    const int64_t k1 = min(end, k0 + chunk);
+    if (split > 0 && split * chunk >= end) return;
+    const uint32_t k0 = (uint32_t)(split * chunk), k1 = keys_within(min(end, split * chunk + chunk), 0x7FFFFFFFu);
 
     const int64_t rw = r0 + 32 * wave;      // the wave's first row
     const bool rows_here = rw < all_rows;
@@ -651,9 +656,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     const int tok = (int)(r / G);
     const int64_t row = (int64_t)(q0 + tok) * a.QH + h * G + (int)(r - (int64_t)tok * G);
     const int64_t pos = start + tok;
-    // the positions of the wave's first and last row
-    const int64_t pos_lo = start + min(rw, all_rows - 1) / G;
-    const int64_t pos_hi = start + min(rw + 31, all_rows - 1) / G;
+    // the keys before this one are seen by this row, the wave's first and last
+    const uint32_t sees = keys_within(pos + 1, k1);
+    const uint32_t sees_lo = keys_within(start + min(rw, all_rows - 1) / G + 1, k1);
+    const uint32_t sees_hi = keys_within(start + min(rw + 31, all_rows - 1) / G + 1, k1);
 
     half8 qh[NS][NQ];
     float c_row;
@@ -692,8 +698,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     // A tile starts at a multiple of 64, so a key's slot is its own low bits,
     // and the tile's in blocks of 128.
     const int32_t *table = sq.table + (int64_t)b * sq.max_blocks;
-    auto entry_at = [&](int64_t t) { return table[min(t, k1 - 1) >> c.t_shift]; };     // as above
-    auto block_of = [&](int64_t t, int entry) {
+    auto entry_at = [&](uint32_t t) { return table[min(t, k1 - 1) >> c.t_shift]; };    // as above
+    auto block_of = [&](uint32_t t, int entry) {
         return t < k1 && entry >= 0 && entry < c.n_blocks ? entry : -1;
     };
     const uint32_t block_bytes = (uint32_t)(c.KVH * c.T) * D;              // < 2^31
@@ -705,13 +711,13 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
     int k_entry[kPieces], v_entry;
     float sk = 0.0f, sv = 0.0f, sk_next, sv_next;           // of granule lane % 4: 16 tokens of a tile
     bool in_use = false, in_use_next;
-    auto load_ids = [&](int64_t tile) {
+    auto load_ids = [&](uint32_t tile) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) k_entry[i] = entry_at(tile + pk + 32 * i);
         v_entry = entry_at(tile + 16 * (gt & 3));
     };
     // what lies behind k1 is read from block 0
-    auto load_tile = [&](int64_t tile) {
+    auto load_tile = [&](uint32_t tile) {
         const int in = (int)tile & (c.T - 1), vid = block_of(tile + 16 * (gt & 3), v_entry);
         const int8_t *vb = vp + (uint64_t)(uint32_t)max(vid, 0) * block_bytes + in;
 #pragma unroll
@@ -769,8 +775,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
         __syncthreads();
     }
     int buf = 0;
-    for (int64_t tile = k0; tile < k1; tile += kTile, buf ^= 1) {
-        const bool here = rows_here && tile <= pos_hi;
+    for (uint32_t tile = k0; tile < k1; tile += kTile, buf ^= 1) {
+        const bool here = rows_here && tile < sees_hi;
         // opaque, or the loop would hold an address for each piece
         int ka = k_get + buf * kBuf, va = v_get + buf * kBuf;
         asm("" : "+v"(ka), "+v"(va));
@@ -808,8 +814,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
         load_tile(tile + 2 * kTile);
         load_ids(tile + 3 * kTile);
         if (here) {
-            if (!(valid && tile + kTile <= k1 && tile + kTile - 1 <= pos_lo)) {       // uniform
-                const int lim = (int)min(min(pos + 1, k1) - tile, (int64_t)kTile);
+            if (!(valid && tile + kTile <= sees_lo)) {                  // uniform
+                const int lim = tile < sees ? (int)min(sees - tile, (uint32_t)kTile) : 0;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int lim_g = lane_value(used ? 1.0f : 0.0f, g) != 0.0f ? lim - 16 * g - 8 * half : 0;
