@@ -169,21 +169,24 @@ __device__ __forceinline__ int64_t key_capacity(const Args &a) {
 // head) over the sequence's keys, in steps of 256 keys (64 of each wave).  The
 // lengths are on the device, so every workgroup works the division out from
 // them, the same for all: U units of W steps in all are cut into pieces of c =
-// ceil(W / max(most - U, most / 2)) steps, or not at all where that saves the
-// longest less than three steps (1.7 us each when they wait for memory), as
-// the join is a launch and 2 to 3 us.  That makes W / c + U pieces at most, 2 W
-// / c of them of units that are cut.  Workgroup i takes piece i of the line of
-// all.  (From max_blocks in
-// the lengths' place: 2000 keys with room for 32768 12.3 us and not 9.3, 16 x
-// 4000 with room for 131072 37 and not 22, 63 x 500 beside 20000 150 and not
-// 22.)
+// ceil(W / most) steps; that makes W / c + U pieces at most, 2 W / c of them of
+// units that are cut.  Workgroup i takes piece i of the line of all.
+//
+// Nothing is cut where that saves the longest unit less than three steps (1.7
+// us each when they wait for memory), as the join is a launch and 2 to 3 us, nor
+// where U >= most / 2 and the longest has less than 2.5 c: then the units fill
+// the GPU evenly enough.  64 ragged sequences of up to 4096 keys, 5 heads: 48.1
+// us uncut, 42.8 cut; 96 of them 63 and 67, 128 73 and 80.  With max_blocks in
+// the lengths' place 2000 keys with room for 32768 took 12.3 us and not 9.1, 16
+// x 4000 with room for 131072 37 and not 22, 63 x 500 beside 20000 150 and not
+// 20.
 //
 // With more than kLineSeqs sequences nothing is cut and a unit's place follows
 // from q_start alone: tile slots of sequence b from floor(q_start[b] G / 16) + b
 // on, or, where sequences of more than kFewRows go to the other kernel, the two
 // that kFewRows make; KVH units each.  (Slots leave some workgroups idle, a
 // fifth with 4 rows a sequence: 64 ragged sequences of up to 4096 keys 54.4 us,
-// in a line 47.9; in a line of 1000 sequences every workgroup would look at all
+// in a line 48.1; in a line of 1000 sequences every workgroup would look at all
 // of them: 250 keys each 73.8 and 128 us.)
 __device__ __forceinline__ int2 *cut_info(const Args &a, int D) {
     return reinterpret_cast<int2 *>(a.cut + (int64_t)a.slots * kRows * (D + 2));
@@ -239,9 +242,8 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) {
 
 __device__ __forceinline__ uint32_t steps_of_piece(const Args &a, uint32_t units, uint32_t steps, uint32_t top) {
     const uint32_t most = (uint32_t)a.most;
-    const uint32_t share = units < most / 2 ? most - units : most / 2;
-    const uint32_t c = max((steps + share - 1) / share, 1u);
-    return top < c + 3 ? top : c;
+    const uint32_t c = max((steps + most - 1) / most, 1u);
+    return top < c + 3 || (2 * units >= most && 2 * top < 5 * c) ? top : c;
 }
 
 // Piece `pos` of the line: which of its unit, and where among the pieces of
@@ -1068,11 +1070,11 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
         auto line = [&] { return units * (((steps - 1) >> (p.step_shift - kStepShift)) + 1); };
         while (line() >= (int64_t)1 << 30) ++p.step_shift;
         p.cuts = steps > 3 && B <= kLineSeqs &&
-                 ((KVH * seqs < p.most / 2 && (!p.many || p.S > 1)) || steps >= kLongSteps);
+                 ((3 * KVH * seqs < 2 * p.most && (!p.many || p.S > 1)) || steps >= kLongSteps);
         p.groups = units;
         if (B > kLineSeqs) p.groups = (p.many ? B * kFewTiles : n_tok * G / kRows + B) * KVH;
         if (p.cuts) {
-            p.groups = units < p.most / 2 ? p.most : units + p.most / 2;
+            p.groups = units + p.most;
             if (p.groups > line()) p.groups = line();
             p.slots = (int)(line() < 2 * p.most ? line() : 2 * p.most);
             p.cut = (int64_t)p.slots * kRows * (D + 2) + 2 * n_tok * QH;
