@@ -153,6 +153,7 @@ struct Args {
     // [S][n_tok * QH][2]
     float *part;
     int S;
+    int64_t many_groups;      // workgroups of a part
     // few rows: pieces for about `most` workgroups; cuts: whether a unit may be
     // cut, `slots` pieces of such at most; [slots][16][D], then [slots][16][2],
     // then (slot and row of the first, pieces) by row of q
@@ -348,14 +349,18 @@ __device__ __forceinline__ bool find_piece(const Args &a, uint32_t pos, Piece &p
 
 // Few rows: one workgroup to a piece; its waves take 64-key tiles in turn, each
 // with sums of its own, joined in LDS.
+template <int D>
+struct FewLds {
+    float join[kWaves][kRows][D + 4];
+    float m[kWaves][kRows], l[kWaves][kRows];
+};
 template <bool BF16, int D>
-__global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
+__device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D> &lds) {
     constexpr int ND = D / 64;              // 64-value pieces of a row
     constexpr int NO = D / 16;              // 16-value tiles of the output
     constexpr int NS = BF16 ? 1 : 2;        // fp16 parts of q and of p sv
-    __shared__ float join[kWaves][kRows][D + 4];
-    __shared__ float join_m[kWaves][kRows], join_l[kWaves][kRows];
-
+    auto &join = lds.join;
+    auto &join_m = lds.m, &join_l = lds.l;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int low = lane & 15, quad = lane >> 4;
     const Kv8Seqs &sq = a.seqs;
@@ -363,7 +368,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows16_kernel(Args a) {
     const uint32_t G = (uint32_t)a.G;
 
     Piece piece;
-    if (!(a.seqs.B <= kLineSeqs ? find_piece(a, blockIdx.x, piece) : find_unit(a, blockIdx.x, piece))) return;
+    if (!(a.seqs.B <= kLineSeqs ? find_piece(a, group, piece) : find_unit(a, group, piece))) return;
     const int b = piece.b, q0 = piece.work.q0, n = piece.work.n;
     const int h = (int)piece.h;
     const uint32_t r0 = piece.tile * kRows;                       // of the sequence's n G < 2^31
@@ -613,22 +618,22 @@ __device__ __forceinline__ int64_t keys_of_part(const Args &a, int length) {
     const uint32_t steps = steps_of(a, length, kStepShift), each = (steps + a.S - 1) / (uint32_t)a.S;
     return (int64_t)(steps - each < 3 ? steps : each) << kStepShift;
 }
+template <int D>
+struct ManyLds {
+    uint4 k[2 * kTile * D / 8], v[2 * kTile * D / 8];
+};
 template <bool BF16, int D>
-__global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
+__device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, ManyLds<D> &lds) {
     constexpr int NS = BF16 ? 1 : 2;
     constexpr int NQ = D / 16;              // steps of K Q^T
     constexpr int NO = D / 32;              // tiles of the output
     constexpr int kPieces = kTile * D / 16 / kThreads;      // 16-byte pieces of K and of V per thread
-    __shared__ uint4 buf_k[2 * kTile * D / 8], buf_v[2 * kTile * D / 8];
-
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, gt = threadIdx.x;
     const int low = lane & 31, half = lane >> 5;
-    const int split = blockIdx.z;
     // Heads of one tile side by side, tiles that see most first.  Two
     // workgroups share a CU: where all start at once, the second of each is to
     // be the first's complement, so the order turns round after the first 256.
-    const int64_t groups = (int64_t)gridDim.x;
-    int64_t at = blockIdx.x;
+    const int64_t groups = a.many_groups;
     if (at >= kCUs && groups <= 2 * kCUs) at = groups - 1 - (at - kCUs);
     const int h = (int)(at % a.c.KVH);
     const int64_t slot = at / a.c.KVH;
@@ -741,7 +746,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
         return D == 128 ? key * 256 + ((piece ^ (key & 15)) << 4) : key * 128 + ((piece ^ ((key >> 1) & 7)) << 4);
     };
     auto v_at = [](int d, int piece) { return d * 128 + ((piece ^ ((d >> 1) & 7)) << 4); };
-    char *const lds_k = reinterpret_cast<char *>(buf_k), *const lds_v = reinterpret_cast<char *>(buf_v);
+    char *const lds_k = reinterpret_cast<char *>(lds.k), *const lds_v = reinterpret_cast<char *>(lds.v);
     constexpr int kBuf = kTile * D * 2;                     // bytes of a tile of K or V
     const int k_put = k_at(pk, 2 * (gt % (D / 16))), v_put = v_at(pv, 2 * (gt & 3));
     auto to_lds = [&](int buf) {
@@ -890,6 +895,36 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_rows128_kernel(Args a) {
         float *ml = a.part + (int64_t)a.S * all * D + ((int64_t)split * all + row) * 2;
         ml[0] = m;
         ml[1] = l;
+    }
+}
+
+template <bool BF16, int D>
+__global__ __launch_bounds__(kThreads, 2) void kv8_few_kernel(Args a) {
+    __shared__ FewLds<D> lds;
+    few_rows<BF16, D>(a, blockIdx.x, lds);
+}
+template <bool BF16, int D>
+__global__ __launch_bounds__(kThreads, 2) void kv8_many_kernel(Args a) {
+    __shared__ ManyLds<D> lds;
+    many_rows<BF16, D>(a, blockIdx.x, blockIdx.z, lds);
+}
+// Both in one launch: many rows wait for instructions, few rows for memory, so
+// they are to share the CUs.  The workgroups for few rows stand behind the
+// first kCUs of the others.
+template <bool BF16, int D>
+__global__ __launch_bounds__(kThreads, 2) void kv8_mixed_kernel(Args a) {
+    __shared__ union {
+        FewLds<D> few;
+        ManyLds<D> many;
+    } lds;
+    const int64_t all = a.many_groups * a.S, first = min(all, (int64_t)kCUs);
+    const int64_t few = gridDim.x - all, i = blockIdx.x;
+    if (i >= first && i < first + few) {
+        few_rows<BF16, D>(a, (uint32_t)(i - first), lds.few);
+    } else {
+        const int64_t at = i < first ? i : i - few;
+        const int split = (int)(at / a.many_groups);
+        many_rows<BF16, D>(a, at - split * a.many_groups, split, lds.many);
     }
 }
 
@@ -1086,22 +1121,22 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
 template <bool BF16, int D>
 hipError_t attend(Args a, const Plan &p, hipStream_t s) {
     const int64_t rows = (int64_t)a.seqs.n_tok * a.QH;
-    if (p.many) {
-        a.min_rows = p.few ? kFewRows : 0;
-        const int64_t groups = ((int64_t)a.seqs.n_tok * a.G / kManyRows + a.seqs.B) * a.c.KVH;
-        if (groups >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL((kv8_rows128_kernel<BF16, D>), dim3((unsigned)groups, 1, (unsigned)p.S),
-                           dim3(kThreads), 0, s, a);
-        if (p.S > 1) join<BF16, D, false>(a, rows, p.S, s);
-    }
-    if (p.few) {
-        a.mixed = p.many;
-        a.max_rows = p.many ? kFewRows : rows;
-        if (p.groups >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL((kv8_rows16_kernel<BF16, D>), dim3((unsigned)p.groups), dim3(kThreads), 0, s, a);
-        if (p.cuts)
-            join<BF16, D, true>(a, p.many ? (int64_t)a.seqs.B * kFewRows * a.c.KVH : rows, p.steps, s);
-    }
+    const dim3 block(kThreads);
+    a.mixed = p.many && p.few;
+    a.min_rows = a.mixed ? kFewRows : 0;
+    a.max_rows = a.mixed ? kFewRows : rows;
+    if (p.many) a.many_groups = ((int64_t)a.seqs.n_tok * a.G / kManyRows + a.seqs.B) * a.c.KVH;
+    const int64_t groups = a.many_groups * p.S + p.groups;
+    if (groups >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidConfiguration;
+    if (a.mixed)
+        hipLaunchKernelGGL((kv8_mixed_kernel<BF16, D>), dim3((unsigned)groups), block, 0, s, a);
+    else if (p.many)
+        hipLaunchKernelGGL((kv8_many_kernel<BF16, D>), dim3((unsigned)a.many_groups, 1, (unsigned)p.S), block, 0, s, a);
+    else
+        hipLaunchKernelGGL((kv8_few_kernel<BF16, D>), dim3((unsigned)groups), block, 0, s, a);
+    if (p.many && p.S > 1) join<BF16, D, false>(a, rows, p.S, s);
+    if (p.cuts)
+        join<BF16, D, true>(a, a.mixed ? (int64_t)a.seqs.B * kFewRows * a.c.KVH : rows, p.steps, s);
     return hipGetLastError();
 }
 
