@@ -41,6 +41,7 @@ constexpr int kFewRows = 32;                // rows of a sequence above which th
 constexpr int kFewTiles = kFewRows / kRows;
 constexpr int kGroups = 512;               // workgroups of 256 that run at once: two to a CU
 constexpr int kStepShift = 8;               // log2 of the keys that a workgroup's waves take in a step
+constexpr int kManyWork = 2048;             // see Plan
 constexpr int kLongSteps = 32;              // see Plan
 constexpr int kLineSeqs = 256;              // sequences that a wave lines up, four to a lane
 
@@ -348,7 +349,16 @@ __device__ __forceinline__ bool find_piece(const Args &a, uint32_t pos, Piece &p
 }
 
 // Few rows: one workgroup to a piece; its waves take 64-key tiles in turn, each
-// with sums of its own, joined in LDS.
+// with sums of its own, joined in LDS.  The products' operands go from memory to
+// registers, no LDS in the loop: a cached byte has one reader.  The next tile's
+// K is under way from the moment this one's has been used, and so is V.
+//
+// Bound by memory where the sequences are alike (64 of 4096 keys, 335 MB: 72 us,
+// 4.65 TB/s, a copy 4.78), else by the longest pieces: a lone wave takes 1.6 us
+// of instructions for a 64-key tile, and while others load, 2.9 us.  (64 ragged,
+// 163 MB: 36.4 us, 4.5 TB/s, and 4.2 the join.)  178 registers in bf16 with D =
+// 128, two workgroups to a CU; a third, with q in LDS, took 79 us for 128
+// sequences instead of 72.5.
 template <int D>
 struct FewLds {
     float join[kWaves][kRows][D + 4];
@@ -524,8 +534,8 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
                 u = u_new;
             }
             half8 ph[NS][2];
-            weights<BF16, 2>([&](int e) { return s[e >> 2][e & 3]; }, cs, m == -INFINITY ? 0.0f : m, id >= 0 ? sv * unit_u : 0.0f, l,
-                             ph[0], ph[NS - 1]);
+            weights<BF16, 2>([&](int e) { return s[e >> 2][e & 3]; }, cs, m == -INFINITY ? 0.0f : m,
+                             id >= 0 ? sv * unit_u : 0.0f, l, ph[0], ph[NS - 1]);
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
                 const half8 v_lo = codes8(vb[i].x, vb[i].y), v_hi = codes8(vb[i].z, vb[i].w);
@@ -595,6 +605,12 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 // once, in LDS, for all rows (16-row workgroups did it for each: four
 // conversions per matrix step).  While tile t is used, t + 1 is turned into
 // the other buffer and the codes of t + 2 are on their way.
+//
+// Bound by vector instructions, about 380 of a wave and tile beside its 32
+// matrix instructions: 40 of them exponentials, logarithms and reciprocals at a
+// quarter of the rate, 87 the conversion.  2 x 2048 ragged rows on 4096 keys, 5
+// heads of 4, bf16, 92 GFLOP: 131 us, 700 TFLOP/s (a large bf16 matrix product
+// 1145); fp32, with two matrix instructions for one, 199 us.
 //
 // Layouts (lane = 32 half + low): S^T = K Q^T puts key 8 (i / 4) + 4 half + i
 // % 4 of the operand's rows, row low, into accumulator i.  Operand row r holds
@@ -909,8 +925,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_many_kernel(Args a) {
     many_rows<BF16, D>(a, blockIdx.x, blockIdx.z, lds);
 }
 // Both in one launch: many rows wait for instructions, few rows for memory, so
-// they are to share the CUs.  The workgroups for few rows stand behind the
-// first kCUs of the others.
+// are to share the CUs.  The workgroups for few rows stand behind the first kCUs
+// of the others.  15 single tokens on 8000 keys each beside a prompt of 500: 63.2
+// us as two launches, 48.9 so; on 2000 keys beside one of 2000 75.9 and 63.7; 2
+// prompts of up to 2048 rows alone 133.5 and 130.7.
 template <bool BF16, int D>
 __global__ __launch_bounds__(kThreads, 2) void kv8_mixed_kernel(Args a) {
     __shared__ union {
@@ -971,7 +989,8 @@ __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
         if (t < q0 || t >= q1 || (int64_t)(q1 - q0) * a.G > a.max_rows) return;
         const int2 info = cut_info(a, D)[row];
         parts = info.y;
-        if (parts < 2 || parts > kMaxParts || info.x < 0 || info.x / kRows > a.slots - parts) return;  // written directly
+        if (parts < 2 || parts > kMaxParts || info.x < 0 || info.x / kRows > a.slots - parts)
+            return;                                             // written directly
         const int64_t first_row = info.x;
         pitch = kRows;
         lines = reinterpret_cast<const float4 *>(a.cut) + first_row * kWide;
@@ -1060,8 +1079,16 @@ void join(const Args &a, int64_t rows, int64_t parts, hipStream_t s) {
 }
 
 // What a call launches, from its sizes alone.  Where the sequences bring many
-// rows on average, those that do go to the kernel for many rows; the other
-// takes the rest, or else all.
+// rows on average and there is much to do (W of the few-rows kernel, with
+// all lengths at their limit, above kManyWork), those that do go to the kernel for many rows; the
+// other takes the rest, or else all.  A lone workgroup of many rows takes 2 us a
+// tile of 64 keys, so with little work the few-rows kernel, cut to fill the GPU,
+// is done first though it reads and converts a code 8 times as often.  In us,
+// few and many rows, 5 heads of 4, bf16: 128 rows on 500 keys 7.5 and 18.9, on
+// 4000 (W = 640) 13 and 19; 256 rows on 4000 (1280) 23.5 and 22.3; 1024 on 1000
+// (4 sequences, 1280) 22.9 and 29.5; 512 on 4000 (2560) 31.7 and 27.7; 256 on
+// 32000 (10000) 116 and 59; and 64 sequences of 32 rows on 4000 110 and 140, of
+// 64 rows 191 and 142.
 //
 // Many rows: as many parts of the keys as keep a workgroup on every CU, if that
 // can save three steps; how many a sequence has, and of what keys, its length
@@ -1085,7 +1112,7 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
     Plan p = {};
     p.steps = steps;
     p.S = 1;
-    p.many = n_tok * G > kFewRows * B;
+    p.many = n_tok * G > kFewRows * B && (double)n_tok * QH / kRows * steps > kManyWork;
     p.few = !p.many || B > 1;
     if (p.many) {
         const double tiles = n_tok * (double)G / kManyRows;

@@ -175,14 +175,14 @@ LINES = [
     # with sequences of many rows
     ([1, 100, 2, 1], [5000, 300, 700, 2600], 64, 2, 4),
     ([0, 400, 1, 1], [0, 1000, 3000, 1], 64, 1, 8),
-    ([1] * 20 + [300], [1 + 37 * i % 1000 for i in range(20)] + [9000], 64, 2, 4),
+    ([1] * 20 + [300], [1 + 37 * i % 1000 for i in range(20)] + [4000], 64, 1, 4),
     ([70], [3000], 64, 2, 4),
     ([40, 50], [4000, 300], 32, 2, 4),
     ([3, 1] * 70 + [1500], [3 + 37 * i % 700 for i in range(140)] + [1500], 128, 1, 2),
 ]
 
 
-@pytest.mark.parametrize("width", [0, 9000])
+@pytest.mark.parametrize("width", [0, 9000, 60000])
 @pytest.mark.parametrize("case", range(len(LINES)))
 def test_cut_by_the_lengths(gpu, case, width):
     n, lens, T, KVH, G = LINES[case]
@@ -195,11 +195,38 @@ def test_cut_by_the_lengths(gpu, case, width):
     assert (out.cpu().float().numpy()[~used] == 77.0).all()
 
 
+MANY = [
+    # n, lens, T, D, KVH, G, width in keys: calls with much to do
+    ([300], [500], 64, 64, 8, 8, 0),
+    ([250, 70, 1], [450, 100, 33], 16, 128, 8, 8, 0),
+    ([400, 0, 40], [400, 7, 590], 128, 64, 7, 7, 0),
+    ([300], [300], 64, 128, 1, 4, 70000),
+    ([40, 1, 90], [100, 31, 90], 16, 128, 2, 3, 70000),
+    ([129, 7], [1500, 7], 128, 128, 1, 8, 70000),
+    ([33], [600], 64, 64, 3, 4, 70000),
+    ([70, 4, 50], [2000, 1500, 300], 32, 64, 2, 4, 30000),
+    ([9, 300], [4000, 2500], 64, 128, 2, 4, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_rows(gpu, case, dtype):
+    n, lens, T, D, KVH, G, width = MANY[case]
+    s = make(70 + case, n, lens, T, D, KVH, dtype, G, before=case % 3, behind=1, width=-(-width // T))
+    d = cuda(s)
+    out = torch.full_like(d["q"], 77.0)
+    attend(gpu, d, out=out)
+    used = check_attention(s, out)
+    assert (out.cpu().float().numpy()[~used] == 77.0).all()
+
+
+@pytest.mark.parametrize("width", [0, 70000])
 @pytest.mark.parametrize("n,lens", [([1] * 3, [500, 1, 90]), ([70, 20, 30], [300, 20, 31])])
-def test_what_is_masked_never_shows(gpu, n, lens):
+def test_what_is_masked_never_shows(gpu, n, lens, width):
     """NaN and infinite scales and any codes in blocks and slots behind a
     length, in spare blocks and in blocks that no valid entry names."""
-    s = make(9, n, lens, 32, 64, 2, F32, 4, spare=8)
+    s = make(9, n, lens, 32, 64, 2, F32, 4, spare=8, width=width // 32)
     want = attend(gpu, cuda(s))
     used = {int(s["table"][b, j]) for b in range(len(n)) for j in range(-(-lens[b] // 32))}
     free = [i for i in range(len(s["sk"])) if i not in used]
@@ -215,10 +242,11 @@ def test_what_is_masked_never_shows(gpu, n, lens):
     assert torch.equal(want, got)
 
 
-@pytest.mark.parametrize("n", [[1, 1, 1], [40, 2, 3]])
-def test_blocks_out_of_range_hold_nothing(gpu, n):
+@pytest.mark.parametrize("width", [0, 70000])
+@pytest.mark.parametrize("n", [[1, 1, 1], [40, 2, 3], [60, 2, 3]])
+def test_blocks_out_of_range_hold_nothing(gpu, n, width):
     lens = [200, 40, 90]
-    s = make(11, n, lens, 16, 64, 2, F32, 2)
+    s = make(11, n, lens, 16, 64, 2, F32, 2, width=width // 16)
     s["table"][0, 2] = -5
     s["table"][0, 5] = len(s["K"])
     s["table"][0, 12] = 2 ** 31 - 1            # the block of the newest tokens
@@ -229,11 +257,12 @@ def test_blocks_out_of_range_hold_nothing(gpu, n):
     assert (out[-n[2]:] == 0).all()
 
 
+@pytest.mark.parametrize("width", [0, 70000])
 @pytest.mark.parametrize("n", [[3, 1, 2], [50, 2, 30]])
-def test_odd_lengths_and_starts(gpu, n):
+def test_odd_lengths_and_starts(gpu, n, width):
     """Lengths below the new tokens' number, zero, negative, beyond the table;
     starts beyond the rows."""
-    s = make(12, n, [max(3, x - 2) for x in n], 16, 64, 1, F32, 2)
+    s = make(12, n, [max(3, x - 2) for x in n], 16, 64, 1, F32, 2, width=width // 16)
     s["lengths"] = torch.tensor([n[0] - 2, 0, s["table"].shape[1] * 16 + 5], dtype=torch.int32)
     s["table"] = torch.arange(s["table"].numel(), dtype=torch.int32).view(s["table"].shape) % len(s["K"])
     s["table"][2] = s["table"][0]
@@ -249,9 +278,10 @@ def test_odd_lengths_and_starts(gpu, n):
     check_attention(s, attend(gpu, cuda(s)))
 
 
-def test_extreme_scales_and_scores(gpu):
+@pytest.mark.parametrize("width", [0, 70000])
+def test_extreme_scales_and_scores(gpu, width):
     """Zero and very different scales from block to block, scores far apart."""
-    s = make(13, [1, 60], [400, 60], 16, 64, 2, F32, 4)
+    s = make(13, [1, 60], [400, 60], 16, 64, 2, F32, 4, width=width // 16)
     s["sv"][::3] = 0
     s["sv"][1::3] *= 1e-7
     s["sk"][::4] = 0
@@ -284,11 +314,12 @@ def test_append_twice_is_append_once(gpu):
     assert all(torch.equal(s[k], once[k]) for k in ("K", "V", "sk", "sv"))
 
 
-def test_offsets_past_32_bits(gpu):
+@pytest.mark.parametrize("width", [0, 70000])
+def test_offsets_past_32_bits(gpu, width):
     """Blocks whose bytes start behind 2^32."""
     T, D, KVH = 128, 128, 8
     nb = 2 ** 32 // (T * D * KVH) + 40
-    s = make(16, [1, 20], [260, 300], T, D, KVH, F32, 4)
+    s = make(16, [1, 20], [260, 300], T, D, KVH, F32, 4, width=width // T)
     small = {k: v.clone() for k, v in s.items()}
     s = cuda(s)
     ids = torch.randperm(40, generator=torch.Generator().manual_seed(1))[:len(s["sk"])].cuda() + nb - 40
