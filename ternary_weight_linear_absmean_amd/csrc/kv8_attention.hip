@@ -389,8 +389,8 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
     // key positions: below 2^31, and so are they with a few tiles more in 32 bits
     const uint32_t k0 = uncut ? 0 : piece.nth * piece.c << a.step_shift;
     const uint32_t k1 = keys_within(end, uncut ? 0x7FFFFFFFu : k0 + (piece.c << a.step_shift));
-    const int64_t slot = piece.slot + (int64_t)piece.nth;         // of what is cut
-    if (!uncut && slot >= a.slots) return;
+    const uint32_t slot = (uint32_t)piece.slot + piece.nth;       // of what is cut
+    if (!uncut && slot >= (uint32_t)a.slots) return;              // starts that overlap
 
     // this lane's row (rows past the last repeat it; they are not written)
     const uint32_t r = r0 + min(low, rows - 1);
@@ -590,9 +590,9 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
             const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
             store4<BF16>(a.out, row_j * D + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
         } else {
-            *reinterpret_cast<float4 *>(a.cut + (slot * kRows + rr) * D + d) = y;
+            *reinterpret_cast<float4 *>(a.cut + ((int64_t)slot * kRows + rr) * D + d) = y;
             if (d == 0) {
-                float *ml = a.cut + (int64_t)a.slots * kRows * D + (slot * kRows + rr) * 2;
+                float *ml = a.cut + (int64_t)a.slots * kRows * D + ((int64_t)slot * kRows + rr) * 2;
                 ml[0] = mm;
                 ml[1] = ll;
             }

@@ -394,6 +394,35 @@ def test_graph_follows_its_arrays(gpu):
         eager["lengths"] += 1
 
 
+def test_graphs_cut_by_new_lengths(gpu):
+    """Two captured calls on one workspace, decode and mixed, replayed in turn as
+    lengths change at random."""
+    one = cuda(make(18, [1] * 5, [9000, 1, 700, 2500, 64], 64, 128, 2, BF16, 4, width=400))
+    two = cuda(make(19, [1, 200, 3], [5000, 1500, 2300], 32, 64, 3, F32, 4, width=2000))
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    graphs, full = [], [s["lengths"].clone() for s in (one, two)]
+    for s in (one, two):
+        out = torch.zeros_like(s["q"])
+        attend(gpu, s, out=out, ws=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            attend(gpu, s, out=out, ws=ws)
+        graphs.append((g, out))
+    r = torch.Generator().manual_seed(3)
+    for step in range(6):
+        for s, most in zip((one, two), full):
+            share = torch.rand(len(most), generator=r).cuda() ** 3 if step else 1.0
+            s["lengths"].copy_((most * share).int())
+        for g, _ in graphs:
+            g.replay()
+        wants = [attend(gpu, s) for s in (one, two)]
+        torch.cuda.synchronize()
+        for s, want, (_, out) in zip((one, two), wants, graphs):
+            assert torch.equal(out, want)
+            check_attention({k: v.cpu() for k, v in s.items()}, out)
+
+
 def test_two_streams(gpu):
     """Calls on streams of their own, outputs and workspaces allocated by the calls."""
     jobs = [cuda(make(20 + i, [1, 1], [3000 + i, 2500], 64, 128, 2, F32, 4)) for i in range(2)]
