@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kStreamThreads, 4) void gemv_w4_stream_kernel(ProdA
         *reinterpret_cast<float4 *>(d + 64) = make_float4(x[4], x[5], x[6], x[7]);
     }
     __syncthreads();
-    const int tiles = (a.N + 4 * R - 1) / (4 * R);
+    const int tiles = (int)(((uint32_t)a.N + 4 * R - 1) / (4 * R));
     const int step = gridDim.x * (kStreamThreads / 64);
     int tile = blockIdx.x * (kStreamThreads / 64) + wave;
     uint4 w[R];
@@ -573,14 +573,14 @@ int waves_for(int parts, int most) {
 
 template <bool BF16, int M, int R>
 void few(const ProdArgs &a, int group, hipStream_t s) {
-    const unsigned grid = (unsigned)((a.N + 4 * R - 1) / (4 * R));
+    const unsigned grid = ((unsigned)a.N + 4 * R - 1) / (4 * R);
     const int waves = waves_for((a.K + kSlice - 1) / kSlice, kMaxWaves);
     hipLaunchKernelGGL((gemv_w4_few_kernel<BF16, M, R>), dim3(grid), dim3(64 * waves), 0, s, a,
                        group == 32 ? 0 : group == 64 ? 1 : 2);
 }
 template <bool BF16, int M, int R>
 void stream(const ProdArgs &a, int group, hipStream_t s) {
-    const int tiles = (a.N + 4 * R - 1) / (4 * R), per = kStreamThreads / 64;
+    const int tiles = (int)(((unsigned)a.N + 4 * R - 1) / (4 * R)), per = kStreamThreads / 64;
     const int groups = (tiles + per - 1) / per;
     hipLaunchKernelGGL((gemv_w4_stream_kernel<BF16, M, R>),
                        dim3(groups < kStreamGroups ? groups : kStreamGroups), dim3(kStreamThreads),
@@ -589,7 +589,7 @@ void stream(const ProdArgs &a, int group, hipStream_t s) {
 template <bool BF16, int GROUP, int R, bool WHOLE, int WAVES>
 void many(const ProdArgs &a, hipStream_t s) {
     static_assert(R * 1024 <= wave_lds<BF16>(), "the final sums fit X's place");
-    const unsigned grid = (unsigned)((a.N + 16 * R - 1) / (16 * R));
+    const unsigned grid = ((unsigned)a.N + 16 * R - 1) / (16 * R);
     const int waves = waves_for((a.K + kChunk - 1) / kChunk, WAVES);
     hipLaunchKernelGGL((gemv_w4_mfma_kernel<BF16, GROUP, R, WHOLE, WAVES>), dim3(grid), dim3(64 * waves),
                        waves * wave_lds<BF16>(), s, a);
