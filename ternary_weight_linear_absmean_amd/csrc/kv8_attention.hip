@@ -41,6 +41,7 @@ constexpr int kFewRows = 32;                // rows of a sequence above which th
 constexpr int kFewTiles = kFewRows / kRows;
 constexpr int kGroups = 512;               // workgroups of 256 that run at once: two to a CU
 constexpr int kStepShift = 8;               // log2 of the keys that a workgroup's waves take in a step
+constexpr int kMaxParts = kGroups;
 constexpr int kManyWork = 2048;             // see Plan
 constexpr int kLongSteps = 32;              // see Plan
 constexpr int kLineSeqs = 256;              // sequences that a wave lines up, four to a lane
@@ -946,19 +947,121 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_mixed_kernel(Args a) {
     }
 }
 
-// Joins the parts of the rows whose keys were read in more than one: one
-// workgroup per (row, head).  The parts' weights 2^(m_s - m) go to LDS first;
-// then D / 4 threads read a part, 16 bytes each, so that the workgroup has 4
-// THREADS / D parts in flight: 1024 threads for up to kJoinRows rows of what may
-// be more than kJoinParts parts, or else 256 (128 parts of 20 rows: 11.4 us
-// with 256 threads, 4.7 with 1024; 4 parts of 1280 rows: 4.9 and 10.3; the
-// whole call with 4 parts of 20 rows 8.6 and 9.2).
+// Joins the parts of the rows whose keys were read in more than one, (m, l) and
+// line of each: sum_s 2^(m_s - m) y_s over the same sum of l_s.
 //
 // Rows of sequences that the few-rows kernel takes (FEW): row r of a call of
 // which it takes all, or else row r % (kFewRows KVH) of sequence r / (kFewRows
 // KVH), of which it has kFewRows rows a head at most.
-constexpr int kMaxParts = kGroups;
-constexpr int kJoinRows = 512, kJoinParts = 16;
+struct Parts {
+    int64_t row;
+    int n;                    // <= kMaxParts
+    const float4 *lines;      // of part 0; `pitch` rows on for the next
+    const float2 *ml;
+    int64_t pitch;
+};
+template <int D, bool FEW>
+__device__ __forceinline__ bool find_parts(const Args &a, int64_t row, Parts &p) {
+    const Kv8Seqs &sq = a.seqs;
+    int b, t;
+    if (FEW && a.mixed) {
+        const int each = kFewRows * a.c.KVH;
+        b = (int)(row / each);
+        const int r = (int)(row - (int64_t)b * each), h = r / kFewRows;
+        t = q_at(sq, b) + r % kFewRows / a.G;
+        row = (int64_t)t * a.QH + h * a.G + r % kFewRows % a.G;
+    } else {
+        t = (int)(row / a.QH);
+        b = find_seq(sq.B, t, [&](int i) { return (int64_t)q_at(sq, i); });
+    }
+    const int q0 = q_at(sq, b), q1 = q_at(sq, b + 1);
+    if (t < q0 || t >= q1) return false;
+    const int64_t rows = (int64_t)(q1 - q0) * a.G;
+    p.row = row;
+    if (FEW) {
+        if (rows > a.max_rows) return false;
+        const int2 info = cut_info(a, D)[row];
+        p.n = info.y;
+        if (p.n < 2 || p.n > kMaxParts || info.x < 0 || info.x / kRows > a.slots - p.n)
+            return false;                                       // written directly
+        p.pitch = kRows;
+        p.lines = reinterpret_cast<const float4 *>(a.cut) + (int64_t)info.x * (D / 4);
+        p.ml = reinterpret_cast<const float2 *>(a.cut + (int64_t)a.slots * kRows * D) + info.x;
+    } else {
+        if (rows <= a.min_rows) return false;
+        const int64_t keys = min((int64_t)sq.lengths[b] - (q1 - t) + 1, key_capacity(a));
+        const int64_t chunk = keys_of_part(a, sq.lengths[b]);
+        if (keys <= chunk) return false;                        // written directly
+        p.n = (int)((keys + chunk - 1) / chunk);                // <= S
+        p.pitch = (int64_t)sq.n_tok * a.QH;
+        p.lines = reinterpret_cast<const float4 *>(a.part) + row * (D / 4);
+        p.ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.S * p.pitch * D) + row;
+    }
+    return true;
+}
+
+// Up to kWaveParts parts: a wave to a row, four rows to a workgroup, no barrier.
+// The whole call with 4 parts of 20 rows 8.1 us (8.6 with a workgroup to a row),
+// with 16 parts 8.4 (8.9); 64 ragged sequences, 1280 rows, 42.3 (42.9).
+constexpr int kWaveParts = 16;
+template <bool BF16, int D, bool FEW>
+__global__ __launch_bounds__(kThreads) void kv8_join_wave_kernel(Args a, int64_t rows) {
+    constexpr int V = D / 64;                                   // values a lane
+    const int lane = threadIdx.x & 63;
+    const int64_t r = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Parts p;
+    if (r >= rows || !find_parts<D, FEW>(a, r, p) || p.n > kWaveParts) return;
+    const float *src = reinterpret_cast<const float *>(p.lines) + V * lane;
+    // all loads in flight together, at clamped places
+    constexpr int kFirst = kWaveParts / 4;
+    float x[kWaveParts][V], y[V];
+    auto load = [&](int s0, int s1) {
+#pragma unroll
+        for (int s = s0; s < s1; ++s)
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[s][e] = src[min(s, p.n - 1) * p.pitch * D + e];
+    };
+    load(0, kFirst);
+    if (p.n > kFirst) load(kFirst, kWaveParts);
+    const float2 v = p.ml[min(lane, p.n - 1) * p.pitch];
+    const float m = group_max(lane < p.n ? v.x : -INFINITY, 16);          // -inf in lanes 16 on
+    const float f = lane < p.n ? exp2_fast(v.x - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+    float l = lane < p.n ? v.y * f : 0.0f;
+    l += dpp_f32<kDppXor1>(l);
+    l += dpp_f32<kDppXor2>(l);
+    l += dpp_f32<kDppHalfMirror>(l);
+    l += dpp_f32<kDppMirror>(l);
+    l = lane_value(l, 0);
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = 0.0f;
+    auto add = [&](int s0, int s1) {
+#pragma unroll
+        for (int s = s0; s < s1; ++s)
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = __builtin_fmaf(x[s][e], lane_value(f, s), y[e]);   // f = 0 from n on
+    };
+    add(0, kFirst);
+    if (p.n > kFirst) add(kFirst, kWaveParts);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int64_t at = p.row * D + V * lane;
+    if (BF16) {
+        uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+        if (V == 2)
+            *reinterpret_cast<uint32_t *>(o) = bf16_round(y[0] * inv) | bf16_round(y[V - 1] * inv) << 16;
+        else
+            *o = (uint16_t)bf16_round(y[0] * inv);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) static_cast<float *>(a.out)[at + e] = y[e] * inv;
+    }
+}
+
+// More: a workgroup to a row.  The parts' weights 2^(m_s - m) go to LDS first;
+// then D / 4 threads read a part, 16 bytes each, so that the workgroup has 4
+// THREADS / D parts in flight: 1024 threads for up to kJoinRows rows, or else
+// 256 (128 parts of 20 rows: 11.4 us with 256 threads, 4.7 with 1024; 4 parts of
+// 1280 rows 4.9 and 10.3).
+constexpr int kJoinRows = 512;
 template <bool BF16, int D, int THREADS, bool FEW>
 __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
     constexpr int kWide = D / 4, kLines = THREADS / kWide, kJoinWaves = THREADS / 64;
@@ -966,49 +1069,12 @@ __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
     __shared__ float red[2][kJoinWaves];
     __shared__ float4 sum[kJoinWaves][kWide];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Kv8Seqs &sq = a.seqs;
-    int64_t row = blockIdx.x;
-    int parts;
-    // lines and (m, l) of part s, `pitch` rows apart
-    const float4 *lines;
-    const float2 *ml;
-    int64_t pitch;
-    if (FEW) {
-        int b, t;
-        if (a.mixed) {
-            const int each = kFewRows * a.c.KVH;
-            b = (int)(row / each);
-            const int r = (int)(row - (int64_t)b * each), h = r / kFewRows;
-            t = q_at(sq, b) + r % kFewRows / a.G;
-            row = (int64_t)t * a.QH + h * a.G + r % kFewRows % a.G;
-        } else {
-            t = (int)(row / a.QH);
-            b = find_seq(sq.B, t, [&](int i) { return (int64_t)q_at(sq, i); });
-        }
-        const int q0 = q_at(sq, b), q1 = q_at(sq, b + 1);
-        if (t < q0 || t >= q1 || (int64_t)(q1 - q0) * a.G > a.max_rows) return;
-        const int2 info = cut_info(a, D)[row];
-        parts = info.y;
-        if (parts < 2 || parts > kMaxParts || info.x < 0 || info.x / kRows > a.slots - parts)
-            return;                                             // written directly
-        const int64_t first_row = info.x;
-        pitch = kRows;
-        lines = reinterpret_cast<const float4 *>(a.cut) + first_row * kWide;
-        ml = reinterpret_cast<const float2 *>(a.cut + (int64_t)a.slots * kRows * D) + first_row;
-    } else {
-        const int t = (int)(row / a.QH);
-        const int b = find_seq(sq.B, t, [&](int i) { return (int64_t)q_at(sq, i); });
-        const int q0 = q_at(sq, b), q1 = q_at(sq, b + 1);
-        if (t < q0 || t >= q1 || (int64_t)(q1 - q0) * a.G <= a.min_rows) return;
-        const int64_t keys = min((int64_t)sq.lengths[b] - (q1 - t) + 1, key_capacity(a));
-        const int64_t chunk = keys_of_part(a, sq.lengths[b]);
-        if (keys <= chunk) return;                              // written directly
-        parts = (int)((keys + chunk - 1) / chunk);              // <= S <= kMaxParts
-        const int64_t all = (int64_t)sq.n_tok * a.QH;
-        pitch = all;
-        lines = reinterpret_cast<const float4 *>(a.part) + row * kWide;
-        ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.S * all * D) + row;
-    }
+    Parts p;
+    if (!find_parts<D, FEW>(a, blockIdx.x, p)) return;
+    const int parts = p.n;
+    const int64_t row = p.row, pitch = p.pitch;
+    const float4 *lines = p.lines;
+    const float2 *ml = p.ml;
     // the first lines are under way while the weights are formed
     const int d = threadIdx.x % kWide, line = threadIdx.x / kWide;
     const float4 first = lines[min(line, parts - 1) * pitch * kWide + d];
@@ -1072,7 +1138,10 @@ __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
 
 template <bool BF16, int D, bool FEW>
 void join(const Args &a, int64_t rows, int64_t parts, hipStream_t s) {
-    if (rows <= kJoinRows && parts > kJoinParts)
+    if (parts <= kWaveParts)
+        hipLaunchKernelGGL((kv8_join_wave_kernel<BF16, D, FEW>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
+                           dim3(kThreads), 0, s, a, rows);
+    else if (rows <= kJoinRows)
         hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 1024, FEW>), dim3((unsigned)rows), dim3(1024), 0, s, a);
     else
         hipLaunchKernelGGL((kv8_join_kernel<BF16, D, 256, FEW>), dim3((unsigned)rows), dim3(256), 0, s, a);
