@@ -179,10 +179,12 @@ __device__ __forceinline__ int64_t key_capacity(const Args &a) {
 // us each when they wait for memory), as the join is a launch and 2 to 3 us, nor
 // where U >= most / 2 and the longest has less than 2.5 c: then the units fill
 // the GPU evenly enough.  64 ragged sequences of up to 4096 keys, 5 heads: 48.1
-// us uncut, 42.8 cut; 96 of them 63 and 67, 128 73 and 80.  With max_blocks in
-// the lengths' place 2000 keys with room for 32768 took 12.3 us and not 9.1, 16
-// x 4000 with room for 131072 37 and not 22, 63 x 500 beside 20000 150 and not
-// 20.
+// us uncut, 42.3 cut; 96 of them 63 and 67, 128 73 and 80.  Units of about one
+// length get as many pieces as keep all within `most`, since a few more would
+// run alone at the end (32 sequences of 4096 keys: 3 pieces of 6 steps 39.4 us,
+// 4 of 5 44.0; ragged, 25).  With max_blocks in the lengths' place 2000 keys with
+// room for 32768 took 12.3 us and not 9.1, 16 x 4000 with room for 131072 37 and
+// not 22, 63 x 500 beside 20000 150 and not 20.
 //
 // With more than kLineSeqs sequences nothing is cut and a unit's place follows
 // from q_start alone: tile slots of sequence b from floor(q_start[b] G / 16) + b
@@ -245,7 +247,12 @@ __device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) {
 
 __device__ __forceinline__ uint32_t steps_of_piece(const Args &a, uint32_t units, uint32_t steps, uint32_t top) {
     const uint32_t most = (uint32_t)a.most;
-    const uint32_t c = max((steps + most - 1) / most, 1u);
+    uint32_t c = max((steps + most - 1) / most, 1u);
+    // W / c <= most either way
+    if (units > 0 && top * units - steps <= steps / 4) {
+        const uint32_t each = max(most / units, 1u);
+        c = max((top + each - 1) / each, 1u);
+    }
     return top < c + 3 || (2 * units >= most && 2 * top < 5 * c) ? top : c;
 }
 

@@ -172,6 +172,8 @@ LINES = [
     ([i % 3 for i in range(256)], [2 + 37 * i % 500 for i in range(256)], 128, 1, 4),
     ([1] * 257, [1 + 37 * i % 500 for i in range(257)], 128, 1, 4),
     ([9] * 30, [9 + 37 * i % 500 for i in range(29)] + [6000], 64, 2, 3),
+    ([1] * 32, [1500] * 30 + [1400, 1500], 64, 5, 4),
+    ([1] * 7, [4000] * 7, 64, 3, 4),
     # with sequences of many rows
     ([1, 100, 2, 1], [5000, 300, 700, 2600], 64, 2, 4),
     ([0, 400, 1, 1], [0, 1000, 3000, 1], 64, 1, 8),
