@@ -532,23 +532,24 @@ _DTYPES = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
 
 
 def _at(t, dtype, dev, shape, name):
-    """Address of tensor t, which must be contiguous, of dtype, on dev, of shape."""
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == dev and t.shape == shape \
+    """Address of tensor t, which must be contiguous, of dtype, on GPU dev (its
+    number: comparing devices takes twice the time), of shape."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape \
             and t.is_contiguous():
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(t, dim, name):
-    """Device, bl_dtype, address and shape of a contiguous fp32 / bf16 tensor
+    """GPU, bl_dtype, address and shape of a contiguous fp32 / bf16 tensor
     with dim dimensions on the GPU."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
@@ -560,7 +561,7 @@ def _rows(t, dim, name):
         raise TypeError(f"{name} must be float32 or bfloat16")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.device, dt, t.data_ptr(), shape
+    return t.get_device(), dt, t.data_ptr(), shape
 
 
 class _Nowhere:
@@ -581,10 +582,10 @@ def _where(dev, stream):
     """The HIP stream to run on, and the context to allocate and launch in."""
     if stream is None:
         # the handle alone: a Stream object costs 1.8 us, as much as a small launch
-        return (torch._C._cuda_getCurrentRawStream(dev.index),
-                _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev))
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return (torch._C._cuda_getCurrentRawStream(dev),
+                _HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev))
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
@@ -677,7 +678,7 @@ def bitlinear_decode_stack_kv(layers, caches, x, q_start, lengths, table, H, KV,
     updated in place; scale defaults to D ** -0.5."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError("x must be a CUDA (HIP) tensor")
-    dev, n = x.device, len(layers)
+    dev, n = x.get_device(), len(layers)
     if len(caches) != n:
         raise ValueError(f"{n} layers and {len(caches)} caches")
     xp = _at(x, torch.float32, dev, (H,), "x")
@@ -733,14 +734,14 @@ def quant_weight_absmax_i4(W, group=128, Wq4=None, s=None, stream=None):
 
 
 def _w4(Wq4, s):
-    """(device, N, K, group, addresses) of 4-bit weights."""
+    """(GPU, N, K, group, addresses) of 4-bit weights."""
     if not isinstance(Wq4, torch.Tensor) or not Wq4.is_cuda:
         raise TypeError("Wq4 must be a CUDA (HIP) tensor")
     packed = Wq4.shape
     if len(packed) != 2 or not isinstance(s, torch.Tensor) or s.dim() != 2:
         raise ValueError("Wq4 must be [N, K/2] and s [N, K/group]")
     N, K2 = packed
-    groups, dev = s.shape[1], Wq4.device
+    groups, dev = s.shape[1], Wq4.get_device()
     group = 2 * K2 // groups if groups else 128
     if 2 * K2 != group * groups or group not in (32, 64, 128):
         raise ValueError(f"Wq4 {list(packed)} and s {list(s.shape)} do not make groups of 32, 64 or "
@@ -772,7 +773,7 @@ def bitlinear_gemv_w4(X, Wq4, s, Y=None, stream=None):
     dev, dt, xp, (M, cols) = _rows(X, 2, "X")
     wdev, N, K, group, wp, sp = _w4(Wq4, s)
     if wdev != dev:
-        raise ValueError(f"Wq4 is on {wdev}, not on {dev}")
+        raise ValueError(f"Wq4 is on cuda:{wdev}, not on cuda:{dev}")
     if cols != K:
         raise ValueError(f"X must be [M, {K}], got {[M, cols]}")
     if Y is not None:
