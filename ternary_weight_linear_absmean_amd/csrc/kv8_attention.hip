@@ -42,7 +42,7 @@ constexpr int kFewTiles = kFewRows / kRows;
 constexpr int kGroups = 512;               // workgroups of 256 that run at once: two to a CU
 constexpr int kStepShift = 8;               // log2 of the keys that a workgroup's waves take in a step
 constexpr int kMaxParts = kGroups;
-constexpr int kManyWork = 2048;             // see Plan
+constexpr int kManyWork = 4500;             // see Plan
 constexpr int kLongSteps = 32;              // see Plan
 constexpr int kLineSeqs = 256;              // sequences that a wave lines up, four to a lane
 
@@ -1155,16 +1155,24 @@ void join(const Args &a, int64_t rows, int64_t parts, hipStream_t s) {
 }
 
 // What a call launches, from its sizes alone.  Where the sequences bring many
-// rows on average and there is much to do (W of the few-rows kernel, with
-// all lengths at their limit, above kManyWork), those that do go to the kernel for many rows; the
-// other takes the rest, or else all.  A lone workgroup of many rows takes 2 us a
-// tile of 64 keys, so with little work the few-rows kernel, cut to fill the GPU,
-// is done first though it reads and converts a code 8 times as often.  In us,
-// few and many rows, 5 heads of 4, bf16: 128 rows on 500 keys 7.5 and 18.9, on
-// 4000 (W = 640) 13 and 19; 256 rows on 4000 (1280) 23.5 and 22.3; 1024 on 1000
-// (4 sequences, 1280) 22.9 and 29.5; 512 on 4000 (2560) 31.7 and 27.7; 256 on
-// 32000 (10000) 116 and 59; and 64 sequences of 32 rows on 4000 110 and 140, of
-// 64 rows 191 and 142.
+// rows on average and there is much to do (16-row units times their steps with
+// all lengths at their limit, and 2 for the start and end of each, above
+// kManyWork), those that do go to the kernel for many rows; the other takes the
+// rest, or else all.  A lone workgroup of many rows takes 2 us a tile of 64 keys,
+// so with little work the few-rows kernel, cut to fill the GPU, is done first
+// though it reads and converts a code 8 times as often.  In us, few and many
+// rows, 5 heads of 4, bf16:
+//   work   120  128 rows on 500 keys      7.5  18.9
+//          720  128 on 4000                13    19
+//         1920  4 x 256 on 1000          22.9  29.5
+//         2880  512 on 4000 / 8 x 64     31.7  27.7 / 35.4 42.5
+//         3840  64 x 48 on 500           25.6    28
+//         4320  8 x 96 on 4000             37    46
+//         5080  128 on 32000             41.2  41.7
+//         5440  4 x 128 on 8000          58.6  45.6
+//         7680  64 x 96 on 500           44.5  29.8
+//        23000  64 x 64 on 4000           191   142
+// and with 32 rows a sequence, 64 on 4000 (work 11500) 110 and 140.
 //
 // Many rows: as many parts of the keys as keep a workgroup on every CU, if that
 // can save three steps; how many a sequence has, and of what keys, its length
@@ -1188,7 +1196,7 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
     Plan p = {};
     p.steps = steps;
     p.S = 1;
-    p.many = n_tok * G > kFewRows * B && (double)n_tok * QH / kRows * steps > kManyWork;
+    p.many = n_tok * G > kFewRows * B && (double)n_tok * QH / kRows * (steps + 2) > kManyWork;
     p.few = !p.many || B > 1;
     if (p.many) {
         const double tiles = n_tok * (double)G / kManyRows;

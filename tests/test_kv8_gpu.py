@@ -207,7 +207,7 @@ MANY = [
     ([129, 7], [1500, 7], 128, 128, 1, 8, 70000),
     ([33], [600], 64, 64, 3, 4, 70000),
     ([70, 4, 50], [2000, 1500, 300], 32, 64, 2, 4, 30000),
-    ([9, 300], [4000, 2500], 64, 128, 2, 4, 0),
+    ([9, 300], [4000, 2500], 64, 128, 2, 4, 9000),
 ]
 
 
@@ -244,7 +244,7 @@ def test_what_is_masked_never_shows(gpu, n, lens, width):
     assert torch.equal(want, got)
 
 
-@pytest.mark.parametrize("width", [0, 70000])
+@pytest.mark.parametrize("width", [0, 120000])
 @pytest.mark.parametrize("n", [[1, 1, 1], [40, 2, 3], [60, 2, 3]])
 def test_blocks_out_of_range_hold_nothing(gpu, n, width):
     lens = [200, 40, 90]
@@ -259,7 +259,7 @@ def test_blocks_out_of_range_hold_nothing(gpu, n, width):
     assert (out[-n[2]:] == 0).all()
 
 
-@pytest.mark.parametrize("width", [0, 70000])
+@pytest.mark.parametrize("width", [0, 120000])
 @pytest.mark.parametrize("n", [[3, 1, 2], [50, 2, 30]])
 def test_odd_lengths_and_starts(gpu, n, width):
     """Lengths below the new tokens' number, zero, negative, beyond the table;
