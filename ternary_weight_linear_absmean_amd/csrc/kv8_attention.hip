@@ -1211,10 +1211,11 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
         int64_t tiles = n_tok * G / kRows + seqs;
         if (p.many && tiles > seqs * kFewTiles) tiles = seqs * kFewTiles;
         const int64_t units = tiles * KVH;
-        // longer steps where their number would pass 32 bits
+        // longer steps where their number would pass 32 bits (units of kLineSeqs
+        // sequences do not: n_tok QH / 16 + 256 KVH < 2^28)
         p.step_shift = kStepShift;
         auto line = [&] { return units * (((steps - 1) >> (p.step_shift - kStepShift)) + 1); };
-        while (line() >= (int64_t)1 << 30) ++p.step_shift;
+        while (B <= kLineSeqs && line() >= (int64_t)1 << 30) ++p.step_shift;
         p.cuts = steps > 3 && B <= kLineSeqs &&
                  ((3 * KVH * seqs < 2 * p.most && (!p.many || p.S > 1)) || steps >= kLongSteps);
         p.groups = units;

@@ -75,6 +75,13 @@ def test_attention_refusals(lib):
     f = lib.bitlinear_kv8_attention_ws_bytes
     assert f(0, 8, 2, 4, 2, 64, 128) == 0 and f(3, 7, 2, 4, 2, 64, 128) == 0
     assert f(3, 8, 2, 4, 2, 63, 128) == 0 and f(3, 8, 2, -4, 2, 64, 128) == 0
+    # the largest sizes: answered at once, and a workspace that a card can hold where a call may
+    big = 2 ** 31 - 1
+    for n, QH, B, nb, KVH, T in ((20000, 65535, 20000, 1000, 65535, 64), (32768, 65535, 2 ** 24 - 1, big // 16, 65535, 16),
+                                 (big, 1, 256, big // 128, 1, 128), (32768, 65535, 256, big // 64, 65535, 64),
+                                 (256, 65535, 256, big // 64, 65535, 64), (1, 65535, 1, big // 64, 1, 64),
+                                 (1, 1, 2 ** 24 - 1, 0, 1, 64), (big, 1, 1, big // 64, 1, 64)):
+        assert f(n, QH, B, nb, KVH, T, 128) < 2 ** 50, (n, QH, B)
 
 
 def test_w4_refusals(lib):
