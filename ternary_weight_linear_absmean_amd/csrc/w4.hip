@@ -337,8 +337,8 @@ __global__ __launch_bounds__(kStreamThreads, 4) void gemv_w4_stream_kernel(ProdA
 // into the operand's order.
 //
 // bf16 tokens go into bf16 products as they are, with the codes + 8 (exact in
-// bf16); one more product with ones sums X, and 8 times that is taken off a
-// group's sum.  The numbers grow by a factor of about 3 for it, against the
+// bf16); one more product, of X with -8, is where a group's sum begins.  The
+// numbers grow by a factor of about 3 for it, against the
 // 2^-24 of the fp32 sums.  fp32 tokens are scaled by a power of two per token
 // and chunk, the largest to [2^13, 2^14), and split in two fp16 halves of 11
 // bits, each with its matrix instructions.
@@ -504,15 +504,15 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_w4_mfma_kernel(ProdArgs a) {
 #pragma unroll
             for (int r = 0; r < R; ++r) w[r] = make_uint4(0, 0, 0, 0);
         }
-        float4v x_sum[NG];                      // of each group's X, in every column
+        float4v x_sum[NG];                      // -8 times the sum of each group's X, in every column
         if (BF16) {
-            const bf8v ones = __builtin_bit_cast(bf8v, make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u));
+            const bf8v minus8 = __builtin_bit_cast(bf8v, make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u));
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 x_sum[g] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = g * (4 / NG); j < (g + 1) * (4 / NG); ++j)
-                    x_sum[g] = mfma_bf16(__builtin_bit_cast(bf8v, xr[0][j]), ones, x_sum[g]);
+                    x_sum[g] = mfma_bf16(__builtin_bit_cast(bf8v, xr[0][j]), minus8, x_sum[g]);
             }
         }
 #pragma unroll
@@ -528,7 +528,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_w4_mfma_kernel(ProdArgs a) {
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                float4v acc = {0.f, 0.f, 0.f, 0.f};
+                float4v acc = BF16 ? x_sum[g] : float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = g * (4 / NG); j < (g + 1) * (4 / NG); ++j) {
                     if (BF16) {
@@ -541,8 +541,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_w4_mfma_kernel(ProdArgs a) {
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    tot[r][e] = __builtin_fmaf(BF16 ? __builtin_fmaf(-8.0f, x_sum[g][e], acc[e]) : acc[e] * f[e],
-                                               sc[r][g], tot[r][e]);
+                    tot[r][e] = __builtin_fmaf(BF16 ? acc[e] : acc[e] * f[e], sc[r][g], tot[r][e]);
             }
         }
     }
