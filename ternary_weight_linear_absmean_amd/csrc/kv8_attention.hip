@@ -615,8 +615,8 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 // the other buffer and the codes of t + 2 are on their way.
 //
 // Bound by vector instructions, about 380 of a wave and tile beside its 32
-// matrix instructions: 40 of them exponentials, logarithms and reciprocals at a
-// quarter of the rate, 87 the conversion.  2 x 2048 ragged rows on 4096 keys, 5
+// matrix instructions: 40 of them exponentials, logarithms and reciprocals at half
+// the rate, 87 the conversion.  2 x 2048 ragged rows on 4096 keys, 5
 // heads of 4, bf16, 92 GFLOP: 131 us, 700 TFLOP/s (a large bf16 matrix product
 // 1145); fp32, with two matrix instructions for one, 199 us.
 //

@@ -336,12 +336,18 @@ __global__ __launch_bounds__(kStreamThreads, 4) void gemv_w4_stream_kernel(ProdA
 // lines (16 lanes a token), made fp16 and passed through LDS of the wave's own
 // into the operand's order.
 //
-// bf16 tokens go into bf16 products as they are, with the codes + 8 (exact in
-// bf16); one more product, of X with -8, is where a group's sum begins.  The
-// numbers grow by a factor of about 3 for it, against the
-// 2^-24 of the fp32 sums.  fp32 tokens are scaled by a power of two per token
-// and chunk, the largest to [2^13, 2^14), and split in two fp16 halves of 11
-// bits, each with its matrix instructions.
+// bf16 tokens go into bf16 products as they are, in the codes' order, with the
+// codes + 24: exact, and one instruction for two codes beside a shift (codes + 8
+// by way of fp32, two conversions and a packing for two codes: 9.8 us where this
+// takes 7.1, 16 x 6912 in groups of 32).  A product of the same X with -24 goes
+// before each of them, so that the sums stay small; for the first of a group it is
+// the same for all rows of W.  The numbers grow by a factor of about 6 for it,
+// against the 2^-24 of the fp32 sums (all of a group's -24 first: by 12, and 2%
+// faster with groups of 128).
+//
+// fp32 tokens are scaled by a power of two per token and chunk, the largest to
+// [2^13, 2^14), and split in two fp16 halves of 11 bits, each with its matrix
+// instructions.
 //
 // A matrix instruction sums over the four quads, and all that it sums has to
 // lie in one scale group.  With groups of 128 any dword of each quad's 16 bytes
@@ -351,7 +357,7 @@ __global__ __launch_bounds__(kStreamThreads, 4) void gemv_w4_stream_kernel(ProdA
 // then.  The sum of a group leaves the matrix accumulators once, times X's
 // factor and the scale, into fp32 totals.
 //
-// 16 x 6912 -> 2560 bf16: 9.9 us, 11.4 MB; 160 workgroups of 16 rows, each with
+// 16 x 6912 -> 2560 bf16: 7.1 us, 11.4 MB; 160 workgroups of 16 rows, each with
 // all of X (221 KB) through its registers: latency and vector instructions in
 // equal parts.  More workgroups would read X oftener or need a join.
 constexpr int kChunk = 128;
@@ -386,24 +392,16 @@ __device__ __forceinline__ void wave_fence() {
 // LDS of a wave: [part of X][instruction, quad][16 tokens + 1 of padding] units
 // of 16 bytes, then 16 factors; the final sums take its place.
 typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
-typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
-typedef float float2v __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ float4v mfma_bf16(bf8v a, bf8v b, float4v c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-// The 8 codes of a dword, + 8, as bf16 in their order.
+// The 8 codes of a dword, + 24, as bf16 in the order 0, 4, 1, 5, 2, 6, 3, 7: with
+// its sign bit flipped a code is code + 8, and below the bits of 16 that reads as
+// 16 + (code + 8).
 __device__ __forceinline__ bf8v codes_to_bf16(uint32_t w) {
-    const uint32_t x = w ^ 0x88888888u;
-    uint32_t even = x & 0x0F0F0F0Fu, odd = (x >> 4) & 0x0F0F0F0Fu, o[4];
-    // opaque: as bytes, which convert in one instruction each, and not as bit
-    // fields of x, which take two
-    asm("" : "+v"(even), "+v"(odd));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2v f = {(float)((even >> (8 * i)) & 255u), (float)((odd >> (8 * i)) & 255u)};
-        o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf2v));
-    }
-    return __builtin_bit_cast(bf8v, make_uint4(o[0], o[1], o[2], o[3]));
+    const uint32_t mask = 0x00780078u, base = 0x41C041C0u;       // 16, and the sign bit to flip
+    return __builtin_bit_cast(bf8v, make_uint4(((w << 3) & mask) ^ base, ((w >> 1) & mask) ^ base,
+                                               ((w >> 5) & mask) ^ base, ((w >> 9) & mask) ^ base));
 }
 
 template <bool BF16>
@@ -463,7 +461,9 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_w4_mfma_kernel(ProdArgs a) {
                                                         (int64_t)min(4 * i + quad, a.M - 1) * a.K + c * kChunk + at);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (4 * i < a.M) dst[4 * i] = x[i];        // the other rows of the operand are not used
+                if (4 * i < a.M)                           // the other rows of the operand are not used
+                    dst[4 * i] = make_uint4(perm(x[i].z, x[i].x, 0x05040100u), perm(x[i].z, x[i].x, 0x07060302u),
+                                            perm(x[i].w, x[i].y, 0x05040100u), perm(x[i].w, x[i].y, 0x07060302u));
         } else {
             float x[4][8];
 #pragma unroll
@@ -504,15 +504,13 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_w4_mfma_kernel(ProdArgs a) {
 #pragma unroll
             for (int r = 0; r < R; ++r) w[r] = make_uint4(0, 0, 0, 0);
         }
-        float4v x_sum[NG];                      // -8 times the sum of each group's X, in every column
+        float4v x_sum[NG];                      // -24 times the sum of each group's first X, in every column
+        const bf8v minus24 = __builtin_bit_cast(bf8v, make_uint4(0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u));
         if (BF16) {
-            const bf8v minus8 = __builtin_bit_cast(bf8v, make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u));
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 x_sum[g] = float4v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = g * (4 / NG); j < (g + 1) * (4 / NG); ++j)
-                    x_sum[g] = mfma_bf16(__builtin_bit_cast(bf8v, xr[0][j]), minus8, x_sum[g]);
+                x_sum[g] = mfma_bf16(__builtin_bit_cast(bf8v, xr[0][g * (4 / NG)]), minus24, x_sum[g]);
             }
         }
 #pragma unroll
@@ -532,6 +530,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_w4_mfma_kernel(ProdArgs a) {
 #pragma unroll
                 for (int j = g * (4 / NG); j < (g + 1) * (4 / NG); ++j) {
                     if (BF16) {
+                        if (j > g * (4 / NG)) acc = mfma_bf16(__builtin_bit_cast(bf8v, xr[0][j]), minus24, acc);
                         acc = mfma_bf16(__builtin_bit_cast(bf8v, xr[0][j]), codes_to_bf16(d[j]), acc);
                     } else {
                         const half8 b = __builtin_bit_cast(half8, codes_to_f16(d[j]));
