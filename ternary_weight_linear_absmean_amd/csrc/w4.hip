@@ -219,12 +219,16 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_w4_few_kernel(ProdArgs a,
 // for its R loads, the next slice's loads in flight.  128256 x 2560 fp32 tokens,
 // 174 MB: 42.6 us, 4.1 TB/s.
 //
-// From kStreamRows rows on: 49152 x 2560 17.9 us (the other kernel 22.2), 24576 x
-// 2560 13.7 (13.3): there no CU gets enough tiles for its waves to pay for X.
+// X costs the other kernel a reading for every 16 rows, and this one a start, so
+// this one is taken from 32768 rows on, with fp32 tokens from 16384 / M: N x 2560,
+// the other kernel and this one in us, M = 1: 12288 fp32 7.5 8.2, 24576 13.0 10.8,
+// bf16 10.6 11.0, 40000 17.2 15.1; M = 2: 8192 fp32 9.1 8.5, 20000 18.8 13.3, bf16
+// 13.0 13.4.  R = 2 for fewer than 65536 rows, which a wave then has no more than
+// eight tiles of (40000: 15.1, 17.2 with 4), 4 from there on (98304: 34.0, 31.8).
 constexpr int kStreamThreads = 256;
 constexpr int kStreamGroups = 1024;
 constexpr size_t kStreamLds = 64 * 1024;
-constexpr int kStreamRows = 32768;
+constexpr int kStreamRows = 32768, kWideRows = 65536;
 size_t stream_lds(int M, int K) {
     return (size_t)M * ((K + kSlice - 1) / kSlice) * kSlice * sizeof(float);
 }
@@ -610,10 +614,13 @@ void many(const ProdArgs &a, hipStream_t s) {
 
 template <bool BF16, int M>
 void one_or_two(const ProdArgs &a, int group, hipStream_t s) {
-    if (a.N >= kStreamRows && stream_lds(M, a.K) <= kStreamLds)
-        stream<BF16, M, 4>(a, group, s);
-    else
+    const int from = BF16 ? kStreamRows : kStreamRows / (2 * M);
+    if (a.N < from || stream_lds(M, a.K) > kStreamLds)
         few<BF16, M, 4>(a, group, s);
+    else if (a.N < kWideRows)
+        stream<BF16, M, 2>(a, group, s);
+    else
+        stream<BF16, M, 4>(a, group, s);
 }
 
 template <bool BF16>
