@@ -598,10 +598,15 @@ void many(const ProdArgs &a, hipStream_t s) {
 }
 template <bool BF16, int GROUP, bool WHOLE>
 void many(const ProdArgs &a, hipStream_t s) {
-    // the widest workgroups that still give every CU one: 16 x 2560 -> 6912
-    // (432, 216 and 108 of them) takes 13.7, 8.8 and 12.9 us with R = 1, 2 and 4
+    // the widest workgroups that still give every CU one: 16 x 2560 -> 6912 fp32
+    // (432, 216 and 108 of them) takes 13.4, 8.8 and 12.9 us with R = 1, 2 and 4.
+    // bf16 tokens, which cost little to bring into the operand's order, go with
+    // small workgroups as long as wide ones would be fewer than 1.5 to a CU: 16 x
+    // 2560 -> 20000 12.3 us, with R = 4 14.5 (fp32 24.9 and 20.0), 30000 17.5 and
+    // 14.7
     if (a.N <= 16 * kCUs) many<BF16, GROUP, 1, WHOLE, 16>(a, s);
     else if (a.N <= 32 * kCUs) many<BF16, GROUP, 2, WHOLE, 16>(a, s);
+    else if (BF16 && a.N <= 96 * kCUs) many<BF16, GROUP, 1, WHOLE, 8>(a, s);
     else many<BF16, GROUP, 4, WHOLE, 8>(a, s);
 }
 template <bool BF16, int GROUP>

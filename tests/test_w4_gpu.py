@@ -93,7 +93,9 @@ def test_product(gpu, M, N, K, group, dtype):
 @pytest.mark.parametrize("M,N,K,group", [
     (1, 8191, 96, 32), (2, 8192, 96, 32), (2, 8199, 640, 64), (1, 16383, 128, 128), (1, 16384, 160, 32),
     (1, 32767, 64, 64), (1, 32769, 544, 32), (2, 32768, 512, 128), (2, 65535, 96, 32), (1, 65537, 64, 32),
-    (2, 65536, 1056, 32), (1, 9000, 16384, 128), (2, 9000, 8192, 64), (2, 9000, 8320, 64)])
+    (2, 65536, 1056, 32), (1, 9000, 16384, 128), (2, 9000, 8192, 64), (2, 9000, 8320, 64),
+    (3, 4096, 96, 32), (7, 4097, 256, 64), (16, 8192, 128, 128), (5, 8200, 96, 32), (16, 9001, 640, 64),
+    (3, 24576, 64, 64), (9, 24577, 160, 32), (16, 33001, 128, 128)])
 def test_product_at_the_bounds_of_the_forms(gpu, M, N, K, group, dtype):
     test_product(gpu, M, N, K, group, dtype)
 
