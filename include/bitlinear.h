@@ -599,7 +599,7 @@ bl_status dequant_weight_i4(const uint8_t *Wq4, const uint16_t *s, int64_t N, in
  *               aligned.
  * Sums are fp32.  M <= 2 multiplies fp32 x as it is; above, fp32 x is held to
  * 22 bits or more of the largest |x| of 128 consecutive elements, bf16 x
- * exactly.  |x| is to stay below 2^117 (sums of codes come before their scale).
+ * exactly.  |x| is to stay below 2^116 (sums of codes come before their scale).
  * Deterministic for given sizes.  M == 0 or N == 0: no-op; K == 0 gives zeros.
  */
 bl_status bitlinear_gemv_w4(const void *X, bl_dtype dtype, int64_t M, const uint8_t *Wq4,

@@ -48,9 +48,9 @@ def check_product(bl, X, Wq4, s, group, **kw):
     """An fp32 x loses at most 2^-22 of the largest of 128 elements; bf16 loses
     nothing.  A sum of K products and K / group group sums, each of at most K
     additions, adds K 2^-24 of the terms' magnitude and two roundings a group.
-    bf16 products from three tokens on run with the codes + 8 and take 8 sum x
-    off again: terms of up to (|code| + 16) |x| s, in sums of at most 128, so
-    another (128 + 8) 2^-24 of those."""
+    bf16 products from three tokens on run with the codes + 24 and take 24 sum x
+    off again, 32 elements at a time: 64 additions of terms that come to (|code|
+    + 48) |x| s at most, so another 64 2^-24 of those."""
     Y = bl.bitlinear_gemv_w4(X.cuda(), Wq4.cuda(), s.cuda(), **kw)
     W = ref.unpack_w4(Wq4.numpy()) * np.repeat(n64(s), group, 1)
     x, K = n64(X), X.shape[1]
@@ -59,7 +59,7 @@ def check_product(bl, X, Wq4, s, group, **kw):
     top = np.repeat(top, 128, 1)[:, :K]
     tol = top @ np.abs(W).T * 2.0 ** -22 + np.abs(x) @ np.abs(W).T * (K + 8) * 2.0 ** -24
     if X.dtype == BF16 and len(x) > 2:
-        tol += np.abs(x) @ (np.abs(W) + 16 * np.abs(np.repeat(n64(s), group, 1))).T * 136 * 2.0 ** -24
+        tol += np.abs(x) @ (np.abs(W) + 48 * np.abs(np.repeat(n64(s), group, 1))).T * 64 * 2.0 ** -24
     got = n64(Y)
     assert np.isfinite(got).all()
     worst = np.max(np.abs(got - x @ W.T) - tol, initial=-1.0)
@@ -113,6 +113,20 @@ def test_product_over_the_number_range(gpu, dtype):
     X[4] = 0
     X[4, 130] = -3.0
     check_product(gpu, X.to(dtype), Wq4, s, 64)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M", [1, 2, 3, 16])
+@pytest.mark.parametrize("group", [32, 128])
+def test_product_at_the_largest_tokens(gpu, M, group, dtype):
+    """Just below 2^116, of one sign and of both, with the codes' extremes."""
+    g = torch.Generator().manual_seed(6)
+    Wq4, s = weights(g, 40, 512, group)
+    Wq4[:8], Wq4[8:16], Wq4[16:24] = 0x77, 0x88, 0x87      # 7 7, -8 -8, 7 -8
+    X = torch.full((M, 512), 2.0 ** 116 * (1 - 2.0 ** -8))
+    X[::2] *= torch.randint(0, 2, X[::2].shape, generator=g) * 2 - 1
+    s *= 2.0 ** -6                                          # the result itself stays in range
+    check_product(gpu, X.to(dtype), Wq4, s, group)
 
 
 def test_product_of_the_quantisers_weights(gpu):
