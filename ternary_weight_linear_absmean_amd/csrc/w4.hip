@@ -215,7 +215,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_w4_few_kernel(ProdArgs a,
 }
 
 // One or two tokens and many rows: X in LDS (fp32), every wave for itself.  A
-// wave takes 4 R rows at a time through all of K, one slice's X in registers
+// wave takes 4 R rows at a time through all of K (> 0), one slice's X in registers
 // for its R loads, the next slice's loads in flight.  128256 x 2560 fp32 tokens,
 // 174 MB: 42.6 us, 4.1 TB/s.
 //
@@ -620,7 +620,8 @@ void many(const ProdArgs &a, hipStream_t s) {
 template <bool BF16, int M>
 void one_or_two(const ProdArgs &a, int group, hipStream_t s) {
     const int from = BF16 ? kStreamRows : kStreamRows / (2 * M);
-    if (a.N < from || stream_lds(M, a.K) > kStreamLds)
+    // K = 0 has no last unit for the streaming form's loads to clamp to
+    if (a.N < from || a.K == 0 || stream_lds(M, a.K) > kStreamLds)
         few<BF16, M, 4>(a, group, s);
     else if (a.N < kWideRows)
         stream<BF16, M, 2>(a, group, s);

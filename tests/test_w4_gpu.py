@@ -204,3 +204,17 @@ def test_refusals(gpu):
     assert gpu.bitlinear_gemv_w4(X, Wq4[:0], s[:0]).shape == (2, 0)
     none, sn = gpu.quant_weight_absmax_i4(W[:, :0], group=32)
     assert (gpu.bitlinear_gemv_w4(X[:, :0].contiguous(), none, sn) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N", [(1, 16383), (1, 16384), (1, 32768), (1, 65536), (2, 8192), (2, 40000), (2, 70000),
+                                 (3, 40000), (16, 70000)])
+def test_product_over_nothing_is_zero(gpu, M, N, dtype):
+    """K = 0 at row counts of every form; the empty operands' addresses are NULL."""
+    for group in (32, 64, 128):
+        X = torch.empty(M, 0, dtype=dtype, device="cuda")
+        Wq4, s = gpu.quant_weight_absmax_i4(torch.empty(N, 0, device="cuda"), group=group)
+        assert X.data_ptr() == Wq4.data_ptr() == s.data_ptr() == 0
+        Y = torch.full((M + 1, N), 5.0, device="cuda")
+        gpu.bitlinear_gemv_w4(X, Wq4, s, Y=Y[:M])
+        assert (Y[:M] == 0).all() and (Y[M] == 5).all()
