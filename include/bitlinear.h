@@ -530,9 +530,11 @@ bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype dtype, int
  * of a product is kept to 22 bits or more, for bf16 rows the softmax weights
  * are rounded to 11 bits.  An operand's smallest step is 2^-38 of the row's
  * largest |q|, and 2^-38 of the largest weight times the largest sv of the
- * sequence.  sk and sv are >= 0, as the append writes them.  Deterministic for
- * given sizes and contents; where a sequence's keys are cut into parts follows
- * from the lengths of all, so beside others its last bits may differ.
+ * sequence (sv below 2^-100 counts as that).  sk and sv are >= 0, as the append
+ * writes them.  Scores may be of any size that |scale| max |q| 127 D max sk <
+ * 2^126 allows, each rounded to fp32.  Deterministic for given sizes and
+ * contents; where a sequence's keys are cut into parts follows from the lengths
+ * of all, so beside others its last bits may differ.
  * Limits as for the append, and n_tok * QH < 2^31.
  */
 bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64_t n_tok, int64_t QH,

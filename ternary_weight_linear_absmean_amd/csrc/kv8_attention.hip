@@ -106,12 +106,26 @@ constexpr float kUnit = 16384.0f;           // p sv / u is held as fp16 times th
 // 2^kSlack kUnit still is in fp16's range, and with scores of one spread the
 // sums are rescaled once or twice a sequence and not at every step.
 constexpr float kSlack = 1.9f;
+// That bound needs the scores' rounding to be small: the maximum is taken of
+// rounded products, the exponent of the unrounded (one multiply-add), and m +
+// kSlack is rounded too, by half a step of a number next to m each: 2^-5 in all
+// at |m| = 2^18, and 2^1.94 kUnit < 62900 < 65504.  bf16 rows' exponent has the
+// value scale in it, rounded with m: 2^-14 at 2^11, a quarter of what rounding
+// the weight to 11 bits takes.  From there on m follows every maximum, and the
+// scores are rounded and m is taken off them before the exponent is formed, so
+// that the largest weight is 1 and a value scale costs nothing.
+template <bool BF16>
+constexpr float kFarScore = BF16 ? 2048.0f : 262144.0f;
+template <bool BF16>
+__device__ __forceinline__ float raise_above(float m) {     // a maximum that makes m follow
+    return fabsf(m) < kFarScore<BF16> ? m + kSlack : -INFINITY;
+}
 constexpr float kTiny = 1.17549435e-38f;    // a score factor of 0 (or none) without 0 * inf
 
 // Scores s (16 keys of a granule in 8 n accumulators: N = 2 of rows16, 1 of 8)
 // to fp16 weights times w_sv: hi, and lo for fp32 rows; their sum into l.  For
-// bf16 rows w_sv goes into the exponent (to 2^-20, against the 2^-12 of the
-// rounding): one multiply-add and one exponential a score.
+// bf16 rows w_sv goes into the exponent (to half a step of base, 2^-14 at most,
+// against the 2^-12 of the rounding): one multiply-add and one exponential a score.
 template <bool BF16, int N, typename S>
 __device__ __forceinline__ void weights(const S &s, float cs, float base, float w_sv, float &l, half8 *hi,
                                         half8 *lo) {
@@ -446,7 +460,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
             }
     }
 
-    float m = -INFINITY, l = 0.0f, u = 0.0f, unit_u = 0.0f;     // unit_u = kUnit / u
+    float m = -INFINITY, above = -INFINITY, l = 0.0f, u = 0.0f, unit_u = 0.0f;      // unit_u = kUnit / u
     float4v o[NO];
 #pragma unroll
     for (int i = 0; i < NO; ++i) o[i] = float4v{0.f, 0.f, 0.f, 0.f};
@@ -514,7 +528,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
                 load_k(next, id_next);
             }
 
-            const float cs = fmaxf(c_row * sk, kTiny);
+            float cs = fmaxf(c_row * sk, kTiny);
             const uint32_t key0 = tile + 16 * quad;
             const bool whole = id >= 0 && key0 + 16 <= sees;
             if (__ballot(!whole) != 0) {
@@ -529,7 +543,8 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
             for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e >> 2][e & 3]);
             top = quad_max(top * cs);
             const float u_new = fmaxf(u, pow2_above(quad_max(id >= 0 ? fabsf(sv) : 0.0f)));
-            if (__builtin_expect(__ballot(top > m + kSlack || u_new != u) != 0, 0)) {
+            float base = m == -INFINITY ? 0.0f : m;
+            if (__builtin_expect(__ballot(top > above || u_new != u) != 0, 0)) {
                 const float m_new = fmaxf(m, top);
                 float fix = m == -INFINITY ? 0.0f : exp2_fast(m - m_new);
                 l *= fix;
@@ -540,9 +555,17 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
                 for (int i = 0; i < NO; ++i) o[i] *= fix;
                 m = m_new;
                 u = u_new;
+                above = raise_above<BF16>(m);
+                base = m == -INFINITY ? 0.0f : m;
+                if (fabsf(base) >= kFarScore<BF16>) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[e >> 2][e & 3] = s[e >> 2][e & 3] * cs - base;
+                    cs = 1.0f;
+                    base = 0.0f;
+                }
             }
             half8 ph[NS][2];
-            weights<BF16, 2>([&](int e) { return s[e >> 2][e & 3]; }, cs, m == -INFINITY ? 0.0f : m,
+            weights<BF16, 2>([&](int e) { return s[e >> 2][e & 3]; }, cs, base,
                              id >= 0 ? sv * unit_u : 0.0f, l, ph[0], ph[NS - 1]);
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
@@ -784,7 +807,7 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
         }
     };
 
-    float m = -INFINITY, l = 0.0f, u = 0.0f, unit_u = 0.0f;     // unit_u = kUnit / u
+    float m = -INFINITY, above = -INFINITY, l = 0.0f, u = 0.0f, unit_u = 0.0f;      // unit_u = kUnit / u
     float16v o[NO];
 #pragma unroll
     for (int i = 0; i < NO; ++i)
@@ -865,7 +888,8 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
             }
             top = half_max(top);
             const float u_new = fmaxf(u, pow2_above(sv_top));
-            if (__builtin_expect(__ballot(top > m + kSlack || u_new != u) != 0, 0)) {
+            float base = m == -INFINITY ? 0.0f : m;
+            if (__builtin_expect(__ballot(top > above || u_new != u) != 0, 0)) {
                 const float m_new = fmaxf(m, top);
                 float fix = m == -INFINITY ? 0.0f : exp2_fast(m - m_new);
                 l *= fix;
@@ -876,8 +900,19 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
                 for (int i = 0; i < NO; ++i) o[i] *= fix;
                 m = m_new;
                 u = u_new;
+                above = raise_above<BF16>(m);
+                base = m == -INFINITY ? 0.0f : m;
+                if (fabsf(base) >= kFarScore<BF16>) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            s[g >> 1][8 * (g & 1) + e] = s[g >> 1][8 * (g & 1) + e] * cs[g] - base;
+                        cs[g] = 1.0f;
+                    }
+                    base = 0.0f;
+                }
             }
-            const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {                  // 16 keys
                 half8 p_hi, p_lo;

@@ -478,3 +478,69 @@ def test_refusals(gpu):
     none = empty[:0]
     bl.bitlinear_kv8_append(s["k"][:0], s["v"][:0], s["q_start"], s["lengths"], s["table"], c)
     assert bl.bitlinear_kv8_attention(ok[:0], empty, none, none.view(0, 3), c).shape == ok[:0].shape
+
+
+FAR = [
+    # n, lens, width in keys: few rows, cut ones, many rows, both, many rows in parts
+    ([1], [400], 0),
+    ([1, 5, 3], [3000, 40, 3], 0),
+    ([200], [400], 70000),
+    ([1, 60], [400, 60], 70000),
+    ([100, 1], [2000, 1000], 70000),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("far", [10, 17, 18, 19, 20, 22, 25, 28, 40, 100])
+@pytest.mark.parametrize("case", range(len(FAR)))
+def test_scores_far_from_zero(gpu, case, far, dtype):
+    """Scores of 2^far and more, of both signs.  A score is off by ds at most (see
+    check_attention; a step of the rounded score is less), so each weight by e^ds
+    either way: the result by (e^ds - 1) e^ds sum p |v - out|, and never by more
+    than the seen values' reach, as it lies among them."""
+    n, lens, width = FAR[case]
+    T, D, KVH, G = 16, 64, 2, 4
+    s = make(100 + case, n, lens, T, D, KVH, dtype, G, width=width // T)
+    s["q"] *= 2.0 ** far
+    got = n64(attend(gpu, cuda(s)))
+    assert np.isfinite(got).all()
+    q, K, V, sk, sv = (n64(s[x]) for x in ("q", "K", "V", "sk", "sv"))
+    for b, r, pos in ref.rows_of(s["q_start"].numpy(), lens, len(q)):
+        p = np.arange(pos + 1)
+        i = s["table"].numpy()[b, p // T]
+        for h in range(KVH):
+            k, v = K[i, h, p % T] * sk[i, h][:, None], V[i, h, :, p % T] * sv[i, h][:, None]
+            x = q[r, h * G:(h + 1) * G] @ k.T * D ** -0.5
+            w = np.exp(x - x.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            out, wide = w @ v, w @ np.abs(v)
+            dev = np.einsum("gj,gjd->gd", w, np.abs(v[None] - out[:, None]))
+            top = np.abs(q[r, h * G:(h + 1) * G])
+            ds = (top @ np.abs(k).T).max(-1) * D ** -0.5 * (2.0 ** -21 + (D + 8) * 2.0 ** -24)
+            ds += top.max(-1) * np.abs(k).sum(-1).max() * D ** -0.5 * 2.0 ** -38
+            reach = np.maximum(v.max(0) - out, out - v.min(0))
+            with np.errstate(divide="ignore", over="ignore"):
+                moved = np.exp(np.minimum(np.log(dev) + np.where(ds < 1, np.log(np.expm1(ds)) + ds, 2 * ds)[:, None], 50))
+            # the weights' roundings also move a result beyond the values
+            keys = len(p)
+            tol = np.minimum(moved, reach) + wide * (keys + 64) * 2.0 ** -24 + keys * 2.0 ** -31 * sv.max()
+            if dtype == BF16:
+                tol = tol + wide * 2.0 ** -11
+                tol = tol + (np.abs(out) + tol) * 2.0 ** -8
+            off = np.abs(got[r, h * G:(h + 1) * G] - out)
+            assert (off <= tol).all(), (b, r, h, (off - tol).max())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("far", [0, 17, 18, 20, 26, 60])
+@pytest.mark.parametrize("case", range(len(FAR)))
+def test_equal_scores_far_from_zero(gpu, case, far, dtype):
+    """One key in every slot: equal scores, however large, and the mean of the values."""
+    n, lens, width = FAR[case]
+    s = make(110 + case, n, lens, 16, 64, 2, dtype, 4, width=width // 16)
+    s["K"][:] = s["K"][0, :, :1]
+    s["sk"][:] = 0.02
+    s["q"] *= 2.0 ** far
+    got = n64(attend(gpu, cuda(s)))
+    s["q"][:] = 0                               # the same weights without a score's rounding
+    check_attention(s, torch.tensor(got))
