@@ -517,7 +517,7 @@ bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype dtype, int
  * their sequences' cached tokens (the new ones among them: append first).
  *   q      in   [n_tok][QH][D] of `dtype`, 16-byte aligned; query head h reads
  *               key/value head h / (QH / KVH); KVH divides QH, QH <= 65535.
- *   scale       factor of the scores, e.g. 1 / sqrt(D); finite.
+ *   scale       factor of the scores, e.g. 1 / sqrt(D); |scale| < 2^127.
  *   out    out  [n_tok][QH][D] of `dtype`, 16-byte aligned: for the row at
  *               position p, sum_j softmax_j(scale q . key_j) value_j over the
  *               tokens at 0 .. p.  A row that sees no token gives zeros.

@@ -735,6 +735,11 @@ BL_EXPORT size_t bitlinear_kv8_attention_ws_bytes(int64_t n_tok, int64_t QH, int
                     256);
 }
 
+// Whether scale * log2(e), which the kernels multiply by, is a finite fp32.
+static bool scale_in_range(float scale) {
+    return scale > -0x1p127f && scale < 0x1p127f;
+}
+
 BL_EXPORT bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64_t n_tok,
                                             int64_t QH, const int32_t *q_start,
                                             const int32_t *lengths, const int32_t *table,
@@ -751,8 +756,8 @@ BL_EXPORT bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64
         return fail(BL_ERR_SHAPE, "%s: need QH in [1, 65535], a multiple of KVH, n_tok * QH < 2^31 "
                     "(QH=%lld KVH=%lld n_tok=%lld)", name, (long long)QH, (long long)cache->KVH,
                     (long long)n_tok);
-    if (!(scale - scale == 0.0f))
-        return fail(BL_ERR_SHAPE, "%s: scale must be finite", name);
+    if (!scale_in_range(scale))
+        return fail(BL_ERR_SHAPE, "%s: |scale| must be below 2^127", name);
     if (noop)
         return ok();
     const size_t need = bitlinear_kv8_attention_ws_bytes(n_tok, QH, B, max_blocks, cache->KVH,
@@ -895,8 +900,8 @@ BL_EXPORT bl_status bitlinear_decode_stack_kv(const bl_layer *layers, const bl_k
     bl_status st = check_stack_kv_dims(name, dims, n_layers > 0 ? caches[0].T : 64, max_blocks);
     if (st != BL_OK)
         return st;
-    if (!(scale - scale == 0.0f))
-        return fail(BL_ERR_SHAPE, "%s: scale must be finite", name);
+    if (!scale_in_range(scale))
+        return fail(BL_ERR_SHAPE, "%s: |scale| must be below 2^127", name);
     if (n_layers == 0)
         return ok();
     st = check_stack_layers(name, layers, n_layers, x, trace);

@@ -175,3 +175,14 @@ def test_stack_kv_refusals(lib):
     size = need(dims(), 64, 4)
     assert size >= lib.bl_workspace_bytes(bl.BL_OP_DECODE_STACK, 1, 512, 128, 640)
     assert call(ws=None) == WS and call(size=size - 1) == WS
+
+
+def test_scales_past_the_kernels_range(lib):
+    """scale * log2(e) is an fp32 in the kernels: refused where it would be infinite."""
+    from ternary_weight_linear_absmean_amd._native import Layer, StackDims
+    q, o, dt, n, qs, ln, tb, B, nb, c = rows()
+    for scale in (2.0 ** 127, 2.4e38, -2.4e38, 3.4e38, -3.4e38):
+        assert lib.bitlinear_kv8_attention(q, dt, n, 8, qs, ln, tb, B, nb, c, scale, o, A16, 1 << 40, None) == SHAPE
+        assert lib.bitlinear_decode_stack_kv(Layer(*[A16] * 14, None), cache(D=64), 1,
+                                             StackDims(512, 128, 640, 64, 1e-5, 0, 0, 0), A4, A4, A4, 4, scale, A16,
+                                             None, A16, 1 << 40, None) == SHAPE
