@@ -521,7 +521,7 @@ bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype dtype, int
  *   out    out  [n_tok][QH][D] of `dtype`, 16-byte aligned: for the row at
  *               position p, sum_j softmax_j(scale q . key_j) value_j over the
  *               tokens at 0 .. p.  A row that sees no token gives zeros.
- *               May not overlap q.
+ *               May not overlap q (BL_ERR_ALIGN).
  *   ws          >= bitlinear_kv8_attention_ws_bytes(...) bytes, 16-byte
  *               aligned (NULL allowed when that is 0): partial results of
  *               sequences that are read in several parts.  Calls that may

@@ -767,6 +767,10 @@ BL_EXPORT bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64
                     need);
     if (!aligned(ws, 16))
         return fail(BL_ERR_ALIGN, "%s: ws must be 16-byte aligned", name);
+    const uintptr_t bytes = (uintptr_t)(n_tok * QH * cache->D) * (dtype == BL_BF16 ? 2 : 4);
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), out0 = reinterpret_cast<uintptr_t>(out);
+    if (q0 < out0 + bytes && out0 < q0 + bytes)
+        return fail(BL_ERR_ALIGN, "%s: out overlaps q (%p, %p, %zu bytes each)", name, out, q, (size_t)bytes);
     st = check_arch();
     if (st != BL_OK)
         return st;

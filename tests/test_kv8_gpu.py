@@ -544,3 +544,20 @@ def test_equal_scores_far_from_zero(gpu, case, far, dtype):
     got = n64(attend(gpu, cuda(s)))
     s["q"][:] = 0                               # the same weights without a score's rounding
     check_attention(s, torch.tensor(got))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_out_beside_q(gpu, dtype):
+    """out may begin where q ends and end where it begins; over q it is refused."""
+    s = cuda(make(120, [1, 3], [300, 40], 16, 64, 2, dtype, 4))
+    want, n = attend(gpu, s), len(s["q"])
+    buf = torch.zeros((3 * n,) + s["q"].shape[1:], dtype=dtype, device="cuda")
+    buf[n:2 * n] = s["q"]
+    s["q"] = buf[n:2 * n]
+    for out in (buf[:n], buf[2 * n:]):
+        assert torch.equal(attend(gpu, s, out=out), want)
+    for at in (1, n, 2 * n - 1):
+        with pytest.raises(gpu.BitLinearError) as e:
+            attend(gpu, s, out=buf[at:at + n])
+        assert e.value.status == 4
+    assert torch.equal(attend(gpu, s), want)

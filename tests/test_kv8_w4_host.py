@@ -186,3 +186,12 @@ def test_scales_past_the_kernels_range(lib):
         assert lib.bitlinear_decode_stack_kv(Layer(*[A16] * 14, None), cache(D=64), 1,
                                              StackDims(512, 128, 640, 64, 1e-5, 0, 0, 0), A4, A4, A4, 4, scale, A16,
                                              None, A16, 1 << 40, None) == SHAPE
+
+
+def test_attention_refuses_out_over_q(lib):
+    """3 rows of 8 heads of 128 values, in each type."""
+    for dt, size in ((0, 3 * 8 * 128 * 4), (1, 3 * 8 * 128 * 2)):
+        for by in (0, 16, -16, size - 16, 16 - size):
+            q, o, _, n, qs, ln, tb, B, nb, c = rows(q=A16 << 4, o=(A16 << 4) + by)
+            assert lib.bitlinear_kv8_attention(q, dt, n, 8, qs, ln, tb, B, nb, c, 1.0, o, A16, 1 << 40, None) == ALIGN
+            assert b"overlaps" in lib.bl_last_error()
