@@ -1178,6 +1178,10 @@ __global__ __launch_bounds__(THREADS) void kv8_join_kernel(Args a) {
     }
 }
 
+int64_t join_threads(int64_t rows, int64_t parts) {
+    if (parts <= kWaveParts) return (rows + kWaves - 1) / kWaves * kThreads;
+    return rows * (rows <= kJoinRows ? 1024 : 256);
+}
 template <bool BF16, int D, bool FEW>
 void join(const Args &a, int64_t rows, int64_t parts, hipStream_t s) {
     if (parts <= kWaveParts)
@@ -1274,7 +1278,12 @@ hipError_t attend(Args a, const Plan &p, hipStream_t s) {
     a.max_rows = a.mixed ? kFewRows : rows;
     if (p.many) a.many_groups = ((int64_t)a.seqs.n_tok * a.G / kManyRows + a.seqs.B) * a.c.KVH;
     const int64_t groups = a.many_groups * p.S + p.groups;
-    if (groups >= ((int64_t)1 << 32) / kThreads) return hipErrorInvalidConfiguration;
+    const int64_t join_rows = a.mixed ? (int64_t)a.seqs.B * kFewRows * a.c.KVH : rows;
+    // all launches or none
+    constexpr int64_t kMost = (int64_t)1 << 32;
+    if (groups * kThreads >= kMost || (p.many && p.S > 1 && join_threads(rows, p.S) >= kMost) ||
+        (p.cuts && join_threads(join_rows, p.steps) >= kMost))
+        return hipErrorInvalidConfiguration;
     if (a.mixed)
         hipLaunchKernelGGL((kv8_mixed_kernel<BF16, D>), dim3((unsigned)groups), block, 0, s, a);
     else if (p.many)
@@ -1282,8 +1291,7 @@ hipError_t attend(Args a, const Plan &p, hipStream_t s) {
     else
         hipLaunchKernelGGL((kv8_few_kernel<BF16, D>), dim3((unsigned)groups), block, 0, s, a);
     if (p.many && p.S > 1) join<BF16, D, false>(a, rows, p.S, s);
-    if (p.cuts)
-        join<BF16, D, true>(a, a.mixed ? (int64_t)a.seqs.B * kFewRows * a.c.KVH : rows, p.steps, s);
+    if (p.cuts) join<BF16, D, true>(a, join_rows, p.steps, s);
     return hipGetLastError();
 }
 

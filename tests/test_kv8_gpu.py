@@ -561,3 +561,20 @@ def test_out_beside_q(gpu, dtype):
             attend(gpu, s, out=buf[at:at + n])
         assert e.value.status == 4
     assert torch.equal(attend(gpu, s), want)
+
+
+def test_a_call_past_the_runtimes_grid_writes_nothing(gpu):
+    """512 rows of 65520 heads in 256 sequences with room for cuts: the join of
+    their 33 million rows would be 2^33 threads."""
+    B, n, KVH, G, T, D = 256, 512, 4095, 16, 16, 64
+    c = gpu.kv8_cache(1, KVH, T, D)
+    q = torch.empty(n, KVH * G, D, dtype=BF16, device="cuda")
+    out = torch.full_like(q, 77.0)
+    q_start = torch.arange(0, n + 1, n // B, dtype=torch.int32, device="cuda")
+    lengths = torch.full((B,), 2, dtype=torch.int32, device="cuda")
+    table = torch.full((B, 512), -1, dtype=torch.int32, device="cuda")
+    with pytest.raises(gpu.BitLinearError) as e:
+        gpu.bitlinear_kv8_attention(q, q_start, lengths, table, c, out=out)
+    assert e.value.status == 7
+    torch.cuda.synchronize()
+    assert all(bool((x == 77.0).all()) for x in out.split(64))
