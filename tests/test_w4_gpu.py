@@ -218,3 +218,59 @@ def test_product_over_nothing_is_zero(gpu, M, N, dtype):
         Y = torch.full((M + 1, N), 5.0, device="cuda")
         gpu.bitlinear_gemv_w4(X, Wq4, s, Y=Y[:M])
         assert (Y[:M] == 0).all() and (Y[M] == 5).all()
+
+
+PRODUCTS = [
+    (1, 1, 32, 32), (1, 17, 64, 64), (2, 33, 96, 32), (3, 100, 160, 32), (16, 1, 128, 64), (1, 640, 2560, 128),
+    (5, 257, 2560, 64), (16, 640, 2560, 32), (7, 48, 6912, 128), (1, 2000, 192, 64), (9, 31, 4096, 64), (4, 70, 224, 32),
+    (13, 5000, 192, 64), (1, 20000, 256, 128), (1, 20000, 544, 32), (2, 9000, 1056, 32), (2, 40000, 576, 64),
+    (1, 66000, 1120, 32), (3, 4097, 2592, 32), (6, 9000, 320, 64), (16, 25000, 288, 32), (16, 40, 20480, 128),
+    (1, 3, 131072, 128), (2, 20, 131008, 64), (3, 5, 131072, 32), (16, 20, 131040, 32), (8, 3, 130944, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K,group", PRODUCTS)
+def test_product_of_small_integers_is_exact(gpu, M, N, K, group, dtype):
+    """Tokens of -3 .. 3 and scales of 1, 2 and 4: every product and sum is an
+    integer below 131072 * 3 * 8 * 4 < 2^24 (with the codes + 24 those of a group,
+    128 * 3 * 48), so nothing is rounded; a value left out or taken twice shows."""
+    g = torch.Generator().manual_seed(K + N)
+    Wq4, s = weights(g, N, K, group)
+    s = (2.0 ** torch.randint(0, 3, s.shape, generator=g)).to(BF16)
+    X = torch.randint(-3, 4, (M, K), generator=g).to(dtype)
+    Y = gpu.bitlinear_gemv_w4(X.cuda(), Wq4.cuda(), s.cuda())
+    q = torch.stack(((Wq4 & 15 ^ 8).to(torch.int8) - 8, (Wq4 >> 4 ^ 8).to(torch.int8) - 8), -1).view(N, K)
+    W = q.double().view(N, -1, group) * s.double()[..., None]
+    assert torch.equal(Y.cpu().double(), X.double() @ W.view(N, K).T)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,N,K,group", PRODUCTS)
+def test_product_by_its_additions(gpu, M, N, K, group, dtype):
+    """A term is rounded once in each addition that it passes through, by 2^-24 of
+    the sum.  One or two tokens: 16 of a lane's 32 values, the two halves, a slice
+    of 512 values after another, 4 steps over the lanes, 8 waves.  More: the
+    products of a group and as many of the other half of X or the -24 (each
+    counted twice, as a matrix instruction may cut and not round), the groups, 16
+    waves.  fp32 tokens from three on lose 2^-22 of the largest of 128 values
+    besides; bf16 tokens' +24 and -24 times x pass through the 64 additions of two
+    matrix instructions, counted twice, and are gone then."""
+    g = torch.Generator().manual_seed(M * N + K + 1)
+    Wq4, s = weights(g, N, K, group)
+    X = torch.randn(M, K, generator=g)
+    X[:, torch.randperm(K, generator=g)[:max(1, K // 100)]] *= 20
+    X = X.to(dtype)
+    got = gpu.bitlinear_gemv_w4(X.cuda(), Wq4.cuda(), s.cuda()).cpu().double()
+    q = torch.stack(((Wq4 & 15 ^ 8).to(torch.int8) - 8, (Wq4 >> 4 ^ 8).to(torch.int8) - 8), -1).view(N, K).double()
+    d = s.double().repeat_interleave(group, 1)
+    x = X.double()
+    want = x @ (q * d).T
+    through = 17 + K / 512 + 1 + 4 + 8 if M <= 2 else 4 * group + K / group + 16
+    tol = x.abs() @ (q.abs() * d).T * through * 1.001 * 2.0 ** -24
+    if M > 2 and dtype == BF16:
+        tol += x.abs() @ d.T * 48 * 128 * 1.001 * 2.0 ** -24
+    if M > 2 and dtype == F32:
+        top = torch.nn.functional.pad(x.abs(), (0, -K % 128)).view(M, -1, 128).amax(-1)
+        tol += top.repeat_interleave(128, 1)[:, :K] @ (q.abs() * d).T * 2.0 ** -22
+    assert ((got - want).abs() <= tol).all(), float(((got - want).abs() - tol).max())
