@@ -558,6 +558,10 @@ size_t bitlinear_kv8_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B, in
  *   q_start       DEVICE int32 [2] holding {0, 1}: one new token.
  *   length, table DEVICE int32 [1] and [max_blocks], as for the append.
  *   scale         as for the attention.
+ * No position enters a score: q and k go from their BitLinears to the cache and
+ * the attention as they are, and nothing can rotate them in between.  A model
+ * with rotary embeddings is run by the single calls (bitlinear_gemv_fused, its
+ * own rotation, append, attention).
  *   ws            >= bitlinear_decode_stack_kv_ws_bytes(dims, T, max_blocks)
  *                 bytes, 16-byte aligned.
  */
@@ -598,10 +602,14 @@ bl_status dequant_weight_i4(const uint8_t *Wq4, const uint16_t *s, int64_t N, in
  *   X      in   [M][K] of `dtype`, 16-byte aligned (not quantised).
  *   Wq4, s in   as above.
  *   Y      out  fp32 [M][N] = sum over the groups of s * sum_k x code, 4-byte
- *               aligned.
- * Sums are fp32.  M <= 2 multiplies fp32 x as it is; above, fp32 x is held to
- * 22 bits or more of the largest |x| of 128 consecutive elements, bf16 x
- * exactly.  |x| is to stay below 2^116 (sums of codes come before their scale).
+ *               aligned; may not overlap an input.
+ * Sums are fp32.  M <= 2 multiplies x as it is.  Above, fp32 x is held to 22
+ * bits or more of the largest |x| of 128 consecutive elements.  bf16 x is held
+ * exactly, but multiplied by code + 24 and by -24: in each of the up to 64
+ * additions until both are in the sum, rounding may leave 2^-24 of (|code| + 48)
+ * |x| s, also where the code is 0 (x 1000 times the others', all at codes of 0,
+ * moved results by 5e-5 of theirs).  |x| is to stay below 2^116 (sums of codes
+ * come before their scale).
  * Deterministic for given sizes.  M == 0 or N == 0: no-op; K == 0 gives zeros.
  */
 bl_status bitlinear_gemv_w4(const void *X, bl_dtype dtype, int64_t M, const uint8_t *Wq4,
