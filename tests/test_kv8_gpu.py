@@ -578,3 +578,28 @@ def test_a_call_past_the_runtimes_grid_writes_nothing(gpu):
     assert e.value.status == 7
     torch.cuda.synchronize()
     assert all(bool((x == 77.0).all()) for x in out.split(64))
+
+
+GUARDED = [("LINES", i) for i in (0, 2, 4, 6, 9, 11, 12, 13, 14, 16)] + [("MANY", i) for i in (0, 3, 4, 5, 7, 8)]
+
+
+@pytest.mark.parametrize("fill", [0, 255])
+@pytest.mark.parametrize("name,case", GUARDED)
+def test_workspace_of_the_asked_size(gpu, name, case, fill):
+    """Cut few rows, prompts in parts, and both, on the first bytes of a buffer
+    and whatever it held; the bytes behind them stay."""
+    if name == "LINES":
+        n, lens, T, KVH, G = LINES[case]
+        D, width = 128, 60000
+    else:
+        n, lens, T, D, KVH, G, width = MANY[case]
+    s = make(130 + case, n, lens, T, D, KVH, (F32, BF16)[case % 2], G, width=-(-width // T))
+    d = cuda(s)
+    need = gpu.load().bitlinear_kv8_attention_ws_bytes(len(s["q"]), KVH * G, len(n), s["table"].shape[1], KVH, T, D)
+    assert need > 0 or (name, case) == ("MANY", 0)
+    buf = torch.full((need + (1 << 20),), fill, dtype=torch.uint8, device="cuda")
+    buf[need:] = 170
+    out = attend(gpu, d, ws=buf[:need])
+    assert (buf[need:] == 170).all()
+    check_attention(s, out)
+    assert torch.equal(out, attend(gpu, d))

@@ -195,3 +195,18 @@ def test_attention_refuses_out_over_q(lib):
             q, o, _, n, qs, ln, tb, B, nb, c = rows(q=A16 << 4, o=(A16 << 4) + by)
             assert lib.bitlinear_kv8_attention(q, dt, n, 8, qs, ln, tb, B, nb, c, 1.0, o, A16, 1 << 40, None) == ALIGN
             assert b"overlaps" in lib.bl_last_error()
+
+
+def test_attention_workspace_is_asked_for_and_checked(lib):
+    """Sizes that are cut or read in parts: a size above 0, and one byte less refused."""
+    f = lib.bitlinear_kv8_attention_ws_bytes
+    for n, QH, B, nb, KVH in ((3, 8, 2, 4000, 2), (1, 8, 1, 63, 2), (64, 8, 64, 4000, 2), (200, 8, 2, 1000, 2),
+                              (300, 8, 1, 1000, 2), (256, 8, 256, 4000, 2)):
+        need = f(n, QH, B, nb, KVH, 64, 128)
+        # a line of 128 values and its two sums for each row of two pieces at least
+        assert need >= 2 * 4 * 130 * min(16, n * QH // KVH), (n, B, nb)
+        q, o, dt, _, qs, ln, tb, _, _, c = rows(q=A16, o=1 << 40)
+        for ws, size in ((None, need), (A16, need - 1), (A16, 0)):
+            assert lib.bitlinear_kv8_attention(q, dt, n, QH, qs, ln, tb, B, nb, c, 1.0, o, ws, size, None) == WS
+    # nothing is cut: short tables, and more than 256 sequences of few rows
+    assert f(3, 8, 2, 4, 2, 64, 128) == 0 and f(257, 8, 257, 4000, 2, 64, 128) == 0
