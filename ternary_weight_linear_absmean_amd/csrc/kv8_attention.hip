@@ -531,6 +531,8 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
             float cs = fmaxf(c_row * sk, kTiny);
             const uint32_t key0 = tile + 16 * quad;
             const bool whole = id >= 0 && key0 + 16 <= sees;
+            // a scale that this row does not see is not to touch u, nor to meet a weight of 0
+            const float sv_seen = id >= 0 && key0 < sees ? sv : 0.0f;
             if (__ballot(!whole) != 0) {
                 const int lim = id >= 0 && key0 < sees ? (int)min(sees - key0, 16u) : 0;
 #pragma unroll
@@ -542,7 +544,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 #pragma unroll
             for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e >> 2][e & 3]);
             top = quad_max(top * cs);
-            const float u_new = fmaxf(u, pow2_above(quad_max(id >= 0 ? fabsf(sv) : 0.0f)));
+            const float u_new = fmaxf(u, pow2_above(quad_max(fabsf(sv_seen))));
             float base = m == -INFINITY ? 0.0f : m;
             if (__builtin_expect(__ballot(top > above || u_new != u) != 0, 0)) {
                 const float m_new = fmaxf(m, top);
@@ -566,7 +568,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
             }
             half8 ph[NS][2];
             weights<BF16, 2>([&](int e) { return s[e >> 2][e & 3]; }, cs, base,
-                             id >= 0 ? sv * unit_u : 0.0f, l, ph[0], ph[NS - 1]);
+                             sv_seen * unit_u, l, ph[0], ph[NS - 1]);
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
                 const half8 v_lo = codes8(vb[i].x, vb[i].y), v_hi = codes8(vb[i].z, vb[i].w);
@@ -870,9 +872,12 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
         if (here) {
             if (!(valid && tile + kTile <= sees_lo)) {                  // uniform
                 const int lim = tile < sees ? (int)min(sees - tile, (uint32_t)kTile) : 0;
+                sv_top = 0.0f;                              // as above: of what the row sees
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int lim_g = lane_value(used ? 1.0f : 0.0f, g) != 0.0f ? lim - 16 * g - 8 * half : 0;
+                    w_sv[g] = lim > 16 * g ? w_sv[g] : 0.0f;
+                    sv_top = fmaxf(sv_top, fabsf(w_sv[g]));
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         s[g >> 1][8 * (g & 1) + e] = e < lim_g ? s[g >> 1][8 * (g & 1) + e] : -INFINITY;

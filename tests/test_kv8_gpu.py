@@ -603,3 +603,27 @@ def test_workspace_of_the_asked_size(gpu, name, case, fill):
     assert (buf[need:] == 170).all()
     check_attention(s, out)
     assert torch.equal(out, attend(gpu, d))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan"), 3e38])
+@pytest.mark.parametrize("n,length,T,D,KVH,G,width", [
+    (60, 70, 16, 64, 2, 4, 0), (40, 1300, 32, 128, 1, 3, 9000), (200, 333, 32, 64, 2, 4, 70000),
+    (200, 333, 16, 128, 2, 8, 70000), (301, 2500, 64, 128, 2, 4, 30000)])
+def test_later_blocks_never_show(gpu, n, length, T, D, KVH, G, width, bad, dtype):
+    """Scales of a block that overflowed: rows whose tokens all stand before it
+    are as if it held ones; also beside rows that see it."""
+    s = make(140, [n, 1], [length, 40], T, D, KVH, dtype, G, width=-(-width // T))
+    at = (length - n // 2) // T                # the block, and where it begins among the rows
+    rows = at * T - (length - n)
+    assert 0 < rows < n
+    block = int(s["table"][0, at])
+    for name in ("sk", "sv"):
+        s[name][block] = bad
+    got = attend(gpu, cuda(s))
+    for name in ("sk", "sv"):
+        s[name][block] = 0.02
+    keep = torch.cat([got[:rows], torch.zeros_like(got[rows:n]), got[n:]]).cpu()
+    plain = attend(gpu, cuda(s)).cpu()
+    keep[rows:n] = plain[rows:n]
+    check_attention(s, keep)
