@@ -15,9 +15,9 @@
 // is never fewer; floor(n_tok / T) + 2 B slots in all.  Unused ones exit.
 //
 // Decode is bound by latency: starts, length, table entry, rows, maximum and
-// quotient follow one another (64 sequences, 5 heads of 128: 4.8 us, 2 of them
+// quotient follow one another (64 sequences, 5 heads of 128: 6.1 us, 2 of them
 // the launch).  Prompts are one pass over the rows, held in registers between
-// the maximum and the codes (4400 fp32 rows, 27 MB: 10.5 us, 2.6 TB/s, start and
+// the maximum and the codes (4400 fp32 rows, 27 MB: 10.9 us, 2.5 TB/s, start and
 // end of one wave of workgroups; a multiplication with a check in the place of
 // the correctly rounded quotients took 5% off).
 #include "kv8_common.h"

@@ -4,7 +4,8 @@
 // q.k_j, m the running maximum: one pass over the keys, the sums rescaled by
 // 2^(m_old - m) when the maximum grows.
 //
-// Both products run on fp16 matrix instructions (16x16x32) with fp32 sums.
+// Both products run on fp16 matrix instructions with fp32 sums, 16x16x32 for few
+// rows and 32x32x16 for many.
 // An int8 code is exact in fp16: the byte with its sign bit flipped, put
 // below the byte 0x64, reads as 1024 + (code + 128), and one packed add of
 // -1152 leaves the code (v_xor per 4 codes, v_perm and v_pk_add_f16 per 2).
@@ -20,7 +21,7 @@
 // of one product, so a cached byte is read once for all of them: row r of
 // sequence b is token r / G, head r % G (G query heads to a key head).
 //
-// Operand layouts (lane = 16 quad + low): S^T = K Q^T puts key 4 quad + i, row
+// Operand layouts for few rows (lane = 16 quad + low): S^T = K Q^T puts key 4 quad + i, row
 // low into accumulator i.  Which key a row of the K operand is, is free: row 4
 // g + i of the operand for keys tt holds key 16 g + 4 tt + i of the tile, so
 // that lane quad g ends up with keys 16 g .. 16 g + 15 of its row -- exactly the
@@ -1205,7 +1206,7 @@ void join(const Args &a, int64_t rows, int64_t parts, hipStream_t s) {
 // rest, or else all.  A lone workgroup of many rows takes 2 us a tile of 64 keys,
 // so with little work the few-rows kernel, cut to fill the GPU, is done first
 // though it reads and converts a code 8 times as often.  In us, few and many
-// rows, 5 heads of 4, bf16:
+// rows, 5 heads of 4, bf16 (not measured for other heads and fp32):
 //   work   120  128 rows on 500 keys      7.5  18.9
 //          720  128 on 4000                13    19
 //         1920  4 x 256 on 1000          22.9  29.5

@@ -6,7 +6,7 @@
 // defined to the bit.  A group is held by group / 8 neighbouring lanes, eight
 // values each (one dword of codes), so its maximum is a few DPP steps and
 // everything is read and written once.  Both directions are bound by memory:
-// 6912 x 2560 fp32 (80 MB) 12.4 us to codes and 13.8 us back, 5.8 to 6.4 TB/s
+// 6912 x 2560 fp32 (80 MB) 13.6 us to codes and 15.4 us back, 5.2 to 5.9 TB/s
 // with part of the matrix in the last cache.
 #include "device_common.h"
 #include "launch.h"
@@ -90,8 +90,9 @@ __global__ __launch_bounds__(kThreads) void dequant_w4_kernel(const uint32_t *__
 }
 
 // ---------------------------------------------------------------------------
-// Y [M][N] = X W^T, M <= 16.  Two kernels: fp32 multiply-adds for one or two
-// tokens, fp16 matrix instructions from three on.
+// Y [M][N] = X W^T, M <= 16, in three forms: one or two tokens in fp32
+// multiply-adds, with X in registers or, for many rows, in LDS; from three tokens
+// on matrix instructions, fp16 for fp32 tokens and bf16 for bf16 tokens.
 //
 // A 4-bit code is exact in fp16: with its sign bit flipped it is code + 8;
 // below the byte 0x64 that reads as 1024 + (code + 8) from bits 0..3 and as
@@ -99,10 +100,10 @@ __global__ __launch_bounds__(kThreads) void dequant_w4_kernel(const uint32_t *__
 // leaves the code: 10 instructions per dword of 8 codes, in the order 0, 4, 1,
 // 5, 2, 6, 3, 7.
 //
-// In both, the waves of a workgroup share its rows of W and divide K among
-// them, so that a wave's part of X stays in its registers for all the rows,
-// W is read with 16-byte loads that are all in flight together, and nothing
-// but the final sums (in the waves' order) goes through LDS.
+// In the first and the last form the waves of a workgroup share its rows of W
+// and divide K among them, so that a wave's part of X serves all the rows, W is
+// read with 16-byte loads that are all in flight together, and the sums are
+// joined once, in the waves' order, through LDS.
 struct Codes {
     half2 p[4];               // codes 0, 4 | 1, 5 | 2, 6 | 3, 7
 };
@@ -220,11 +221,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_w4_few_kernel(ProdArgs a,
 // 174 MB: 42.6 us, 4.1 TB/s.
 //
 // X costs the other kernel a reading for every 16 rows, and this one a start, so
-// this one is taken from 32768 rows on, with fp32 tokens from 16384 / M: N x 2560,
-// the other kernel and this one in us, M = 1: 12288 fp32 7.5 8.2, 24576 13.0 10.8,
+// this one is taken from 32768 rows on, with fp32 tokens from 16384 / M (measured
+// at K = 2560 alone; both the start and a row's work grow with K): N x 2560, the
+// other kernel and this one in us, M = 1: 12288 fp32 7.5 8.2, 24576 13.0 10.8,
 // bf16 10.6 11.0, 40000 17.2 15.1; M = 2: 8192 fp32 9.1 8.5, 20000 18.8 13.3, bf16
-// 13.0 13.4.  R = 2 for fewer than 65536 rows, which a wave then has no more than
-// eight tiles of (40000: 15.1, 17.2 with 4), 4 from there on (98304: 34.0, 31.8).
+// 13.0 13.4.  R = 2 for fewer than 65536 rows, of which a wave then has two tiles
+// at most (40000: 15.1, 17.2 with 4), 4 from there on (98304: 34.0, 31.8).
 constexpr int kStreamThreads = 256;
 constexpr int kStreamGroups = 1024;
 constexpr size_t kStreamLds = 64 * 1024;
@@ -393,8 +395,6 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// LDS of a wave: [part of X][instruction, quad][16 tokens + 1 of padding] units
-// of 16 bytes, then 16 factors; the final sums take its place.
 typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ float4v mfma_bf16(bf8v a, bf8v b, float4v c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -408,6 +408,8 @@ __device__ __forceinline__ bf8v codes_to_bf16(uint32_t w) {
                                                ((w >> 5) & mask) ^ base, ((w >> 9) & mask) ^ base));
 }
 
+// LDS of a wave: [part of X][instruction, quad][16 tokens + 1 of padding] units
+// of 16 bytes, then 16 factors; the final sums take its place.
 template <bool BF16>
 constexpr int wave_lds() { return (BF16 ? 1 : 2) * 16 * 17 * 16 + 64; }
 
@@ -598,12 +600,14 @@ void many(const ProdArgs &a, hipStream_t s) {
 }
 template <bool BF16, int GROUP, bool WHOLE>
 void many(const ProdArgs &a, hipStream_t s) {
-    // the widest workgroups that still give every CU one: 16 x 2560 -> 6912 fp32
-    // (432, 216 and 108 of them) takes 13.4, 8.8 and 12.9 us with R = 1, 2 and 4.
-    // bf16 tokens, which cost little to bring into the operand's order, go with
-    // small workgroups as long as wide ones would be fewer than 1.5 to a CU: 16 x
-    // 2560 -> 20000 12.3 us, with R = 4 14.5 (fp32 24.9 and 20.0), 30000 17.5 and
-    // 14.7
+    // 16 rows a workgroup while each has a CU of its own, then 32, then 64 (the 16
+    // waves of a workgroup fill a CU's LDS with fp32 tokens, so one more than 256
+    // workgroups is a second turn): 16 x 2560 -> 6912 fp32 (432, 216 and 108 of
+    // them) takes 13.4, 8.8 and 12.9 us with R = 1, 2 and 4.  Just above a bound half
+    // the CUs have nothing to do.  bf16 tokens, which cost little to bring into the
+    // operand's order, go with small workgroups as long as wide ones would be fewer
+    // than 1.5 to a CU: 16 x 2560 -> 20000 12.3 us, with R = 4 14.5 (fp32 24.9 and
+    // 20.0), 30000 17.5 and 14.7
     if (a.N <= 16 * kCUs) many<BF16, GROUP, 1, WHOLE, 16>(a, s);
     else if (a.N <= 32 * kCUs) many<BF16, GROUP, 2, WHOLE, 16>(a, s);
     else if (BF16 && a.N <= 96 * kCUs) many<BF16, GROUP, 1, WHOLE, 8>(a, s);
