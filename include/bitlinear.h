@@ -503,8 +503,8 @@ typedef struct {
  * Then the scale is d and the new codes are clamp(rne(fp32(x / d)), -127,
  * 127), 0 where d = 0.  Bit-exact.  Slots behind the sequence's length hold
  * codes of no meaning, which are never used.
- * Two sequences of one call must not get new tokens in the same block, and no
- * other work may use the blocks that are written.
+ * The blocks that get new tokens must all be different, within a sequence and
+ * between those of a call, and no other work may use them meanwhile.
  *   n_tok < 2^31, B < 2^24, max_blocks * T < 2^31 (BL_ERR_HIP if a grid
  *   passes the runtime's 2^32 threads).  n_tok == 0 or B == 0: no-op.
  */

@@ -639,7 +639,8 @@ def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=N
                             stream=None):
     """Causal attention of q [n_tok, QH, D] (fp32 or bf16) over the cache:
     out [n_tok, QH, D].  scale defaults to D ** -0.5; q_start, lengths, table
-    as for bitlinear_kv8_append.  Rows of no sequence are left as they are."""
+    as for bitlinear_kv8_append.  Rows of no sequence are left as they are.
+    out may not overlap q."""
     dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
     c = _kv8(cache, dev)
     if D != c.D:
@@ -673,7 +674,8 @@ def bitlinear_decode_stack_kv(layers, caches, x, q_start, lengths, table, H, KV,
                               scale=None, trace=False, ws=None, stream=None):
     """bitlinear_decode_stack with the attention over 8-bit caches: one token of
     one sequence through len(layers) layers, each appending to its Kv8Cache and
-    attending over it.  q_start int32 [2] = [0, 1], lengths int32 [1] (with the
+    attending over it, q and k as their BitLinears give them (not rotated).
+    q_start int32 [2] = [0, 1], lengths int32 [1] (with the
     new token) and table int32 [1, max_blocks] on the GPU.  x fp32 [H] is
     updated in place; scale defaults to D ** -0.5."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:

@@ -114,7 +114,9 @@ constexpr float kSlack = 1.9f;
 // value scale in it, rounded with m: 2^-14 at 2^11, a quarter of what rounding
 // the weight to 11 bits takes.  From there on m follows every maximum, and the
 // scores are rounded and m is taken off them before the exponent is formed, so
-// that the largest weight is 1 and a value scale costs nothing.
+// that the largest weight is 1 and a value scale costs nothing.  Such scores cost
+// 1 to 3% (2 prompts of 2048 and 1500 bf16 rows 166 and 170 us, 64 ragged
+// sequences of up to 4096 keys 43.3 and 43.8).
 template <bool BF16>
 constexpr float kFarScore = BF16 ? 2048.0f : 262144.0f;
 template <bool BF16>
@@ -1222,6 +1224,10 @@ void join(const Args &a, int64_t rows, int64_t parts, hipStream_t s) {
 // Many rows: as many parts of the keys as keep a workgroup on every CU, if that
 // can save three steps; how many a sequence has, and of what keys, its length
 // says on the device (parts behind its end exit at once).
+//
+// The form and whether there is a join at all go by max_blocks, as a launch's grid
+// has to: with room for 8192 keys 128 rows on 500 take 22 us and not 8, and one
+// row on 200 takes 7.9 and not 5.8.
 //
 // Few rows: units are cut where one sequence may be longer than three steps and
 // they are few, or where the longest could hold up the others or a prompt for
