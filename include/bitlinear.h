@@ -547,6 +547,94 @@ bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64_t n_tok, 
 size_t bitlinear_kv8_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
                                         int64_t KVH, int64_t T, int64_t D);
 
+/* Rotation of rows by their positions (rotary embedding).  cos_sin is a DEVICE
+ * table: row p holds the cosines of the rot / 2 angles of position p, then their
+ * sines.  Pair i of a head's first rot values is (i, i + rot / 2), or (2i, 2i +
+ * 1) where interleaved; (x, y) becomes
+ *   x' = fp32(x c - y s),  y' = fp32(y c + x s),
+ * products and sums in 64 bits, rounded once.  Values from rot on stay.
+ *   rows          >= max_blocks * T of the call (BL_ERR_SHAPE): every position
+ *                 that a cache can hold has a row.
+ *   rot           a multiple of 16, 16 <= rot <= D.
+ */
+typedef struct {
+    const float *cos_sin;      /* fp32 [rows][rot], 16-byte aligned */
+    int64_t rows, rot;
+    int32_t interleaved, reserved;
+} bl_rope;
+
+/* bitlinear_kv8_append_rope -- bitlinear_kv8_append of the keys rotated by their
+ * tokens' positions (v as it is), and the queries of the same rows rotated.
+ *   q      in   [n_tok][QH][D] of `dtype`, 16-byte aligned; QH = 0: no queries (q
+ *               and q_out may be NULL).  0 <= QH <= 65535, n_tok * QH < 2^31.
+ *   q_out  out  [n_tok][QH][D] of `dtype`, 16-byte aligned: q rotated, rounded
+ *               once more for bf16.  It may be q; it may not overlap q otherwise
+ *               (BL_ERR_ALIGN), nor k, v or the cache.  Rows of no sequence are left, rows at positions
+ *               that the cache has no room for (below 0, from max_blocks * T on)
+ *               are copied.
+ * The key's codes are formed of the rotated fp32 values; everything else as for
+ * bitlinear_kv8_append.
+ */
+bl_status bitlinear_kv8_append_rope(const void *k, const void *v, const void *q, void *q_out,
+                                    bl_dtype dtype, int64_t n_tok, int64_t QH,
+                                    const int32_t *q_start, const int32_t *lengths,
+                                    const int32_t *table, int64_t B, int64_t max_blocks,
+                                    const bl_kv8 *cache, const bl_rope *rope, void *stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit key/value cache: the paged cache in half the bytes.  Blocks, heads,
+ * sequences and the arrays of a call as for the 8-bit cache; the format:
+ *
+ *     K   uint8 [n_blocks][KVH][T][D/2]: byte i of a token holds the code of
+ *         value 2i in bits 0..3, of value 2i + 1 in bits 4..7.
+ *     V   uint8 [n_blocks][KVH][T/16][D][8]: byte i of a value holds the code of
+ *         token 2i of the 16 in bits 0..3, of token 2i + 1 in bits 4..7 (the
+ *         second product of the attention reads 16 tokens of a value).
+ *     zk, zv  fp16 [n_blocks][KVH][T][2]: a token's least value z and step s.
+ * A value is z + code * s, code = 0 .. 15.  Each token and head has a z and an s of its
+ * own, so an append never touches what is there.
+ */
+typedef struct {
+    uint8_t *K, *V;            /* 16-byte aligned */
+    uint16_t *zk, *zv;         /* 16-byte aligned */
+    int64_t n_blocks, KVH, T, D;
+} bl_kv4;
+
+/* bitlinear_kv4_append -- the new tokens' rows into the 4-bit cache.
+ *   k, v   in   [n_tok][KVH][D] of `dtype`, 16-byte aligned; values beyond
+ *               +-65504 (fp16's largest) count as that, NaN as -65504.
+ *   rope   in   NULL: rows as they are, q, q_out and QH are not used.  Else k and q
+ *               are rotated as by bitlinear_kv8_append_rope, and q, q_out and QH
+ *               are as there.
+ * Per token and head, for K and for V: z = the largest fp16 <= min x, s =
+ * fp16(fp32(fp32(max x - z) / 15)), code = clamp(rne(fp32(fp32(x - z) / s)), 0,
+ * 15), 0 where s = 0.  Bit-exact.  Slots without a new token keep their codes, z
+ * and s.
+ * Blocks, limits and no-ops as for bitlinear_kv8_append.
+ */
+bl_status bitlinear_kv4_append(const void *k, const void *v, const void *q, void *q_out,
+                               bl_dtype dtype, int64_t n_tok, int64_t QH, const int32_t *q_start,
+                               const int32_t *lengths, const int32_t *table, int64_t B,
+                               int64_t max_blocks, const bl_kv4 *cache, const bl_rope *rope,
+                               void *stream);
+
+/* bitlinear_kv8_read / bitlinear_kv4_read -- cached rows as values, in order: row
+ * i of the n_b rows of sequence b is its token at lengths[b] - n_b + i, so
+ * with q_start over whole lengths a call reads whole sequences.  Reading from
+ * one cache and appending to the other moves sequences between them.
+ *   k, v   out  [n_tok][KVH][D] of `dtype`, 16-byte aligned: fp32(code * s), or
+ *               fp32(z + code * s) of the 4-bit cache, rounded to `dtype`.  Rows
+ *               whose position holds no token become zeros, rows of no sequence
+ *               are left.  k and v may not overlap (BL_ERR_ALIGN).
+ * Limits and no-ops as for the append.
+ */
+bl_status bitlinear_kv8_read(const bl_kv8 *cache, const int32_t *q_start, const int32_t *lengths,
+                             const int32_t *table, int64_t B, int64_t max_blocks, int64_t n_tok,
+                             void *k, void *v, bl_dtype dtype, void *stream);
+bl_status bitlinear_kv4_read(const bl_kv4 *cache, const int32_t *q_start, const int32_t *lengths,
+                             const int32_t *table, int64_t B, int64_t max_blocks, int64_t n_tok,
+                             void *k, void *v, bl_dtype dtype, void *stream);
+
 /* bitlinear_decode_stack_kv -- bitlinear_decode_stack with an attention in the
  * place of its one-key stand-in: in each layer k and v (fp32) are appended to
  * the layer's cache and a = bitlinear_kv8_attention of q over it.

@@ -32,6 +32,7 @@ EXPORTS = ["quant_weight_absmean_pack", "quant_weight_absmean_pack_noalloc", "qu
            "bitlinear_backward_input", "bitlinear_backward_weight",
            "bitlinear_t5_row_bytes", "bitlinear_repack_t5", "bitlinear_gemv_t5",
            "bitlinear_kv8_append", "bitlinear_kv8_attention", "bitlinear_kv8_attention_ws_bytes",
+           "bitlinear_kv8_append_rope", "bitlinear_kv8_read", "bitlinear_kv4_append", "bitlinear_kv4_read",
            "bitlinear_decode_stack_kv", "bitlinear_decode_stack_kv_ws_bytes",
            "quant_weight_absmax_i4", "dequant_weight_i4", "bitlinear_gemv_w4",
            "bl_workspace_bytes", "bl_status_string", "bl_last_error", "bl_abi_version"]
@@ -75,9 +76,28 @@ class Kv8(ctypes.Structure):
                 ("T", ctypes.c_int64), ("D", ctypes.c_int64)]
 
 
+class Kv4(ctypes.Structure):
+    """bl_kv4 (include/bitlinear.h)."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("zk", ctypes.c_void_p),
+                ("zv", ctypes.c_void_p), ("n_blocks", ctypes.c_int64), ("KVH", ctypes.c_int64),
+                ("T", ctypes.c_int64), ("D", ctypes.c_int64)]
+
+
+class BlRope(ctypes.Structure):
+    """bl_rope (include/bitlinear.h)."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("rows", ctypes.c_int64), ("rot", ctypes.c_int64),
+                ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 # An 8-bit key/value cache: K int8 [n_blocks, KVH, T, D], V int8 [n_blocks,
 # KVH, D, T], sk and sv fp32 [n_blocks, KVH].  Calls take any such 4-tuple.
 Kv8Cache = collections.namedtuple("Kv8Cache", ("K", "V", "sk", "sv"))
+# A 4-bit one: K uint8 [n_blocks, KVH, T, D/2], V uint8 [n_blocks, KVH, T/16, D,
+# 8], zk and zv fp16 [n_blocks, KVH, T, 2] (least value and step).
+Kv4Cache = collections.namedtuple("Kv4Cache", ("K", "V", "zk", "zv"))
+# A rotation: cos_sin fp32 [positions, rot], rot / 2 cosines and then rot / 2
+# sines a row; pairs (2i, 2i + 1) where interleaved, else (i, i + rot / 2).
+Rope = collections.namedtuple("Rope", ("cos_sin", "interleaved"), defaults=(False,))
 
 _lib = None
 _p = ctypes.c_void_p
@@ -145,6 +165,16 @@ def load():
                                             ctypes.POINTER(Kv8), ctypes.c_float, _p, _p, _sz, _p]
     lib.bitlinear_kv8_attention_ws_bytes.restype = _sz
     lib.bitlinear_kv8_attention_ws_bytes.argtypes = [_i64] * 7
+    lib.bitlinear_kv8_append_rope.restype = st
+    lib.bitlinear_kv8_append_rope.argtypes = [_p, _p, _p, _p, i32, _i64, _i64, _p, _p, _p, _i64, _i64,
+                                              ctypes.POINTER(Kv8), ctypes.POINTER(BlRope), _p]
+    lib.bitlinear_kv4_append.restype = st
+    lib.bitlinear_kv4_append.argtypes = [_p, _p, _p, _p, i32, _i64, _i64, _p, _p, _p, _i64, _i64,
+                                         ctypes.POINTER(Kv4), ctypes.POINTER(BlRope), _p]
+    for name, kind in (("bitlinear_kv8_read", Kv8), ("bitlinear_kv4_read", Kv4)):
+        f = getattr(lib, name)
+        f.restype = st
+        f.argtypes = [ctypes.POINTER(kind), _p, _p, _p, _i64, _i64, _i64, _p, _p, i32, _p]
     lib.bitlinear_decode_stack_kv.restype = st
     lib.bitlinear_decode_stack_kv.argtypes = [
         ctypes.POINTER(Layer), ctypes.POINTER(Kv8), i32, ctypes.POINTER(StackDims), _p, _p, _p, _i64,
@@ -608,6 +638,33 @@ def _kv8(cache, dev):
                _at(sv, torch.float32, dev, (nb, KVH), "cache sv"), nb, KVH, T, D)
 
 
+def kv4_cache(n_blocks, KVH, T=64, D=128, device="cuda"):
+    """A zeroed Kv4Cache."""
+    def z(*shape, dtype=torch.uint8):
+        return torch.zeros(shape, dtype=dtype, device=device)
+    return Kv4Cache(z(n_blocks, KVH, T, D // 2), z(n_blocks, KVH, T // 16, D, 8),
+                    z(n_blocks, KVH, T, 2, dtype=torch.float16), z(n_blocks, KVH, T, 2, dtype=torch.float16))
+
+
+def _kv4(cache, dev):
+    K, V, zk, zv = cache
+    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise ValueError("the cache's K must be a tensor [n_blocks, KVH, T, D/2]")
+    nb, KVH, T, half = K.shape
+    return Kv4(_at(K, torch.uint8, dev, (nb, KVH, T, half), "cache K"),
+               _at(V, torch.uint8, dev, (nb, KVH, T // 16, 2 * half, 8), "cache V"),
+               _at(zk, torch.float16, dev, (nb, KVH, T, 2), "cache zk"),
+               _at(zv, torch.float16, dev, (nb, KVH, T, 2), "cache zv"), nb, KVH, T, 2 * half)
+
+
+def _rope(rope, dev):
+    cos_sin, interleaved = rope
+    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+        raise ValueError("the rotation's cos_sin must be a tensor [positions, rot]")
+    rows, rot = cos_sin.shape
+    return BlRope(_at(cos_sin, torch.float32, dev, (rows, rot), "cos_sin"), rows, rot, bool(interleaved), 0)
+
+
 def _seqs(q_start, lengths, table, dev):
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be a tensor [B, max_blocks]")
@@ -633,6 +690,96 @@ def bitlinear_kv8_append(k, v, q_start, lengths, table, cache, stream=None):
         st = load().bitlinear_kv8_append(kp, vp, dt, n, *meta, c, handle)
     if st:
         _check("bitlinear_kv8_append", st)
+
+
+def _append_turned(call, device_cache, k, v, q_start, lengths, table, cache, rope, q, q_out, stream):
+    dev, dt, kp, shape = _rows(k, 3, "k")
+    c = device_cache(cache, dev)
+    n = shape[0]
+    if shape[1] != c.KVH or shape[2] != c.D:
+        raise ValueError(f"k must be [n_tok, {c.KVH}, {c.D}], got {list(shape)}")
+    vp = _at(v, k.dtype, dev, shape, "v")
+    meta = _seqs(q_start, lengths, table, dev)
+    r = None if rope is None else _rope(rope, dev)
+    qp, op, QH = None, None, 0
+    if q is not None:
+        if r is None:
+            raise ValueError("q is rotated with the keys: without rope there is nothing to do with it")
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError(f"q must be a tensor [{n}, QH, {c.D}]")
+        QH = q.shape[1]
+        qp = _at(q, k.dtype, dev, (n, QH, c.D), "q")
+    if q_out is not None:
+        if q is None:
+            raise ValueError("q_out without q")
+        op = _at(q_out, k.dtype, dev, (n, QH, c.D), "q_out")
+    handle, context = _where(dev, stream)
+    with context:
+        if q is not None and q_out is None:
+            q_out = torch.empty_like(q)
+            op = q_out.data_ptr()
+        st = getattr(load(), call)(kp, vp, qp, op, dt, n, QH, *meta, c, r, handle)
+    if st:
+        _check(call, st)
+    return q_out
+
+
+def bitlinear_kv8_append_rope(k, v, q_start, lengths, table, cache, rope, q=None, q_out=None, stream=None):
+    """bitlinear_kv8_append of the keys rotated by their tokens' positions (rope:
+    Rope, a row of cos_sin for each of the table's positions at least).  Returns q
+    [n_tok, QH, D] rotated the same way, in q_out if given (which may be q), None
+    without q; its rows of no sequence are left as they are."""
+    if rope is None:
+        raise ValueError("bitlinear_kv8_append_rope without rope")
+    return _append_turned("bitlinear_kv8_append_rope", _kv8, k, v, q_start, lengths, table, cache, rope, q,
+                          q_out, stream)
+
+
+def bitlinear_kv4_append(k, v, q_start, lengths, table, cache, rope=None, q=None, q_out=None, stream=None):
+    """The new tokens' rows k, v [n_tok, KVH, D] (fp32 or bf16) into the 4-bit cache
+    (Kv4Cache, updated in place), as they are or, with rope, keys and q rotated as
+    by bitlinear_kv8_append_rope (which see for q and what is returned)."""
+    return _append_turned("bitlinear_kv4_append", _kv4, k, v, q_start, lengths, table, cache, rope, q, q_out,
+                          stream)
+
+
+def _read(call, device_cache, q_start, lengths, table, cache, n_tok, dtype, k, v, stream):
+    K = cache[0]
+    if not isinstance(K, torch.Tensor) or not K.is_cuda:
+        raise TypeError("the cache's K must be a CUDA (HIP) tensor")
+    dev = K.get_device()
+    c = device_cache(cache, dev)
+    meta = _seqs(q_start, lengths, table, dev)
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be float32 or bfloat16")
+    if n_tok < 0:
+        raise ValueError(f"n_tok must not be negative, got {n_tok}")
+    shape = (n_tok, c.KVH, c.D)
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None:
+            _at(t, dtype, dev, shape, name)
+    handle, context = _where(dev, stream)
+    with context:
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=K.device)
+        if v is None:
+            v = torch.empty(shape, dtype=dtype, device=K.device)
+        st = getattr(load(), call)(c, *meta, n_tok, k.data_ptr(), v.data_ptr(), _DTYPES[dtype], handle)
+    if st:
+        _check(call, st)
+    return k, v
+
+
+def bitlinear_kv8_read(q_start, lengths, table, cache, n_tok, dtype=torch.float32, k=None, v=None, stream=None):
+    """The cached tokens of rows 0 .. n_tok - 1 of a call as values, k and v
+    [n_tok, KVH, D] of dtype (fp32 or bf16): the n_b rows of sequence b are its
+    last n_b tokens.  q_start, lengths, table as for bitlinear_kv8_append."""
+    return _read("bitlinear_kv8_read", _kv8, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
+
+
+def bitlinear_kv4_read(q_start, lengths, table, cache, n_tok, dtype=torch.float32, k=None, v=None, stream=None):
+    """bitlinear_kv8_read of a 4-bit cache."""
+    return _read("bitlinear_kv4_read", _kv4, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
 
 
 def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,

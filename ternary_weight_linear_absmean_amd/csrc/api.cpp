@@ -664,15 +664,15 @@ BL_EXPORT bl_status bitlinear_gemv_t5(const int8_t *Xq, const float *d, int64_t 
                     name);
 }
 
-// Shared checks of the two calls on the 8-bit cache (rows: k or q; rows2: v or
-// out); *noop is set when there is no row.
-static bl_status check_kv8(const char *name, const void *rows, const void *rows2, bl_dtype dtype,
-                           int64_t n_tok, const int32_t *q_start, const int32_t *lengths,
-                           const int32_t *table, int64_t B, int64_t max_blocks,
-                           const bl_kv8 *c, bool *noop) {
+// Shared checks of the calls on a cache C = bl_kv8 or bl_kv4, whose scales s1,
+// s2 are s_align-byte aligned (rows: k or q; rows2: v or out); *noop is set when
+// there is no row.
+template <typename C>
+static bl_status check_cache(const char *name, const void *rows, const void *rows2, bl_dtype dtype,
+                             int64_t n_tok, const int32_t *q_start, const int32_t *lengths,
+                             const int32_t *table, int64_t B, int64_t max_blocks, const C *c,
+                             const void *s1, const void *s2, size_t s_align, bool *noop) {
     *noop = false;
-    if (!c)
-        return fail(BL_ERR_NULL, "%s: cache is NULL", name);
     if ((c->T != 16 && c->T != 32 && c->T != 64 && c->T != 128) || (c->D != 64 && c->D != 128))
         return fail(BL_ERR_SHAPE, "%s: need T = 16, 32, 64 or 128 and D = 64 or 128 (T=%lld D=%lld)",
                     name, (long long)c->T, (long long)c->D);
@@ -691,18 +691,35 @@ static bl_status check_kv8(const char *name, const void *rows, const void *rows2
         return ok();
     }
     if (!rows || !rows2 || !q_start || !lengths || (max_blocks > 0 && !table) ||
-        (c->n_blocks > 0 && (!c->K || !c->V || !c->sk || !c->sv)))
+        (c->n_blocks > 0 && (!c->K || !c->V || !s1 || !s2)))
         return fail(BL_ERR_NULL, "%s: NULL pointer (rows=%p %p q_start=%p lengths=%p table=%p K=%p "
-                    "V=%p sk=%p sv=%p)", name, rows, rows2, (const void *)q_start,
-                    (const void *)lengths, (const void *)table, (void *)c->K, (void *)c->V,
-                    (void *)c->sk, (void *)c->sv);
+                    "V=%p scales=%p %p)", name, rows, rows2, (const void *)q_start,
+                    (const void *)lengths, (const void *)table, (void *)c->K, (void *)c->V, s1, s2);
     if (!aligned(rows, 16) || !aligned(rows2, 16) || !aligned(c->K, 16) || !aligned(c->V, 16))
         return fail(BL_ERR_ALIGN, "%s: rows, K and V must be 16-byte aligned", name);
-    if (!aligned(q_start, 4) || !aligned(lengths, 4) || !aligned(table, 4) ||
-        !aligned(c->sk, 4) || !aligned(c->sv, 4))
-        return fail(BL_ERR_ALIGN, "%s: q_start, lengths, table, sk and sv must be 4-byte aligned",
-                    name);
+    if (!aligned(q_start, 4) || !aligned(lengths, 4) || !aligned(table, 4) || !aligned(s1, s_align) ||
+        !aligned(s2, s_align))
+        return fail(BL_ERR_ALIGN, "%s: q_start, lengths and table must be 4-byte aligned, the scales "
+                    "%zu-byte", name, s_align);
     return BL_OK;
+}
+static bl_status check_kv8(const char *name, const void *rows, const void *rows2, bl_dtype dtype,
+                           int64_t n_tok, const int32_t *q_start, const int32_t *lengths,
+                           const int32_t *table, int64_t B, int64_t max_blocks,
+                           const bl_kv8 *c, bool *noop) {
+    if (!c)
+        return fail(BL_ERR_NULL, "%s: cache is NULL", name);
+    return check_cache(name, rows, rows2, dtype, n_tok, q_start, lengths, table, B, max_blocks, c, c->sk,
+                       c->sv, 4, noop);
+}
+static bl_status check_kv4(const char *name, const void *rows, const void *rows2, bl_dtype dtype,
+                           int64_t n_tok, const int32_t *q_start, const int32_t *lengths,
+                           const int32_t *table, int64_t B, int64_t max_blocks,
+                           const bl_kv4 *c, bool *noop) {
+    if (!c)
+        return fail(BL_ERR_NULL, "%s: cache is NULL", name);
+    return check_cache(name, rows, rows2, dtype, n_tok, q_start, lengths, table, B, max_blocks, c, c->zk,
+                       c->zv, 16, noop);
 }
 
 BL_EXPORT bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype dtype,
@@ -721,6 +738,138 @@ BL_EXPORT bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype 
     const bl::Kv8Seqs seqs = {q_start, lengths, table, (int)n_tok, (int)B, (int)max_blocks};
     return launched(bl::launch_kv8_append(k, v, dtype == BL_BF16 ? 1 : 0, seqs, *cache,
                                           static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+// Whether two buffers of `bytes` each share a byte.
+static bool overlap(const void *p, const void *q, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + bytes && b < a + bytes;
+}
+
+// A rotation of D-value heads for positions below `room`, and the queries that
+// are rotated with the keys (checked also where there is no row).
+static bl_status check_rope(const char *name, const bl_rope *r, int64_t D, int64_t room, const void *q,
+                            const void *q_out, bl_dtype dtype, int64_t n_tok, int64_t QH) {
+    if (r->rot < 16 || r->rot > D || r->rot % 16 != 0 || r->rows < room)
+        return fail(BL_ERR_SHAPE, "%s: need rot a multiple of 16 in [16, %lld], rows >= max_blocks * T = "
+                    "%lld (rot=%lld rows=%lld)", name, (long long)D, (long long)room, (long long)r->rot,
+                    (long long)r->rows);
+    if (QH < 0 || QH > 65535 || (QH > 0 && n_tok > kI32Max / QH))
+        return fail(BL_ERR_SHAPE, "%s: need QH in [0, 65535], n_tok * QH < 2^31 (QH=%lld n_tok=%lld)",
+                    name, (long long)QH, (long long)n_tok);
+    if (n_tok == 0)
+        return BL_OK;
+    if ((room > 0 && !r->cos_sin) || (QH > 0 && (!q || !q_out)))
+        return fail(BL_ERR_NULL, "%s: NULL pointer (cos_sin=%p q=%p q_out=%p)", name,
+                    (const void *)r->cos_sin, q, q_out);
+    if (!aligned(r->cos_sin, 16) || (QH > 0 && (!aligned(q, 16) || !aligned(q_out, 16))))
+        return fail(BL_ERR_ALIGN, "%s: cos_sin, q and q_out must be 16-byte aligned", name);
+    const size_t bytes = (size_t)(n_tok * QH * D) * (dtype == BL_BF16 ? 2 : 4);
+    if (q != q_out && overlap(q, q_out, bytes))
+        return fail(BL_ERR_ALIGN, "%s: q_out overlaps q (%p, %p, %zu bytes each)", name, q_out, q,
+                    bytes);
+    return BL_OK;
+}
+
+BL_EXPORT bl_status bitlinear_kv8_append_rope(const void *k, const void *v, const void *q, void *q_out,
+                                              bl_dtype dtype, int64_t n_tok, int64_t QH,
+                                              const int32_t *q_start, const int32_t *lengths,
+                                              const int32_t *table, int64_t B, int64_t max_blocks,
+                                              const bl_kv8 *cache, const bl_rope *rope,
+                                              void *stream) {
+    const char *name = "bitlinear_kv8_append_rope";
+    bool noop = false;
+    if (!rope)
+        return fail(BL_ERR_NULL, "%s: rope is NULL", name);
+    bl_status st = check_kv8(name, k, v, dtype, n_tok, q_start, lengths, table, B, max_blocks,
+                             cache, &noop);
+    if (st != BL_OK)
+        return st;
+    st = check_rope(name, rope, cache->D, max_blocks * cache->T, q, q_out, dtype, noop ? 0 : n_tok, QH);
+    if (st != BL_OK || noop)
+        return st;
+    st = check_arch();
+    if (st != BL_OK)
+        return st;
+    const bl::Kv8Seqs seqs = {q_start, lengths, table, (int)n_tok, (int)B, (int)max_blocks};
+    return launched(bl::launch_kv8_append_rope(k, v, q, q_out, dtype == BL_BF16 ? 1 : 0, (int)QH, seqs,
+                                               *cache, *rope, static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+BL_EXPORT bl_status bitlinear_kv4_append(const void *k, const void *v, const void *q, void *q_out,
+                                         bl_dtype dtype, int64_t n_tok, int64_t QH,
+                                         const int32_t *q_start, const int32_t *lengths,
+                                         const int32_t *table, int64_t B, int64_t max_blocks,
+                                         const bl_kv4 *cache, const bl_rope *rope, void *stream) {
+    const char *name = "bitlinear_kv4_append";
+    bool noop = false;
+    bl_status st = check_kv4(name, k, v, dtype, n_tok, q_start, lengths, table, B, max_blocks,
+                             cache, &noop);
+    if (st != BL_OK)
+        return st;
+    if (rope)
+        st = check_rope(name, rope, cache->D, max_blocks * cache->T, q, q_out, dtype, noop ? 0 : n_tok, QH);
+    if (st != BL_OK || noop)
+        return st;
+    st = check_arch();
+    if (st != BL_OK)
+        return st;
+    const bl::Kv8Seqs seqs = {q_start, lengths, table, (int)n_tok, (int)B, (int)max_blocks};
+    return launched(bl::launch_kv4_append(k, v, q, q_out, dtype == BL_BF16 ? 1 : 0, rope ? (int)QH : 0,
+                                          seqs, *cache, rope, static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+static bl_status check_read_out(const char *name, const void *k, const void *v, int64_t n_tok,
+                                int64_t KVH, int64_t D, bl_dtype dtype) {
+    if (overlap(k, v, (size_t)n_tok * (size_t)(KVH * D) * (dtype == BL_BF16 ? 2 : 4)))
+        return fail(BL_ERR_ALIGN, "%s: k and v overlap (%p, %p)", name, k, v);
+    return BL_OK;
+}
+
+BL_EXPORT bl_status bitlinear_kv8_read(const bl_kv8 *cache, const int32_t *q_start,
+                                       const int32_t *lengths, const int32_t *table, int64_t B,
+                                       int64_t max_blocks, int64_t n_tok, void *k, void *v,
+                                       bl_dtype dtype, void *stream) {
+    const char *name = "bitlinear_kv8_read";
+    bool noop = false;
+    bl_status st = check_kv8(name, k, v, dtype, n_tok, q_start, lengths, table, B, max_blocks,
+                             cache, &noop);
+    if (st != BL_OK || noop)
+        return st;
+    st = check_read_out(name, k, v, n_tok, cache->KVH, cache->D, dtype);
+    if (st != BL_OK)
+        return st;
+    st = check_arch();
+    if (st != BL_OK)
+        return st;
+    const bl::Kv8Seqs seqs = {q_start, lengths, table, (int)n_tok, (int)B, (int)max_blocks};
+    return launched(bl::launch_kv8_read(seqs, *cache, k, v, dtype == BL_BF16 ? 1 : 0,
+                                        static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+BL_EXPORT bl_status bitlinear_kv4_read(const bl_kv4 *cache, const int32_t *q_start,
+                                       const int32_t *lengths, const int32_t *table, int64_t B,
+                                       int64_t max_blocks, int64_t n_tok, void *k, void *v,
+                                       bl_dtype dtype, void *stream) {
+    const char *name = "bitlinear_kv4_read";
+    bool noop = false;
+    bl_status st = check_kv4(name, k, v, dtype, n_tok, q_start, lengths, table, B, max_blocks,
+                             cache, &noop);
+    if (st != BL_OK || noop)
+        return st;
+    st = check_read_out(name, k, v, n_tok, cache->KVH, cache->D, dtype);
+    if (st != BL_OK)
+        return st;
+    st = check_arch();
+    if (st != BL_OK)
+        return st;
+    const bl::Kv8Seqs seqs = {q_start, lengths, table, (int)n_tok, (int)B, (int)max_blocks};
+    return launched(bl::launch_kv4_read(seqs, *cache, k, v, dtype == BL_BF16 ? 1 : 0,
+                                        static_cast<hipStream_t>(stream)),
                     name);
 }
 
@@ -767,10 +916,9 @@ BL_EXPORT bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64
                     need);
     if (!aligned(ws, 16))
         return fail(BL_ERR_ALIGN, "%s: ws must be 16-byte aligned", name);
-    const uintptr_t bytes = (uintptr_t)(n_tok * QH * cache->D) * (dtype == BL_BF16 ? 2 : 4);
-    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), out0 = reinterpret_cast<uintptr_t>(out);
-    if (q0 < out0 + bytes && out0 < q0 + bytes)
-        return fail(BL_ERR_ALIGN, "%s: out overlaps q (%p, %p, %zu bytes each)", name, out, q, (size_t)bytes);
+    const size_t bytes = (size_t)(n_tok * QH * cache->D) * (dtype == BL_BF16 ? 2 : 4);
+    if (overlap(q, out, bytes))
+        return fail(BL_ERR_ALIGN, "%s: out overlaps q (%p, %p, %zu bytes each)", name, out, q, bytes);
     st = check_arch();
     if (st != BL_OK)
         return st;

@@ -1,0 +1,177 @@
+// kv4.hip -- new key / value rows into the 4-bit cache, keys and queries turned
+// by their positions on the way.
+//
+// Per token and head, for K and for V apart, over the D values x (within
+// +-65504, the largest fp16; what is beyond counts as that, NaN as -65504):
+//   z = the largest fp16 <= min x,  s = fp16(fl(fl(max x - z) / 15)),
+//   code = clamp(rne(fl(fl(x - z) / s)), 0, 15), 0 where s = 0;
+// the value is z + s code.  z is rounded down so that no value lies below the
+// first code; a step that is rounded down costs the largest value at most 15 /
+// 2048 of a step.  Scales of a token, not of a block: 4-bit codes do not survive
+// being rescaled when a block's largest value grows.  Quotients are correctly
+// rounded, so the cache's bytes are defined to the bit.
+//
+// One workgroup per (16 consecutive positions of a sequence, head, K or V): 16
+// tokens' codes of one value of V are the 8 bytes of a group, so it alone writes
+// them, also where it brings a single token and the others' codes stay.  D / 8
+// threads to a token, 8 values each.  The grid is known without the lengths:
+// sequence b with n_b new tokens touches at most ceil(n_b / 16) + 1 such groups,
+// and the slots first(b) = floor(q_start[b] / 16) + 2 b leave it no fewer.
+#include "kv4_common.h"
+#include "rope.h"
+
+namespace bl {
+namespace {
+
+constexpr int kTokens = 16;       // of a workgroup
+
+// The largest fp16 that is at most x, |x| <= 65504.
+__device__ __forceinline__ _Float16 f16_below(float x) {
+    const _Float16 h = (_Float16)x;
+    const uint16_t w = __builtin_bit_cast(uint16_t, h);
+    const uint16_t down = (w & 0x7FFF) == 0 ? 0x8001 : w & 0x8000 ? w + 1 : w - 1;
+    return (float)h > x ? __builtin_bit_cast(_Float16, down) : h;
+}
+
+template <int D>
+struct Args {
+    Kv8Seqs seqs;
+    Kv4Cache c;
+    Rope rope;
+    const void *k, *v, *q;
+    void *q_out;
+    int QH;
+    int64_t slots;                // of 16 positions; then the queries' workgroups
+};
+
+template <typename E, int D, bool ROPE>
+__global__ __launch_bounds__(2 * D) void kv4_append_kernel(Args<D> a) {
+    constexpr int kThreads = 2 * D, kPer = D / 8;         // threads, those of a token
+    __shared__ alignas(16) uint8_t codes[D][kTokens];
+    const Kv8Seqs &seqs = a.seqs;
+    const Kv4Cache &c = a.c;
+    const int64_t appends = a.slots * c.KVH * 2;
+    if (ROPE && blockIdx.x >= appends) {
+        turn_queries<kThreads>(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, D == 64 ? 6 : 7, seqs,
+                               (int64_t)seqs.max_blocks << c.t_shift, a.rope, blockIdx.x - appends);
+        return;
+    }
+    const uint32_t pair = blockIdx.x / 2, slot = pair / (uint32_t)c.KVH;
+    const bool is_v = blockIdx.x & 1;
+    const int h = (int)(pair - slot * c.KVH);
+    const int b = find_seq(seqs.B, slot, [&](int i) { return (int64_t)(q_at(seqs, i) >> 4) + 2 * (int64_t)i; });
+    const int q0 = q_at(seqs, b), n = q_at(seqs, b + 1) - q0;
+    const int64_t nth = (int64_t)slot - ((q0 >> 4) + 2 * (int64_t)b);
+    if (nth < 0 || n <= 0) return;
+    const int64_t len = seqs.lengths[b], start = len - n;          // of row q0
+    const int64_t j = (max(start, (int64_t)0) >> 4) + nth;         // the sequence's group
+    const int64_t first = max(max(start, (int64_t)0), 16 * j), last = min(len, 16 * j + 16);
+    if (j >= (int64_t)seqs.max_blocks << c.t_shift >> 4 || first >= last) return;
+    const int id = seqs.table[(int64_t)b * seqs.max_blocks + (16 * j >> c.t_shift)];
+    if (id < 0 || id >= c.n_blocks) return;                        // uniform: the block holds no token
+
+    // this thread's token and values; slots without a new token repeat the first
+    const int t = threadIdx.x / kPer, td = threadIdx.x % kPer;
+    const bool mine = 16 * j + t >= first && 16 * j + t < last;
+    const int64_t pos = mine ? 16 * j + t : first;
+    const int64_t row = ((q0 + (pos - start)) * c.KVH + h) * (int64_t)D;
+    const int64_t head = (int64_t)id * c.KVH + h;
+    uint8_t *const group = c.V + (head * (c.T / 16) + (j & (c.T / 16 - 1))) * (int64_t)(8 * D);
+    const int s0 = (int)(first - 16 * j), s1 = (int)(last - 16 * j);
+    const bool whole = s1 - s0 == kTokens;
+    uint2 old = make_uint2(0u, 0u);
+    if (is_v && !whole && threadIdx.x < D) old = *reinterpret_cast<const uint2 *>(group + 8 * threadIdx.x);
+
+    float4 x[2];
+    if (ROPE && !is_v) {
+        const E *const p = static_cast<const E *>(a.k) + row, *rows[2] = {p, p};
+        const int at[2] = {8 * td, 8 * td + 4};
+        const int64_t place[2] = {pos, pos};
+        load_turned<2>(rows, at, place, a.rope, x);
+    } else {
+        const E *p = static_cast<const E *>(is_v ? a.v : a.k) + row + 8 * td;
+        x[0] = load_row4(p);
+        x[1] = load_row4(p + 4);
+    }
+    float f[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    float lo = 65504.0f, hi = -65504.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f[e] = fminf(fmaxf(f[e], -65504.0f), 65504.0f);
+        lo = fminf(lo, f[e]);
+        hi = fmaxf(hi, f[e]);
+    }
+    lo = -group_max(-lo, kPer);
+    hi = group_max(hi, kPer);
+    const _Float16 z = f16_below(lo);
+    const float zf = (float)z;
+    const _Float16 step = (_Float16)__fdiv_rn(__fsub_rn(hi, zf), 15.0f);
+    const float sf = (float)step;
+    uint32_t u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float r = __builtin_rintf(__fdiv_rn(__fsub_rn(f[e], zf), sf));
+        u[e] = sf > 0.0f ? (uint32_t)fminf(fmaxf(r, 0.0f), 15.0f) : 0u;
+    }
+    if (mine && td == 0)
+        (is_v ? c.zv : c.zk)[head * c.T + (int)(pos & (c.T - 1))] = __builtin_bit_cast(uint32_t, half2{z, step});
+    if (!is_v) {
+        if (!mine) return;
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w |= u[e] << (4 * e);
+        *reinterpret_cast<uint32_t *>(c.K + (head * c.T + (int)(pos & (c.T - 1))) * (int64_t)(D / 2) + 4 * td) = w;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) codes[8 * td + e][t] = (uint8_t)u[e];
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    const uint4 w = *reinterpret_cast<const uint4 *>(codes[threadIdx.x]);
+    // bytes 0 n 0 n -> nibbles
+    auto pack = [](uint32_t lo4, uint32_t hi4) {
+        const uint32_t p = lo4 | lo4 >> 4, r = hi4 | hi4 >> 4;
+        return perm(r, p, 0x06040200u);
+    };
+    uint2 fresh = make_uint2(pack(w.x, w.y), pack(w.z, w.w));
+    if (!whole) {
+        const uint64_t keep = ~((~0ull >> (64 - 4 * (s1 - s0))) << (4 * s0));
+        fresh.x = (old.x & (uint32_t)keep) | (fresh.x & ~(uint32_t)keep);
+        fresh.y = (old.y & (uint32_t)(keep >> 32)) | (fresh.y & ~(uint32_t)(keep >> 32));
+    }
+    *reinterpret_cast<uint2 *>(group + 8 * threadIdx.x) = fresh;
+}
+
+template <typename E, int D>
+hipError_t append(const void *k, const void *v, const void *q, void *q_out, int QH, const Kv8Seqs &seqs,
+                  const Kv4Cache &c, const Rope *rope, hipStream_t s) {
+    Args<D> a = {seqs, c, {}, k, v, q, q_out, QH, (seqs.n_tok >> 4) + 2 * (int64_t)seqs.B};
+    int64_t groups = a.slots * c.KVH * 2;
+    if (rope) {
+        a.rope = *rope;
+        groups += rope_groups<2 * D>(seqs.n_tok, QH, D);
+    }
+    if (groups * 2 * D >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
+    if (rope)
+        hipLaunchKernelGGL((kv4_append_kernel<E, D, true>), dim3((unsigned)groups), dim3(2 * D), 0, s, a);
+    else
+        hipLaunchKernelGGL((kv4_append_kernel<E, D, false>), dim3((unsigned)groups), dim3(2 * D), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv4_append(const void *k, const void *v, const void *q, void *q_out, int dtype, int QH,
+                             const Kv8Seqs &seqs, const bl_kv4 &cache, const bl_rope *rope, hipStream_t s) {
+    const Kv4Cache c = kv4_device(cache);
+    Rope r = {};
+    if (rope) r = rope_device(*rope);
+    const Rope *rp = rope ? &r : nullptr;
+    if (c.D == 64)
+        return dtype ? append<uint16_t, 64>(k, v, q, q_out, QH, seqs, c, rp, s)
+                     : append<float, 64>(k, v, q, q_out, QH, seqs, c, rp, s);
+    return dtype ? append<uint16_t, 128>(k, v, q, q_out, QH, seqs, c, rp, s)
+                 : append<float, 128>(k, v, q, q_out, QH, seqs, c, rp, s);
+}
+
+}  // namespace bl

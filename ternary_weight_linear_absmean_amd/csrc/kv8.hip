@@ -21,19 +21,14 @@
 // end of one wave of workgroups; a multiplication with a check in the place of
 // the correctly rounded quotients took 5% off).
 #include "kv8_common.h"
+#include "rope.h"
+
+#include <type_traits>
 
 namespace bl {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float4 load4(const float *p) {
-    return *reinterpret_cast<const float4 *>(p);
-}
-__device__ __forceinline__ float4 load4(const uint16_t *p) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
 
 __device__ __forceinline__ int kv8_code(float x, float d) {
     const float r = __builtin_rintf(__fdiv_rn(x, d));
@@ -55,16 +50,19 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float r) {
 }
 
 // NC = T * D / (4 * kThreads): 4-value pieces of a whole block per thread.
+// ROPE: k's rows are turned on the way to the maximum and the codes.
 template <typename E, int NC>
-__global__ __launch_bounds__(kThreads) void kv8_append_kernel(const E *__restrict__ k,
-                                                              const E *__restrict__ v,
-                                                              Kv8Seqs seqs, Kv8Cache c) {
-    __shared__ alignas(16) uint32_t tile[NC * kThreads];   // the new codes, [slot][D]
-    __shared__ float wave_max[kThreads / 64];
+struct AppendLds {
+    alignas(16) uint32_t tile[NC * kThreads];   // the new codes, [slot][D]
+    float wave_max[kThreads / 64];
+};
+template <typename E, int NC, bool ROPE>
+__device__ __forceinline__ void append_block(const E *__restrict__ k, const E *__restrict__ v, const Kv8Seqs &seqs,
+                                             const Kv8Cache &c, const Rope &rope, int64_t slot, int h, bool is_v,
+                                             AppendLds<E, NC> &lds) {
+    auto &tile = lds.tile;
+    auto &wave_max = lds.wave_max;
     const int T = c.T, D = c.D, sh = c.t_shift;
-    const int64_t slot = blockIdx.x;
-    const int h = blockIdx.y;
-    const bool is_v = blockIdx.z != 0;
 
     const int b = find_seq(seqs.B, slot, [&](int i) {
         return (int64_t)(q_at(seqs, i) >> sh) + 2 * (int64_t)i;
@@ -93,15 +91,41 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(const E *__restric
     float4 r[NC];
     float a = 0.0f;
     const int pieces = total <= kThreads ? 1 : NC;
-    if (pieces == 1) {
+    if (ROPE && !is_v) {
+        // four pieces' 16 loads in flight together
+        auto turned_pieces = [&](auto count, int i0) {
+            constexpr int kAtOnce = decltype(count)::value;
+            const E *rows[kAtOnce];
+            int at[kAtOnce];
+            int64_t pos[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int u = min((int)threadIdx.x + (i0 + i) * kThreads, total - 1);
+                rows[i] = x + (u >> u_shift) * row_step;
+                at[i] = 4 * (u & (units - 1));
+                pos[i] = first + (u >> u_shift);
+            }
+            load_turned<kAtOnce>(rows, at, pos, rope, r + i0);
+#pragma unroll
+            for (int i = i0; i < i0 + kAtOnce; ++i)
+                a = fmaxf(a, fmaxf(fmaxf(fabsf(r[i].x), fabsf(r[i].y)), fmaxf(fabsf(r[i].z), fabsf(r[i].w))));
+        };
+        if (pieces == 1) {
+            turned_pieces(std::integral_constant<int, 1>{}, 0);
+        } else {
+            constexpr int kAtOnce = NC < 4 ? NC : 4;
+#pragma unroll
+            for (int i0 = 0; i0 < NC; i0 += kAtOnce) turned_pieces(std::integral_constant<int, kAtOnce>{}, i0);
+        }
+    } else if (pieces == 1) {
         const int u = min((int)threadIdx.x, total - 1);
-        r[0] = load4(x + (u >> u_shift) * row_step + 4 * (u & (units - 1)));
+        r[0] = load_row4(x + (u >> u_shift) * row_step + 4 * (u & (units - 1)));
         a = fmaxf(fmaxf(fabsf(r[0].x), fabsf(r[0].y)), fmaxf(fabsf(r[0].z), fabsf(r[0].w)));
     } else {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int u = min((int)threadIdx.x + i * kThreads, total - 1);
-            r[i] = load4(x + (u >> u_shift) * row_step + 4 * (u & (units - 1)));
+            r[i] = load_row4(x + (u >> u_shift) * row_step + 4 * (u & (units - 1)));
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i)
@@ -190,6 +214,39 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(const E *__restric
     }
 }
 
+template <typename E, int NC>
+__global__ __launch_bounds__(kThreads) void kv8_append_kernel(const E *__restrict__ k,
+                                                              const E *__restrict__ v,
+                                                              Kv8Seqs seqs, Kv8Cache c) {
+    __shared__ AppendLds<E, NC> lds;
+    append_block<E, NC, false>(k, v, seqs, c, Rope{}, blockIdx.x, blockIdx.y, blockIdx.z != 0, lds);
+}
+
+// The same with the keys turned by their positions, and in the workgroups behind
+// the queries.
+struct RopeArgs {
+    Kv8Seqs seqs;
+    Kv8Cache c;
+    Rope rope;
+    const void *k, *v, *q;
+    void *q_out;
+    int QH;
+    int64_t slots;
+};
+template <typename E, int NC>
+__global__ __launch_bounds__(kThreads) void kv8_append_rope_kernel(RopeArgs a) {
+    __shared__ AppendLds<E, NC> lds;
+    const int64_t appends = a.slots * a.c.KVH * 2;
+    if (blockIdx.x >= appends) {
+        turn_queries<kThreads>(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, a.c.D == 64 ? 6 : 7,
+                               a.seqs, (int64_t)a.seqs.max_blocks << a.c.t_shift, a.rope, blockIdx.x - appends);
+        return;
+    }
+    const uint32_t pair = blockIdx.x / 2, slot = pair / (uint32_t)a.c.KVH;
+    append_block<E, NC, true>(static_cast<const E *>(a.k), static_cast<const E *>(a.v), a.seqs, a.c, a.rope, slot,
+                              (int)(pair - slot * a.c.KVH), blockIdx.x & 1, lds);
+}
+
 template <typename E>
 hipError_t append(const E *k, const E *v, const Kv8Seqs &seqs, const Kv8Cache &c, hipStream_t s) {
     const int64_t slots = (seqs.n_tok >> c.t_shift) + 2 * (int64_t)seqs.B;
@@ -204,6 +261,19 @@ hipError_t append(const E *k, const E *v, const Kv8Seqs &seqs, const Kv8Cache &c
     return hipGetLastError();
 }
 
+template <typename E>
+hipError_t append_rope(const RopeArgs &a, int64_t groups, hipStream_t s) {
+    const dim3 grid((unsigned)groups), block(kThreads);
+    switch (a.c.T * a.c.D / (4 * kThreads)) {
+    case 1: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 1>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 2>), grid, block, 0, s, a); break;
+    case 4: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 4>), grid, block, 0, s, a); break;
+    case 8: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 8>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 16>), grid, block, 0, s, a);
+    }
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_kv8_append(const void *k, const void *v, int dtype, const Kv8Seqs &seqs,
@@ -212,6 +282,15 @@ hipError_t launch_kv8_append(const void *k, const void *v, int dtype, const Kv8S
     return dtype ? append(static_cast<const uint16_t *>(k), static_cast<const uint16_t *>(v), seqs,
                           c, s)
                  : append(static_cast<const float *>(k), static_cast<const float *>(v), seqs, c, s);
+}
+
+hipError_t launch_kv8_append_rope(const void *k, const void *v, const void *q, void *q_out, int dtype, int QH,
+                                  const Kv8Seqs &seqs, const bl_kv8 &cache, const bl_rope &rope, hipStream_t s) {
+    const Kv8Cache c = kv8_device(cache);
+    const RopeArgs a = {seqs, c, rope_device(rope), k, v, q, q_out, QH, (seqs.n_tok >> c.t_shift) + 2 * (int64_t)seqs.B};
+    const int64_t groups = a.slots * c.KVH * 2 + rope_groups<kThreads>(seqs.n_tok, QH, c.D);
+    if (groups * kThreads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
+    return dtype ? append_rope<uint16_t>(a, groups, s) : append_rope<float>(a, groups, s);
 }
 
 }  // namespace bl

@@ -156,6 +156,16 @@ struct Kv8Seqs {
 };
 hipError_t launch_kv8_append(const void *k, const void *v, int dtype, const Kv8Seqs &seqs,
                              const bl_kv8 &cache, hipStream_t s);
+// The same with k turned by the tokens' positions, and q [n_tok][QH][D] into
+// q_out (kv8.hip, rope.h); QH = 0: no queries.
+hipError_t launch_kv8_append_rope(const void *k, const void *v, const void *q, void *q_out, int dtype, int QH,
+                                  const Kv8Seqs &seqs, const bl_kv8 &cache, const bl_rope &rope, hipStream_t s);
+// 4-bit key/value cache (kv4.hip); rope NULL: rows as they are, no queries.
+hipError_t launch_kv4_append(const void *k, const void *v, const void *q, void *q_out, int dtype, int QH,
+                             const Kv8Seqs &seqs, const bl_kv4 &cache, const bl_rope *rope, hipStream_t s);
+// Cached rows as values (kv_read.hip).
+hipError_t launch_kv8_read(const Kv8Seqs &seqs, const bl_kv8 &cache, void *k, void *v, int dtype, hipStream_t s);
+hipError_t launch_kv4_read(const Kv8Seqs &seqs, const bl_kv4 &cache, void *k, void *v, int dtype, hipStream_t s);
 // The caches of a stack whose attention is over cached tokens: one per layer,
 // the arrays of one sequence with one new token, and the attention's workspace.
 struct StackKv {

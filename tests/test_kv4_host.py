@@ -1,0 +1,136 @@
+"""Host-side checks of the rotated appends, the 4-bit cache and the reads, and of
+their oracle (CPU only: every call below is refused or empty)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import ternary_weight_linear_absmean_amd as bl
+from oracle import kv4 as ref
+from ternary_weight_linear_absmean_amd._native import BlRope, Kv4, Kv8
+
+OK, NULL, SHAPE, DTYPE, ALIGN, WS = 0, 1, 2, 3, 4, 5
+A16, B16, A4, A1 = 0x10000, 0x10000000, 0x10004, 0x10001
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return bl.load()
+
+
+def kind(bits, **kw):
+    d = dict(K=A16, V=A16, s1=A16, s2=A16, n_blocks=8, KVH=2, T=64, D=128)
+    d.update(kw)
+    return (Kv8 if bits == 8 else Kv4)(*d.values())
+
+
+def rope(**kw):
+    d = dict(cos_sin=A16, rows=1 << 40, rot=64, interleaved=0, reserved=0)
+    d.update(kw)
+    return BlRope(*d.values())
+
+
+def each(lib, k=A16, v=B16, q=A16, o=B16, dt=0, n=3, QH=8, qs=A4, ln=A4, tb=A4, B=2, nb=4, r=None, c=None):
+    """Status of the two appends and the two reads."""
+    c = c or {}
+    r = rope() if r is None else r
+    rows = qs, ln, tb, B, nb
+    return (lib.bitlinear_kv8_append_rope(k, v, q, o, dt, n, QH, *rows, kind(8, **c), r, None),
+            lib.bitlinear_kv4_append(k, v, q, o, dt, n, QH, *rows, kind(4, **c), r, None),
+            lib.bitlinear_kv8_read(kind(8, **c), *rows, n, k, v, dt, None),
+            lib.bitlinear_kv4_read(kind(4, **c), *rows, n, k, v, dt, None))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n=-1), dict(n=2 ** 31), dict(B=-1), dict(B=1 << 24), dict(nb=-1), dict(nb=INT_MAX // 64 + 1),
+    dict(c=dict(T=8)), dict(c=dict(T=48)), dict(c=dict(T=256)), dict(c=dict(D=32)), dict(c=dict(D=96)),
+    dict(c=dict(D=0)), dict(c=dict(KVH=0)), dict(c=dict(KVH=65536)), dict(c=dict(n_blocks=-1)),
+    dict(c=dict(n_blocks=2 ** 31))])
+def test_shapes(lib, bad):
+    assert each(lib, **bad) == (SHAPE,) * 4
+
+
+@pytest.mark.parametrize("bad", [
+    dict(r=rope(rot=0)), dict(r=rope(rot=8)), dict(r=rope(rot=24)), dict(r=rope(rot=-16)), dict(r=rope(rot=144)),
+    dict(r=rope(rot=80), c=dict(D=64)), dict(r=rope(rows=255)), dict(r=rope(rows=-1)), dict(QH=-1), dict(QH=65536),
+    dict(QH=65535, n=32769), dict(n=0, r=rope(rot=8)), dict(n=0, r=rope(rows=3))])
+def test_rotations(lib, bad):
+    assert each(lib, **bad)[:2] == (SHAPE,) * 2
+
+
+def test_refusals(lib):
+    assert each(lib, dt=7) == (DTYPE,) * 4
+    for bad in (dict(k=None), dict(v=None), dict(qs=None), dict(ln=None), dict(tb=None), dict(c=dict(K=None)),
+                dict(c=dict(V=None)), dict(c=dict(s1=None)), dict(c=dict(s2=None))):
+        assert each(lib, **bad) == (NULL,) * 4, bad
+    for bad in (dict(k=A4), dict(v=A4), dict(qs=A1), dict(ln=A1), dict(tb=A1), dict(c=dict(K=A4)),
+                dict(c=dict(V=A4)), dict(c=dict(s1=A1)), dict(c=dict(s2=A1))):
+        assert each(lib, **bad) == (ALIGN,) * 4, bad
+    # 4-bit scales are read 16 bytes at a time
+    assert each(lib, c=dict(s1=A4))[1::2] == (ALIGN,) * 2 and each(lib, c=dict(s2=A4))[1::2] == (ALIGN,) * 2
+    for bad in (dict(q=None), dict(o=None), dict(r=rope(cos_sin=None))):
+        assert each(lib, **bad)[:2] == (NULL,) * 2, bad
+    for bad in (dict(q=A4), dict(o=A4), dict(r=rope(cos_sin=A4))):
+        assert each(lib, **bad)[:2] == (ALIGN,) * 2, bad
+    # no rows, no sequences, no room for a token
+    assert each(lib, n=0, k=None, v=None, q=None, o=None) == (OK,) * 4
+    assert each(lib, B=0, qs=None, ln=None, tb=None) == (OK,) * 4
+    rows = A4, A4, A4, 2, 4
+    assert lib.bitlinear_kv8_append_rope(A16, B16, None, None, 0, 3, 0, *rows, kind(8), None, None) == NULL
+    for f, c, r in ((lib.bitlinear_kv8_append_rope, Kv8, rope()), (lib.bitlinear_kv4_append, Kv4, None)):
+        assert f(A16, B16, None, None, 0, 3, 0, *rows, ctypes.POINTER(c)(), r, None) == NULL
+    for f, c in ((lib.bitlinear_kv8_read, Kv8), (lib.bitlinear_kv4_read, Kv4)):
+        assert f(ctypes.POINTER(c)(), *rows, 3, A16, B16, 0, None) == NULL
+
+
+def test_overlaps(lib):
+    """3 rows of 8 heads (q) or 2 (k, v) of 128 values, in each type."""
+    for dt, es in ((0, 4), (1, 2)):
+        size = 3 * 8 * 128 * es
+        for by in (16, -16, size - 16, 16 - size):
+            assert each(lib, dt=dt, q=B16, o=B16 + by)[:2] == (ALIGN,) * 2
+        size = 3 * 2 * 128 * es
+        for by in (0, 16, -16, size - 16, 16 - size):
+            assert each(lib, dt=dt, k=B16, v=B16 + by)[2:] == (ALIGN,) * 2
+
+
+# ------------------------------------------------------------- the oracle
+
+def test_oracle_rotation_by_hand():
+    """A quarter and an eighth of a turn, both pairings; the last two values stay."""
+    h = np.float32(0.5) ** np.float32(0.5)
+    table = np.array([[1, 1, 0, 0], [0, h, 1, h]], np.float32)
+    x = np.array([[[1.0, 2, 3, 4, 5, 6]]] * 3)
+    halves = ref.rotate(x, [0, 1, 7], table, False, 2)
+    assert halves[0].tolist() == halves[2].tolist() == x[0].tolist()
+    r = float(h)
+    assert np.allclose(halves[1, 0], [-3, -2 * r, 1, 6 * r, 5, 6], rtol=1e-7)
+    near = ref.rotate(x, [1], table, True, 2)
+    assert np.allclose(near[0, 0], [-2, 1, -r, 7 * r, 5, 6], rtol=1e-7)
+
+
+def test_oracle_codes_by_hand():
+    z, s, u = ref.codes(np.array([[0.0, 15, 7.4, 7.5], [-2, -2, -2, -2], [1e6, -1e6, 0, 1]]))
+    assert z.tolist() == [0, -2, -65504] and s.tolist() == [1, 0, 8736]
+    assert u.tolist() == [[0, 15, 7, 8], [0, 0, 0, 0], [15, 0, 7, 7]]
+    below = ref.f16_below(np.array([1.0, 1 + 2.0 ** -11, -1 - 2.0 ** -11, 0, -1e-9, 1e-9, 65504, -65504, 2.0 ** -24]))
+    assert below.tolist() == [1, 1, -1 - 2.0 ** -10, 0, -2.0 ** -24, 0, 65504, -65504, 2.0 ** -24]
+
+
+def test_oracle_f16_below_is_the_neighbour():
+    x = np.random.default_rng(1).standard_normal(4000) * 10.0 ** np.random.default_rng(2).uniform(-8, 4, 4000)
+    b = ref.f16_below(x)
+    assert (b.astype(np.float16) == b).all() and (b <= x).all()
+    up = np.nextafter(b.astype(np.float16), np.float16(np.inf)).astype(np.float64)
+    assert (up > x).all()
+
+
+def test_oracle_packing():
+    u = np.random.default_rng(0).integers(0, 16, (2, 2, 3, 32, 64))
+    K, V = ref.pack(*u)
+    assert K.shape == (2, 3, 32, 32) and V.shape == (2, 3, 2, 64, 8)
+    assert K[1, 2, 5, 3] == u[0, 1, 2, 5, 6] | u[0, 1, 2, 5, 7] << 4
+    assert V[1, 2, 1, 9, 3] == u[1, 1, 2, 22, 9] | u[1, 1, 2, 23, 9] << 4
+    k, v = ref.unpack(K, V)
+    assert np.array_equal(k, u[0]) and np.array_equal(v, u[1])
