@@ -618,6 +618,26 @@ bl_status bitlinear_kv4_append(const void *k, const void *v, const void *q, void
                                int64_t max_blocks, const bl_kv4 *cache, const bl_rope *rope,
                                void *stream);
 
+/* bitlinear_kv4_attention -- bitlinear_kv8_attention over the 4-bit cache; all
+ * arguments as there.  Steps are >= 0 and finite, as the append writes them, and so
+ * are the least values finite.
+ * The scores, the softmax and all sums are fp32 and no code is rounded; for fp32
+ * rows q and the softmax weights times their step are kept to 22 bits or more, for
+ * bf16 rows the latter are rounded to 11 bits.  An operand's smallest step is 2^-38
+ * of the row's largest |q|, and 2^-38 of the largest weight times a power of two
+ * above the largest step of the values.  Errors scale with sums over |z| + s code
+ * in the place of |value|.
+ */
+bl_status bitlinear_kv4_attention(const void *q, bl_dtype dtype, int64_t n_tok, int64_t QH,
+                                  const int32_t *q_start, const int32_t *lengths,
+                                  const int32_t *table, int64_t B, int64_t max_blocks,
+                                  const bl_kv4 *cache, float scale, void *out, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/* Workspace bytes of bitlinear_kv4_attention; 0 also for sizes it refuses. */
+size_t bitlinear_kv4_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
+                                        int64_t KVH, int64_t T, int64_t D);
+
 /* bitlinear_kv8_read / bitlinear_kv4_read -- cached rows as values, in order: row
  * i of the n_b rows of sequence b is its token at lengths[b] - n_b + i, so
  * with q_start over whole lengths a call reads whole sequences.  Reading from

@@ -10,7 +10,7 @@ from ._native import (  # noqa: F401
     BL_STACK_PERSISTENT, bitlinear_a4, bitlinear_backward_input, bitlinear_backward_weight,
     bitlinear_decode_stack, bitlinear_decode_stack_kv, bitlinear_decode_stack_status,
     bitlinear_ffn_relu2, bitlinear_gemm, bitlinear_gemv, bitlinear_gemv_fused,
-    bitlinear_gemv_t5, bitlinear_gemv_w4, bitlinear_kv4_append, bitlinear_kv4_read,
+    bitlinear_gemv_t5, bitlinear_gemv_w4, bitlinear_kv4_append, bitlinear_kv4_attention, bitlinear_kv4_read,
     bitlinear_kv8_append, bitlinear_kv8_append_rope, bitlinear_kv8_attention, bitlinear_kv8_read,
     bitlinear_repack_t5, BitLinearError, dequant_weight_i4, EXPORTS, GemvJob, kv4_cache, Kv4Cache,
     kv8_cache, Kv8Cache, Layer, LAYER_GAMMAS, LAYER_WEIGHTS, LIB_PATH, load, quant_act_absmax_i4,

@@ -33,6 +33,7 @@ EXPORTS = ["quant_weight_absmean_pack", "quant_weight_absmean_pack_noalloc", "qu
            "bitlinear_t5_row_bytes", "bitlinear_repack_t5", "bitlinear_gemv_t5",
            "bitlinear_kv8_append", "bitlinear_kv8_attention", "bitlinear_kv8_attention_ws_bytes",
            "bitlinear_kv8_append_rope", "bitlinear_kv8_read", "bitlinear_kv4_append", "bitlinear_kv4_read",
+           "bitlinear_kv4_attention", "bitlinear_kv4_attention_ws_bytes",
            "bitlinear_decode_stack_kv", "bitlinear_decode_stack_kv_ws_bytes",
            "quant_weight_absmax_i4", "dequant_weight_i4", "bitlinear_gemv_w4",
            "bl_workspace_bytes", "bl_status_string", "bl_last_error", "bl_abi_version"]
@@ -171,6 +172,11 @@ def load():
     lib.bitlinear_kv4_append.restype = st
     lib.bitlinear_kv4_append.argtypes = [_p, _p, _p, _p, i32, _i64, _i64, _p, _p, _p, _i64, _i64,
                                          ctypes.POINTER(Kv4), ctypes.POINTER(BlRope), _p]
+    lib.bitlinear_kv4_attention.restype = st
+    lib.bitlinear_kv4_attention.argtypes = [_p, i32, _i64, _i64, _p, _p, _p, _i64, _i64,
+                                            ctypes.POINTER(Kv4), ctypes.c_float, _p, _p, _sz, _p]
+    lib.bitlinear_kv4_attention_ws_bytes.restype = _sz
+    lib.bitlinear_kv4_attention_ws_bytes.argtypes = [_i64] * 7
     for name, kind in (("bitlinear_kv8_read", Kv8), ("bitlinear_kv4_read", Kv4)):
         f = getattr(lib, name)
         f.restype = st
@@ -782,14 +788,9 @@ def bitlinear_kv4_read(q_start, lengths, table, cache, n_tok, dtype=torch.float3
     return _read("bitlinear_kv4_read", _kv4, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
 
 
-def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
-                            stream=None):
-    """Causal attention of q [n_tok, QH, D] (fp32 or bf16) over the cache:
-    out [n_tok, QH, D].  scale defaults to D ** -0.5; q_start, lengths, table
-    as for bitlinear_kv8_append.  Rows of no sequence are left as they are.
-    out may not overlap q."""
+def _attend(call, ws_call, device_cache, q, q_start, lengths, table, cache, scale, out, ws, stream):
     dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
-    c = _kv8(cache, dev)
+    c = device_cache(cache, dev)
     if D != c.D:
         raise ValueError(f"q must be [n_tok, QH, {c.D}], got {list(q.shape)}")
     meta = _seqs(q_start, lengths, table, dev)
@@ -803,18 +804,35 @@ def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=N
     handle, context = _where(dev, stream)
     with context:
         if ws is None:
-            size = lib.bitlinear_kv8_attention_ws_bytes(n, QH, meta[3], meta[4], c.KVH, c.T, D)
+            size = getattr(lib, ws_call)(n, QH, meta[3], meta[4], c.KVH, c.T, D)
             if size:
                 ws = torch.empty((size,), dtype=torch.uint8, device=dev)
                 wp = ws.data_ptr()
         if out is None:
             out = torch.empty_like(q)
-        st = lib.bitlinear_kv8_attention(
+        st = getattr(lib, call)(
             qp, dt, n, QH, *meta, c, D ** -0.5 if scale is None else scale, out.data_ptr(), wp, size,
             handle)
     if st:
-        _check("bitlinear_kv8_attention", st)
+        _check(call, st)
     return out
+
+
+def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
+                            stream=None):
+    """Causal attention of q [n_tok, QH, D] (fp32 or bf16) over the cache:
+    out [n_tok, QH, D].  scale defaults to D ** -0.5; q_start, lengths, table
+    as for bitlinear_kv8_append.  Rows of no sequence are left as they are.
+    out may not overlap q."""
+    return _attend("bitlinear_kv8_attention", "bitlinear_kv8_attention_ws_bytes", _kv8, q, q_start, lengths,
+                   table, cache, scale, out, ws, stream)
+
+
+def bitlinear_kv4_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
+                            stream=None):
+    """bitlinear_kv8_attention over a 4-bit cache (Kv4Cache)."""
+    return _attend("bitlinear_kv4_attention", "bitlinear_kv4_attention_ws_bytes", _kv4, q, q_start, lengths,
+                   table, cache, scale, out, ws, stream)
 
 
 def bitlinear_decode_stack_kv(layers, caches, x, q_start, lengths, table, H, KV, F, D, eps=1e-5,

@@ -22,8 +22,8 @@ LIB = os.path.join(HERE, "libbitlinear.so")
 
 SOURCES = ["api.cpp", "quant.hip", "gemv.hip", "gemm.hip", "gemm_skinny.hip", "ffn.hip",
            "stack.hip", "stack_persistent.hip", "backward.hip", "t5.hip",
-           "kv8.hip", "kv8_attention.hip", "kv4.hip", "kv_read.hip",
-           "w4.hip"]
+           "kv8.hip", "kv8_attention.hip", "kv4.hip",
+           "kv4_attention.hip", "kv_read.hip", "w4.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

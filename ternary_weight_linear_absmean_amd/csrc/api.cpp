@@ -873,20 +873,53 @@ BL_EXPORT bl_status bitlinear_kv4_read(const bl_kv4 *cache, const int32_t *q_sta
                     name);
 }
 
-BL_EXPORT size_t bitlinear_kv8_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B,
-                                                  int64_t max_blocks, int64_t KVH, int64_t T,
-                                                  int64_t D) {
+// Bytes of `floats`' workspace; 0 for sizes that the attentions refuse.
+static size_t attention_ws_bytes(size_t (*floats)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t),
+                                 int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH,
+                                 int64_t T, int64_t D) {
     if (n_tok <= 0 || B <= 0 || B >= (1 << 24) || QH < 1 || QH > 65535 || KVH < 1 || QH % KVH != 0 ||
         n_tok > kI32Max / QH || (T != 16 && T != 32 && T != 64 && T != 128) ||
         (D != 64 && D != 128) || max_blocks < 0 || max_blocks > kI32Max / T)
         return 0;
-    return round_up(bl::kv8_attention_ws_floats(n_tok, QH, B, max_blocks, KVH, T, D) * sizeof(float),
-                    256);
+    return round_up(floats(n_tok, QH, B, max_blocks, KVH, T, D) * sizeof(float), 256);
+}
+BL_EXPORT size_t bitlinear_kv8_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B,
+                                                  int64_t max_blocks, int64_t KVH, int64_t T,
+                                                  int64_t D) {
+    return attention_ws_bytes(bl::kv8_attention_ws_floats, n_tok, QH, B, max_blocks, KVH, T, D);
+}
+BL_EXPORT size_t bitlinear_kv4_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B,
+                                                  int64_t max_blocks, int64_t KVH, int64_t T,
+                                                  int64_t D) {
+    return attention_ws_bytes(bl::kv4_attention_ws_floats, n_tok, QH, B, max_blocks, KVH, T, D);
 }
 
 // Whether scale * log2(e), which the kernels multiply by, is a finite fp32.
 static bool scale_in_range(float scale) {
     return scale > -0x1p127f && scale < 0x1p127f;
+}
+
+// The checks of an attention that come after its cache's.
+static bl_status check_attention(const char *name, const void *q, const void *out, bl_dtype dtype,
+                                 int64_t n_tok, int64_t QH, int64_t KVH, int64_t D, float scale,
+                                 const void *ws, size_t ws_bytes, size_t need, bool noop) {
+    if (QH < 1 || QH > 65535 || QH % KVH != 0 || n_tok > kI32Max / QH)
+        return fail(BL_ERR_SHAPE, "%s: need QH in [1, 65535], a multiple of KVH, n_tok * QH < 2^31 "
+                    "(QH=%lld KVH=%lld n_tok=%lld)", name, (long long)QH, (long long)KVH,
+                    (long long)n_tok);
+    if (!scale_in_range(scale))
+        return fail(BL_ERR_SHAPE, "%s: |scale| must be below 2^127", name);
+    if (noop)
+        return ok();
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(BL_ERR_WORKSPACE, "%s: workspace %zu bytes at %p, need %zu", name, ws_bytes, ws,
+                    need);
+    if (!aligned(ws, 16))
+        return fail(BL_ERR_ALIGN, "%s: ws must be 16-byte aligned", name);
+    const size_t bytes = (size_t)(n_tok * QH * D) * (dtype == BL_BF16 ? 2 : 4);
+    if (overlap(q, out, bytes))
+        return fail(BL_ERR_ALIGN, "%s: out overlaps q (%p, %p, %zu bytes each)", name, out, q, bytes);
+    return check_arch();
 }
 
 BL_EXPORT bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64_t n_tok,
@@ -901,29 +934,39 @@ BL_EXPORT bl_status bitlinear_kv8_attention(const void *q, bl_dtype dtype, int64
                              cache, &noop);
     if (st != BL_OK)
         return st;
-    if (QH < 1 || QH > 65535 || QH % cache->KVH != 0 || n_tok > kI32Max / QH)
-        return fail(BL_ERR_SHAPE, "%s: need QH in [1, 65535], a multiple of KVH, n_tok * QH < 2^31 "
-                    "(QH=%lld KVH=%lld n_tok=%lld)", name, (long long)QH, (long long)cache->KVH,
-                    (long long)n_tok);
-    if (!scale_in_range(scale))
-        return fail(BL_ERR_SHAPE, "%s: |scale| must be below 2^127", name);
-    if (noop)
-        return ok();
     const size_t need = bitlinear_kv8_attention_ws_bytes(n_tok, QH, B, max_blocks, cache->KVH,
                                                          cache->T, cache->D);
-    if (need > 0 && (!ws || ws_bytes < need))
-        return fail(BL_ERR_WORKSPACE, "%s: workspace %zu bytes at %p, need %zu", name, ws_bytes, ws,
-                    need);
-    if (!aligned(ws, 16))
-        return fail(BL_ERR_ALIGN, "%s: ws must be 16-byte aligned", name);
-    const size_t bytes = (size_t)(n_tok * QH * cache->D) * (dtype == BL_BF16 ? 2 : 4);
-    if (overlap(q, out, bytes))
-        return fail(BL_ERR_ALIGN, "%s: out overlaps q (%p, %p, %zu bytes each)", name, out, q, bytes);
-    st = check_arch();
-    if (st != BL_OK)
+    st = check_attention(name, q, out, dtype, n_tok, QH, cache->KVH, cache->D, scale, ws, ws_bytes, need,
+                         noop);
+    if (st != BL_OK || noop)
         return st;
     const bl::Kv8Seqs seqs = {q_start, lengths, table, (int)n_tok, (int)B, (int)max_blocks};
     return launched(bl::launch_kv8_attention(q, dtype == BL_BF16 ? 1 : 0, (int)QH, seqs, *cache,
+                                             scale, out, static_cast<float *>(ws),
+                                             static_cast<hipStream_t>(stream)),
+                    name);
+}
+
+BL_EXPORT bl_status bitlinear_kv4_attention(const void *q, bl_dtype dtype, int64_t n_tok,
+                                            int64_t QH, const int32_t *q_start,
+                                            const int32_t *lengths, const int32_t *table,
+                                            int64_t B, int64_t max_blocks, const bl_kv4 *cache,
+                                            float scale, void *out, void *ws, size_t ws_bytes,
+                                            void *stream) {
+    const char *name = "bitlinear_kv4_attention";
+    bool noop = false;
+    bl_status st = check_kv4(name, q, out, dtype, n_tok, q_start, lengths, table, B, max_blocks,
+                             cache, &noop);
+    if (st != BL_OK)
+        return st;
+    const size_t need = bitlinear_kv4_attention_ws_bytes(n_tok, QH, B, max_blocks, cache->KVH,
+                                                         cache->T, cache->D);
+    st = check_attention(name, q, out, dtype, n_tok, QH, cache->KVH, cache->D, scale, ws, ws_bytes, need,
+                         noop);
+    if (st != BL_OK || noop)
+        return st;
+    const bl::Kv8Seqs seqs = {q_start, lengths, table, (int)n_tok, (int)B, (int)max_blocks};
+    return launched(bl::launch_kv4_attention(q, dtype == BL_BF16 ? 1 : 0, (int)QH, seqs, *cache,
                                              scale, out, static_cast<float *>(ws),
                                              static_cast<hipStream_t>(stream)),
                     name);

@@ -201,12 +201,18 @@ hipError_t launch_ffn_tail(const float *G, const float *U, const float *norm_w,
                            float eps, int M, int F, int8_t *Hq, float *dh, float *dz,
                            hipStream_t s);
 
-// Attention over the cache (kv8_attention.hip); ws holds
-// kv8_attention_ws_floats() floats.
+// Attention over the caches (kv8_attention.hip, kv4_attention.hip); ws holds
+// kv8_attention_ws_floats() or kv4_attention_ws_floats() floats.
 size_t kv8_attention_ws_floats(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
                                int64_t KVH, int64_t T, int64_t D);
 hipError_t launch_kv8_attention(const void *q, int dtype, int QH, const Kv8Seqs &seqs,
                                 const bl_kv8 &cache, float scale, void *out, float *ws,
+                                hipStream_t s);
+
+size_t kv4_attention_ws_floats(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
+                               int64_t KVH, int64_t T, int64_t D);
+hipError_t launch_kv4_attention(const void *q, int dtype, int QH, const Kv8Seqs &seqs,
+                                const bl_kv4 &cache, float scale, void *out, float *ws,
                                 hipStream_t s);
 
 // 4-bit weights with group scales (w4.hip); group = 32, 64 or 128.

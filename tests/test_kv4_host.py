@@ -95,6 +95,46 @@ def test_overlaps(lib):
             assert each(lib, dt=dt, k=B16, v=B16 + by)[2:] == (ALIGN,) * 2
 
 
+def attend(lib, q=A16, o=1 << 40, dt=0, n=3, QH=8, qs=A4, ln=A4, tb=A4, B=2, nb=4, c=None, scale=1.0, ws=A16,
+           size=1 << 40):
+    c = kind(4, **(c or {}))
+    return lib.bitlinear_kv4_attention(q, dt, n, QH, qs, ln, tb, B, nb, c, scale, o, ws, size, None)
+
+
+def test_attention_refusals(lib):
+    for bad in (dict(n=-1), dict(B=1 << 24), dict(nb=INT_MAX // 64 + 1), dict(c=dict(T=48)), dict(c=dict(D=96)),
+                dict(c=dict(KVH=0)), dict(c=dict(n_blocks=-1)), dict(QH=0), dict(QH=-2), dict(QH=3), dict(QH=65536),
+                dict(n=2 ** 28), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=2.0 ** 127)):
+        assert attend(lib, **bad) == SHAPE, bad
+    assert attend(lib, dt=2) == DTYPE
+    for bad in (dict(q=None), dict(o=None), dict(qs=None), dict(ln=None), dict(tb=None), dict(c=dict(K=None)),
+                dict(c=dict(s2=None))):
+        assert attend(lib, **bad) == NULL, bad
+    for bad in (dict(q=A4), dict(o=A4), dict(qs=A1), dict(c=dict(V=A4)), dict(c=dict(s1=A4)), dict(c=dict(s2=A4)),
+                dict(ws=A4, nb=4000), dict(o=A16), dict(o=A16 + 3 * 8 * 128 * 4 - 16)):
+        assert attend(lib, **bad) == ALIGN, bad
+    assert attend(lib, n=0, q=None, o=None) == OK and attend(lib, B=0, qs=None, ln=None, tb=None) == OK
+
+
+def test_attention_workspace(lib):
+    """Sizes that are cut or read in parts ask for one; one byte less is refused.  The
+    largest sizes are answered at once."""
+    f = lib.bitlinear_kv4_attention_ws_bytes
+    for n, QH, B, nb, KVH in ((3, 8, 2, 4000, 2), (64, 8, 64, 4000, 2), (300, 8, 1, 1000, 2), (256, 8, 256, 4000, 2)):
+        need = f(n, QH, B, nb, KVH, 64, 128)
+        assert need >= 2 * 4 * 130 * min(16, n * QH // KVH), (n, B, nb)
+        for ws, size in ((None, need), (A16, need - 1), (A16, 0)):
+            assert attend(lib, n=n, QH=QH, B=B, nb=nb, ws=ws, size=size) == WS
+    assert f(3, 8, 2, 4, 2, 64, 128) == 0
+    for bad in ((0, 8, 2, 4, 2, 64, 128), (3, 7, 2, 4, 2, 64, 128), (3, 8, 2, 4, 2, 63, 128), (3, 8, 2, -4, 2, 64, 128)):
+        assert f(*bad) == 0
+    big = 2 ** 31 - 1
+    for n, QH, B, nb, KVH, T in ((20000, 65535, 20000, 1000, 65535, 64), (32768, 65535, 2 ** 24 - 1, big // 16, 65535, 16),
+                                 (big, 1, 256, big // 128, 1, 128), (32768, 65535, 256, big // 64, 65535, 64),
+                                 (1, 65535, 1, big // 64, 1, 64), (big, 1, 1, big // 64, 1, 64)):
+        assert f(n, QH, B, nb, KVH, T, 128) < 2 ** 50, (n, QH, B)
+
+
 # ------------------------------------------------------------- the oracle
 
 def test_oracle_rotation_by_hand():
