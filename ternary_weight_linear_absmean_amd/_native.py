@@ -788,9 +788,14 @@ def bitlinear_kv4_read(q_start, lengths, table, cache, n_tok, dtype=torch.float3
     return _read("bitlinear_kv4_read", _kv4, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
 
 
-def _attend(call, ws_call, device_cache, q, q_start, lengths, table, cache, scale, out, ws, stream):
+def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
+                            stream=None):
+    """Causal attention of q [n_tok, QH, D] (fp32 or bf16) over the cache:
+    out [n_tok, QH, D].  scale defaults to D ** -0.5; q_start, lengths, table
+    as for bitlinear_kv8_append.  Rows of no sequence are left as they are.
+    out may not overlap q."""
     dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
-    c = device_cache(cache, dev)
+    c = _kv8(cache, dev)
     if D != c.D:
         raise ValueError(f"q must be [n_tok, QH, {c.D}], got {list(q.shape)}")
     meta = _seqs(q_start, lengths, table, dev)
@@ -804,35 +809,50 @@ def _attend(call, ws_call, device_cache, q, q_start, lengths, table, cache, scal
     handle, context = _where(dev, stream)
     with context:
         if ws is None:
-            size = getattr(lib, ws_call)(n, QH, meta[3], meta[4], c.KVH, c.T, D)
+            size = lib.bitlinear_kv8_attention_ws_bytes(n, QH, meta[3], meta[4], c.KVH, c.T, D)
             if size:
                 ws = torch.empty((size,), dtype=torch.uint8, device=dev)
                 wp = ws.data_ptr()
         if out is None:
             out = torch.empty_like(q)
-        st = getattr(lib, call)(
+        st = lib.bitlinear_kv8_attention(
             qp, dt, n, QH, *meta, c, D ** -0.5 if scale is None else scale, out.data_ptr(), wp, size,
             handle)
     if st:
-        _check(call, st)
+        _check("bitlinear_kv8_attention", st)
     return out
-
-
-def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
-                            stream=None):
-    """Causal attention of q [n_tok, QH, D] (fp32 or bf16) over the cache:
-    out [n_tok, QH, D].  scale defaults to D ** -0.5; q_start, lengths, table
-    as for bitlinear_kv8_append.  Rows of no sequence are left as they are.
-    out may not overlap q."""
-    return _attend("bitlinear_kv8_attention", "bitlinear_kv8_attention_ws_bytes", _kv8, q, q_start, lengths,
-                   table, cache, scale, out, ws, stream)
 
 
 def bitlinear_kv4_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
                             stream=None):
     """bitlinear_kv8_attention over a 4-bit cache (Kv4Cache)."""
-    return _attend("bitlinear_kv4_attention", "bitlinear_kv4_attention_ws_bytes", _kv4, q, q_start, lengths,
-                   table, cache, scale, out, ws, stream)
+    dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
+    c = _kv4(cache, dev)
+    if D != c.D:
+        raise ValueError(f"q must be [n_tok, QH, {c.D}], got {list(q.shape)}")
+    meta = _seqs(q_start, lengths, table, dev)
+    if out is not None:
+        _at(out, q.dtype, dev, (n, QH, D), "out")
+    wp = size = 0
+    if ws is not None:
+        size = ws.numel()
+        wp = _at(ws, torch.uint8, dev, (size,), "ws")
+    lib = load()
+    handle, context = _where(dev, stream)
+    with context:
+        if ws is None:
+            size = lib.bitlinear_kv4_attention_ws_bytes(n, QH, meta[3], meta[4], c.KVH, c.T, D)
+            if size:
+                ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+                wp = ws.data_ptr()
+        if out is None:
+            out = torch.empty_like(q)
+        st = lib.bitlinear_kv4_attention(
+            qp, dt, n, QH, *meta, c, D ** -0.5 if scale is None else scale, out.data_ptr(), wp, size,
+            handle)
+    if st:
+        _check("bitlinear_kv4_attention", st)
+    return out
 
 
 def bitlinear_decode_stack_kv(layers, caches, x, q_start, lengths, table, H, KV, F, D, eps=1e-5,

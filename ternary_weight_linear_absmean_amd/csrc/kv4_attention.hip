@@ -8,10 +8,15 @@
 // z and s meet its score and its weight in fp32, straight from their fp16 halves
 // (v_fma_mix), so that no code is rounded.
 //
-// A code as fp16: the nibble put below 0x64 (0x54 where it stands four bits
-// higher) reads as 1024 + u (64 + u); one packed add leaves u.  Eight codes of a
+// A code as fp16.  The nibble put below 0x64 (0x54 where it stands four bits
+// higher) reads as 1024 + u (64 + u), and one packed add leaves u, or u - 8.  fp32
+// rows take u - 8 with z + 8 s in z's place: with u itself the two sums of a
+// result cancel (8 steps against what is left of a mean over many values), and
+// errors of 1e-6 became 3e-6.  bf16 rows of the few-rows kernel take the nibble as it is, fp16's u 2^-24 or u
+// 2^-20 (matrix instructions keep subnormals): two operations fewer of nine for
+// eight codes; the other operand's odd pairs are 2^-4 instead.  Eight codes of a
 // dword come out as the pairs (0, 4) (1, 5) (2, 6) (3, 7): a product's order of
-// terms is free, so q and the weights are put into that order instead.
+// terms is free, so q and the weights are put into that order.
 //
 // The other operand is scaled by a power of two into fp16's range and, for fp32
 // rows, split into two halves of 11 bits each (two matrix instructions):
@@ -35,16 +40,39 @@ namespace {
 
 using Args = KvArgs<Kv4Cache>;
 
-// Eight codes -> fp16, pairs (0, 4) (1, 5) (2, 6) (3, 7).
+// (w & mask) | base in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t base) {
+    uint32_t o;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(o) : "v"(w), "s"(mask), "v"(base));
+    return o;
+}
+// Eight codes u -> fp16 u - CENTRE, pairs (0, 4) (1, 5) (2, 6) (3, 7).
+template <int CENTRE>
 __device__ __forceinline__ half8 codes8(uint32_t w) {
-    const half2 b0 = {(_Float16)-1024.0f, (_Float16)-1024.0f}, b1 = {(_Float16)-64.0f, (_Float16)-64.0f};
+    const half2 b0 = {(_Float16)(-1024.0f - CENTRE), (_Float16)(-1024.0f - CENTRE)};
+    const half2 b1 = {(_Float16)(-64.0f - CENTRE), (_Float16)(-64.0f - CENTRE)};
     const uint32_t v = w >> 8;
     uint4 o;
-    o.x = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, (w & 0x000F000Fu) | 0x64006400u) + b0);
-    o.y = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, (w & 0x00F000F0u) | 0x54005400u) + b1);
-    o.z = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, (v & 0x000F000Fu) | 0x64006400u) + b0);
-    o.w = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, (v & 0x00F000F0u) | 0x54005400u) + b1);
+    o.x = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, and_or(w, 0x000F000Fu, 0x64006400u)) + b0);
+    o.y = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, and_or(w, 0x00F000F0u, 0x54005400u)) + b1);
+    o.z = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, and_or(v, 0x000F000Fu, 0x64006400u)) + b0);
+    o.w = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, and_or(v, 0x00F000F0u, 0x54005400u)) + b1);
     return __builtin_bit_cast(half8, o);
+}
+// The same pairs as they stand: u 2^-24 and, the odd ones, u 2^-20.
+__device__ __forceinline__ half8 codes8_raw(uint32_t w) {
+    const uint32_t v = w >> 8;
+    return __builtin_bit_cast(half8, make_uint4(w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u));
+}
+constexpr float kRaw = 16777216.0f;         // 2^24
+// A pair of the other operand times 2^-4.
+__device__ __forceinline__ uint32_t sixteenth(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, w) * half2{(_Float16)0.0625f, (_Float16)0.0625f});
+}
+
+// z + 8 s.
+__device__ __forceinline__ float middle(uint32_t zs) {
+    return __builtin_fmaf((float)zs_s(zs), 8.0f, (float)zs_z(zs));
 }
 
 // A power of two above a step (0 <= s < 2^16), 2^-24 at least.
@@ -64,14 +92,13 @@ struct Reference {
     float m = -INFINITY, above = -INFINITY, u = 0.0f, r1 = 0.0f, r2 = 0.0f;
     bool far = false;
     // To a maximum `top` and steps below u_new; what the sums are to be multiplied by.
-    template <bool BF16>
     __device__ __forceinline__ float follow(float top, float u_new) {
         const bool none = m == -INFINITY;
         m = fmaxf(m, top);
         u = u_new;
-        above = raise_above<BF16>(m);
+        above = raise_above<false>(m);
         const float base = m == -INFINITY ? 0.0f : m, shift = log2_of(u) - kUnitBits;
-        far = fabsf(base) >= kFarScore<BF16>;
+        far = fabsf(base) >= kFarScore<false>;
         const float n1 = far ? base : base + shift, n2 = far ? shift : 0.0f;
         const float fix = none ? 0.0f : exp2_fast((r1 - n1) + (r2 - n2));
         r1 = n1;
@@ -144,7 +171,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
         top = quad_max(top);
         q_sum = quad_sum(q_sum) * a.scale2;
         const float f = a.scale2 < 0.0f ? -to_f16_range(top) : to_f16_range(top);
-        c_row = a.scale2 / f;
+        c_row = BF16 ? a.scale2 / f * kRaw : a.scale2 / f;
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const float x[8] = {v[j][0].x * f, v[j][0].y * f, v[j][0].z * f, v[j][0].w * f,
@@ -153,7 +180,8 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 w[e] = f16_pair(x[e], x[e + 4]);
-                z[e] = f16_rest(x[e], x[e + 4], w[e]);
+                if (!BF16) z[e] = f16_rest(x[e], x[e + 4], w[e]);
+                if (BF16 && (e & 1)) w[e] = sixteenth(w[e]);
             }
             qh[0][j] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
             if (NS == 2) qh[NS - 1][j] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
@@ -234,23 +262,22 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
                 float4v s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
-                    const half8 k = codes8(kb[tt][j]);
+                    const half8 k = BF16 ? codes8_raw(kb[tt][j]) : codes8<8>(kb[tt][j]);
 #pragma unroll
                     for (int e = 0; e < NS; ++e) s = mfma_16x16x32(k, qh[e][j], s);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t zs = zk[4 * tt + i];
-                    x[4 * tt + i] = __builtin_fmaf(s[i] * c_row, (float)zs_s(zs),
-                                                   __builtin_fmaf(q_sum, (float)zs_z(zs), 0.0f));
+                    const float z_part = BF16 ? __builtin_fmaf(q_sum, (float)zs_z(zs), 0.0f) : q_sum * middle(zs);
+                    x[4 * tt + i] = __builtin_fmaf(s[i] * c_row, (float)zs_s(zs), z_part);
                 }
             }
+            // also behind the last tile (block 0's then): a branch would cost a copy of
+            // every register that is loaded
             const uint32_t next = tile + kStep;
-            const bool more = next < k1;
-            if (more) {
-                id_next = block_of(next, entry);
-                load_k(next, id_next);
-            }
+            id_next = block_of(next, entry);
+            load_k(next, id_next);
 
             const uint32_t key0 = tile + 16 * quad;
             const bool whole = id >= 0 && key0 + 16 <= sees;
@@ -273,7 +300,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
             top = quad_max(top);
             const float u_new = fmaxf(ref.u, step_above(quad_max((float)zs_s(zs_top))));
             if (__builtin_expect(__ballot(top > ref.above || u_new != ref.u) != 0, 0)) {
-                const float fix = ref.follow<BF16>(top, u_new);
+                const float fix = ref.follow(top, u_new);
                 l *= fix;
                 o_z *= fix;
 #pragma unroll
@@ -294,21 +321,24 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
                     const uint32_t zs = zv[8 * k + e];
                     const float p = exp2_fast(x[8 * k + e] - base);
                     l += p;
-                    o_z = __builtin_fmaf(p, (float)zs_z(zs), o_z);
+                    o_z = __builtin_fmaf(p, BF16 ? (float)zs_z(zs) : middle(zs), o_z);
                     y[e] = __builtin_fmaf(p, (float)zs_s(zs), 0.0f);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     hi[e] = f16_pair(y[e], y[e + 4]);
                     if (!BF16) lo[e] = f16_rest(y[e], y[e + 4], hi[e]);
+                    if (BF16 && (e & 1)) hi[e] = sixteenth(hi[e]);
                 }
                 ph[0][k] = __builtin_bit_cast(half8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                 if (!BF16) ph[NS - 1][k] = __builtin_bit_cast(half8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             }
 #pragma unroll
             for (int i = 0; i < NO / 2; ++i) {
-                const half8 v00 = codes8(vb[i].x), v01 = codes8(vb[i].y);
-                const half8 v10 = codes8(vb[i].z), v11 = codes8(vb[i].w);
+                const half8 v00 = BF16 ? codes8_raw(vb[i].x) : codes8<8>(vb[i].x);
+                const half8 v01 = BF16 ? codes8_raw(vb[i].y) : codes8<8>(vb[i].y);
+                const half8 v10 = BF16 ? codes8_raw(vb[i].z) : codes8<8>(vb[i].z);
+                const half8 v11 = BF16 ? codes8_raw(vb[i].w) : codes8<8>(vb[i].w);
 #pragma unroll
                 for (int e = 0; e < NS; ++e) {
                     o[2 * i] = mfma_16x16x32(v00, ph[e][0], o[2 * i]);
@@ -317,11 +347,9 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
                     o[2 * i + 1] = mfma_16x16x32(v11, ph[e][1], o[2 * i + 1]);
                 }
             }
-            if (more) {
-                id = id_next;
-                entry = entry_at(next + kStep);            // before V: loads come back in order
-                load_v(next, id);
-            }
+            id = id_next;
+            entry = entry_at(next + kStep);                // before V: loads come back in order
+            load_v(next, id);
         }
     }
     // from 2^(r1 + r2) to 2^r1
@@ -334,7 +362,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
     for (int i = 0; i < NO; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            join[wave][low][32 * (i / 2) + 2 * (4 * quad + e) + (i & 1)] = (o[i][e] + o_z) * f_r2;
+            join[wave][low][32 * (i / 2) + 2 * (4 * quad + e) + (i & 1)] = ((BF16 ? o[i][e] * kRaw : o[i][e]) + o_z) * f_r2;
     if (quad == 0) {
         join_m[wave][low] = ref.m == -INFINITY ? -INFINITY : ref.r1;
         join_l[wave][low] = l;
@@ -375,6 +403,409 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
     }
 }
 
+// Many rows: one workgroup per (128 rows, key head, part of the keys), 32 rows
+// a wave, 64 keys at a time, the tile's codes turned into fp16 once, in LDS, for
+// all rows.  While tile t is used, t + 1 is turned into the other buffer and
+// the codes of t + 2 are on their way.
+//
+// bf16 rows: what goes to LDS are the keys and values themselves, fp16(z + s u), an
+// error of 2^-12 beside the result's 2^-9: no z or s is left in the loop over
+// scores.  fp32 rows: the codes less 8, exact, and the tokens' z and s beside them.
+// z and s that are not finite (never written by the append) count as 0 there, and
+// a step with which a code of 15 would pass fp16 as the largest that does not:
+// a token that rows do not see is in their products, times 0.
+//
+// Layouts (lane = 32 half + low): S^T = K Q^T puts key 8 (i / 4) + 4 half + i
+// % 4 of the operand's rows, row low, into accumulator i.  Operand row r holds
+// key r with its bits 2 and 3 swapped, so accumulators 8 s .. 8 s + 7 are keys
+// 16 s + 8 half .. + 7: the P^T operand of step s.
+//
+// LDS: K [64][D] and V^T [D][64] in 16-byte pieces, piece p of line y at p ^ y
+// (K, D = 128) or p ^ (y / 2) (lines of 128 bytes), so that 16 lanes reading
+// one piece of 16 lines touch every bank once.
+constexpr float kMostF16 = 65504.0f;
+
+// A token's z and s as the tile takes them; CAP: for values in fp16.
+template <bool CAP>
+__device__ __forceinline__ uint32_t sound(uint32_t zs) {
+    const float z = (float)zs_z(zs), s = (float)zs_s(zs);
+    const bool fine = fabsf(z) <= kMostF16 && s >= 0.0f && s <= kMostF16;
+    // less a half step of an 11-bit mantissa and its rounding: 15 s + z <= 65504
+    const float most = (kMostF16 - z) * (0.99951172f / 15.0f);
+    const half2 h = {(_Float16)z, (_Float16)(CAP ? fminf(s, most) : s)};
+    return fine ? __builtin_bit_cast(uint32_t, h) : 0u;
+}
+// Eight codes as the values z + s u, pairs as codes8; s and z by pair.
+__device__ __forceinline__ half8 values8(uint32_t w, const uint32_t *s, const uint32_t *z) {
+    const uint4 u = __builtin_bit_cast(uint4, codes8<0>(w));
+    auto value = [&](uint32_t x, int i) {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2, x),
+                                                                      __builtin_bit_cast(half2, s[i]),
+                                                                      __builtin_bit_cast(half2, z[i])));
+    };
+    return __builtin_bit_cast(half8, make_uint4(value(u.x, 0), value(u.y, 1), value(u.z, 2), value(u.w, 3)));
+}
+
+template <int D>
+struct ManyLds {
+    uint4 k[2 * kTile * D / 8], v[2 * kTile * D / 8];
+    uint32_t zk[2][kTile], zv[2][kTile];    // fp32 rows: z and s by token
+    uint32_t pairs[kWaves][16];             // bf16 rows: of a wave's 16 tokens of V, s and z by pair of codes8
+};
+template <bool BF16, int D>
+__device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, ManyLds<D> &lds) {
+    constexpr int NS = BF16 ? 1 : 2;
+    constexpr int NQ = D / 16;              // steps of K Q^T
+    constexpr int NO = D / 32;              // tiles of the output
+    constexpr int NW = D / 32;              // dwords of K's and of V's codes per thread
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, gt = threadIdx.x;
+    const int low = lane & 31, half = lane >> 5;
+    // Heads of one tile side by side, tiles that see most first.  Two
+    // workgroups share a CU: where all start at once, the second of each is to
+    // be the first's complement, so the order turns round after the first 256.
+    const int64_t groups = a.many_groups;
+    if (at >= kCUs && groups <= 2 * kCUs) at = groups - 1 - (at - kCUs);
+    const int h = (int)(at % a.c.KVH);
+    const int64_t slot = at / a.c.KVH;
+    const Kv8Seqs &sq = a.seqs;
+    const Kv4Cache &c = a.c;
+    const int G = a.G;
+    const int b = find_seq(sq.B, slot, [&](int i) {
+        return (int64_t)q_at(sq, i) * G / kManyRows + i;
+    });
+    const int q0 = q_at(sq, b), n = q_at(sq, b + 1) - q0;
+    int64_t nth = slot - ((int64_t)q0 * G / kManyRows + b);
+    const int64_t all_rows = (int64_t)n * G;
+    const int64_t tiles = (all_rows + kManyRows - 1) / kManyRows;
+    if (nth < 0 || n <= 0 || nth >= tiles || all_rows <= a.min_rows) return;
+    nth = tiles - 1 - nth;                  // the rows that see most first
+    const int64_t r0 = nth * kManyRows;
+    const int64_t start = (int64_t)sq.lengths[b] - n;
+    const int64_t cap = key_capacity(a);
+    const int64_t end = min(start + (min(r0 + kManyRows, all_rows) - 1) / G + 1, cap);
+    const int64_t chunk = keys_of_part(a, sq.lengths[b]);
+    if (split > 0 && split * chunk >= end) return;
+    const uint32_t k0 = (uint32_t)(split * chunk), k1 = keys_within(min(end, split * chunk + chunk), 0x7FFFFFFFu);
+
+    const int64_t rw = r0 + 32 * wave;      // the wave's first row
+    const bool rows_here = rw < all_rows;
+    const int64_t r = min(rw + low, all_rows - 1);
+    const int tok = (int)(r / G);
+    const int64_t row = (int64_t)(q0 + tok) * a.QH + h * G + (int)(r - (int64_t)tok * G);
+    const int64_t pos = start + tok;
+    // the keys before this one are seen by this row, the wave's first and last
+    const uint32_t sees = keys_within(pos + 1, k1);
+    const uint32_t sees_lo = keys_within(start + min(rw, all_rows - 1) / G + 1, k1);
+    const uint32_t sees_hi = keys_within(start + min(rw + 31, all_rows - 1) / G + 1, k1);
+
+    half8 qh[NS][NQ];
+    float c_row, q_sum = 0.0f;
+    {
+        float4 v[NQ][2];
+        float top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < NQ; ++s)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float4 x = load4<BF16>(a.q, row * D + 16 * s + 8 * half + 4 * e);
+                v[s][e] = x;
+                q_sum += (x.x + x.y) + (x.z + x.w);
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+            }
+        top = half_max(top);
+        q_sum = (q_sum + __shfl_xor(q_sum, 32)) * a.scale2;
+        const float f = a.scale2 < 0.0f ? -to_f16_range(top) : to_f16_range(top);
+        c_row = a.scale2 / f;
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) {
+            const float x[8] = {v[s][0].x * f, v[s][0].y * f, v[s][0].z * f, v[s][0].w * f,
+                                v[s][1].x * f, v[s][1].y * f, v[s][1].z * f, v[s][1].w * f};
+            uint32_t w[4], z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = f16_pair(x[e], x[e + 4]);
+                if (NS == 2) z[e] = f16_rest(x[e], x[e + 4], w[e]);
+            }
+            qh[0][s] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
+            if (NS == 2) qh[NS - 1][s] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
+        }
+    }
+
+    // A tile starts at a multiple of 64, so a key's slot is its own low bits,
+    // and the tile's in blocks of 128.  A thread brings D / 4 values of key gt /
+    // 4, and of V D / 64 values of the 16 tokens of granule `wave`.
+    const int32_t *table = sq.table + (int64_t)b * sq.max_blocks;
+    auto entry_at = [&](uint32_t t) { return table[min(t, k1 - 1) >> c.t_shift]; };    // as above
+    auto block_of = [&](uint32_t t, int entry) {
+        return t < k1 && entry >= 0 && entry < c.n_blocks ? entry : -1;
+    };
+    const int pk = gt >> 2, tv = 16 * wave + (lane & 15);   // the tokens whose z and s this thread brings
+    uint32_t kr[NW], vr[NW], zk_raw, zv_raw;
+    int k_entry, v_entry;
+    bool k_ok, v_ok, in_use = false, in_use_next = false;   // whether granule lane % 4 of the tile holds tokens
+    int g_entry;
+    auto load_ids = [&](uint32_t tile) {
+        k_entry = entry_at(tile + pk);
+        v_entry = entry_at(tile + 16 * wave);
+        g_entry = entry_at(tile + 16 * (gt & 3));
+    };
+    // what lies behind k1 is read from block 0
+    auto load_tile = [&](uint32_t tile) {
+        const int in = (int)tile & (c.T - 1);
+        const int kid = block_of(tile + pk, k_entry), vid = block_of(tile + 16 * wave, v_entry);
+        k_ok = kid >= 0;
+        v_ok = vid >= 0 && tile + tv < k1;
+        in_use_next = block_of(tile + 16 * (gt & 3), g_entry) >= 0;
+        const int64_t kt = (((int64_t)max(kid, 0) * c.KVH + h) << c.t_shift) + ((in + pk) & (c.T - 1));
+        const int64_t vt = (((int64_t)max(vid, 0) * c.KVH + h) << c.t_shift) + ((in + 16 * wave) & (c.T - 1));
+        const uint8_t *kp = c.K + kt * (D / 2) + D / 8 * (gt & 3), *vp = c.V + vt * (D / 2) + D / 8 * lane;
+        if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(kp), y = *reinterpret_cast<const uint4 *>(vp);
+            kr[0] = x.x; kr[1] = x.y; kr[NW - 2] = x.z; kr[NW - 1] = x.w;
+            vr[0] = y.x; vr[1] = y.y; vr[NW - 2] = y.z; vr[NW - 1] = y.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(kp), y = *reinterpret_cast<const uint2 *>(vp);
+            kr[0] = x.x; kr[1] = x.y;
+            vr[0] = y.x; vr[1] = y.y;
+        }
+        zk_raw = c.zk[kt];
+        zv_raw = c.zv[vt + (lane & 15)];
+    };
+    // LDS bytes: K line of 2 D bytes, V^T line of 128; a piece's place is its
+    // number's 16 bytes XOR the line's, so that pieces of one line are reached
+    // by an XOR of the thread's address, and lines 32 apart by an offset
+    auto k_at = [](int key, int piece) {
+        return D == 128 ? key * 256 + ((piece ^ (key & 15)) << 4) : key * 128 + ((piece ^ ((key >> 1) & 7)) << 4);
+    };
+    auto v_at = [](int d, int piece) { return d * 128 + ((piece ^ ((d >> 1) & 7)) << 4); };
+    char *const lds_k = reinterpret_cast<char *>(lds.k), *const lds_v = reinterpret_cast<char *>(lds.v);
+    constexpr int kBuf = kTile * D * 2;                     // bytes of a tile of K or V
+    constexpr int VD = D / 64;                              // values of V per thread
+    const int k_put = k_at(pk, NW * (gt & 3)), v_put = v_at(VD * lane, 2 * wave);
+    auto to_lds = [&](int buf) {
+        const int ka = k_put + buf * kBuf, va = v_put + buf * kBuf;
+        const uint32_t zk = k_ok ? sound<BF16>(zk_raw) : 0u, zv = v_ok ? sound<BF16>(zv_raw) : 0u;
+        if (BF16) {
+            uint32_t sp[8], zp[8];
+            // token t of 8 is half t / 4 of pair t % 4
+            uint16_t *put = reinterpret_cast<uint16_t *>(lds.pairs[wave]) +
+                            2 * (4 * ((lane >> 3) & 1) + (lane & 3)) + ((lane >> 2) & 1);
+            if (lane < 16) {
+                put[0] = (uint16_t)(zv >> 16);
+                put[16] = (uint16_t)zv;
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // one wave's LDS accesses are in order
+            const uint4 *get = reinterpret_cast<const uint4 *>(lds.pairs[wave]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 w = get[i];
+                uint32_t *to = i < 2 ? sp + 4 * i : zp + 4 * (i - 2);
+                to[0] = w.x; to[1] = w.y; to[2] = w.z; to[3] = w.w;
+            }
+            const uint32_t ks = perm(zk, zk, 0x03020302u), kz = perm(zk, zk, 0x01000100u);
+            const uint32_t ks4[4] = {ks, ks, ks, ks}, kz4[4] = {kz, kz, kz, kz};
+#pragma unroll
+            for (int j = 0; j < NW; ++j)
+                *reinterpret_cast<half8 *>(lds_k + (ka ^ 16 * j)) = values8(kr[j], ks4, kz4);
+#pragma unroll
+            for (int j = 0; j < NW; ++j)
+                *reinterpret_cast<half8 *>(lds_v + (va ^ 16 * (j & 1)) + (j >> 1) * 128) =
+                    values8(vr[j], sp + 4 * (j & 1), zp + 4 * (j & 1));
+        } else {
+#pragma unroll
+            for (int j = 0; j < NW; ++j) *reinterpret_cast<half8 *>(lds_k + (ka ^ 16 * j)) = codes8<8>(kr[j]);
+#pragma unroll
+            for (int j = 0; j < NW; ++j)
+                *reinterpret_cast<half8 *>(lds_v + (va ^ 16 * (j & 1)) + (j >> 1) * 128) = codes8<8>(vr[j]);
+            if ((gt & 3) == 0) lds.zk[buf][pk] = zk;
+            if (lane < 16) lds.zv[buf][tv] = zv;
+        }
+    };
+
+    Reference ref;
+    float l = 0.0f, o_z = 0.0f;
+    float16v o[NO];
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] = 0.0f;
+    // operand row low holds key low, bits 2 and 3 swapped, of 32
+    const int k_get = k_at((low & 0x13) | (low & 4) << 1 | (low & 8) >> 1, half), v_get = v_at(low, half);
+
+    if (k0 < k1) {
+        load_ids(k0);
+        load_tile(k0);
+        load_ids(k0 + kTile);
+        to_lds(0);
+        in_use = in_use_next;
+        load_tile(k0 + kTile);
+        load_ids(k0 + 2 * kTile);
+        __syncthreads();
+    }
+    int buf = 0;
+    for (uint32_t tile = k0; tile < k1; tile += kTile, buf ^= 1) {
+        const bool here = rows_here && tile < sees_hi;
+        // opaque, or the loop would hold an address for each piece
+        int ka = k_get + buf * kBuf, va = v_get + buf * kBuf;
+        asm("" : "+v"(ka), "+v"(va));
+        __builtin_amdgcn_s_setprio(1);            // the CU's other workgroup fills what this leaves
+        // also where the wave's rows do not see the tile: one block to schedule
+        float16v s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < NQ; ++st)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const half8 k = *reinterpret_cast<const half8 *>(lds_k + (ka ^ 32 * st) + t * 64 * D);
+#pragma unroll
+                for (int x = 0; x < NS; ++x) s[t] = mfma_32x32x16(k, qh[x][st], s[t]);
+            }
+        to_lds(buf ^ 1);
+        __builtin_amdgcn_s_setprio(0);
+        const uint64_t used = __ballot(in_use);             // bit g: granule g holds tokens
+        in_use = in_use_next;
+        load_tile(tile + 2 * kTile);
+        load_ids(tile + 3 * kTile);
+        if (here) {
+            const bool whole = (used & 15) == 15 && tile + kTile <= sees_lo;            // uniform
+            const int lim = tile < sees ? (int)min(sees - tile, (uint32_t)kTile) : 0;
+            float u_new = 1.0f;
+            if (!BF16) {
+                uint32_t zs_top = 0;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const uint4 *zk = reinterpret_cast<const uint4 *>(&lds.zk[buf][16 * g + 8 * half]);
+                    const uint4 *zv = reinterpret_cast<const uint4 *>(&lds.zv[buf][16 * g + 8 * half]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 w = zk[i], y = zv[i];
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = s[g >> 1][8 * (g & 1) + 4 * i + e] * c_row;
+                            s[g >> 1][8 * (g & 1) + 4 * i + e] =
+                                __builtin_fmaf(x, (float)zs_s(ws[e]), q_sum * middle(ws[e]));
+                            const bool seen = whole || 16 * g + 8 * half + 4 * i + e < lim;
+                            zs_top = max(zs_top, seen ? ys[e] : 0u);
+                        }
+                    }
+                }
+                u_new = fmaxf(ref.u, step_above(half_max((float)zs_s(zs_top))));
+            }
+            if (!whole) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int lim_g = used >> g & 1 ? lim - 16 * g - 8 * half : 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        s[g >> 1][8 * (g & 1) + e] = e < lim_g ? s[g >> 1][8 * (g & 1) + e] : -INFINITY;
+                }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, s[t][e]);
+            float cs = 1.0f;
+            if (BF16) {
+                cs = fmaxf(c_row, kTiny);                  // positive: q has the scale's sign
+                top *= cs;
+            }
+            top = half_max(top);
+            if (__builtin_expect(__ballot(top > ref.above || u_new != ref.u) != 0, 0)) {
+                const float fix = ref.follow(top, u_new);
+                l *= fix;
+                o_z *= fix;
+#pragma unroll
+                for (int i = 0; i < NO; ++i) o[i] *= fix;
+            }
+            float base = ref.r1;
+            if (__ballot(ref.far) != 0) {
+                // r1 is exact for rows far from zero, and so is r1 with r2 = 0 for the others
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[t][e] = s[t][e] * cs - ref.r1;
+                cs = 1.0f;
+                base = ref.r2;
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {                  // 16 keys
+                uint32_t hi[4], lo[4];
+                float y[8];
+                uint32_t zv[8];
+                if (!BF16) {
+                    const uint4 *from = reinterpret_cast<const uint4 *>(&lds.zv[buf][16 * g + 8 * half]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 w = from[i];
+                        zv[4 * i] = w.x; zv[4 * i + 1] = w.y; zv[4 * i + 2] = w.z; zv[4 * i + 3] = w.w;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x = s[g >> 1][8 * (g & 1) + e];
+                    const float p = exp2_fast(BF16 ? __builtin_fmaf(x, cs, -base) : x - base);
+                    l += p;
+                    y[e] = p;
+                    if (!BF16) {
+                        o_z = __builtin_fmaf(p, middle(zv[e]), o_z);
+                        y[e] = __builtin_fmaf(p, (float)zs_s(zv[e]), 0.0f);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    hi[e] = f16_pair(y[e], y[e + 4]);
+                    if (!BF16) lo[e] = f16_rest(y[e], y[e + 4], hi[e]);
+                }
+                const half8 p_hi = __builtin_bit_cast(half8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                half8 p_lo;
+                if (!BF16) p_lo = __builtin_bit_cast(half8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+                for (int i = 0; i < NO; ++i) {
+                    const half8 v = *reinterpret_cast<const half8 *>(lds_v + (va ^ 32 * g) + i * 32 * 128);
+                    o[i] = mfma_32x32x16(v, p_hi, o[i]);
+                    if (NS == 2) o[i] = mfma_32x32x16(v, p_lo, o[i]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+
+    if (rw + low >= all_rows) return;
+    l = l + __shfl_xor(l, 32);
+    o_z = o_z + __shfl_xor(o_z, 32);
+    // from 2^(r1 + r2) to 2^r1
+    float f0 = exp2_fast(ref.r2);
+    l *= f0;
+    const bool direct = min(pos + 1, cap) <= chunk;
+    if (direct) {
+        if (split > 0) return;
+        f0 = l > 0.0f ? f0 / l : 0.0f;
+    }
+    const int64_t all = (int64_t)sq.n_tok * a.QH;
+    float *dst = a.part + ((int64_t)split * all + row) * D;
+#pragma unroll
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            float y[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) y[x] = (o[i][e + x] + o_z) * f0;
+            const int d = 32 * i + 2 * e + 4 * half;
+            if (direct) store4<BF16>(a.out, row * D + d, make_float4(y[0], y[1], y[2], y[3]));
+            else store4<false>(dst, d, make_float4(y[0], y[1], y[2], y[3]));
+        }
+    if (!direct && half == 0) {
+        float *ml = a.part + (int64_t)a.S * all * D + ((int64_t)split * all + row) * 2;
+        ml[0] = ref.m == -INFINITY ? -INFINITY : ref.r1;
+        ml[1] = l;
+    }
+}
+
 template <bool BF16, int D>
 __global__ __launch_bounds__(kThreads, 2) void kv4_few_kernel(Args a) {
     __shared__ FewLds<D> lds;
@@ -382,22 +813,47 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_few_kernel(Args a) {
 }
 
 template <bool BF16, int D>
+__global__ __launch_bounds__(kThreads, 2) void kv4_many_kernel(Args a) {
+    __shared__ ManyLds<D> lds;
+    many_rows<BF16, D>(a, blockIdx.x, blockIdx.z, lds);
+}
+// Both in one launch: many rows wait for instructions, few rows for memory, so
+// are to share the CUs.  The workgroups for few rows stand behind the first kCUs
+// of the others.
+template <bool BF16, int D>
+__global__ __launch_bounds__(kThreads, 2) void kv4_mixed_kernel(Args a) {
+    __shared__ union {
+        FewLds<D> few;
+        ManyLds<D> many;
+    } lds;
+    const int64_t all = a.many_groups * a.S, first = min(all, (int64_t)kCUs);
+    const int64_t few = gridDim.x - all, i = blockIdx.x;
+    if (i >= first && i < first + few) {
+        few_rows<BF16, D>(a, (uint32_t)(i - first), lds.few);
+    } else {
+        const int64_t at = i < first ? i : i - few;
+        const int split = (int)(at / a.many_groups);
+        many_rows<BF16, D>(a, at - split * a.many_groups, split, lds.many);
+    }
+}
+
+template <bool BF16, int D>
 Kernels<Kv4Cache> kernels() {
-    return {kv4_few_kernel<BF16, D>, nullptr, nullptr};
+    return {kv4_few_kernel<BF16, D>, kv4_many_kernel<BF16, D>, kv4_mixed_kernel<BF16, D>};
 }
 
 }  // namespace
 
 size_t kv4_attention_ws_floats(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
                                int64_t KVH, int64_t T, int64_t D) {
-    const Plan p = plan_for(n_tok, QH, B, max_blocks, KVH, T, D, false);
+    const Plan p = plan_for(n_tok, QH, B, max_blocks, KVH, T, D);
     return (size_t)(p.part + p.cut);
 }
 
 hipError_t launch_kv4_attention(const void *q, int dtype, int QH, const Kv8Seqs &seqs,
                                 const bl_kv4 &cache, float scale, void *out, float *ws,
                                 hipStream_t s) {
-    const Plan p = plan_for(seqs.n_tok, QH, seqs.B, seqs.max_blocks, cache.KVH, cache.T, cache.D, false);
+    const Plan p = plan_for(seqs.n_tok, QH, seqs.B, seqs.max_blocks, cache.KVH, cache.T, cache.D);
     const Args a = kv_args(p, q, QH, seqs, kv4_device(cache), scale, out, ws);
     if (cache.D == 64)
         return dtype ? attend<true, 64>(a, p, kernels<true, 64>(), s) : attend<false, 64>(a, p, kernels<false, 64>(), s);

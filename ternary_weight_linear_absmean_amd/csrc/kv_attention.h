@@ -573,15 +573,14 @@ struct Plan {
     int most, slots, step_shift;
     int64_t part, cut;        // floats of the workspace
 };
-Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH, int64_t T, int64_t D,
-              bool may_many = true) {
+Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH, int64_t T, int64_t D) {
     const int64_t G = QH / KVH, keys = max_blocks * T, unit = kTile * kWaves;
     const int64_t steps = keys > 0 ? (keys + unit - 1) / unit : 1;
     const int64_t seqs = n_tok < B ? n_tok : B;
     Plan p = {};
     p.steps = steps;
     p.S = 1;
-    p.many = may_many && n_tok * G > kFewRows * B && (double)n_tok * QH / kRows * (steps + 2) > kManyWork;
+    p.many = n_tok * G > kFewRows * B && (double)n_tok * QH / kRows * (steps + 2) > kManyWork;
     p.few = !p.many || B > 1;
     if (p.many) {
         const double tiles = n_tok * (double)G / kManyRows;

@@ -218,7 +218,10 @@ def test_scores_far_from_zero(gpu, case, far, dtype):
     """Scores of 2^far and more, of both signs.  A score is off by ds at most (see
     check; a step of the rounded score is less), so each weight by e^ds either way:
     the result by (e^ds - 1) e^ds sum p |v - out|, and never by more than the seen
-    values' reach, as it lies among them."""
+    values' reach, as it lies among them.  Where ds is 1 and more that sum is below
+    64 bits' range; but a key whose score is 2 ds + 40 below the largest stays 40
+    below it, with a weight under e^-40: the result is a mean of the other keys'
+    values up to keys e^-40 of the reach."""
     n, lens, width = FAR[case]
     T, D, KVH, G = 16, 64, 2, 4
     s = make(100 + case, n, lens, T, D, KVH, dtype, G, width=width // T)
@@ -246,10 +249,12 @@ def test_scores_far_from_zero(gpu, case, far, dtype):
             if dtype == BF16:
                 ds += (top @ np.abs(k).T).max(-1) * D ** -0.5 * 2.0 ** -11 + D ** 0.5 * top.max(-1) * 2.0 ** -25
             reach = np.maximum(v.max(0) - out, out - v.min(0))
-            with np.errstate(divide="ignore", over="ignore"):
-                moved = np.exp(np.minimum(np.log(dev) + np.where(ds < 1, np.log(np.expm1(ds)) + ds, 2 * ds)[:, None], 50))
-            # the weights' roundings also move a result beyond the values
             keys = len(p)
+            moved = dev * (np.expm1(np.minimum(ds, 1)) * np.exp(np.minimum(ds, 1)))[:, None]
+            for g in np.nonzero(ds >= 1)[0]:
+                near = x[g] >= x[g].max() - 2 * ds[g] - 40
+                moved[g] = np.abs(v[near] - out[g]).max(0) + keys * np.exp(-40.0) * reach[g]
+            # the weights' roundings also move a result beyond the values
             tol = np.minimum(moved, reach) + np.maximum(wide, va.max(0)) * (keys + 64) * 2.0 ** -24
             tol = tol + keys * 2.0 ** -33 * c[3][..., 1].max().astype(float)
             if dtype == BF16:
