@@ -70,6 +70,18 @@ __device__ __forceinline__ uint32_t sixteenth(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2, w) * half2{(_Float16)0.0625f, (_Float16)0.0625f});
 }
 
+// What fp16 leaves of a pair that was rounded to `h`; `minus` is -1 in a register,
+// so that each half is one mixed multiply-add.
+__device__ __forceinline__ uint32_t rest_of(float a, float b, uint32_t h, float minus) {
+    const half2 v = __builtin_bit_cast(half2, h);
+    const half2 r = {(_Float16)__builtin_fmaf((float)v[0], minus, a), (_Float16)__builtin_fmaf((float)v[1], minus, b)};
+    return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ float minus_one() {
+    float m = -1.0f;
+    asm("" : "+s"(m));
+    return m;
+}
 // z + 8 s.
 __device__ __forceinline__ float middle(uint32_t zs) {
     return __builtin_fmaf((float)zs_s(zs), 8.0f, (float)zs_z(zs));
@@ -153,6 +165,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
         cut_info(a, D)[row] = make_int2(uncut ? -1 : piece.slot * kRows + low, (int)piece.pieces);
     const uint32_t sees = keys_within(start + tok + 1, k1);       // keys before this one
 
+    const float minus = minus_one();
     // q of the row: values D / 4 quad + 8 j + 0 .. 7 for matrix step j
     half8 qh[NS][NQ];
     float c_row, q_sum = 0.0f;
@@ -169,9 +182,9 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
                 top = fmaxf(top, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
             }
         top = quad_max(top);
-        q_sum = quad_sum(q_sum) * a.scale2;
         const float f = a.scale2 < 0.0f ? -to_f16_range(top) : to_f16_range(top);
-        c_row = BF16 ? a.scale2 / f * kRaw : a.scale2 / f;
+        q_sum = quad_sum(q_sum) * (BF16 ? f / kRaw : f);
+        c_row = fmaxf(BF16 ? a.scale2 / f * kRaw : a.scale2 / f, kTiny);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
             const float x[8] = {v[j][0].x * f, v[j][0].y * f, v[j][0].z * f, v[j][0].w * f,
@@ -180,7 +193,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 w[e] = f16_pair(x[e], x[e + 4]);
-                if (!BF16) z[e] = f16_rest(x[e], x[e + 4], w[e]);
+                if (!BF16) z[e] = rest_of(x[e], x[e + 4], w[e], minus);
                 if (BF16 && (e & 1)) w[e] = sixteenth(w[e]);
             }
             qh[0][j] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
@@ -256,7 +269,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
         int entry = entry_at(first_tile + kStep), id_next = -1;
         load_v(first_tile, id);
         for (uint32_t tile = first_tile; tile < k1; tile += kStep) {
-            float x[16];                    // scores of the quad's tokens, in powers of two
+            float x[16];                    // scores of the quad's tokens over c_row
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt) {
                 float4v s = {0.f, 0.f, 0.f, 0.f};
@@ -270,7 +283,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t zs = zk[4 * tt + i];
                     const float z_part = BF16 ? __builtin_fmaf(q_sum, (float)zs_z(zs), 0.0f) : q_sum * middle(zs);
-                    x[4 * tt + i] = __builtin_fmaf(s[i] * c_row, (float)zs_s(zs), z_part);
+                    x[4 * tt + i] = __builtin_fmaf(s[i], (float)zs_s(zs), z_part);
                 }
             }
             // also behind the last tile (block 0's then): a branch would cost a copy of
@@ -297,7 +310,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
                 top = fmaxf(top, x[e]);
                 zs_top = max(zs_top, zv[e]);
             }
-            top = quad_max(top);
+            top = quad_max(top * c_row);
             const float u_new = fmaxf(ref.u, step_above(quad_max((float)zs_s(zs_top))));
             if (__builtin_expect(__ballot(top > ref.above || u_new != ref.u) != 0, 0)) {
                 const float fix = ref.follow(top, u_new);
@@ -306,10 +319,12 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 #pragma unroll
                 for (int i = 0; i < NO; ++i) o[i] *= fix;
             }
-            const float base = ref.far ? ref.r2 : ref.r1;
-            if (__ballot(ref.far) != 0) {
+            float base = ref.r1, cs = c_row;
+            if (__ballot(ref.far) != 0) {                  // r2 is 0 for rows that are not
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] -= ref.far ? ref.r1 : 0.0f;
+                for (int e = 0; e < 16; ++e) x[e] = x[e] * c_row - ref.r1;
+                base = ref.r2;
+                cs = 1.0f;
             }
             half8 ph[NS][2];
 #pragma unroll
@@ -319,15 +334,16 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint32_t zs = zv[8 * k + e];
-                    const float p = exp2_fast(x[8 * k + e] - base);
+                    const float p = exp2_fast(__builtin_fmaf(x[8 * k + e], cs, -base));
                     l += p;
                     o_z = __builtin_fmaf(p, BF16 ? (float)zs_z(zs) : middle(zs), o_z);
                     y[e] = __builtin_fmaf(p, (float)zs_s(zs), 0.0f);
+                    if (!BF16) asm("" : "+v"(y[e]));       // formed once, for both halves
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     hi[e] = f16_pair(y[e], y[e + 4]);
-                    if (!BF16) lo[e] = f16_rest(y[e], y[e + 4], hi[e]);
+                    if (!BF16) lo[e] = rest_of(y[e], y[e + 4], hi[e], minus);
                     if (BF16 && (e & 1)) hi[e] = sixteenth(hi[e]);
                 }
                 ph[0][k] = __builtin_bit_cast(half8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
@@ -449,9 +465,35 @@ __device__ __forceinline__ half8 values8(uint32_t w, const uint32_t *s, const ui
 template <int D>
 struct ManyLds {
     uint4 k[2 * kTile * D / 8], v[2 * kTile * D / 8];
-    uint32_t zk[2][kTile], zv[2][kTile];    // fp32 rows: z and s by token
-    uint32_t pairs[kWaves][16];             // bf16 rows: of a wave's 16 tokens of V, s and z by pair of codes8
+    // fp32 rows, by token: z + 8 s, and the steps
+    alignas(16) float k_mid[2][kTile], v_mid[2][kTile];
+    alignas(16) uint16_t k_step[2][kTile], v_step[2][kTile];
+    alignas(16) uint32_t pairs[kWaves][16];             // bf16 rows: of a wave's 16 tokens of V, s and z by pair of codes8
 };
+// Eight tokens' z + 8 s and s out of LDS.
+struct Steps8 {
+    float mid[8];
+    uint32_t step[4];
+    __device__ __forceinline__ Steps8() {}
+    __device__ __forceinline__ Steps8(const float *mids, const uint16_t *steps, int at) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 w = *reinterpret_cast<const float4 *>(mids + at + 4 * i);
+            mid[4 * i] = w.x; mid[4 * i + 1] = w.y; mid[4 * i + 2] = w.z; mid[4 * i + 3] = w.w;
+        }
+        const uint4 w = *reinterpret_cast<const uint4 *>(steps + at);
+        step[0] = w.x; step[1] = w.y; step[2] = w.z; step[3] = w.w;
+    }
+    __device__ __forceinline__ float s(int i) const {
+        return (float)__builtin_bit_cast(half2, step[i >> 1])[i & 1];
+    }
+};
+// The larger of each half.
+__device__ __forceinline__ uint32_t max_u16(uint32_t a, uint32_t b) {
+    typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2v, a),
+                                                                  __builtin_bit_cast(ushort2v, b)));
+}
 template <bool BF16, int D>
 __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, ManyLds<D> &lds) {
     constexpr int NS = BF16 ? 1 : 2;
@@ -498,6 +540,7 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
     const uint32_t sees_lo = keys_within(start + min(rw, all_rows - 1) / G + 1, k1);
     const uint32_t sees_hi = keys_within(start + min(rw + 31, all_rows - 1) / G + 1, k1);
 
+    const float minus = minus_one();
     half8 qh[NS][NQ];
     float c_row, q_sum = 0.0f;
     {
@@ -513,9 +556,9 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
                 top = fmaxf(top, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
             }
         top = half_max(top);
-        q_sum = (q_sum + __shfl_xor(q_sum, 32)) * a.scale2;
         const float f = a.scale2 < 0.0f ? -to_f16_range(top) : to_f16_range(top);
-        c_row = a.scale2 / f;
+        q_sum = (q_sum + __shfl_xor(q_sum, 32)) * f;
+        c_row = fmaxf(a.scale2 / f, kTiny);
 #pragma unroll
         for (int s = 0; s < NQ; ++s) {
             const float x[8] = {v[s][0].x * f, v[s][0].y * f, v[s][0].z * f, v[s][0].w * f,
@@ -524,7 +567,7 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 w[e] = f16_pair(x[e], x[e + 4]);
-                if (NS == 2) z[e] = f16_rest(x[e], x[e + 4], w[e]);
+                if (NS == 2) z[e] = rest_of(x[e], x[e + 4], w[e], minus);
             }
             qh[0][s] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
             if (NS == 2) qh[NS - 1][s] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
@@ -617,8 +660,14 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
 #pragma unroll
             for (int j = 0; j < NW; ++j)
                 *reinterpret_cast<half8 *>(lds_v + (va ^ 16 * (j & 1)) + (j >> 1) * 128) = codes8<8>(vr[j]);
-            if ((gt & 3) == 0) lds.zk[buf][pk] = zk;
-            if (lane < 16) lds.zv[buf][tv] = zv;
+            if ((gt & 3) == 0) {
+                lds.k_mid[buf][pk] = middle(zk);
+                lds.k_step[buf][pk] = (uint16_t)(zk >> 16);
+            }
+            if (lane < 16) {
+                lds.v_mid[buf][tv] = middle(zv);
+                lds.v_step[buf][tv] = (uint16_t)(zv >> 16);
+            }
         }
     };
 
@@ -656,13 +705,15 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
 #pragma unroll
-        for (int st = 0; st < NQ; ++st)
+        for (int st = 0; st < NQ; ++st) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const half8 k = *reinterpret_cast<const half8 *>(lds_k + (ka ^ 32 * st) + t * 64 * D);
 #pragma unroll
                 for (int x = 0; x < NS; ++x) s[t] = mfma_32x32x16(k, qh[x][st], s[t]);
             }
+            if (!BF16 && (st & 1)) __builtin_amdgcn_sched_barrier(0);
+        }
         to_lds(buf ^ 1);
         __builtin_amdgcn_s_setprio(0);
         const uint64_t used = __ballot(in_use);             // bit g: granule g holds tokens
@@ -670,38 +721,41 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
         load_tile(tile + 2 * kTile);
         load_ids(tile + 3 * kTile);
         if (here) {
-            const bool whole = (used & 15) == 15 && tile + kTile <= sees_lo;            // uniform
-            const int lim = tile < sees ? (int)min(sees - tile, (uint32_t)kTile) : 0;
+            const bool whole = __builtin_amdgcn_readfirstlane((used & 15) == 15 && tile + kTile <= sees_lo);
+            // of the tile's keys this lane's, 16 g + 8 half + e, are seen below lim = 16 g + e
+            const int lim = (tile < sees ? (int)min(sees - tile, (uint32_t)kTile) : 0) - 8 * half;
             float u_new = 1.0f;
             if (!BF16) {
-                uint32_t zs_top = 0;
+                uint32_t top2 = 0;                          // of two steps each; they are not negative
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint4 *zk = reinterpret_cast<const uint4 *>(&lds.zk[buf][16 * g + 8 * half]);
-                    const uint4 *zv = reinterpret_cast<const uint4 *>(&lds.zv[buf][16 * g + 8 * half]);
+                    __builtin_amdgcn_sched_barrier(0);     // a granule's registers at a time, here and below
+                    const Steps8 zk(lds.k_mid[buf], lds.k_step[buf], 16 * g + 8 * half);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 w = zk[i], y = zv[i];
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                    for (int e = 0; e < 8; ++e)
+                        s[g >> 1][8 * (g & 1) + e] =
+                            __builtin_fmaf(s[g >> 1][8 * (g & 1) + e], zk.s(e), q_sum * zk.mid[e]);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(&lds.v_step[buf][16 * g + 8 * half]);
+                    uint32_t ys[4] = {y.x, y.y, y.z, y.w};
+                    if (!whole) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float x = s[g >> 1][8 * (g & 1) + 4 * i + e] * c_row;
-                            s[g >> 1][8 * (g & 1) + 4 * i + e] =
-                                __builtin_fmaf(x, (float)zs_s(ws[e]), q_sum * middle(ws[e]));
-                            const bool seen = whole || 16 * g + 8 * half + 4 * i + e < lim;
-                            zs_top = max(zs_top, seen ? ys[e] : 0u);
+                        for (int i = 0; i < 4; ++i) {
+                            const int at = 16 * g + 2 * i;
+                            ys[i] &= at + 1 < lim ? 0xFFFFFFFFu : at < lim ? 0xFFFFu : 0u;
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top2 = max_u16(top2, ys[i]);
                 }
-                u_new = fmaxf(ref.u, step_above(half_max((float)zs_s(zs_top))));
+                u_new = fmaxf(ref.u, step_above(half_max((float)zs_s(max_u16(top2, top2 << 16)))));
             }
             if (!whole) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int lim_g = used >> g & 1 ? lim - 16 * g - 8 * half : 0;
+                    const int lim_g = used >> g & 1 ? lim : 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        s[g >> 1][8 * (g & 1) + e] = e < lim_g ? s[g >> 1][8 * (g & 1) + e] : -INFINITY;
+                        s[g >> 1][8 * (g & 1) + e] = 16 * g + e < lim_g ? s[g >> 1][8 * (g & 1) + e] : -INFINITY;
                 }
             }
             float top = -INFINITY;
@@ -709,12 +763,8 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, s[t][e]);
-            float cs = 1.0f;
-            if (BF16) {
-                cs = fmaxf(c_row, kTiny);                  // positive: q has the scale's sign
-                top *= cs;
-            }
-            top = half_max(top);
+            float cs = c_row;                              // positive: q has the scale's sign
+            top = half_max(top * cs);
             if (__builtin_expect(__ballot(top > ref.above || u_new != ref.u) != 0, 0)) {
                 const float fix = ref.follow(top, u_new);
                 l *= fix;
@@ -734,32 +784,25 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {                  // 16 keys
+                if (!BF16) __builtin_amdgcn_sched_barrier(0);
                 uint32_t hi[4], lo[4];
                 float y[8];
-                uint32_t zv[8];
-                if (!BF16) {
-                    const uint4 *from = reinterpret_cast<const uint4 *>(&lds.zv[buf][16 * g + 8 * half]);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 w = from[i];
-                        zv[4 * i] = w.x; zv[4 * i + 1] = w.y; zv[4 * i + 2] = w.z; zv[4 * i + 3] = w.w;
-                    }
-                }
+                const Steps8 zv = BF16 ? Steps8() : Steps8(lds.v_mid[buf], lds.v_step[buf], 16 * g + 8 * half);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float x = s[g >> 1][8 * (g & 1) + e];
-                    const float p = exp2_fast(BF16 ? __builtin_fmaf(x, cs, -base) : x - base);
+                    const float p = exp2_fast(__builtin_fmaf(s[g >> 1][8 * (g & 1) + e], cs, -base));
                     l += p;
                     y[e] = p;
                     if (!BF16) {
-                        o_z = __builtin_fmaf(p, middle(zv[e]), o_z);
-                        y[e] = __builtin_fmaf(p, (float)zs_s(zv[e]), 0.0f);
+                        o_z = __builtin_fmaf(p, zv.mid[e], o_z);
+                        y[e] = __builtin_fmaf(p, zv.s(e), 0.0f);
+                        asm("" : "+v"(y[e]));              // formed once, for both halves
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     hi[e] = f16_pair(y[e], y[e + 4]);
-                    if (!BF16) lo[e] = f16_rest(y[e], y[e + 4], hi[e]);
+                    if (!BF16) lo[e] = rest_of(y[e], y[e + 4], hi[e], minus);
                 }
                 const half8 p_hi = __builtin_bit_cast(half8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                 half8 p_lo;
