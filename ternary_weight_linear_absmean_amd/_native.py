@@ -6,9 +6,14 @@ workspace) with torch when the caller gives none, and passes raw device
 pointers and the current HIP stream to the C entry point of the same name.
 Every step of the computation runs in libbitlinear's kernels.  There is no
 fallback: if the library is missing, ``load()`` raises.
+
+The calls on the paged caches are made by ``_calls`` (csrc/torch_calls.cpp) where
+nothing about their arguments is out of the ordinary, as a decode step waits for
+the host otherwise; what that leaves is made, or refused, here.
 """
 import collections
 import ctypes
+import importlib
 import os
 
 import torch
@@ -101,6 +106,10 @@ Kv4Cache = collections.namedtuple("Kv4Cache", ("K", "V", "zk", "zv"))
 Rope = collections.namedtuple("Rope", ("cos_sin", "interleaved"), defaults=(False,))
 
 _lib = None
+_calls = None
+_ENTRIES = ("bitlinear_kv8_append", "bitlinear_kv8_append_rope", "bitlinear_kv4_append", "bitlinear_kv8_read",
+            "bitlinear_kv4_read", "bitlinear_kv8_attention", "bitlinear_kv4_attention",
+            "bitlinear_kv8_attention_ws_bytes", "bitlinear_kv4_attention_ws_bytes")
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
@@ -113,8 +122,9 @@ class BitLinearError(RuntimeError):
 
 
 def load():
-    """Load libbitlinear.so (built in-tree by build.py); raise if it is missing."""
-    global _lib
+    """Load libbitlinear.so and _calls.so (built in-tree by build.py); raise if one is
+    missing."""
+    global _lib, _calls
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -199,7 +209,9 @@ def load():
     lib.bl_last_error.argtypes = []
     lib.bl_abi_version.restype = ctypes.c_int
     lib.bl_abi_version.argtypes = []
-    _lib = lib
+    calls = importlib.import_module("._calls", __package__)
+    calls.bind(*(ctypes.cast(getattr(lib, name), _p).value for name in _ENTRIES))
+    _lib, _calls = lib, calls
     return lib
 
 
@@ -684,6 +696,9 @@ def bitlinear_kv8_append(k, v, q_start, lengths, table, cache, stream=None):
     """The new tokens' rows k, v [n_tok, KVH, D] (fp32 or bf16) into the cache
     (Kv8Cache, updated in place).  int32 on the GPU: q_start [B + 1], lengths
     [B] (with the new tokens), table [B, max_blocks]."""
+    if stream is None and _calls is not None:
+        if _calls.append(8, k, v, q_start, lengths, table, cache, None, None, None) is not NotImplemented:
+            return
     dev, dt, kp, shape = _rows(k, 3, "k")
     c = _kv8(cache, dev)
     n = shape[0]
@@ -737,6 +752,10 @@ def bitlinear_kv8_append_rope(k, v, q_start, lengths, table, cache, rope, q=None
     without q; its rows of no sequence are left as they are."""
     if rope is None:
         raise ValueError("bitlinear_kv8_append_rope without rope")
+    if stream is None and _calls is not None:
+        r = _calls.append(8, k, v, q_start, lengths, table, cache, rope, q, q_out)
+        if r is not NotImplemented:
+            return r
     return _append_turned("bitlinear_kv8_append_rope", _kv8, k, v, q_start, lengths, table, cache, rope, q,
                           q_out, stream)
 
@@ -745,11 +764,20 @@ def bitlinear_kv4_append(k, v, q_start, lengths, table, cache, rope=None, q=None
     """The new tokens' rows k, v [n_tok, KVH, D] (fp32 or bf16) into the 4-bit cache
     (Kv4Cache, updated in place), as they are or, with rope, keys and q rotated as
     by bitlinear_kv8_append_rope (which see for q and what is returned)."""
+    if stream is None and _calls is not None:
+        r = _calls.append(4, k, v, q_start, lengths, table, cache, rope, q, q_out)
+        if r is not NotImplemented:
+            return r
     return _append_turned("bitlinear_kv4_append", _kv4, k, v, q_start, lengths, table, cache, rope, q, q_out,
                           stream)
 
 
-def _read(call, device_cache, q_start, lengths, table, cache, n_tok, dtype, k, v, stream):
+def _read(call, bits, q_start, lengths, table, cache, n_tok, dtype, k, v, stream):
+    if stream is None and _calls is not None and dtype in _DTYPES:
+        r = _calls.read(bits, q_start, lengths, table, cache, n_tok, dtype is torch.bfloat16, k, v)
+        if r is not NotImplemented:
+            return r
+    device_cache = _kv8 if bits == 8 else _kv4
     K = cache[0]
     if not isinstance(K, torch.Tensor) or not K.is_cuda:
         raise TypeError("the cache's K must be a CUDA (HIP) tensor")
@@ -780,12 +808,12 @@ def bitlinear_kv8_read(q_start, lengths, table, cache, n_tok, dtype=torch.float3
     """The cached tokens of rows 0 .. n_tok - 1 of a call as values, k and v
     [n_tok, KVH, D] of dtype (fp32 or bf16): the n_b rows of sequence b are its
     last n_b tokens.  q_start, lengths, table as for bitlinear_kv8_append."""
-    return _read("bitlinear_kv8_read", _kv8, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
+    return _read("bitlinear_kv8_read", 8, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
 
 
 def bitlinear_kv4_read(q_start, lengths, table, cache, n_tok, dtype=torch.float32, k=None, v=None, stream=None):
     """bitlinear_kv8_read of a 4-bit cache."""
-    return _read("bitlinear_kv4_read", _kv4, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
+    return _read("bitlinear_kv4_read", 4, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
 
 
 def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
@@ -794,6 +822,10 @@ def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=N
     out [n_tok, QH, D].  scale defaults to D ** -0.5; q_start, lengths, table
     as for bitlinear_kv8_append.  Rows of no sequence are left as they are.
     out may not overlap q."""
+    if stream is None and _calls is not None:
+        r = _calls.attention(8, q, q_start, lengths, table, cache, scale, out, ws)
+        if r is not NotImplemented:
+            return r
     dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
     c = _kv8(cache, dev)
     if D != c.D:
@@ -826,6 +858,10 @@ def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=N
 def bitlinear_kv4_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
                             stream=None):
     """bitlinear_kv8_attention over a 4-bit cache (Kv4Cache)."""
+    if stream is None and _calls is not None:
+        r = _calls.attention(4, q, q_start, lengths, table, cache, scale, out, ws)
+        if r is not NotImplemented:
+            return r
     dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
     c = _kv4(cache, dev)
     if D != c.D:

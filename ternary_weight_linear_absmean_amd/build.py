@@ -6,12 +6,16 @@ Each source is compiled to an object (in parallel), then linked into
 ``ternary_weight_linear_absmean_amd/libbitlinear.so``.  Device code is built
 with FMA contraction off (every fp32 step of the quantisers and the rescale
 is one IEEE rounding), without packed-fp32 instructions, and with the leading
-kernel arguments preloaded into SGPRs.
+kernel arguments preloaded into SGPRs.  Beside it ``_calls.so``, the Python
+binding's short way into the calls on the paged caches (host code, with torch's
+headers).
 """
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libbitlinear.so")
+CALLS = os.path.join(HERE, "_calls.so")
 
 SOURCES = ["api.cpp", "quant.hip", "gemv.hip", "gemm.hip", "gemm_skinny.hip", "ffn.hip",
            "stack.hip", "stack_persistent.hip", "backward.hip", "t5.hip",
@@ -56,10 +61,30 @@ def _compile(src, verbose):
     return obj
 
 
+def _build_calls(verbose):
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    tmp = CALLS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(rocm, "include"), os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp,
+           "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on torch_calls.cpp:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(jobs, len(SOURCES)))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(jobs, len(SOURCES) + 1))) as ex:
+        calls = ex.submit(_build_calls, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:
