@@ -46,13 +46,13 @@ struct Args {
 
 template <typename E, int D, bool ROPE>
 __global__ __launch_bounds__(2 * D) void kv4_append_kernel(Args<D> a) {
-    constexpr int kThreads = 2 * D, kPer = D / 8;         // threads, those of a token
+    constexpr int kPer = D / 8;                           // threads of a token
     __shared__ alignas(16) uint8_t codes[D][kTokens];
     const Kv8Seqs &seqs = a.seqs;
     const Kv4Cache &c = a.c;
     const int64_t appends = a.slots * c.KVH * 2;
     if (ROPE && blockIdx.x >= appends) {
-        turn_queries<kThreads>(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, D == 64 ? 6 : 7, seqs,
+        turn_queries(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(seqs.n_tok, a.QH, D), D == 64 ? 6 : 7, seqs,
                                (int64_t)seqs.max_blocks << c.t_shift, a.rope, blockIdx.x - appends);
         return;
     }
@@ -84,10 +84,14 @@ __global__ __launch_bounds__(2 * D) void kv4_append_kernel(Args<D> a) {
 
     float4 x[2];
     if (ROPE && !is_v) {
-        const E *const p = static_cast<const E *>(a.k) + row, *rows[2] = {p, p};
-        const int at[2] = {8 * td, 8 * td + 4};
-        const int64_t place[2] = {pos, pos};
-        load_turned<2>(rows, at, place, a.rope, x);
+        const E *const p = static_cast<const E *>(a.k) + row;
+        const bool on = 8 * td < a.rope.rot;
+        const Turn8 turn(a.rope, pos, on ? 8 * td : 0);
+        float4 y[2];
+        x[0] = load_row4(p + 8 * td);
+        x[1] = load_row4(p + 8 * td + 4);
+        turn.load_others(p, y);
+        if (on) turn.apply(x, y);
     } else {
         const E *p = static_cast<const E *>(is_v ? a.v : a.k) + row + 8 * td;
         x[0] = load_row4(p);
@@ -149,7 +153,7 @@ hipError_t append(const void *k, const void *v, const void *q, void *q_out, int 
     int64_t groups = a.slots * c.KVH * 2;
     if (rope) {
         a.rope = *rope;
-        groups += rope_groups<2 * D>(seqs.n_tok, QH, D);
+        groups += rope_groups(seqs.n_tok, QH, D, 2 * D);
     }
     if (groups * 2 * D >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     if (rope)

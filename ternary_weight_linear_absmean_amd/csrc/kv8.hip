@@ -238,8 +238,8 @@ __global__ __launch_bounds__(kThreads) void kv8_append_rope_kernel(RopeArgs a) {
     __shared__ AppendLds<E, NC> lds;
     const int64_t appends = a.slots * a.c.KVH * 2;
     if (blockIdx.x >= appends) {
-        turn_queries<kThreads>(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, a.c.D == 64 ? 6 : 7,
-                               a.seqs, (int64_t)a.seqs.max_blocks << a.c.t_shift, a.rope, blockIdx.x - appends);
+        turn_queries(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(a.seqs.n_tok, a.QH, a.c.D),
+                     a.c.D == 64 ? 6 : 7,                               a.seqs, (int64_t)a.seqs.max_blocks << a.c.t_shift, a.rope, blockIdx.x - appends);
         return;
     }
     const uint32_t pair = blockIdx.x / 2, slot = pair / (uint32_t)a.c.KVH;
@@ -288,7 +288,7 @@ hipError_t launch_kv8_append_rope(const void *k, const void *v, const void *q, v
                                   const Kv8Seqs &seqs, const bl_kv8 &cache, const bl_rope &rope, hipStream_t s) {
     const Kv8Cache c = kv8_device(cache);
     const RopeArgs a = {seqs, c, rope_device(rope), k, v, q, q_out, QH, (seqs.n_tok >> c.t_shift) + 2 * (int64_t)seqs.B};
-    const int64_t groups = a.slots * c.KVH * 2 + rope_groups<kThreads>(seqs.n_tok, QH, c.D);
+    const int64_t groups = a.slots * c.KVH * 2 + rope_groups(seqs.n_tok, QH, c.D, kThreads);
     if (groups * kThreads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     return dtype ? append_rope<uint16_t>(a, groups, s) : append_rope<float>(a, groups, s);
 }

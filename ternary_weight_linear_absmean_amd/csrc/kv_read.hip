@@ -3,9 +3,12 @@
 // The value of a code is formed in fp32: fl(code s) for 8 bits, fl(z + code s)
 // for 4 (code s is exact), then rounded to the rows' type.
 //
-// One workgroup per (16 consecutive positions of a sequence, head, K or V), as
-// the 4-bit append's.  K's codes are in the rows' order; V's are 16 tokens of
-// one value side by side and cross LDS.
+// One workgroup per (16 consecutive positions of a sequence, HEADS heads, K or V),
+// as the 4-bit append's groups.  K's codes are in the rows' order; V's are 16
+// tokens of one value side by side and cross LDS.  A workgroup's time is its
+// chain of loads (starts, length, table entry, codes), so where there are more of them than run at
+// once each takes four heads, their loads all in flight: 16 sequences of up to
+// 4096 tokens, 5 heads.
 #include "kv4_common.h"
 #include "kv8_common.h"
 #include "rope.h"
@@ -21,16 +24,17 @@ struct Args {
     int64_t slots;
 };
 
-template <typename E, int D, typename C>
+template <typename E, int D, int HEADS, typename C>
 __global__ __launch_bounds__(2 * D) void kv_read_kernel(Args<C> a) {
     constexpr bool kFour = __is_same(C, Kv4Cache);
     constexpr int kPer = D / 8;                           // threads of a token
-    __shared__ alignas(16) uint8_t codes[16][D + 16];
+    __shared__ alignas(16) uint8_t codes[HEADS][16][D + 16];
     const Kv8Seqs &seqs = a.seqs;
     const C &c = a.c;
-    const uint32_t pair = blockIdx.x / 2, slot = pair / (uint32_t)c.KVH;
+    const uint32_t chunks = (uint32_t)(c.KVH + HEADS - 1) / HEADS;
+    const uint32_t pair = blockIdx.x / 2, slot = pair / chunks;
     const bool is_v = blockIdx.x & 1;
-    const int h = (int)(pair - slot * c.KVH);
+    const int h0 = (int)(pair - slot * chunks) * HEADS, heads = min(HEADS, c.KVH - h0);
     const int b = find_seq(seqs.B, slot, [&](int i) { return (int64_t)(q_at(seqs, i) >> 4) + 2 * (int64_t)i; });
     const int q0 = q_at(seqs, b), n = q_at(seqs, b + 1) - q0;
     const int64_t nth = (int64_t)slot - ((q0 >> 4) + 2 * (int64_t)b);
@@ -46,73 +50,98 @@ __global__ __launch_bounds__(2 * D) void kv_read_kernel(Args<C> a) {
     const int t = threadIdx.x / kPer, td = threadIdx.x % kPer;
     const int64_t pos = 16 * j + t;
     const bool mine = pos >= first && pos < last;
-    float4 o[2] = {};
-    if (held) {
-        const int64_t head = (int64_t)id * c.KVH + h;
-        const int in = (int)(16 * j & (c.T - 1));         // first of the 16 slots
-        float w[8];
+    E *const dst = static_cast<E *>(is_v ? a.v : a.k) + ((q0 + (pos - start)) * c.KVH + h0) * (int64_t)D + 8 * td;
+    if (!held) {
+        if (mine)
+            for (int i = 0; i < heads; ++i) {
+                store_row4(dst + i * D, make_float4(0.f, 0.f, 0.f, 0.f));
+                store_row4(dst + i * D + 4, make_float4(0.f, 0.f, 0.f, 0.f));
+            }
+        return;
+    }
+    const int64_t head = (int64_t)id * c.KVH + h0;
+    const int in = (int)(16 * j & (c.T - 1));             // first of the 16 slots
+    uint32_t scale[HEADS];                                // z and s, or a scale
+    uint2 u[HEADS];                                       // K: this thread's codes
+    uint4 g[HEADS];                                       // V: value threadIdx.x of the 16 tokens
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+        const int64_t hi = head + min(i, heads - 1);
         if constexpr (kFour) {
-            const uint32_t zs = (is_v ? c.zv : c.zk)[head * c.T + in + t];
-            uint32_t u = 0;
+            scale[i] = (is_v ? c.zv : c.zk)[hi * c.T + in + t];
             if (!is_v) {
-                u = *reinterpret_cast<const uint32_t *>(c.K + (head * c.T + in + t) * (int64_t)(D / 2) + 4 * td);
-            } else {
-                // value d's 8 bytes, two tokens to a byte; line i of LDS: tokens 2i, 2i + 1
-                if (threadIdx.x < D) {
-                    const uint2 g = *reinterpret_cast<const uint2 *>(
-                        c.V + (head * (c.T / 16) + in / 16) * (int64_t)(8 * D) + 8 * threadIdx.x);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        codes[i][threadIdx.x] = (uint8_t)(g.x >> (8 * i));
-                        codes[4 + i][threadIdx.x] = (uint8_t)(g.y >> (8 * i));
-                    }
-                }
-                __syncthreads();
-                const uint2 p = *reinterpret_cast<const uint2 *>(&codes[t >> 1][8 * td]);
-                const int sh = 4 * (t & 1);
-                const uint32_t x = p.x >> sh & 0x0F0F0F0Fu, y = p.y >> sh & 0x0F0F0F0Fu;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) u |= (x >> (8 * e) & 15u) << (4 * e) | (y >> (8 * e) & 15u) << (16 + 4 * e);
+                u[i].x = *reinterpret_cast<const uint32_t *>(c.K + (hi * c.T + in + t) * (int64_t)(D / 2) + 4 * td);
+            } else if (threadIdx.x < D) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(c.V + (hi * (c.T / 16) + in / 16) * (int64_t)(8 * D) +
+                                                                 8 * threadIdx.x);
+                g[i].x = w.x;
+                g[i].y = w.y;
             }
-            const float z = (float)zs_z(zs), s = (float)zs_s(zs);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = __builtin_fmaf((float)(u >> (4 * e) & 15u), s, z);
         } else {
-            const float s = (is_v ? c.sv : c.sk)[head];
-            uint2 u;
-            if (!is_v) {
-                u = *reinterpret_cast<const uint2 *>(c.K + (head * c.T + in + t) * (int64_t)D + 8 * td);
-            } else {
-                if (threadIdx.x < D) {
-                    const uint4 g = *reinterpret_cast<const uint4 *>(c.V + (head * D + threadIdx.x) * (int64_t)c.T + in);
-                    const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+            scale[i] = __float_as_uint((is_v ? c.sv : c.sk)[hi]);
+            if (!is_v)
+                u[i] = *reinterpret_cast<const uint2 *>(c.K + (hi * c.T + in + t) * (int64_t)D + 8 * td);
+            else if (threadIdx.x < D)
+                g[i] = *reinterpret_cast<const uint4 *>(c.V + (hi * D + threadIdx.x) * (int64_t)c.T + in);
+        }
+    }
+    if (is_v) {
+        // line of LDS: a token, or two of 4 bits
+        if (threadIdx.x < D) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) codes[i][threadIdx.x] = (uint8_t)(gw[i >> 2] >> (8 * (i & 3)));
-                }
-                __syncthreads();
-                u = *reinterpret_cast<const uint2 *>(&codes[t][8 * td]);
-            }
+            for (int i = 0; i < HEADS; ++i) {
+                const uint32_t w[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[e] = __fmul_rn((float)(int8_t)(u.x >> (8 * e)), s);
-                w[4 + e] = __fmul_rn((float)(int8_t)(u.y >> (8 * e)), s);
+                for (int y = 0; y < (kFour ? 8 : 16); ++y) codes[i][y][threadIdx.x] = (uint8_t)(w[y >> 2] >> (8 * (y & 3)));
             }
         }
-        o[0] = make_float4(w[0], w[1], w[2], w[3]);
-        o[1] = make_float4(w[4], w[5], w[6], w[7]);
+        __syncthreads();
     }
     if (!mine) return;
-    E *dst = static_cast<E *>(is_v ? a.v : a.k) + ((q0 + (pos - start)) * c.KVH + h) * (int64_t)D + 8 * td;
-    store_row4(dst, o[0]);
-    store_row4(dst + 4, o[1]);
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+        if (i >= heads) break;
+        float w[8];
+        if constexpr (kFour) {
+            const float z = (float)zs_z(scale[i]), s = (float)zs_s(scale[i]);
+            if (!is_v) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = __builtin_fmaf((float)(u[i].x >> (4 * e) & 15u), s, z);
+            } else {
+                const uint2 p = *reinterpret_cast<const uint2 *>(&codes[i][t >> 1][8 * td]);
+                const int sh = 4 * (t & 1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = __builtin_fmaf((float)(p.x >> (sh + 8 * e) & 15u), s, z);
+                    w[4 + e] = __builtin_fmaf((float)(p.y >> (sh + 8 * e) & 15u), s, z);
+                }
+            }
+        } else {
+            const float s = __uint_as_float(scale[i]);
+            const uint2 p = is_v ? *reinterpret_cast<const uint2 *>(&codes[i][t][8 * td]) : u[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = __fmul_rn((float)(int8_t)(p.x >> (8 * e)), s);
+                w[4 + e] = __fmul_rn((float)(int8_t)(p.y >> (8 * e)), s);
+            }
+        }
+        store_row4(dst + i * D, make_float4(w[0], w[1], w[2], w[3]));
+        store_row4(dst + i * D + 4, make_float4(w[4], w[5], w[6], w[7]));
+    }
 }
+
+constexpr int64_t kAtOnce = 4096;                         // workgroups
 
 template <typename E, int D, typename C>
 hipError_t read(const Kv8Seqs &seqs, const C &c, void *k, void *v, hipStream_t s) {
     const Args<C> a = {seqs, c, k, v, (seqs.n_tok >> 4) + 2 * (int64_t)seqs.B};
-    const int64_t groups = a.slots * c.KVH * 2;
+    const bool four = a.slots * c.KVH * 2 > kAtOnce;
+    const int64_t groups = a.slots * (four ? (c.KVH + 3) / 4 : c.KVH) * 2;
     if (groups * 2 * D >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((kv_read_kernel<E, D, C>), dim3((unsigned)groups), dim3(2 * D), 0, s, a);
+    if (four)
+        hipLaunchKernelGGL((kv_read_kernel<E, D, 4, C>), dim3((unsigned)groups), dim3(2 * D), 0, s, a);
+    else
+        hipLaunchKernelGGL((kv_read_kernel<E, D, 1, C>), dim3((unsigned)groups), dim3(2 * D), 0, s, a);
     return hipGetLastError();
 }
 template <typename C>

@@ -24,6 +24,16 @@ inline Rope rope_device(const bl_rope &r) {
     return {r.cos_sin, (int)r.rot, r.interleaved};
 }
 
+// Rows that this kernel does not read again: past the caches.
+__device__ __forceinline__ void store_row4(float *p, float4 v) {
+    __builtin_nontemporal_store(float4v{v.x, v.y, v.z, v.w}, reinterpret_cast<float4v *>(p));
+}
+__device__ __forceinline__ void store_row4(uint16_t *p, float4 v) {
+    typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+    __builtin_nontemporal_store(uint2v{bf16_round(v.x) | bf16_round(v.y) << 16, bf16_round(v.z) | bf16_round(v.w) << 16},
+                                reinterpret_cast<uint2v *>(p));
+}
+
 // x c - y s (or + with s negated), rounded once to fp32.
 __device__ __forceinline__ float turned(float x, float c, float y, float s) {
     return (float)__builtin_fma((double)x, (double)c, -((double)y * (double)s));
@@ -83,53 +93,111 @@ __device__ __forceinline__ void load_turned(const E *const *rows, const int *d, 
     }
 }
 
-// The query rows of a call, turned: workgroup `group` of THREADS takes 8 values
-// a thread of the line of all.  Rows of no sequence are left; a row whose
-// position the cache has no room for is copied as it is.
-template <int THREADS>
-constexpr int64_t rope_groups(int64_t n_tok, int64_t QH, int64_t D) {
-    return (n_tok * QH * D / 8 + THREADS - 1) / THREADS;
-}
-__device__ __forceinline__ void store_row4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void store_row4(uint16_t *p, float4 v) {
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(bf16_round(v.x) | bf16_round(v.y) << 16, bf16_round(v.z) | bf16_round(v.w) << 16);
-}
-template <int THREADS, typename E>
-__device__ __forceinline__ void turn_queries(const E *q, E *out, int QH, int d_shift, const Kv8Seqs &seqs,
-                                             int64_t room, const Rope &rope, int64_t group) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int per_shift = d_shift - 3;                            // threads of a head
-    const int64_t heads = (int64_t)seqs.n_tok * QH;
-    const int64_t first = (group * THREADS + wave * 64) >> per_shift;      // a wave's heads
-    if (first >= heads) return;                                   // uniform
-    const int64_t head = first + (lane >> per_shift);
-    const int64_t last = min(first + (64 >> per_shift), heads) - 1;
-    const int row0 = (int)(first / QH), row1 = (int)(last / QH);
-    const int row = head < heads ? (int)(head / QH) : row1;
-    int64_t pos = -1;
-    bool mine = false;
-    for (int r = row0; r <= row1; ++r) {                          // one row of most calls, eight at most
-        const int b = find_seq(seqs.B, r, [&](int i) { return (int64_t)q_at(seqs, i); });
-        const int q0 = q_at(seqs, b), q1 = q_at(seqs, b + 1);
-        if (r == row && r >= q0 && r < q1) {
-            mine = true;
-            pos = (int64_t)seqs.lengths[b] - (q1 - r);
+// The same for 8 values of several heads at one position: d .. d + 7, in range.
+struct Turn8 {
+    float4 c[2], s[2];
+    int other;                    // where the second half of the pairs stands; -1: among the values
+    __device__ __forceinline__ Turn8(const Rope &rope, int64_t pos, int d) {
+        const int half = rope.rot / 2;
+        const float *line = rope.cos_sin + pos * rope.rot;
+        if (rope.neighbours) {                                    // uniform
+            other = -1;
+            const float4 c4 = load_row4(line + d / 2), s4 = load_row4(line + half + d / 2);
+            c[0] = make_float4(c4.x, c4.x, c4.y, c4.y);
+            c[1] = make_float4(c4.z, c4.z, c4.w, c4.w);
+            s[0] = make_float4(s4.x, -s4.x, s4.y, -s4.y);
+            s[1] = make_float4(s4.z, -s4.z, s4.w, -s4.w);
+        } else {
+            const bool upper = d >= half;
+            const int at = upper ? d - half : d;
+            other = upper ? at : d + half;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                c[i] = load_row4(line + at + 4 * i);
+                s[i] = load_row4(line + half + at + 4 * i);
+                if (upper) s[i] = make_float4(-s[i].x, -s[i].y, -s[i].z, -s[i].w);
+            }
         }
     }
-    if (!mine || head >= heads) return;
-    const int d = 8 * (lane & ((1 << per_shift) - 1));
-    const E *const src = q + (head << d_shift), *rows[2] = {src, src};
+    template <typename E>
+    __device__ __forceinline__ void load_others(const E *row, float4 *y) const {
+        if (other < 0) return;                                    // uniform
+        y[0] = load_row4(row + other);
+        y[1] = load_row4(row + other + 4);
+    }
+    __device__ __forceinline__ void apply(float4 *x, float4 *y) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 v = x[i], w = other < 0 ? make_float4(v.y, v.x, v.w, v.z) : y[i];
+            x[i] = make_float4(turned(v.x, c[i].x, w.x, s[i].x), turned(v.y, c[i].y, w.y, s[i].y),
+                               turned(v.z, c[i].z, w.z, s[i].z), turned(v.w, c[i].w, w.w, s[i].w));
+        }
+    }
+};
+
+// The query rows of a call, turned: a wave to a row, 8 values a lane, D / 8 lanes
+// to a head, the row's heads in turn, so that a row's place and its line of cos_sin are
+// found and loaded once.  Rows of no sequence are left; a row whose position
+// the cache has no room for is copied as it is.
+// A wave takes all heads of a row, or in calls of few rows those of one step: a
+// decode step waits for one wave's chain of loads, a prompt for the bytes.
+constexpr int64_t kFewTurnedRows = 512;
+constexpr int rope_heads(int64_t n_tok, int64_t QH, int64_t D) {
+    return n_tok > kFewTurnedRows ? (int)QH : (int)(512 / D);
+}
+constexpr int64_t rope_groups(int64_t n_tok, int64_t QH, int64_t D, int threads) {
+    if (QH == 0) return 0;
+    const int64_t per = rope_heads(n_tok, QH, D), waves = n_tok * ((QH + per - 1) / per);
+    return (waves + threads / 64 - 1) / (threads / 64);
+}
+template <int AT_ONCE, typename E>
+__device__ __forceinline__ void turn_heads(const E *q, E *out, int64_t row0, int h0, int h1, int step, int d_shift,
+                                           int d, bool on, const Turn8 &turn) {
+    for (; h0 < h1; h0 += AT_ONCE * step) {
+        float4 x[AT_ONCE][2], y[AT_ONCE][2];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {                       // all loads in flight, at clamped places
+            const E *src = q + ((row0 + min(h0 + i * step, h1 - 1)) << d_shift);
+            x[i][0] = load_row4(src + d);
+            x[i][1] = load_row4(src + d + 4);
+            turn.load_others(src, y[i]);
+        }
+        // out may be q: a head's threads are lanes of one wave, all of whose loads
+        // stand before its first store, and its heads are read by no other wave
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int h = h0 + i * step;
+            if (h >= h1) continue;
+            if (on) turn.apply(x[i], y[i]);
+            E *dst = out + ((row0 + h) << d_shift) + d;
+            store_row4(dst, x[i][0]);
+            store_row4(dst + 4, x[i][1]);
+        }
+    }
+}
+template <typename E>
+__device__ __forceinline__ void turn_queries(const E *q, E *out, int QH, int per, int d_shift, const Kv8Seqs &seqs,
+                                             int64_t room, const Rope &rope, int64_t group) {
+    const int lane = threadIdx.x & 63;
+    const int64_t unit = group * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int chunks = (QH + per - 1) / per;
+    const int64_t row = unit / chunks;
+    const int first = (int)(unit - row * chunks) * per, h1 = min(first + per, QH);
+    if (row >= seqs.n_tok) return;                                // uniform
+    const int b = find_seq(seqs.B, row, [&](int i) { return (int64_t)q_at(seqs, i); });
+    const int q0 = q_at(seqs, b), q1 = q_at(seqs, b + 1);
+    if (row < q0 || row >= q1) return;
+    int64_t pos = (int64_t)seqs.lengths[b] - (q1 - row);
     if (pos >= room) pos = -1;
-    const int at[2] = {d, d + 4};
-    const int64_t place[2] = {pos, pos};
-    float4 v[2];
-    load_turned<2>(rows, at, place, rope, v);
-    // out may be q: a head's threads are lanes of one wave, all of whose loads
-    // stand before its first store
-    __builtin_amdgcn_wave_barrier();
-    store_row4(out + (head << d_shift) + d, v[0]);
-    store_row4(out + (head << d_shift) + d + 4, v[1]);
+    const int per_shift = d_shift - 3, step = 64 >> per_shift;    // lanes of a head, heads at once
+    const int d = 8 * (lane & ((1 << per_shift) - 1));
+    const bool on = pos >= 0 && d < rope.rot;
+    const Turn8 turn(rope, on ? pos : 0, on ? d : 0);
+    if (h1 - first <= step)
+        turn_heads<1>(q, out, row * QH, first + (lane >> per_shift), h1, step, d_shift, d, on, turn);
+    else
+        turn_heads<4>(q, out, row * QH, first + (lane >> per_shift), h1, step, d_shift, d, on, turn);
 }
 
 }  // namespace bl
