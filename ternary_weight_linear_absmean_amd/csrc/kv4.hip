@@ -52,18 +52,18 @@ __global__ __launch_bounds__(2 * D) void kv4_append_kernel(Args<D> a) {
     const Kv4Cache &c = a.c;
     const int64_t appends = a.slots * c.KVH * 2;
     if (ROPE && blockIdx.x >= appends) {
-        turn_queries(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(seqs.n_tok, a.QH, D), D == 64 ? 6 : 7, seqs,
-                               (int64_t)seqs.max_blocks << c.t_shift, a.rope, blockIdx.x - appends);
+        turn_queries(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(seqs.n_tok, a.QH, D),
+                     D == 64 ? 6 : 7, seqs, (int64_t)seqs.max_blocks << c.t_shift, a.rope, blockIdx.x - appends);
         return;
     }
     const uint32_t pair = blockIdx.x / 2, slot = pair / (uint32_t)c.KVH;
     const bool is_v = blockIdx.x & 1;
     const int h = (int)(pair - slot * c.KVH);
-    const int b = find_seq(seqs.B, slot, [&](int i) { return (int64_t)(q_at(seqs, i) >> 4) + 2 * (int64_t)i; });
-    const int q0 = q_at(seqs, b), n = q_at(seqs, b + 1) - q0;
+    const SeqPlace in_seq = find_place(seqs, slot, [](int q, int i) { return (int64_t)(q >> 4) + 2 * (int64_t)i; });
+    const int b = in_seq.b, q0 = in_seq.q0, n = in_seq.q1 - q0;
     const int64_t nth = (int64_t)slot - ((q0 >> 4) + 2 * (int64_t)b);
     if (nth < 0 || n <= 0) return;
-    const int64_t len = seqs.lengths[b], start = len - n;          // of row q0
+    const int64_t len = in_seq.length, start = len - n;            // of row q0
     const int64_t j = (max(start, (int64_t)0) >> 4) + nth;         // the sequence's group
     const int64_t first = max(max(start, (int64_t)0), 16 * j), last = min(len, 16 * j + 16);
     if (j >= (int64_t)seqs.max_blocks << c.t_shift >> 4 || first >= last) return;

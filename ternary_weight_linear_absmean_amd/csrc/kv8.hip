@@ -64,14 +64,11 @@ __device__ __forceinline__ void append_block(const E *__restrict__ k, const E *_
     auto &wave_max = lds.wave_max;
     const int T = c.T, D = c.D, sh = c.t_shift;
 
-    const int b = find_seq(seqs.B, slot, [&](int i) {
-        return (int64_t)(q_at(seqs, i) >> sh) + 2 * (int64_t)i;
-    });
-    const int q0 = q_at(seqs, b);
+    const SeqPlace in_seq = find_place(seqs, slot, [&](int q, int i) { return (int64_t)(q >> sh) + 2 * (int64_t)i; });
+    const int b = in_seq.b, q0 = in_seq.q0, n = in_seq.q1 - q0;
     const int64_t nth = slot - ((q0 >> sh) + 2 * (int64_t)b);
-    const int n = q_at(seqs, b + 1) - q0;
     if (nth < 0 || n <= 0) return;
-    const int64_t len = seqs.lengths[b];
+    const int64_t len = in_seq.length;
     const int64_t start = len - n;                     // position of row q0
     const int64_t j = (max(start, (int64_t)0) >> sh) + nth;
     if (j >= seqs.max_blocks) return;
@@ -239,7 +236,8 @@ __global__ __launch_bounds__(kThreads) void kv8_append_rope_kernel(RopeArgs a) {
     const int64_t appends = a.slots * a.c.KVH * 2;
     if (blockIdx.x >= appends) {
         turn_queries(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(a.seqs.n_tok, a.QH, a.c.D),
-                     a.c.D == 64 ? 6 : 7,                               a.seqs, (int64_t)a.seqs.max_blocks << a.c.t_shift, a.rope, blockIdx.x - appends);
+                     a.c.D == 64 ? 6 : 7, a.seqs, (int64_t)a.seqs.max_blocks << a.c.t_shift, a.rope,
+                     blockIdx.x - appends);
         return;
     }
     const uint32_t pair = blockIdx.x / 2, slot = pair / (uint32_t)a.c.KVH;

@@ -31,4 +31,24 @@ __device__ __forceinline__ int find_seq(int B, int64_t i, F first) {
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// find_seq with what a kernel asks of the sequence next, its rows and length; first
+// takes q_start[b] and b.  Up to 64 sequences take one step of loads in all (a
+// wait for each after another costs a decode step 0.5 us).
+struct SeqPlace {
+    int b, q0, q1, length;
+};
+template <typename F>
+__device__ __forceinline__ SeqPlace find_place(const Kv8Seqs &s, int64_t i, F first) {
+    if (s.B <= 64) {
+        const int lane = threadIdx.x & 63, at = min(lane, s.B - 1);
+        const int q = q_at(s, at), next = q_at(s, at + 1), length = s.lengths[at];
+        const uint64_t below = __ballot(lane < s.B && first(q, lane) <= i);
+        const int b = max(__popcll(below), 1) - 1;
+        return {b, __builtin_amdgcn_readlane(q, b), __builtin_amdgcn_readlane(next, b),
+                __builtin_amdgcn_readlane(length, b)};
+    }
+    const int b = find_seq(s.B, i, [&](int at) { return (int64_t)first(q_at(s, at), at); });
+    return {b, q_at(s, b), q_at(s, b + 1), s.lengths[b]};
+}
+
 }  // namespace bl

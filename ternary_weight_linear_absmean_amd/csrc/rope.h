@@ -185,10 +185,9 @@ __device__ __forceinline__ void turn_queries(const E *q, E *out, int QH, int per
     const int64_t row = unit / chunks;
     const int first = (int)(unit - row * chunks) * per, h1 = min(first + per, QH);
     if (row >= seqs.n_tok) return;                                // uniform
-    const int b = find_seq(seqs.B, row, [&](int i) { return (int64_t)q_at(seqs, i); });
-    const int q0 = q_at(seqs, b), q1 = q_at(seqs, b + 1);
-    if (row < q0 || row >= q1) return;
-    int64_t pos = (int64_t)seqs.lengths[b] - (q1 - row);
+    const SeqPlace in = find_place(seqs, row, [](int q, int) { return (int64_t)q; });
+    if (row < in.q0 || row >= in.q1) return;
+    int64_t pos = (int64_t)in.length - (in.q1 - row);
     if (pos >= room) pos = -1;
     const int per_shift = d_shift - 3, step = 64 >> per_shift;    // lanes of a head, heads at once
     const int d = 8 * (lane & ((1 << per_shift) - 1));
