@@ -468,6 +468,7 @@ struct ManyLds {
     // fp32 rows, by token: z + 8 s, and the steps
     alignas(16) float k_mid[2][kTile], v_mid[2][kTile];
     alignas(16) uint16_t k_step[2][kTile], v_step[2][kTile];
+    alignas(16) uint32_t held[2][kWaves];   // whether a granule holds tokens
     alignas(16) uint32_t pairs[kWaves][16];             // bf16 rows: of a wave's 16 tokens of V, s and z by pair of codes8
 };
 // Eight tokens' z + 8 s and s out of LDS.
@@ -585,20 +586,18 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
     const int pk = gt >> 2, tv = 16 * wave + (lane & 15);   // the tokens whose z and s this thread brings
     uint32_t kr[NW], vr[NW], zk_raw, zv_raw;
     int k_entry, v_entry;
-    bool k_ok, v_ok, in_use = false, in_use_next = false;   // whether granule lane % 4 of the tile holds tokens
-    int g_entry;
+    bool k_ok, v_held, v_seen;              // whether the key's block, granule `wave`'s hold tokens; token tv is seen
     auto load_ids = [&](uint32_t tile) {
         k_entry = entry_at(tile + pk);
         v_entry = entry_at(tile + 16 * wave);
-        g_entry = entry_at(tile + 16 * (gt & 3));
     };
     // what lies behind k1 is read from block 0
     auto load_tile = [&](uint32_t tile) {
         const int in = (int)tile & (c.T - 1);
         const int kid = block_of(tile + pk, k_entry), vid = block_of(tile + 16 * wave, v_entry);
         k_ok = kid >= 0;
-        v_ok = vid >= 0 && tile + tv < k1;
-        in_use_next = block_of(tile + 16 * (gt & 3), g_entry) >= 0;
+        v_held = vid >= 0;
+        v_seen = tile + tv < k1;
         const int64_t kt = (((int64_t)max(kid, 0) * c.KVH + h) << c.t_shift) + ((in + pk) & (c.T - 1));
         const int64_t vt = (((int64_t)max(vid, 0) * c.KVH + h) << c.t_shift) + ((in + 16 * wave) & (c.T - 1));
         const uint8_t *kp = c.K + kt * (D / 2) + D / 8 * (gt & 3), *vp = c.V + vt * (D / 2) + D / 8 * lane;
@@ -627,7 +626,8 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
     const int k_put = k_at(pk, NW * (gt & 3)), v_put = v_at(VD * lane, 2 * wave);
     auto to_lds = [&](int buf) {
         const int ka = k_put + buf * kBuf, va = v_put + buf * kBuf;
-        const uint32_t zk = k_ok ? sound<BF16>(zk_raw) : 0u, zv = v_ok ? sound<BF16>(zv_raw) : 0u;
+        const uint32_t zk = k_ok ? sound<BF16>(zk_raw) : 0u, zv = v_held && v_seen ? sound<BF16>(zv_raw) : 0u;
+        if (lane == 0) lds.held[buf][wave] = v_held;
         if (BF16) {
             uint32_t sp[8], zp[8];
             // token t of 8 is half t / 4 of pair t % 4
@@ -686,7 +686,6 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
         load_tile(k0);
         load_ids(k0 + kTile);
         to_lds(0);
-        in_use = in_use_next;
         load_tile(k0 + kTile);
         load_ids(k0 + 2 * kTile);
         __syncthreads();
@@ -716,12 +715,12 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
         }
         to_lds(buf ^ 1);
         __builtin_amdgcn_s_setprio(0);
-        const uint64_t used = __ballot(in_use);             // bit g: granule g holds tokens
-        in_use = in_use_next;
         load_tile(tile + 2 * kTile);
         load_ids(tile + 3 * kTile);
         if (here) {
-            const bool whole = __builtin_amdgcn_readfirstlane((used & 15) == 15 && tile + kTile <= sees_lo);
+            const uint4 held = *reinterpret_cast<const uint4 *>(lds.held[buf]);
+            const bool whole = __builtin_amdgcn_readfirstlane((held.x & held.y & held.z & held.w) != 0 &&
+                                                              tile + kTile <= sees_lo);
             // of the tile's keys this lane's, 16 g + 8 half + e, are seen below lim = 16 g + e
             const int lim = (tile < sees ? (int)min(sees - tile, (uint32_t)kTile) : 0) - 8 * half;
             float u_new = 1.0f;
@@ -752,7 +751,7 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
             if (!whole) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int lim_g = used >> g & 1 ? lim : 0;
+                    const int lim_g = (g == 0 ? held.x : g == 1 ? held.y : g == 2 ? held.z : held.w) ? lim : 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         s[g >> 1][8 * (g & 1) + e] = 16 * g + e < lim_g ? s[g >> 1][8 * (g & 1) + e] : -INFINITY;
@@ -764,9 +763,9 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, s[t][e]);
             float cs = c_row;                              // positive: q has the scale's sign
-            top = half_max(top * cs);
+            top *= cs;
             if (__builtin_expect(__ballot(top > ref.above || u_new != ref.u) != 0, 0)) {
-                const float fix = ref.follow(top, u_new);
+                const float fix = ref.follow(half_max(top), u_new);
                 l *= fix;
                 o_z *= fix;
 #pragma unroll
