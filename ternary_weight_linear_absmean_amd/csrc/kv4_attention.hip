@@ -419,15 +419,15 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
     }
 }
 
-// Many rows: one workgroup per (128 rows, key head, part of the keys), 32 rows
-// a wave, 64 keys at a time, the tile's codes turned into fp16 once, in LDS, for
-// all rows.  While tile t is used, t + 1 is turned into the other buffer and
-// the codes of t + 2 are on their way.
+// Many bf16 rows: one workgroup per (128 rows, key head, part of the keys), 32 rows
+// a wave, 64 keys at a time, the tile turned into fp16 once, in LDS, for all rows.  While
+// tile t is used, t + 1 is turned into the other buffer and the codes of t + 2
+// are on their way.  What goes to LDS are the keys and values themselves, fp16(z
+// + s u), an error of 2^-12 beside the result's 2^-9: no z or s is left in the loop over scores.
+// (fp32 rows would need the codes and each token's z and s: that took 283 us for 2048
+// rows on 4096 keys, 5 heads of 4 and D = 128, where the kernel above takes 198.)
 //
-// bf16 rows: what goes to LDS are the keys and values themselves, fp16(z + s u), an
-// error of 2^-12 beside the result's 2^-9: no z or s is left in the loop over
-// scores.  fp32 rows: the codes less 8, exact, and the tokens' z and s beside them.
-// z and s that are not finite (never written by the append) count as 0 there, and
+// z and s that are not finite (never written by the append) count as 0 here, and
 // a step with which a code of 15 would pass fp16 as the largest that does not:
 // a token that rows do not see is in their products, times 0.
 //
@@ -441,14 +441,13 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 // one piece of 16 lines touch every bank once.
 constexpr float kMostF16 = 65504.0f;
 
-// A token's z and s as the tile takes them; CAP: for values in fp16.
-template <bool CAP>
+// A token's z and s as the tile takes them.
 __device__ __forceinline__ uint32_t sound(uint32_t zs) {
     const float z = (float)zs_z(zs), s = (float)zs_s(zs);
     const bool fine = fabsf(z) <= kMostF16 && s >= 0.0f && s <= kMostF16;
     // less a half step of an 11-bit mantissa and its rounding: 15 s + z <= 65504
     const float most = (kMostF16 - z) * (0.99951172f / 15.0f);
-    const half2 h = {(_Float16)z, (_Float16)(CAP ? fminf(s, most) : s)};
+    const half2 h = {(_Float16)z, (_Float16)fminf(s, most)};
     return fine ? __builtin_bit_cast(uint32_t, h) : 0u;
 }
 // Eight codes as the values z + s u, pairs as codes8; s and z by pair.
@@ -465,39 +464,11 @@ __device__ __forceinline__ half8 values8(uint32_t w, const uint32_t *s, const ui
 template <int D>
 struct ManyLds {
     uint4 k[2 * kTile * D / 8], v[2 * kTile * D / 8];
-    // fp32 rows, by token: z + 8 s, and the steps
-    alignas(16) float k_mid[2][kTile], v_mid[2][kTile];
-    alignas(16) uint16_t k_step[2][kTile], v_step[2][kTile];
     alignas(16) uint32_t held[2][kWaves];   // whether a granule holds tokens
-    alignas(16) uint32_t pairs[kWaves][16];             // bf16 rows: of a wave's 16 tokens of V, s and z by pair of codes8
+    alignas(16) uint32_t pairs[kWaves][16]; // of a wave's 16 tokens of V, s and z by pair of codes8
 };
-// Eight tokens' z + 8 s and s out of LDS.
-struct Steps8 {
-    float mid[8];
-    uint32_t step[4];
-    __device__ __forceinline__ Steps8() {}
-    __device__ __forceinline__ Steps8(const float *mids, const uint16_t *steps, int at) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 w = *reinterpret_cast<const float4 *>(mids + at + 4 * i);
-            mid[4 * i] = w.x; mid[4 * i + 1] = w.y; mid[4 * i + 2] = w.z; mid[4 * i + 3] = w.w;
-        }
-        const uint4 w = *reinterpret_cast<const uint4 *>(steps + at);
-        step[0] = w.x; step[1] = w.y; step[2] = w.z; step[3] = w.w;
-    }
-    __device__ __forceinline__ float s(int i) const {
-        return (float)__builtin_bit_cast(half2, step[i >> 1])[i & 1];
-    }
-};
-// The larger of each half.
-__device__ __forceinline__ uint32_t max_u16(uint32_t a, uint32_t b) {
-    typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2v, a),
-                                                                  __builtin_bit_cast(ushort2v, b)));
-}
-template <bool BF16, int D>
+template <int D>
 __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, ManyLds<D> &lds) {
-    constexpr int NS = BF16 ? 1 : 2;
     constexpr int NQ = D / 16;              // steps of K Q^T
     constexpr int NO = D / 32;              // tiles of the output
     constexpr int NW = D / 32;              // dwords of K's and of V's codes per thread
@@ -541,9 +512,8 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
     const uint32_t sees_lo = keys_within(start + min(rw, all_rows - 1) / G + 1, k1);
     const uint32_t sees_hi = keys_within(start + min(rw + 31, all_rows - 1) / G + 1, k1);
 
-    const float minus = minus_one();
-    half8 qh[NS][NQ];
-    float c_row, q_sum = 0.0f;
+    half8 qh[NQ];
+    float c_row;
     {
         float4 v[NQ][2];
         float top = 0.0f;
@@ -551,27 +521,19 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
         for (int s = 0; s < NQ; ++s)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float4 x = load4<BF16>(a.q, row * D + 16 * s + 8 * half + 4 * e);
+                const float4 x = load4<true>(a.q, row * D + 16 * s + 8 * half + 4 * e);
                 v[s][e] = x;
-                q_sum += (x.x + x.y) + (x.z + x.w);
                 top = fmaxf(top, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
             }
         top = half_max(top);
         const float f = a.scale2 < 0.0f ? -to_f16_range(top) : to_f16_range(top);
-        q_sum = (q_sum + __shfl_xor(q_sum, 32)) * f;
         c_row = fmaxf(a.scale2 / f, kTiny);
 #pragma unroll
         for (int s = 0; s < NQ; ++s) {
             const float x[8] = {v[s][0].x * f, v[s][0].y * f, v[s][0].z * f, v[s][0].w * f,
                                 v[s][1].x * f, v[s][1].y * f, v[s][1].z * f, v[s][1].w * f};
-            uint32_t w[4], z[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[e] = f16_pair(x[e], x[e + 4]);
-                if (NS == 2) z[e] = rest_of(x[e], x[e + 4], w[e], minus);
-            }
-            qh[0][s] = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
-            if (NS == 2) qh[NS - 1][s] = __builtin_bit_cast(half8, make_uint4(z[0], z[1], z[2], z[3]));
+            qh[s] = __builtin_bit_cast(half8, make_uint4(f16_pair(x[0], x[4]), f16_pair(x[1], x[5]),
+                                                         f16_pair(x[2], x[6]), f16_pair(x[3], x[7])));
         }
     }
 
@@ -626,53 +588,36 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
     const int k_put = k_at(pk, NW * (gt & 3)), v_put = v_at(VD * lane, 2 * wave);
     auto to_lds = [&](int buf) {
         const int ka = k_put + buf * kBuf, va = v_put + buf * kBuf;
-        const uint32_t zk = k_ok ? sound<BF16>(zk_raw) : 0u, zv = v_held && v_seen ? sound<BF16>(zv_raw) : 0u;
+        const uint32_t zk = k_ok ? sound(zk_raw) : 0u, zv = v_held && v_seen ? sound(zv_raw) : 0u;
         if (lane == 0) lds.held[buf][wave] = v_held;
-        if (BF16) {
-            uint32_t sp[8], zp[8];
-            // token t of 8 is half t / 4 of pair t % 4
-            uint16_t *put = reinterpret_cast<uint16_t *>(lds.pairs[wave]) +
-                            2 * (4 * ((lane >> 3) & 1) + (lane & 3)) + ((lane >> 2) & 1);
-            if (lane < 16) {
-                put[0] = (uint16_t)(zv >> 16);
-                put[16] = (uint16_t)zv;
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // one wave's LDS accesses are in order
-            const uint4 *get = reinterpret_cast<const uint4 *>(lds.pairs[wave]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 w = get[i];
-                uint32_t *to = i < 2 ? sp + 4 * i : zp + 4 * (i - 2);
-                to[0] = w.x; to[1] = w.y; to[2] = w.z; to[3] = w.w;
-            }
-            const uint32_t ks = perm(zk, zk, 0x03020302u), kz = perm(zk, zk, 0x01000100u);
-            const uint32_t ks4[4] = {ks, ks, ks, ks}, kz4[4] = {kz, kz, kz, kz};
-#pragma unroll
-            for (int j = 0; j < NW; ++j)
-                *reinterpret_cast<half8 *>(lds_k + (ka ^ 16 * j)) = values8(kr[j], ks4, kz4);
-#pragma unroll
-            for (int j = 0; j < NW; ++j)
-                *reinterpret_cast<half8 *>(lds_v + (va ^ 16 * (j & 1)) + (j >> 1) * 128) =
-                    values8(vr[j], sp + 4 * (j & 1), zp + 4 * (j & 1));
-        } else {
-#pragma unroll
-            for (int j = 0; j < NW; ++j) *reinterpret_cast<half8 *>(lds_k + (ka ^ 16 * j)) = codes8<8>(kr[j]);
-#pragma unroll
-            for (int j = 0; j < NW; ++j)
-                *reinterpret_cast<half8 *>(lds_v + (va ^ 16 * (j & 1)) + (j >> 1) * 128) = codes8<8>(vr[j]);
-            if ((gt & 3) == 0) {
-                lds.k_mid[buf][pk] = middle(zk);
-                lds.k_step[buf][pk] = (uint16_t)(zk >> 16);
-            }
-            if (lane < 16) {
-                lds.v_mid[buf][tv] = middle(zv);
-                lds.v_step[buf][tv] = (uint16_t)(zv >> 16);
-            }
+        uint32_t sp[8], zp[8];
+        // token t of 8 is half t / 4 of pair t % 4
+        uint16_t *put = reinterpret_cast<uint16_t *>(lds.pairs[wave]) +
+                        2 * (4 * ((lane >> 3) & 1) + (lane & 3)) + ((lane >> 2) & 1);
+        if (lane < 16) {
+            put[0] = (uint16_t)(zv >> 16);
+            put[16] = (uint16_t)zv;
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");           // one wave's LDS accesses are in order
+        const uint4 *get = reinterpret_cast<const uint4 *>(lds.pairs[wave]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 w = get[i];
+            uint32_t *to = i < 2 ? sp + 4 * i : zp + 4 * (i - 2);
+            to[0] = w.x; to[1] = w.y; to[2] = w.z; to[3] = w.w;
+        }
+        const uint32_t ks = perm(zk, zk, 0x03020302u), kz = perm(zk, zk, 0x01000100u);
+        const uint32_t ks4[4] = {ks, ks, ks, ks}, kz4[4] = {kz, kz, kz, kz};
+#pragma unroll
+        for (int j = 0; j < NW; ++j) *reinterpret_cast<half8 *>(lds_k + (ka ^ 16 * j)) = values8(kr[j], ks4, kz4);
+#pragma unroll
+        for (int j = 0; j < NW; ++j)
+            *reinterpret_cast<half8 *>(lds_v + (va ^ 16 * (j & 1)) + (j >> 1) * 128) =
+                values8(vr[j], sp + 4 * (j & 1), zp + 4 * (j & 1));
     };
 
     Reference ref;
-    float l = 0.0f, o_z = 0.0f;
+    float l = 0.0f;
     float16v o[NO];
 #pragma unroll
     for (int i = 0; i < NO; ++i)
@@ -696,7 +641,6 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
         // opaque, or the loop would hold an address for each piece
         int ka = k_get + buf * kBuf, va = v_get + buf * kBuf;
         asm("" : "+v"(ka), "+v"(va));
-        __builtin_amdgcn_s_setprio(1);            // the CU's other workgroup fills what this leaves
         // also where the wave's rows do not see the tile: one block to schedule
         float16v s[2];
 #pragma unroll
@@ -708,13 +652,10 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const half8 k = *reinterpret_cast<const half8 *>(lds_k + (ka ^ 32 * st) + t * 64 * D);
-#pragma unroll
-                for (int x = 0; x < NS; ++x) s[t] = mfma_32x32x16(k, qh[x][st], s[t]);
+                s[t] = mfma_32x32x16(k, qh[st], s[t]);
             }
-            if (!BF16 && (st & 1)) __builtin_amdgcn_sched_barrier(0);
         }
         to_lds(buf ^ 1);
-        __builtin_amdgcn_s_setprio(0);
         load_tile(tile + 2 * kTile);
         load_ids(tile + 3 * kTile);
         if (here) {
@@ -723,31 +664,6 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
                                                               tile + kTile <= sees_lo);
             // of the tile's keys this lane's, 16 g + 8 half + e, are seen below lim = 16 g + e
             const int lim = (tile < sees ? (int)min(sees - tile, (uint32_t)kTile) : 0) - 8 * half;
-            float u_new = 1.0f;
-            if (!BF16) {
-                uint32_t top2 = 0;                          // of two steps each; they are not negative
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    __builtin_amdgcn_sched_barrier(0);     // a granule's registers at a time, here and below
-                    const Steps8 zk(lds.k_mid[buf], lds.k_step[buf], 16 * g + 8 * half);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        s[g >> 1][8 * (g & 1) + e] =
-                            __builtin_fmaf(s[g >> 1][8 * (g & 1) + e], zk.s(e), q_sum * zk.mid[e]);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(&lds.v_step[buf][16 * g + 8 * half]);
-                    uint32_t ys[4] = {y.x, y.y, y.z, y.w};
-                    if (!whole) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int at = 16 * g + 2 * i;
-                            ys[i] &= at + 1 < lim ? 0xFFFFFFFFu : at < lim ? 0xFFFFu : 0u;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top2 = max_u16(top2, ys[i]);
-                }
-                u_new = fmaxf(ref.u, step_above(half_max((float)zs_s(max_u16(top2, top2 << 16)))));
-            }
             if (!whole) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -764,10 +680,9 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, s[t][e]);
             float cs = c_row;                              // positive: q has the scale's sign
             top *= cs;
-            if (__builtin_expect(__ballot(top > ref.above || u_new != ref.u) != 0, 0)) {
-                const float fix = ref.follow(half_max(top), u_new);
+            if (__builtin_expect(__ballot(top > ref.above) != 0, 0)) {
+                const float fix = ref.follow(half_max(top), 1.0f);
                 l *= fix;
-                o_z *= fix;
 #pragma unroll
                 for (int i = 0; i < NO; ++i) o[i] *= fix;
             }
@@ -783,34 +698,20 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {                  // 16 keys
-                if (!BF16) __builtin_amdgcn_sched_barrier(0);
-                uint32_t hi[4], lo[4];
-                float y[8];
-                const Steps8 zv = BF16 ? Steps8() : Steps8(lds.v_mid[buf], lds.v_step[buf], 16 * g + 8 * half);
+                uint32_t w[4];
+                float p[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float p = exp2_fast(__builtin_fmaf(s[g >> 1][8 * (g & 1) + e], cs, -base));
-                    l += p;
-                    y[e] = p;
-                    if (!BF16) {
-                        o_z = __builtin_fmaf(p, zv.mid[e], o_z);
-                        y[e] = __builtin_fmaf(p, zv.s(e), 0.0f);
-                        asm("" : "+v"(y[e]));              // formed once, for both halves
-                    }
+                    p[e] = exp2_fast(__builtin_fmaf(s[g >> 1][8 * (g & 1) + e], cs, -base));
+                    l += p[e];
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    hi[e] = f16_pair(y[e], y[e + 4]);
-                    if (!BF16) lo[e] = rest_of(y[e], y[e + 4], hi[e], minus);
-                }
-                const half8 p_hi = __builtin_bit_cast(half8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                half8 p_lo;
-                if (!BF16) p_lo = __builtin_bit_cast(half8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                for (int e = 0; e < 4; ++e) w[e] = f16_pair(p[e], p[e + 4]);
+                const half8 ph = __builtin_bit_cast(half8, make_uint4(w[0], w[1], w[2], w[3]));
 #pragma unroll
                 for (int i = 0; i < NO; ++i) {
                     const half8 v = *reinterpret_cast<const half8 *>(lds_v + (va ^ 32 * g) + i * 32 * 128);
-                    o[i] = mfma_32x32x16(v, p_hi, o[i]);
-                    if (NS == 2) o[i] = mfma_32x32x16(v, p_lo, o[i]);
+                    o[i] = mfma_32x32x16(v, ph, o[i]);
                 }
             }
         }
@@ -819,7 +720,6 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
 
     if (rw + low >= all_rows) return;
     l = l + __shfl_xor(l, 32);
-    o_z = o_z + __shfl_xor(o_z, 32);
     // from 2^(r1 + r2) to 2^r1
     float f0 = exp2_fast(ref.r2);
     l *= f0;
@@ -836,9 +736,9 @@ __device__ __forceinline__ void many_rows(const Args &a, int64_t at, int split, 
         for (int e = 0; e < 16; e += 4) {
             float y[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) y[x] = (o[i][e + x] + o_z) * f0;
+            for (int x = 0; x < 4; ++x) y[x] = o[i][e + x] * f0;
             const int d = 32 * i + 2 * e + 4 * half;
-            if (direct) store4<BF16>(a.out, row * D + d, make_float4(y[0], y[1], y[2], y[3]));
+            if (direct) store4<true>(a.out, row * D + d, make_float4(y[0], y[1], y[2], y[3]));
             else store4<false>(dst, d, make_float4(y[0], y[1], y[2], y[3]));
         }
     if (!direct && half == 0) {
@@ -854,15 +754,15 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_few_kernel(Args a) {
     few_rows<BF16, D>(a, blockIdx.x, lds);
 }
 
-template <bool BF16, int D>
+template <int D>
 __global__ __launch_bounds__(kThreads, 2) void kv4_many_kernel(Args a) {
     __shared__ ManyLds<D> lds;
-    many_rows<BF16, D>(a, blockIdx.x, blockIdx.z, lds);
+    many_rows<D>(a, blockIdx.x, blockIdx.z, lds);
 }
 // Both in one launch: many rows wait for instructions, few rows for memory, so
 // are to share the CUs.  The workgroups for few rows stand behind the first kCUs
 // of the others.
-template <bool BF16, int D>
+template <int D>
 __global__ __launch_bounds__(kThreads, 2) void kv4_mixed_kernel(Args a) {
     __shared__ union {
         FewLds<D> few;
@@ -871,31 +771,52 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_mixed_kernel(Args a) {
     const int64_t all = a.many_groups * a.S, first = min(all, (int64_t)kCUs);
     const int64_t few = gridDim.x - all, i = blockIdx.x;
     if (i >= first && i < first + few) {
-        few_rows<BF16, D>(a, (uint32_t)(i - first), lds.few);
+        few_rows<true, D>(a, (uint32_t)(i - first), lds.few);
     } else {
         const int64_t at = i < first ? i : i - few;
         const int split = (int)(at / a.many_groups);
-        many_rows<BF16, D>(a, at - split * a.many_groups, split, lds.many);
+        many_rows<D>(a, at - split * a.many_groups, split, lds.many);
     }
 }
 
+// By type.  bf16 rows, few and many, 5 heads of 4 and D = 128, in us:
+//   work  7680  4 x 256 on 1000      35.0  37.8
+//        11520  512 on 4000          50.8  51.0
+//        17280  8 x 96 on 4000       69.2  88.3
+//        20320  128 on 32000         84.4   102
+//        21760  4 x 128 on 8000      96.5  84.3
+//        30720  64 x 96 on 500        112  70.3
+//        46080  2048 on 4096          138   124
+// (8 heads of 2, D = 64: 30720 58 and 42, 46080 84 and 80, but 64 x 64 on 4000 178
+// and 209.)  A workgroup of many rows for half the CUs only: 1000 rows on 1777
+// keys 57.8 us, for two a CU 46.7.  One sequence of more than 32 units for 256
+// pieces: 128 rows on 32000 keys 133 us, for 512 84.
+constexpr Rules kRules[2] = {{1e30, kCUs, 32}, {21000, 2 * kCUs, 32}};
+
 template <bool BF16, int D>
 Kernels<Kv4Cache> kernels() {
-    return {kv4_few_kernel<BF16, D>, kv4_many_kernel<BF16, D>, kv4_mixed_kernel<BF16, D>};
+    if constexpr (BF16) return {kv4_few_kernel<BF16, D>, kv4_many_kernel<D>, kv4_mixed_kernel<D>};
+    else return {kv4_few_kernel<BF16, D>, nullptr, nullptr};
 }
 
 }  // namespace
 
 size_t kv4_attention_ws_floats(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
                                int64_t KVH, int64_t T, int64_t D) {
-    const Plan p = plan_for(n_tok, QH, B, max_blocks, KVH, T, D);
-    return (size_t)(p.part + p.cut);
+    size_t most = 0;                        // of the two types
+    for (const Rules &r : kRules) {
+        const Plan p = plan_for(n_tok, QH, B, max_blocks, KVH, T, D, r);
+        const size_t need = (size_t)(p.part + p.cut);
+        most = need > most ? need : most;
+    }
+    return most;
 }
 
 hipError_t launch_kv4_attention(const void *q, int dtype, int QH, const Kv8Seqs &seqs,
                                 const bl_kv4 &cache, float scale, void *out, float *ws,
                                 hipStream_t s) {
-    const Plan p = plan_for(seqs.n_tok, QH, seqs.B, seqs.max_blocks, cache.KVH, cache.T, cache.D);
+    const Plan p = plan_for(seqs.n_tok, QH, seqs.B, seqs.max_blocks, cache.KVH, cache.T, cache.D,
+                            kRules[dtype]);
     const Args a = kv_args(p, q, QH, seqs, kv4_device(cache), scale, out, ws);
     if (cache.D == 64)
         return dtype ? attend<true, 64>(a, p, kernels<true, 64>(), s) : attend<false, 64>(a, p, kernels<false, 64>(), s);

@@ -688,6 +688,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_mixed_kernel(Args a) {
     }
 }
 
+constexpr Rules kRules = {kManyWork, kCUs, INT32_MAX};
+
 template <bool BF16, int D>
 Kernels<Kv8Cache> kernels() {
     return {kv8_few_kernel<BF16, D>, kv8_many_kernel<BF16, D>, kv8_mixed_kernel<BF16, D>};
@@ -697,14 +699,15 @@ Kernels<Kv8Cache> kernels() {
 
 size_t kv8_attention_ws_floats(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
                                int64_t KVH, int64_t T, int64_t D) {
-    const Plan p = plan_for(n_tok, QH, B, max_blocks, KVH, T, D);
+    const Plan p = plan_for(n_tok, QH, B, max_blocks, KVH, T, D, kRules);
     return (size_t)(p.part + p.cut);
 }
 
 hipError_t launch_kv8_attention(const void *q, int dtype, int QH, const Kv8Seqs &seqs,
                                 const bl_kv8 &cache, float scale, void *out, float *ws,
                                 hipStream_t s) {
-    const Plan p = plan_for(seqs.n_tok, QH, seqs.B, seqs.max_blocks, cache.KVH, cache.T, cache.D);
+    const Plan p = plan_for(seqs.n_tok, QH, seqs.B, seqs.max_blocks, cache.KVH, cache.T, cache.D,
+                            kRules);
     const Args a = kv_args(p, q, QH, seqs, kv8_device(cache), scale, out, ws);
     if (cache.D == 64)
         return dtype ? attend<true, 64>(a, p, kernels<true, 64>(), s) : attend<false, 64>(a, p, kernels<false, 64>(), s);

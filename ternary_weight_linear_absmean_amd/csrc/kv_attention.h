@@ -573,28 +573,35 @@ struct Plan {
     int most, slots, step_shift;
     int64_t part, cut;        // floats of the workspace
 };
-Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH, int64_t T, int64_t D) {
+// What differs between the caches' formats.
+struct Rules {
+    double many_work;         // above which rows go to the kernel for many
+    int many_groups;          // workgroups of that kernel to aim at with parts of the keys
+    int one_seq_units;        // units of a single sequence above which pieces are for kGroups workgroups
+};
+Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH, int64_t T, int64_t D,
+              const Rules &rules) {
     const int64_t G = QH / KVH, keys = max_blocks * T, unit = kTile * kWaves;
     const int64_t steps = keys > 0 ? (keys + unit - 1) / unit : 1;
     const int64_t seqs = n_tok < B ? n_tok : B;
     Plan p = {};
     p.steps = steps;
     p.S = 1;
-    p.many = n_tok * G > kFewRows * B && (double)n_tok * QH / kRows * (steps + 2) > kManyWork;
+    p.many = n_tok * G > kFewRows * B && (double)n_tok * QH / kRows * (steps + 2) > rules.many_work;
     p.few = !p.many || B > 1;
     if (p.many) {
         const double tiles = n_tok * (double)G / kManyRows;
-        int64_t parts = (int64_t)(kCUs / (KVH * (tiles > seqs ? tiles : seqs)));
+        int64_t parts = (int64_t)(rules.many_groups / (KVH * (tiles > seqs ? tiles : seqs)));
         parts = parts < 1 ? 1 : parts < steps ? parts : steps;
         if (steps - (steps + parts - 1) / parts >= 3) p.S = (int)parts;
         if (p.S > 1) p.part = (p.S * n_tok * QH * (D + 2) + 3) / 4 * 4;
     }
     if (p.few) {
-        // one sequence: 32768 keys of 5 heads 19.6 us with 512, 16.5 with 256
-        p.most = seqs == 1 ? kCUs : kGroups;
         int64_t tiles = n_tok * G / kRows + seqs;
         if (p.many && tiles > seqs * kFewTiles) tiles = seqs * kFewTiles;
         const int64_t units = tiles * KVH;
+        // one sequence: 32768 keys of 5 heads 19.6 us with 512, 16.5 with 256
+        p.most = seqs == 1 && units <= rules.one_seq_units ? kCUs : kGroups;
         // longer steps where their number would pass 32 bits (units of kLineSeqs
         // sequences do not: n_tok QH / 16 + 256 KVH < 2^28)
         p.step_shift = kStepShift;

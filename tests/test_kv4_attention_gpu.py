@@ -340,7 +340,7 @@ def test_graph_follows_its_arrays(gpu):
     start = copied(s)
     eager = copied(s)
     out, q = torch.zeros_like(s["q"]), torch.zeros_like(s["q"])
-    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
 
     def step(x, **kw):
         return attend(bl, dict(x, q=append(bl, x, q_out=kw.pop("q_out", None))), **kw)
@@ -369,7 +369,7 @@ def test_graphs_cut_by_new_lengths(gpu):
     lengths change at random."""
     one = cuda(make(18, [1] * 5, [9000, 1, 700, 2500, 64], 64, 128, 2, BF16, 4, width=400))
     two = cuda(make(19, [1, 200, 3], [5000, 1500, 2300], 32, 64, 3, F32, 4, width=2000))
-    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
     graphs, full = [], [s["lengths"].clone() for s in (one, two)]
     for s in (one, two):
         out = torch.zeros_like(s["q"])
