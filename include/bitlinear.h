@@ -621,12 +621,14 @@ bl_status bitlinear_kv4_append(const void *k, const void *v, const void *q, void
 /* bitlinear_kv4_attention -- bitlinear_kv8_attention over the 4-bit cache; all
  * arguments as there.  Steps are >= 0 and finite, as the append writes them, and so
  * are the least values finite.
- * The scores, the softmax and all sums are fp32 and no code is rounded; for fp32
- * rows q and the softmax weights times their step are kept to 22 bits or more, for
- * bf16 rows the latter are rounded to 11 bits.  An operand's smallest step is 2^-38
- * of the row's largest |q|, and 2^-38 of the largest weight times a power of two
- * above the largest step of the values.  Errors scale with sums over |z| + s code
- * in the place of |value|.
+ * The scores, the softmax and all sums are fp32.  For fp32 rows no code is rounded,
+ * and q and the softmax weights times their step are kept to 22 bits or more; for
+ * bf16 rows q is exact and the latter are rounded to 11 bits, and where a call
+ * brings many rows the keys and values are rounded to fp16 (11 bits, 2^-24 at
+ * least).  An operand's smallest step is 2^-38 of the row's largest |q|, and
+ * 2^-38 of the largest weight times a power of two above the largest step of the
+ * values (2^-34 for bf16 rows).  Errors scale with sums over |z| + s code in the
+ * place of |value|.  |scale| max |q| is to stay below 2^115.
  */
 bl_status bitlinear_kv4_attention(const void *q, bl_dtype dtype, int64_t n_tok, int64_t QH,
                                   const int32_t *q_start, const int32_t *lengths,
@@ -667,9 +669,7 @@ bl_status bitlinear_kv4_read(const bl_kv4 *cache, const int32_t *q_start, const 
  *   length, table DEVICE int32 [1] and [max_blocks], as for the append.
  *   scale         as for the attention.
  * No position enters a score: q and k go from their BitLinears to the cache and
- * the attention as they are, and nothing can rotate them in between.  A model
- * with rotary embeddings is run by the single calls (bitlinear_gemv_fused, its
- * own rotation, append, attention).
+ * the attention as they are (bitlinear_decode_stack_kv_rope rotates them).
  *   ws            >= bitlinear_decode_stack_kv_ws_bytes(dims, T, max_blocks)
  *                 bytes, 16-byte aligned.
  */
@@ -682,6 +682,31 @@ bl_status bitlinear_decode_stack_kv(const bl_layer *layers, const bl_kv8 *caches
 /* Workspace bytes of bitlinear_decode_stack_kv; 0 also for sizes it refuses. */
 size_t bitlinear_decode_stack_kv_ws_bytes(const bl_stack_dims *dims, int64_t T,
                                           int64_t max_blocks);
+
+/* bitlinear_decode_stack_kv_rope -- bitlinear_decode_stack_kv with q and k rotated
+ * by the token's position (bitlinear_kv8_append_rope): a stack with rotary
+ * embeddings.  rope as there, the same in all layers; the trace holds q and k as
+ * their BitLinears give them.  Workspace as bitlinear_decode_stack_kv.
+ * bitlinear_decode_stack_kv4 -- the same over 4-bit caches (bitlinear_kv4_append,
+ * bitlinear_kv4_attention); rope NULL: no rotation.
+ *   ws            >= bitlinear_decode_stack_kv4_ws_bytes(dims, T, max_blocks)
+ *                 bytes, 16-byte aligned.
+ */
+bl_status bitlinear_decode_stack_kv_rope(const bl_layer *layers, const bl_kv8 *caches,
+                                         int n_layers, const bl_stack_dims *dims,
+                                         const int32_t *q_start, const int32_t *length,
+                                         const int32_t *table, int64_t max_blocks,
+                                         const bl_rope *rope, float scale, float *x, float *trace,
+                                         void *ws, size_t ws_bytes, void *stream);
+bl_status bitlinear_decode_stack_kv4(const bl_layer *layers, const bl_kv4 *caches, int n_layers,
+                                     const bl_stack_dims *dims, const int32_t *q_start,
+                                     const int32_t *length, const int32_t *table,
+                                     int64_t max_blocks, const bl_rope *rope, float scale, float *x,
+                                     float *trace, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of bitlinear_decode_stack_kv4; 0 also for sizes it refuses. */
+size_t bitlinear_decode_stack_kv4_ws_bytes(const bl_stack_dims *dims, int64_t T,
+                                           int64_t max_blocks);
 
 /* ------------------------------------------------------------------------
  * 4-bit weights with group scales -- for the layers that stay out of the

@@ -40,6 +40,7 @@ EXPORTS = ["quant_weight_absmean_pack", "quant_weight_absmean_pack_noalloc", "qu
            "bitlinear_kv8_append_rope", "bitlinear_kv8_read", "bitlinear_kv4_append", "bitlinear_kv4_read",
            "bitlinear_kv4_attention", "bitlinear_kv4_attention_ws_bytes",
            "bitlinear_decode_stack_kv", "bitlinear_decode_stack_kv_ws_bytes",
+           "bitlinear_decode_stack_kv_rope", "bitlinear_decode_stack_kv4", "bitlinear_decode_stack_kv4_ws_bytes",
            "quant_weight_absmax_i4", "dequant_weight_i4", "bitlinear_gemv_w4",
            "bl_workspace_bytes", "bl_status_string", "bl_last_error", "bl_abi_version"]
 BL_OP_DECODE_STACK = 2
@@ -197,6 +198,13 @@ def load():
         ctypes.c_float, _p, _p, _p, _sz, _p]
     lib.bitlinear_decode_stack_kv_ws_bytes.restype = _sz
     lib.bitlinear_decode_stack_kv_ws_bytes.argtypes = [ctypes.POINTER(StackDims), _i64, _i64]
+    for name, kind in (("bitlinear_decode_stack_kv_rope", Kv8), ("bitlinear_decode_stack_kv4", Kv4)):
+        f = getattr(lib, name)
+        f.restype = st
+        f.argtypes = [ctypes.POINTER(Layer), ctypes.POINTER(kind), i32, ctypes.POINTER(StackDims), _p, _p, _p, _i64,
+                      ctypes.POINTER(BlRope), ctypes.c_float, _p, _p, _p, _sz, _p]
+    lib.bitlinear_decode_stack_kv4_ws_bytes.restype = _sz
+    lib.bitlinear_decode_stack_kv4_ws_bytes.argtypes = [ctypes.POINTER(StackDims), _i64, _i64]
     lib.quant_weight_absmax_i4.restype = st
     lib.quant_weight_absmax_i4.argtypes = [_p, i32, _i64, _i64, _i64, _p, _p, _p]
     lib.dequant_weight_i4.restype = st
@@ -891,6 +899,44 @@ def bitlinear_kv4_attention(q, q_start, lengths, table, cache, scale=None, out=N
     return out
 
 
+def _stack_cached(call, ws_call, kind, device_cache, layers, caches, x, q_start, lengths, table, H, KV, F, D, rope,
+                  eps, scale, trace, ws, stream):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA (HIP) tensor")
+    dev, n = x.get_device(), len(layers)
+    if len(caches) != n:
+        raise ValueError(f"{n} layers and {len(caches)} caches")
+    xp = _at(x, torch.float32, dev, (H,), "x")
+    arr, kvs = (Layer * max(1, n))(), (kind * max(1, n))()
+    wide = {"Wd": F}
+    rows = {"Wq": H, "Wk": KV, "Wv": KV, "Wo": H, "Wg": F, "Wu": F, "Wd": H}
+    for i, L in enumerate(layers):
+        vals = [_at(L[k], torch.uint8, dev, (rows[k], wide.get(k, H) // 4), k) for k in LAYER_WEIGHTS]
+        vals += [_at(L[k], torch.float32, dev, (1,), k) for k in LAYER_GAMMAS]
+        nw = L.get("ffn_norm")
+        arr[i] = Layer(*vals, None if nw is None else _at(nw, torch.float32, dev, (F,), "ffn_norm"))
+        kvs[i] = device_cache(caches[i], dev)
+    qp, lp, tp, B, nb = _seqs(q_start, lengths, table, dev)
+    if B != 1:
+        raise ValueError(f"one sequence, got {B}")
+    turn = () if call == "bitlinear_decode_stack_kv" else (None if rope is None else _rope(rope, dev),)
+    dims = StackDims(H, KV, F, D, float(eps), BL_STACK_AUTO, 0, 0)
+    lib = load()
+    handle, context = _where(dev, stream)
+    with context:
+        tr = torch.empty((n, 5 * H + 2 * KV), dtype=torch.float32, device=dev) if trace else None
+        if ws is None:
+            need = getattr(lib, ws_call)(ctypes.byref(dims), kvs[0].T if n else 64, nb)
+            ws = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+        st = getattr(lib, call)(
+            arr, kvs, n, ctypes.byref(dims), qp, lp, tp, nb, *turn, D ** -0.5 if scale is None else scale, xp,
+            None if tr is None else tr.data_ptr(), _at(ws, torch.uint8, dev, (ws.numel(),), "ws"),
+            ws.numel(), handle)
+    if st:
+        _check(call, st)
+    return tr
+
+
 def bitlinear_decode_stack_kv(layers, caches, x, q_start, lengths, table, H, KV, F, D, eps=1e-5,
                               scale=None, trace=False, ws=None, stream=None):
     """bitlinear_decode_stack with the attention over 8-bit caches: one token of
@@ -899,39 +945,26 @@ def bitlinear_decode_stack_kv(layers, caches, x, q_start, lengths, table, H, KV,
     q_start int32 [2] = [0, 1], lengths int32 [1] (with the
     new token) and table int32 [1, max_blocks] on the GPU.  x fp32 [H] is
     updated in place; scale defaults to D ** -0.5."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise TypeError("x must be a CUDA (HIP) tensor")
-    dev, n = x.get_device(), len(layers)
-    if len(caches) != n:
-        raise ValueError(f"{n} layers and {len(caches)} caches")
-    xp = _at(x, torch.float32, dev, (H,), "x")
-    arr, kvs = (Layer * max(1, n))(), (Kv8 * max(1, n))()
-    wide = {"Wd": F}
-    rows = {"Wq": H, "Wk": KV, "Wv": KV, "Wo": H, "Wg": F, "Wu": F, "Wd": H}
-    for i, L in enumerate(layers):
-        vals = [_at(L[k], torch.uint8, dev, (rows[k], wide.get(k, H) // 4), k) for k in LAYER_WEIGHTS]
-        vals += [_at(L[k], torch.float32, dev, (1,), k) for k in LAYER_GAMMAS]
-        nw = L.get("ffn_norm")
-        arr[i] = Layer(*vals, None if nw is None else _at(nw, torch.float32, dev, (F,), "ffn_norm"))
-        kvs[i] = _kv8(caches[i], dev)
-    qp, lp, tp, B, nb = _seqs(q_start, lengths, table, dev)
-    if B != 1:
-        raise ValueError(f"one sequence, got {B}")
-    dims = StackDims(H, KV, F, D, float(eps), BL_STACK_AUTO, 0, 0)
-    lib = load()
-    handle, context = _where(dev, stream)
-    with context:
-        tr = torch.empty((n, 5 * H + 2 * KV), dtype=torch.float32, device=dev) if trace else None
-        if ws is None:
-            need = lib.bitlinear_decode_stack_kv_ws_bytes(ctypes.byref(dims), kvs[0].T if n else 64, nb)
-            ws = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-        st = lib.bitlinear_decode_stack_kv(
-            arr, kvs, n, ctypes.byref(dims), qp, lp, tp, nb, D ** -0.5 if scale is None else scale, xp,
-            None if tr is None else tr.data_ptr(), _at(ws, torch.uint8, dev, (ws.numel(),), "ws"),
-            ws.numel(), handle)
-    if st:
-        _check("bitlinear_decode_stack_kv", st)
-    return tr
+    return _stack_cached("bitlinear_decode_stack_kv", "bitlinear_decode_stack_kv_ws_bytes", Kv8, _kv8, layers,
+                         caches, x, q_start, lengths, table, H, KV, F, D, None, eps, scale, trace, ws, stream)
+
+
+def bitlinear_decode_stack_kv_rope(layers, caches, x, q_start, lengths, table, H, KV, F, D, rope, eps=1e-5,
+                                   scale=None, trace=False, ws=None, stream=None):
+    """bitlinear_decode_stack_kv with q and k rotated by the token's position (rope:
+    Rope, the same in all layers); the trace holds them as their BitLinears do."""
+    if rope is None:
+        raise ValueError("bitlinear_decode_stack_kv_rope without rope")
+    return _stack_cached("bitlinear_decode_stack_kv_rope", "bitlinear_decode_stack_kv_ws_bytes", Kv8, _kv8, layers,
+                         caches, x, q_start, lengths, table, H, KV, F, D, rope, eps, scale, trace, ws, stream)
+
+
+def bitlinear_decode_stack_kv4(layers, caches, x, q_start, lengths, table, H, KV, F, D, rope=None, eps=1e-5,
+                               scale=None, trace=False, ws=None, stream=None):
+    """bitlinear_decode_stack_kv over 4-bit caches (Kv4Cache), q and k rotated by the
+    token's position where rope (Rope) is given."""
+    return _stack_cached("bitlinear_decode_stack_kv4", "bitlinear_decode_stack_kv4_ws_bytes", Kv4, _kv4, layers,
+                         caches, x, q_start, lengths, table, H, KV, F, D, rope, eps, scale, trace, ws, stream)
 
 
 def quant_weight_absmax_i4(W, group=128, Wq4=None, s=None, stream=None):

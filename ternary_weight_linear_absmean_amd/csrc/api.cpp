@@ -1080,14 +1080,36 @@ BL_EXPORT size_t bitlinear_decode_stack_kv_ws_bytes(const bl_stack_dims *dims, i
            bitlinear_kv8_attention_ws_bytes(1, dims->H / dims->D, 1, max_blocks,
                                             dims->KV / dims->D, T, dims->D);
 }
+BL_EXPORT size_t bitlinear_decode_stack_kv4_ws_bytes(const bl_stack_dims *dims, int64_t T,
+                                                     int64_t max_blocks) {
+    if (check_stack_kv_dims("bitlinear_decode_stack_kv4_ws_bytes", dims, T, max_blocks) != BL_OK)
+        return 0;
+    return bl_workspace_bytes(BL_OP_DECODE_STACK, 1, dims->H, dims->KV, dims->F) +
+           bitlinear_kv4_attention_ws_bytes(1, dims->H / dims->D, 1, max_blocks,
+                                            dims->KV / dims->D, T, dims->D);
+}
 
-BL_EXPORT bl_status bitlinear_decode_stack_kv(const bl_layer *layers, const bl_kv8 *caches,
-                                              int n_layers, const bl_stack_dims *dims,
-                                              const int32_t *q_start, const int32_t *length,
-                                              const int32_t *table, int64_t max_blocks,
-                                              float scale, float *x, float *trace, void *ws,
-                                              size_t ws_bytes, void *stream) {
-    const char *name = "bitlinear_decode_stack_kv";
+static bl_status check_layer_cache(const char *name, const bl_kv8 *c, const void *x, const int32_t *q_start,
+                                   const int32_t *length, const int32_t *table, int64_t max_blocks) {
+    bool noop = false;
+    return check_kv8(name, x, x, BL_F32, 1, q_start, length, table, 1, max_blocks, c, &noop);
+}
+static bl_status check_layer_cache(const char *name, const bl_kv4 *c, const void *x, const int32_t *q_start,
+                                   const int32_t *length, const int32_t *table, int64_t max_blocks) {
+    bool noop = false;
+    return check_kv4(name, x, x, BL_F32, 1, q_start, length, table, 1, max_blocks, c, &noop);
+}
+static void set_caches(bl::StackKv &kv, const bl_kv8 *c) { kv.caches = c; }
+static void set_caches(bl::StackKv &kv, const bl_kv4 *c) { kv.caches4 = c; }
+
+// The stack over caches C = bl_kv8 or bl_kv4; rope NULL: no rotation.
+template <typename C>
+static bl_status decode_stack_cached(const char *name, const bl_layer *layers, const C *caches, int n_layers,
+                                     const bl_stack_dims *dims, const int32_t *q_start,
+                                     const int32_t *length, const int32_t *table, int64_t max_blocks,
+                                     const bl_rope *rope, float scale, float *x, float *trace, void *ws,
+                                     size_t ws_bytes, size_t (*need_bytes)(const bl_stack_dims *, int64_t, int64_t),
+                                     void *stream) {
     if (n_layers < 0)
         return fail(BL_ERR_SHAPE, "%s: n_layers=%d must be >= 0", name, n_layers);
     if (n_layers > 0 && !caches)
@@ -1103,19 +1125,24 @@ BL_EXPORT bl_status bitlinear_decode_stack_kv(const bl_layer *layers, const bl_k
     if (st != BL_OK)
         return st;
     for (int l = 0; l < n_layers; ++l) {
-        const bl_kv8 &c = caches[l];
+        const C &c = caches[l];
         if (c.D != dims->D || c.KVH != dims->KV / dims->D || c.T != caches[0].T)
             return fail(BL_ERR_SHAPE, "%s: layer %d: need a cache of %lld heads of %lld, T as in the "
                         "first layer (KVH=%lld D=%lld T=%lld)", name, l,
                         (long long)(dims->KV / dims->D), (long long)dims->D, (long long)c.KVH,
                         (long long)c.D, (long long)c.T);
-        bool noop = false;
-        st = check_kv8(name, x, x, BL_F32, 1, q_start, length, table, 1, max_blocks, &c, &noop);
+        st = check_layer_cache(name, &c, x, q_start, length, table, max_blocks);
+        if (st != BL_OK)
+            return st;
+    }
+    if (rope) {
+        // q and where it goes are the workspace's own
+        st = check_rope(name, rope, dims->D, max_blocks * caches[0].T, nullptr, nullptr, BL_F32, 1, 0);
         if (st != BL_OK)
             return st;
     }
     const size_t own = bl_workspace_bytes(BL_OP_DECODE_STACK, 1, dims->H, dims->KV, dims->F);
-    const size_t need = bitlinear_decode_stack_kv_ws_bytes(dims, caches[0].T, max_blocks);
+    const size_t need = need_bytes(dims, caches[0].T, max_blocks);
     if (!ws || ws_bytes < need)
         return fail(BL_ERR_WORKSPACE, "%s: workspace %zu bytes at %p, need %zu", name, ws_bytes,
                     ws, need);
@@ -1124,12 +1151,50 @@ BL_EXPORT bl_status bitlinear_decode_stack_kv(const bl_layer *layers, const bl_k
     st = check_arch();
     if (st != BL_OK)
         return st;
-    const bl::StackKv kv = {caches, {q_start, length, table, 1, 1, (int)max_blocks}, scale,
-                            reinterpret_cast<float *>(static_cast<char *>(ws) + own)};
+    bl::StackKv kv = {nullptr, nullptr, {q_start, length, table, 1, 1, (int)max_blocks}, rope, scale,
+                      reinterpret_cast<float *>(static_cast<char *>(ws) + own)};
+    set_caches(kv, caches);
     return launched(bl::launch_decode_stack(layers, n_layers, (int)dims->H, (int)dims->KV,
                                             (int)dims->F, (int)dims->D, dims->eps, dims->wait_us,
                                             x, trace, static_cast<float *>(ws),
                                             BL_STACK_LAUNCHES, &kv,
                                             static_cast<hipStream_t>(stream)),
                     name);
+}
+
+BL_EXPORT bl_status bitlinear_decode_stack_kv(const bl_layer *layers, const bl_kv8 *caches,
+                                              int n_layers, const bl_stack_dims *dims,
+                                              const int32_t *q_start, const int32_t *length,
+                                              const int32_t *table, int64_t max_blocks,
+                                              float scale, float *x, float *trace, void *ws,
+                                              size_t ws_bytes, void *stream) {
+    return decode_stack_cached("bitlinear_decode_stack_kv", layers, caches, n_layers, dims, q_start, length,
+                               table, max_blocks, nullptr, scale, x, trace, ws, ws_bytes,
+                               bitlinear_decode_stack_kv_ws_bytes, stream);
+}
+
+BL_EXPORT bl_status bitlinear_decode_stack_kv_rope(const bl_layer *layers, const bl_kv8 *caches,
+                                                   int n_layers, const bl_stack_dims *dims,
+                                                   const int32_t *q_start, const int32_t *length,
+                                                   const int32_t *table, int64_t max_blocks,
+                                                   const bl_rope *rope, float scale, float *x,
+                                                   float *trace, void *ws, size_t ws_bytes,
+                                                   void *stream) {
+    if (!rope)
+        return fail(BL_ERR_NULL, "bitlinear_decode_stack_kv_rope: rope is NULL");
+    return decode_stack_cached("bitlinear_decode_stack_kv_rope", layers, caches, n_layers, dims, q_start,
+                               length, table, max_blocks, rope, scale, x, trace, ws, ws_bytes,
+                               bitlinear_decode_stack_kv_ws_bytes, stream);
+}
+
+BL_EXPORT bl_status bitlinear_decode_stack_kv4(const bl_layer *layers, const bl_kv4 *caches,
+                                               int n_layers, const bl_stack_dims *dims,
+                                               const int32_t *q_start, const int32_t *length,
+                                               const int32_t *table, int64_t max_blocks,
+                                               const bl_rope *rope, float scale, float *x,
+                                               float *trace, void *ws, size_t ws_bytes,
+                                               void *stream) {
+    return decode_stack_cached("bitlinear_decode_stack_kv4", layers, caches, n_layers, dims, q_start, length,
+                               table, max_blocks, rope, scale, x, trace, ws, ws_bytes,
+                               bitlinear_decode_stack_kv4_ws_bytes, stream);
 }

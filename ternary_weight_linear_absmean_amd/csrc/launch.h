@@ -166,11 +166,14 @@ hipError_t launch_kv4_append(const void *k, const void *v, const void *q, void *
 // Cached rows as values (kv_read.hip).
 hipError_t launch_kv8_read(const Kv8Seqs &seqs, const bl_kv8 &cache, void *k, void *v, int dtype, hipStream_t s);
 hipError_t launch_kv4_read(const Kv8Seqs &seqs, const bl_kv4 &cache, void *k, void *v, int dtype, hipStream_t s);
-// The caches of a stack whose attention is over cached tokens: one per layer,
-// the arrays of one sequence with one new token, and the attention's workspace.
+// The caches of a stack whose attention is over cached tokens: one per layer, of
+// 8 or of 4 bits (the other NULL), the arrays of one sequence with one new
+// token, a rotation or NULL, and the attention's workspace.
 struct StackKv {
     const bl_kv8 *caches;
+    const bl_kv4 *caches4;
     Kv8Seqs seqs;
+    const bl_rope *rope;
     float scale;
     float *ws;
 };

@@ -12,8 +12,9 @@
 //   y       = down(requant(subln(relu(G)^2 * U)));   x = x + y
 // q and k are computed (their weights are streamed like every other
 // projection) but, with one key, do not change a.  With caches, k and v are
-// appended to the layer's and a is the attention over its tokens (two launches
-// in the place of one, three where the tokens are read in parts).
+// appended to the layer's, 8- or 4-bit, k and q turned by the token's position on
+// the way where a rotation is given, and a is the attention over its tokens
+// (two launches in the place of one, three where the tokens are read in parts).
 #include "device_common.h"
 #include "launch.h"
 
@@ -104,9 +105,18 @@ hipError_t launch_decode_stack(const StackLayer *layers, int n_layers, int H, in
         hipError_t e = launch_gemv_fused(qkv, 3, 1, s);
         if (e != hipSuccess) return e;
         if (kv) {
-            e = launch_kv8_append(tk, tv, 0, kv->seqs, kv->caches[l], s);
+            // turned q: in what the layer's last product will write
+            const float *qa = kv->rope ? w.y : tq;
+            if (kv->caches4)
+                e = launch_kv4_append(tk, tv, tq, w.y, 0, kv->rope ? H / D : 0, kv->seqs, kv->caches4[l], kv->rope, s);
+            else if (kv->rope)
+                e = launch_kv8_append_rope(tk, tv, tq, w.y, 0, H / D, kv->seqs, kv->caches[l], *kv->rope, s);
+            else
+                e = launch_kv8_append(tk, tv, 0, kv->seqs, kv->caches[l], s);
             if (e != hipSuccess) return e;
-            e = launch_kv8_attention(tq, 0, H / D, kv->seqs, kv->caches[l], kv->scale, a, kv->ws, s);
+            e = kv->caches4
+                    ? launch_kv4_attention(qa, 0, H / D, kv->seqs, kv->caches4[l], kv->scale, a, kv->ws, s)
+                    : launch_kv8_attention(qa, 0, H / D, kv->seqs, kv->caches[l], kv->scale, a, kv->ws, s);
             if (e != hipSuccess) return e;
         } else {
             hipLaunchKernelGGL(expand_heads_kernel, eb, dim3(kThreads), 0, s, (const float *)tv, a,

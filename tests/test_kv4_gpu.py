@@ -402,3 +402,37 @@ def test_refusals(gpu):
     with pytest.raises(bl.BitLinearError) as e:              # T = 48
         bl.bitlinear_kv4_append(s["k"], s["v"], *meta(s), bl.kv4_cache(4, 2, 48, 64))
     assert e.value.status == 2
+
+
+def test_calls_from_python_and_from_c(gpu):
+    """The same results whichever way the binding takes: its short one for plain
+    arguments, and the long one that a stream of the caller's asks for."""
+    bl = gpu
+    calls = bl._native._calls
+    for bits in (4, 8):
+        s = make(19, [2, 40, 1], [40, 90, 300], 16, 64, 2, BF16, 4, bits, 32)
+        one, two = cuda(s), cuda(s)
+        c = one["cache"]
+        q = append(bl, one)
+        assert torch.equal(q, append(bl, two, stream=torch.cuda.current_stream()))
+        assert all(torch.equal(a, b) for a, b in zip(c, two["cache"]))
+        for a, b in zip(read(bl, one, 43, dtype=BF16), read(bl, two, 43, dtype=BF16, stream=torch.cuda.current_stream())):
+            assert torch.equal(a, b)
+        f = bl.bitlinear_kv8_attention if bits == 8 else bl.bitlinear_kv4_attention
+        for kw in (dict(), dict(scale=0.3), dict(scale=1)):
+            assert torch.equal(f(q, *meta(one), c, **kw), f(q, *meta(one), c, stream=torch.cuda.current_stream(), **kw))
+        # the short way took them
+        rope = bl.Rope(one["cos_sin"])
+        assert calls.append(bits, one["k"], one["v"], *meta(one), c, rope, one["q"], None) is not NotImplemented
+        assert calls.read(bits, *meta(one), tuple(c), 43, True, None, None) is not NotImplemented
+        assert calls.attention(bits, q, *meta(one), c, None, None, None) is not NotImplemented
+        # and leaves alone what is not as it should be
+        for bad in (q.float(), q[:, :, :32], q.transpose(0, 1), q.cpu(), None, 3):
+            assert calls.attention(bits, bad, *meta(one), c, None, None, None) is NotImplemented
+        assert calls.attention(bits, q, *meta(one), c[:3], None, None, None) is NotImplemented
+        assert calls.attention(bits, q, *meta(one), c, "x", None, None) is NotImplemented
+        assert calls.attention(bits, q, *meta(one), c, None, q[1:], None) is NotImplemented
+        assert calls.attention(12 - bits, q, *meta(one), c, None, None, None) is NotImplemented
+        assert calls.read(bits, *meta(one), c, -1, True, None, None) is NotImplemented
+        assert calls.append(bits, one["k"], one["v"], *meta(one), c, rope, None, q) is NotImplemented
+        assert calls.append(bits, one["k"], one["v"]) is NotImplemented

@@ -135,6 +135,36 @@ def test_attention_workspace(lib):
         assert f(n, QH, B, nb, KVH, T, 128) < 2 ** 50, (n, QH, B)
 
 
+def test_stack_refusals(lib):
+    from ternary_weight_linear_absmean_amd._native import Layer, StackDims
+    need8, need4 = lib.bitlinear_decode_stack_kv_ws_bytes, lib.bitlinear_decode_stack_kv4_ws_bytes
+
+    def dims(H=512, KV=128, F=640, D=64, eps=1e-5, path=0):
+        return StackDims(H, KV, F, D, eps, path, 0, 0)
+
+    def call(d=None, L=None, n=1, c=None, x=A16, ws=A16, size=1 << 40, nb=4, qs=A4, ln=A4, tb=A4, scale=1.0, r=None):
+        L = L or Layer(*[A16] * 14, None)
+        c, r = dict(D=64) if c is None else c, rope() if r is None else r
+        rest = n, d or dims(), qs, ln, tb, nb, r, scale, x, None, ws, size, None
+        return (lib.bitlinear_decode_stack_kv_rope(L, kind(8, **c), *rest),
+                lib.bitlinear_decode_stack_kv4(L, kind(4, **c), *rest))
+    for d in (dims(H=500), dims(D=32), dims(path=2), dims(eps=-1.0), dims(KV=192)):
+        assert call(d) == (SHAPE,) * 2 and need4(d, 64, 4) == 0
+    for kw in (dict(c=dict(D=128)), dict(c=dict(D=64, KVH=1)), dict(c=dict(D=64, T=8)), dict(nb=-1), dict(n=-1),
+               dict(scale=float("nan")), dict(r=rope(rot=24)), dict(r=rope(rot=128)), dict(r=rope(rows=255))):
+        assert call(**kw) == (SHAPE,) * 2, kw
+    assert call(n=0, x=None, ws=None) == (OK,) * 2
+    for kw in (dict(x=None), dict(qs=None), dict(c=dict(D=64, s1=None)), dict(r=rope(cos_sin=None))):
+        assert call(**kw) == (NULL,) * 2, kw
+    for kw in (dict(x=A4), dict(ws=A4), dict(c=dict(D=64, V=A4)), dict(r=rope(cos_sin=A4))):
+        assert call(**kw) == (ALIGN,) * 2, kw
+    assert lib.bitlinear_decode_stack_kv_rope(Layer(*[A16] * 14, None), kind(8, D=64), 1, dims(), A4, A4, A4, 4, None, 1.0,
+                                              A16, None, A16, 1 << 40, None) == NULL
+    for need in (need8, need4):
+        assert need(dims(), 64, 4) >= lib.bl_workspace_bytes(bl.BL_OP_DECODE_STACK, 1, 512, 128, 640)
+    assert call(ws=None) == (WS,) * 2 and call(size=min(need8(dims(), 64, 4), need4(dims(), 64, 4)) - 1) == (WS,) * 2
+
+
 # ------------------------------------------------------------- the oracle
 
 def test_oracle_rotation_by_hand():
