@@ -427,7 +427,7 @@ def test_calls_from_python_and_from_c(gpu):
         assert calls.read(bits, *meta(one), tuple(c), 43, True, None, None) is not NotImplemented
         assert calls.attention(bits, q, *meta(one), c, None, None, None) is not NotImplemented
         # and leaves alone what is not as it should be
-        for bad in (q.float(), q[:, :, :32], q.transpose(0, 1), q.cpu(), None, 3):
+        for bad in (q.half(), q[:, :, :32], q.transpose(0, 1), q.cpu(), None, 3):
             assert calls.attention(bits, bad, *meta(one), c, None, None, None) is NotImplemented
         assert calls.attention(bits, q, *meta(one), c[:3], None, None, None) is NotImplemented
         assert calls.attention(bits, q, *meta(one), c, "x", None, None) is NotImplemented
