@@ -3,8 +3,8 @@
 // The value of a code is formed in fp32: fl(code s) for 8 bits, fl(z + code s)
 // for 4 (code s is exact), then rounded to the rows' type.
 //
-// One workgroup per (16 consecutive positions of a sequence, HEADS heads, K or V),
-// as the 4-bit append's groups.  K's codes are in the rows' order; V's are 16
+// One workgroup per (16 consecutive positions of a sequence, HEADS heads), as the
+// 4-bit append's groups.  K's codes are in the rows' order; V's are 16
 // tokens of one value side by side and cross LDS.  A workgroup's time is its
 // chain of loads (starts, length, table entry, codes), so where there are more of them than run at
 // once each takes four heads, their loads all in flight: 16 sequences of up to
@@ -32,9 +32,8 @@ __global__ __launch_bounds__(2 * D) void kv_read_kernel(Args<C> a) {
     const Kv8Seqs &seqs = a.seqs;
     const C &c = a.c;
     const uint32_t chunks = (uint32_t)(c.KVH + HEADS - 1) / HEADS;
-    const uint32_t pair = blockIdx.x / 2, slot = pair / chunks;
-    const bool is_v = blockIdx.x & 1;
-    const int h0 = (int)(pair - slot * chunks) * HEADS, heads = min(HEADS, c.KVH - h0);
+    const uint32_t slot = blockIdx.x / chunks;
+    const int h0 = (int)(blockIdx.x - slot * chunks) * HEADS, heads = min(HEADS, c.KVH - h0);
     const SeqPlace in_seq = find_place(seqs, slot, [](int q, int i) { return (int64_t)(q >> 4) + 2 * (int64_t)i; });
     const int b = in_seq.b, q0 = in_seq.q0, n = in_seq.q1 - q0;
     const int64_t nth = (int64_t)slot - ((q0 >> 4) + 2 * (int64_t)b);
@@ -50,83 +49,80 @@ __global__ __launch_bounds__(2 * D) void kv_read_kernel(Args<C> a) {
     const int t = threadIdx.x / kPer, td = threadIdx.x % kPer;
     const int64_t pos = 16 * j + t;
     const bool mine = pos >= first && pos < last;
-    E *const dst = static_cast<E *>(is_v ? a.v : a.k) + ((q0 + (pos - start)) * c.KVH + h0) * (int64_t)D + 8 * td;
+    const int64_t to = ((q0 + (pos - start)) * c.KVH + h0) * (int64_t)D + 8 * td;
+    E *const k = static_cast<E *>(a.k) + to, *const v = static_cast<E *>(a.v) + to;
     if (!held) {
         if (mine)
             for (int i = 0; i < heads; ++i) {
-                store_row4(dst + i * D, make_float4(0.f, 0.f, 0.f, 0.f));
-                store_row4(dst + i * D + 4, make_float4(0.f, 0.f, 0.f, 0.f));
+                const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+                store_row4(k + i * D, none);
+                store_row4(k + i * D + 4, none);
+                store_row4(v + i * D, none);
+                store_row4(v + i * D + 4, none);
             }
         return;
     }
     const int64_t head = (int64_t)id * c.KVH + h0;
     const int in = (int)(16 * j & (c.T - 1));             // first of the 16 slots
-    uint32_t scale[HEADS];                                // z and s, or a scale
-    uint2 u[HEADS];                                       // K: this thread's codes
-    uint4 g[HEADS];                                       // V: value threadIdx.x of the 16 tokens
+    uint32_t sk[HEADS], sv[HEADS];                        // z and s, or a scale
+    uint2 u[HEADS];                                       // this thread's codes of K
+    uint4 g[HEADS];                                       // value threadIdx.x of the 16 tokens of V
+    const int vd = min((int)threadIdx.x, D - 1);
 #pragma unroll
     for (int i = 0; i < HEADS; ++i) {
         const int64_t hi = head + min(i, heads - 1);
         if constexpr (kFour) {
-            scale[i] = (is_v ? c.zv : c.zk)[hi * c.T + in + t];
-            if (!is_v) {
-                u[i].x = *reinterpret_cast<const uint32_t *>(c.K + (hi * c.T + in + t) * (int64_t)(D / 2) + 4 * td);
-            } else if (threadIdx.x < D) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(c.V + (hi * (c.T / 16) + in / 16) * (int64_t)(8 * D) +
-                                                                 8 * threadIdx.x);
-                g[i].x = w.x;
-                g[i].y = w.y;
-            }
+            sk[i] = c.zk[hi * c.T + in + t];
+            sv[i] = c.zv[hi * c.T + in + t];
+            u[i].x = *reinterpret_cast<const uint32_t *>(c.K + (hi * c.T + in + t) * (int64_t)(D / 2) + 4 * td);
+            const uint2 w = *reinterpret_cast<const uint2 *>(c.V + (hi * (c.T / 16) + in / 16) * (int64_t)(8 * D) + 8 * vd);
+            g[i].x = w.x;
+            g[i].y = w.y;
         } else {
-            scale[i] = __float_as_uint((is_v ? c.sv : c.sk)[hi]);
-            if (!is_v)
-                u[i] = *reinterpret_cast<const uint2 *>(c.K + (hi * c.T + in + t) * (int64_t)D + 8 * td);
-            else if (threadIdx.x < D)
-                g[i] = *reinterpret_cast<const uint4 *>(c.V + (hi * D + threadIdx.x) * (int64_t)c.T + in);
+            sk[i] = __float_as_uint(c.sk[hi]);
+            sv[i] = __float_as_uint(c.sv[hi]);
+            u[i] = *reinterpret_cast<const uint2 *>(c.K + (hi * c.T + in + t) * (int64_t)D + 8 * td);
+            g[i] = *reinterpret_cast<const uint4 *>(c.V + (hi * D + vd) * (int64_t)c.T + in);
         }
     }
-    if (is_v) {
+    auto put = [&](E *to, uint32_t scale, uint2 p, int shift) {      // 8 codes, a byte or 4 bits of it each
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t x = (e < 4 ? p.x : p.y) >> (8 * (e & 3));
+            if constexpr (kFour) w[e] = __builtin_fmaf((float)(x >> shift & 15u), (float)zs_s(scale), (float)zs_z(scale));
+            else w[e] = __fmul_rn((float)(int8_t)x, __uint_as_float(scale));
+        }
+        store_row4(to, make_float4(w[0], w[1], w[2], w[3]));
+        store_row4(to + 4, make_float4(w[4], w[5], w[6], w[7]));
+    };
+    if (threadIdx.x < D) {
         // line of LDS: a token, or two of 4 bits
-        if (threadIdx.x < D) {
 #pragma unroll
-            for (int i = 0; i < HEADS; ++i) {
-                const uint32_t w[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+        for (int i = 0; i < HEADS; ++i) {
+            const uint32_t w[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
 #pragma unroll
-                for (int y = 0; y < (kFour ? 8 : 16); ++y) codes[i][y][threadIdx.x] = (uint8_t)(w[y >> 2] >> (8 * (y & 3)));
-            }
+            for (int y = 0; y < (kFour ? 8 : 16); ++y) codes[i][y][threadIdx.x] = (uint8_t)(w[y >> 2] >> (8 * (y & 3)));
         }
-        __syncthreads();
     }
+    if (mine) {
+#pragma unroll
+        for (int i = 0; i < HEADS; ++i) {
+            if (i >= heads) break;
+            uint2 p = u[i];
+            if constexpr (kFour) {                        // values 2 e, 2 e + 1 of byte e -> bytes
+                const uint32_t lo = u[i].x & 0x0F0F0F0Fu, hi = u[i].x >> 4 & 0x0F0F0F0Fu;
+                p = make_uint2(perm(hi, lo, 0x05010400u), perm(hi, lo, 0x07030602u));
+            }
+            put(k + i * D, sk[i], p, 0);
+        }
+    }
+    __syncthreads();
     if (!mine) return;
 #pragma unroll
     for (int i = 0; i < HEADS; ++i) {
         if (i >= heads) break;
-        float w[8];
-        if constexpr (kFour) {
-            const float z = (float)zs_z(scale[i]), s = (float)zs_s(scale[i]);
-            if (!is_v) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = __builtin_fmaf((float)(u[i].x >> (4 * e) & 15u), s, z);
-            } else {
-                const uint2 p = *reinterpret_cast<const uint2 *>(&codes[i][t >> 1][8 * td]);
-                const int sh = 4 * (t & 1);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[e] = __builtin_fmaf((float)(p.x >> (sh + 8 * e) & 15u), s, z);
-                    w[4 + e] = __builtin_fmaf((float)(p.y >> (sh + 8 * e) & 15u), s, z);
-                }
-            }
-        } else {
-            const float s = __uint_as_float(scale[i]);
-            const uint2 p = is_v ? *reinterpret_cast<const uint2 *>(&codes[i][t][8 * td]) : u[i];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[e] = __fmul_rn((float)(int8_t)(p.x >> (8 * e)), s);
-                w[4 + e] = __fmul_rn((float)(int8_t)(p.y >> (8 * e)), s);
-            }
-        }
-        store_row4(dst + i * D, make_float4(w[0], w[1], w[2], w[3]));
-        store_row4(dst + i * D + 4, make_float4(w[4], w[5], w[6], w[7]));
+        put(v + i * D, sv[i], *reinterpret_cast<const uint2 *>(&codes[i][kFour ? t >> 1 : t][8 * td]), kFour ? 4 * (t & 1) : 0);
     }
 }
 
@@ -137,8 +133,8 @@ constexpr int64_t kAtOnce = 4 * 256 * 2048;
 template <typename E, int D, typename C>
 hipError_t read(const Kv8Seqs &seqs, const C &c, void *k, void *v, hipStream_t s) {
     const Args<C> a = {seqs, c, k, v, (seqs.n_tok >> 4) + 2 * (int64_t)seqs.B};
-    const bool four = a.slots * c.KVH * 2 * 2 * D > kAtOnce;
-    const int64_t groups = a.slots * (four ? (c.KVH + 3) / 4 : c.KVH) * 2;
+    const bool four = a.slots * c.KVH * 2 * D > kAtOnce;
+    const int64_t groups = a.slots * (four ? (c.KVH + 3) / 4 : c.KVH);
     if (groups * 2 * D >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     if (four)
         hipLaunchKernelGGL((kv_read_kernel<E, D, 4, C>), dim3((unsigned)groups), dim3(2 * D), 0, s, a);
