@@ -11,7 +11,7 @@
 // being rescaled when a block's largest value grows.  Quotients are correctly
 // rounded, so the cache's bytes are defined to the bit.
 //
-// One workgroup per (16 consecutive positions of a sequence, head, K or V): 16
+// One workgroup per (16 consecutive positions of a sequence, head): 16
 // tokens' codes of one value of V are the 8 bytes of a group, so it alone writes
 // them, also where it brings a single token and the others' codes stay.  D / 8
 // threads to a token, 8 values each.  The grid is known without the lengths:
@@ -44,21 +44,46 @@ struct Args {
     int64_t slots;                // of 16 positions; then the queries' workgroups
 };
 
+// Eight values of a row, and with those of the row's other threads its z and s and
+// these values' codes.
+template <int PER>
+__device__ __forceinline__ uint32_t quantised(const float4 *x, uint32_t *u) {
+    float f[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    float lo = 65504.0f, hi = -65504.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f[e] = fminf(fmaxf(f[e], -65504.0f), 65504.0f);
+        lo = fminf(lo, f[e]);
+        hi = fmaxf(hi, f[e]);
+    }
+    lo = -group_max(-lo, PER);
+    hi = group_max(hi, PER);
+    const _Float16 z = f16_below(lo);
+    const float zf = (float)z;
+    const _Float16 step = (_Float16)__fdiv_rn(__fsub_rn(hi, zf), 15.0f);
+    const float sf = (float)step;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float r = __builtin_rintf(__fdiv_rn(__fsub_rn(f[e], zf), sf));
+        u[e] = sf > 0.0f ? (uint32_t)fminf(fmaxf(r, 0.0f), 15.0f) : 0u;
+    }
+    return __builtin_bit_cast(uint32_t, half2{z, step});
+}
+
 template <typename E, int D, bool ROPE>
 __global__ __launch_bounds__(2 * D) void kv4_append_kernel(Args<D> a) {
     constexpr int kPer = D / 8;                           // threads of a token
     __shared__ alignas(16) uint8_t codes[D][kTokens];
     const Kv8Seqs &seqs = a.seqs;
     const Kv4Cache &c = a.c;
-    const int64_t appends = a.slots * c.KVH * 2;
+    const int64_t appends = a.slots * c.KVH;
     if (ROPE && blockIdx.x >= appends) {
         turn_queries(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(seqs.n_tok, a.QH, D),
                      D == 64 ? 6 : 7, seqs, (int64_t)seqs.max_blocks << c.t_shift, a.rope, blockIdx.x - appends);
         return;
     }
-    const uint32_t pair = blockIdx.x / 2, slot = pair / (uint32_t)c.KVH;
-    const bool is_v = blockIdx.x & 1;
-    const int h = (int)(pair - slot * c.KVH);
+    const uint32_t slot = blockIdx.x / (uint32_t)c.KVH;
+    const int h = (int)(blockIdx.x - slot * c.KVH);
     const SeqPlace in_seq = find_place(seqs, slot, [](int q, int i) { return (int64_t)(q >> 4) + 2 * (int64_t)i; });
     const int b = in_seq.b, q0 = in_seq.q0, n = in_seq.q1 - q0;
     const int64_t nth = (int64_t)slot - ((q0 >> 4) + 2 * (int64_t)b);
@@ -68,76 +93,56 @@ __global__ __launch_bounds__(2 * D) void kv4_append_kernel(Args<D> a) {
     const int64_t first = max(max(start, (int64_t)0), 16 * j), last = min(len, 16 * j + 16);
     if (j >= (int64_t)seqs.max_blocks << c.t_shift >> 4 || first >= last) return;
     const int id = seqs.table[(int64_t)b * seqs.max_blocks + (16 * j >> c.t_shift)];
-    if (id < 0 || id >= c.n_blocks) return;                        // uniform: the block holds no token
 
     // this thread's token and values; slots without a new token repeat the first
     const int t = threadIdx.x / kPer, td = threadIdx.x % kPer;
     const bool mine = 16 * j + t >= first && 16 * j + t < last;
     const int64_t pos = mine ? 16 * j + t : first;
     const int64_t row = ((q0 + (pos - start)) * c.KVH + h) * (int64_t)D;
-    const int64_t head = (int64_t)id * c.KVH + h;
+    const E *const k = static_cast<const E *>(a.k) + row, *const v = static_cast<const E *>(a.v) + row;
+    float4 x[2], y[2], w[2];
+    x[0] = load_row4(k + 8 * td);
+    x[1] = load_row4(k + 8 * td + 4);
+    w[0] = load_row4(v + 8 * td);
+    w[1] = load_row4(v + 8 * td + 4);
+    if (ROPE) {
+        const bool on = 8 * td < a.rope.rot;
+        const Turn8 turn(a.rope, pos, on ? 8 * td : 0);
+        turn.load_others(k, y);
+        if (on) turn.apply(x, y);
+    }
+    if (id < 0 || id >= c.n_blocks) return;                        // uniform: the block holds no token
+    const int64_t head = (int64_t)id * c.KVH + h, token = head * c.T + (pos & (c.T - 1));
     uint8_t *const group = c.V + (head * (c.T / 16) + (j & (c.T / 16 - 1))) * (int64_t)(8 * D);
     const int s0 = (int)(first - 16 * j), s1 = (int)(last - 16 * j);
     const bool whole = s1 - s0 == kTokens;
     uint2 old = make_uint2(0u, 0u);
-    if (is_v && !whole && threadIdx.x < D) old = *reinterpret_cast<const uint2 *>(group + 8 * threadIdx.x);
+    if (!whole && threadIdx.x < D) old = *reinterpret_cast<const uint2 *>(group + 8 * threadIdx.x);
 
-    float4 x[2];
-    if (ROPE && !is_v) {
-        const E *const p = static_cast<const E *>(a.k) + row;
-        const bool on = 8 * td < a.rope.rot;
-        const Turn8 turn(a.rope, pos, on ? 8 * td : 0);
-        float4 y[2];
-        x[0] = load_row4(p + 8 * td);
-        x[1] = load_row4(p + 8 * td + 4);
-        turn.load_others(p, y);
-        if (on) turn.apply(x, y);
-    } else {
-        const E *p = static_cast<const E *>(is_v ? a.v : a.k) + row + 8 * td;
-        x[0] = load_row4(p);
-        x[1] = load_row4(p + 4);
-    }
-    float f[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-    float lo = 65504.0f, hi = -65504.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        f[e] = fminf(fmaxf(f[e], -65504.0f), 65504.0f);
-        lo = fminf(lo, f[e]);
-        hi = fmaxf(hi, f[e]);
-    }
-    lo = -group_max(-lo, kPer);
-    hi = group_max(hi, kPer);
-    const _Float16 z = f16_below(lo);
-    const float zf = (float)z;
-    const _Float16 step = (_Float16)__fdiv_rn(__fsub_rn(hi, zf), 15.0f);
-    const float sf = (float)step;
     uint32_t u[8];
+    const uint32_t zk = quantised<kPer>(x, u);
+    if (mine) {
+        uint32_t p = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float r = __builtin_rintf(__fdiv_rn(__fsub_rn(f[e], zf), sf));
-        u[e] = sf > 0.0f ? (uint32_t)fminf(fmaxf(r, 0.0f), 15.0f) : 0u;
+        for (int e = 0; e < 8; ++e) p |= u[e] << (4 * e);
+        *reinterpret_cast<uint32_t *>(c.K + token * (D / 2) + 4 * td) = p;
     }
-    if (mine && td == 0)
-        (is_v ? c.zv : c.zk)[head * c.T + (int)(pos & (c.T - 1))] = __builtin_bit_cast(uint32_t, half2{z, step});
-    if (!is_v) {
-        if (!mine) return;
-        uint32_t w = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w |= u[e] << (4 * e);
-        *reinterpret_cast<uint32_t *>(c.K + (head * c.T + (int)(pos & (c.T - 1))) * (int64_t)(D / 2) + 4 * td) = w;
-        return;
+    const uint32_t zv = quantised<kPer>(w, u);
+    if (mine && td == 0) {
+        c.zk[token] = zk;
+        c.zv[token] = zv;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) codes[8 * td + e][t] = (uint8_t)u[e];
     __syncthreads();
     if (threadIdx.x >= D) return;
-    const uint4 w = *reinterpret_cast<const uint4 *>(codes[threadIdx.x]);
+    const uint4 g = *reinterpret_cast<const uint4 *>(codes[threadIdx.x]);
     // bytes 0 n 0 n -> nibbles
     auto pack = [](uint32_t lo4, uint32_t hi4) {
         const uint32_t p = lo4 | lo4 >> 4, r = hi4 | hi4 >> 4;
         return perm(r, p, 0x06040200u);
     };
-    uint2 fresh = make_uint2(pack(w.x, w.y), pack(w.z, w.w));
+    uint2 fresh = make_uint2(pack(g.x, g.y), pack(g.z, g.w));
     if (!whole) {
         const uint64_t keep = ~((~0ull >> (64 - 4 * (s1 - s0))) << (4 * s0));
         fresh.x = (old.x & (uint32_t)keep) | (fresh.x & ~(uint32_t)keep);
@@ -150,7 +155,7 @@ template <typename E, int D>
 hipError_t append(const void *k, const void *v, const void *q, void *q_out, int QH, const Kv8Seqs &seqs,
                   const Kv4Cache &c, const Rope *rope, hipStream_t s) {
     Args<D> a = {seqs, c, {}, k, v, q, q_out, QH, (seqs.n_tok >> 4) + 2 * (int64_t)seqs.B};
-    int64_t groups = a.slots * c.KVH * 2;
+    int64_t groups = a.slots * c.KVH;
     if (rope) {
         a.rope = *rope;
         groups += rope_groups(seqs.n_tok, QH, D, 2 * D);
