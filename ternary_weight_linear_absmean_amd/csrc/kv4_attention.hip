@@ -119,10 +119,20 @@ struct Reference {
     }
 };
 
-// Few rows: one workgroup to a piece; its waves take 64-key tiles in turn, each
-// with sums of its own, joined in LDS.  Operands go from memory to registers:
-// a cached byte has one reader.  The next tile's K is under way from the
-// moment this one's has been used, and so is V.
+// One workgroup to a piece; its waves take 64-key tiles in turn, each with sums of
+// its own, joined in LDS.  Operands go from memory to registers, no LDS and no
+// barrier in the loop: a cached byte has one reader.  The next tile's K is under way
+// from the moment this one's has been used, and so is V.
+//
+// Single tokens are bound by memory and, at the ends, by the chain starts -> entry
+// -> K -> scores -> V and by the join: 64 ragged sequences of up to 4096 keys, 5
+// heads of 4, bf16, 87 MB: 25.5 us, 3.4 TB/s and 4.1 of its middle, where a sum over
+// memory reads 4.0; the whole call 27.4.  About 370 vector instructions a wave and
+// tile (662 with one more add for each pair of codes, scores multiplied twice, and
+// loads behind a branch, which copied every loaded register: 36.2 us).  Loads of V
+// held in front of the loop's end: the same.  A third workgroup on a CU (168
+// registers, 768 pieces): 25.2.  Units of 32 rows, which turn a code once for two
+// products: 2048 bf16 rows on 4096 keys 135 us, of 16 rows 138.
 template <int D>
 struct FewLds {
     float join[kWaves][kRows][D + 4];
@@ -423,9 +433,15 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 // a wave, 64 keys at a time, the tile turned into fp16 once, in LDS, for all rows.  While
 // tile t is used, t + 1 is turned into the other buffer and the codes of t + 2
 // are on their way.  What goes to LDS are the keys and values themselves, fp16(z
-// + s u), an error of 2^-12 beside the result's 2^-9: no z or s is left in the loop over scores.
-// (fp32 rows would need the codes and each token's z and s: that took 283 us for 2048
-// rows on 4096 keys, 5 heads of 4 and D = 128, where the kernel above takes 198.)
+// + s u), an error of 2^-12 beside the result's 2^-9: no z or s is left in the
+// loop over scores.  (fp32 rows would need the codes and each token's z and s: 283 us
+// for 2048 rows on 4096 keys, 5 heads of 4 and D = 128, where 16-row units take 198.)
+//
+// Bound by vector and matrix instructions that hardly overlap: 2 x 2048 ragged rows
+// on 4096 keys, 5 heads of 4, 92 GFLOP: 133 us, 690 TFLOP/s (a large fp16 product
+// 1420); of a SIMD's time 53% vector and 30% matrix instructions, 1.55 waves on
+// average.  Scores of the next tile interleaved with this one's weights: 147; a
+// raised priority for either part: the same.
 //
 // z and s that are not finite (never written by the append) count as 0 here, and
 // a step with which a code of 15 would pass fp16 as the largest that does not:

