@@ -228,6 +228,13 @@ def _check(call, status):
         raise BitLinearError(call, status, load().bl_last_error().decode())
 
 
+def _made(call, r):
+    """Whether _calls made a call; raises for a launch that failed."""
+    if type(r) is int:
+        _check(call, r)
+    return r is not NotImplemented
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -705,7 +712,7 @@ def bitlinear_kv8_append(k, v, q_start, lengths, table, cache, stream=None):
     (Kv8Cache, updated in place).  int32 on the GPU: q_start [B + 1], lengths
     [B] (with the new tokens), table [B, max_blocks]."""
     if stream is None and _calls is not None:
-        if _calls.append(8, k, v, q_start, lengths, table, cache, None, None, None) is not NotImplemented:
+        if _made("bitlinear_kv8_append", _calls.append(8, k, v, q_start, lengths, table, cache, None, None, None)):
             return
     dev, dt, kp, shape = _rows(k, 3, "k")
     c = _kv8(cache, dev)
@@ -762,7 +769,7 @@ def bitlinear_kv8_append_rope(k, v, q_start, lengths, table, cache, rope, q=None
         raise ValueError("bitlinear_kv8_append_rope without rope")
     if stream is None and _calls is not None:
         r = _calls.append(8, k, v, q_start, lengths, table, cache, rope, q, q_out)
-        if r is not NotImplemented:
+        if _made("bitlinear_kv8_append_rope", r):
             return r
     return _append_turned("bitlinear_kv8_append_rope", _kv8, k, v, q_start, lengths, table, cache, rope, q,
                           q_out, stream)
@@ -774,7 +781,7 @@ def bitlinear_kv4_append(k, v, q_start, lengths, table, cache, rope=None, q=None
     by bitlinear_kv8_append_rope (which see for q and what is returned)."""
     if stream is None and _calls is not None:
         r = _calls.append(4, k, v, q_start, lengths, table, cache, rope, q, q_out)
-        if r is not NotImplemented:
+        if _made("bitlinear_kv4_append", r):
             return r
     return _append_turned("bitlinear_kv4_append", _kv4, k, v, q_start, lengths, table, cache, rope, q, q_out,
                           stream)
@@ -783,7 +790,7 @@ def bitlinear_kv4_append(k, v, q_start, lengths, table, cache, rope=None, q=None
 def _read(call, bits, q_start, lengths, table, cache, n_tok, dtype, k, v, stream):
     if stream is None and _calls is not None and dtype in _DTYPES:
         r = _calls.read(bits, q_start, lengths, table, cache, n_tok, dtype is torch.bfloat16, k, v)
-        if r is not NotImplemented:
+        if _made(call, r):
             return r
     device_cache = _kv8 if bits == 8 else _kv4
     K = cache[0]
@@ -832,7 +839,7 @@ def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=N
     out may not overlap q."""
     if stream is None and _calls is not None:
         r = _calls.attention(8, q, q_start, lengths, table, cache, scale, out, ws)
-        if r is not NotImplemented:
+        if _made("bitlinear_kv8_attention", r):
             return r
     dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
     c = _kv8(cache, dev)
@@ -868,7 +875,7 @@ def bitlinear_kv4_attention(q, q_start, lengths, table, cache, scale=None, out=N
     """bitlinear_kv8_attention over a 4-bit cache (Kv4Cache)."""
     if stream is None and _calls is not None:
         r = _calls.attention(4, q, q_start, lengths, table, cache, scale, out, ws)
-        if r is not NotImplemented:
+        if _made("bitlinear_kv4_attention", r):
             return r
     dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
     c = _kv4(cache, dev)

@@ -8,6 +8,9 @@
 // contiguous, of the types and shapes that the call wants, on the current GPU --
 // and return NotImplemented, with nothing done, for anything else and for whatever the library
 // refuses: the Python of _native.py then makes the call, or says what is wrong with it.
+// A launch that the runtime reports as failed may be under way all the same (the
+// runtime gives an earlier call's error too), so that status is returned as a number and the
+// call is not made again: queries rotated in place would turn twice.
 //
 // The library's entry points come in by address (bind), so this module is not
 // linked against it.
@@ -115,6 +118,7 @@ at::Tensor fresh(at::IntArrayRef shape, const at::Tensor &like, at::ScalarType t
 }
 
 PyObject *left() { Py_RETURN_NOTIMPLEMENTED; }
+PyObject *failed(bl_status st) { return st == BL_ERR_HIP ? PyLong_FromLong(st) : left(); }
 
 template <typename F>
 bl_status without_gil(F f) {
@@ -192,7 +196,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
             return lib.kv8_append_rope(kp, vp, qp, op, dt, rows, QH, s.q_start, s.lengths, s.table, s.B, s.max_blocks,
                                        &c.c8, &rope, stream);
         });
-        if (st != BL_OK) return left();
+        if (st != BL_OK) return failed(st);
         if (made.defined()) return THPVariable_Wrap(made);
         Py_INCREF(a[9]);
         return a[9];
@@ -228,7 +232,7 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n) {
                              : lib.kv8_read(&c.c8, s.q_start, s.lengths, s.table, s.B, s.max_blocks, rows, p[0], p[1], dt,
                                             stream);
         });
-        if (st != BL_OK) return left();
+        if (st != BL_OK) return failed(st);
         PyObject *both = PyTuple_New(2);
         if (!both) return nullptr;
         for (int i = 0; i < 2; ++i) {
@@ -291,7 +295,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
                              : lib.kv8_attention(qp, dt, rows, QH, s.q_start, s.lengths, s.table, s.B, s.max_blocks, &c.c8,
                                                  scale, op, wp, bytes, stream);
         });
-        if (st != BL_OK) return left();
+        if (st != BL_OK) return failed(st);
         if (made.defined()) return THPVariable_Wrap(made);
         Py_INCREF(a[7]);
         return a[7];

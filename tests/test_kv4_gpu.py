@@ -1,5 +1,7 @@
 """The rotated appends, the 4-bit key/value cache and the reads of both caches
 against the 64-bit oracle: bytes, scales and rotated values exactly."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -436,3 +438,33 @@ def test_calls_from_python_and_from_c(gpu):
         assert calls.read(bits, *meta(one), c, -1, True, None, None) is NotImplemented
         assert calls.append(bits, one["k"], one["v"], *meta(one), c, rope, None, q) is NotImplemented
         assert calls.append(bits, one["k"], one["v"]) is NotImplemented
+
+
+def test_a_failed_launch_is_not_made_again(gpu):
+    """A launch that is reported as failed may have been made (an earlier error of the
+    runtime is reported too): queries rotated in place may not be rotated again."""
+    bl, native = gpu, gpu._native
+    entries = [ctypes.cast(getattr(native.load(), name), ctypes.c_void_p).value for name in native._ENTRIES]
+    calls = []
+    failing = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: calls.append(1) or 7)
+    address = ctypes.cast(failing, ctypes.c_void_p).value
+    try:
+        native._calls.bind(*([address] * 7 + entries[7:]))
+        for bits in (4, 8):
+            s = cuda(make(20, [2, 1], [40, 30], 16, 64, 2, F32, 4, bits, 32))
+            was = copied(s)
+            attend = bl.bitlinear_kv8_attention if bits == 8 else bl.bitlinear_kv4_attention
+            out = [torch.full_like(s["q"], 7.0), torch.full_like(s["k"], 7.0), torch.full_like(s["k"], 7.0)]
+            for call in (lambda: append(bl, s, q_out=s["q"]), lambda: attend(s["q"], *meta(s), s["cache"], out=out[0]),
+                         lambda: read(bl, s, 3, k=out[1], v=out[2])) + \
+                        ((lambda: bl.bitlinear_kv8_append(s["k"], s["v"], *meta(s), s["cache"]),) if bits == 8 else ()):
+                del calls[:]
+                with pytest.raises(bl.BitLinearError) as e:
+                    call()
+                assert e.value.status == 7 and len(calls) == 1
+            torch.cuda.synchronize()
+            assert torch.equal(s["q"], was["q"]) and all(bool((x == 7.0).all()) for x in out)
+            for a, b in zip(s["cache"], was["cache"]):
+                assert torch.equal(a, b)
+    finally:
+        native._calls.bind(*entries)
