@@ -568,10 +568,10 @@ typedef struct {
  *   q      in   [n_tok][QH][D] of `dtype`, 16-byte aligned; QH = 0: no queries (q
  *               and q_out may be NULL).  0 <= QH <= 65535, n_tok * QH < 2^31.
  *   q_out  out  [n_tok][QH][D] of `dtype`, 16-byte aligned: q rotated, rounded
- *               once more for bf16.  It may be q; it may not overlap q otherwise
- *               (BL_ERR_ALIGN), nor k, v or the cache.  Rows of no sequence are left, rows at positions
- *               that the cache has no room for (below 0, from max_blocks * T on)
- *               are copied.
+ *               once more for bf16.  It may be q; it may not overlap q otherwise,
+ *               nor k and v (BL_ERR_ALIGN), nor the cache.  Rows of no sequence are
+ *               left, rows at positions that the cache has no room for (below 0, from
+ *               max_blocks * T on) are copied.
  * The key's codes are formed of the rotated fp32 values; everything else as for
  * bitlinear_kv8_append.
  */
@@ -628,7 +628,10 @@ bl_status bitlinear_kv4_append(const void *k, const void *v, const void *q, void
  * least).  An operand's smallest step is 2^-38 of the row's largest |q|, and
  * 2^-38 of the largest weight times a power of two above the largest step of the
  * values (2^-34 for bf16 rows).  Errors scale with sums over |z| + s code in the
- * place of |value|.  |scale| max |q| is to stay below 2^115.
+ * place of |value|.  Where keys and values are rounded to fp16, a step with which
+ * code 15 would pass 65504 counts as the largest that does not (2^-10 smaller).
+ * Scores may be of any size that |scale| max |q| < 2^115 and |scale| max |q| D
+ * max(|z| + 15 s) < 2^125 allow, each rounded to fp32.
  */
 bl_status bitlinear_kv4_attention(const void *q, bl_dtype dtype, int64_t n_tok, int64_t QH,
                                   const int32_t *q_start, const int32_t *lengths,
@@ -647,7 +650,7 @@ size_t bitlinear_kv4_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B, in
  *   k, v   out  [n_tok][KVH][D] of `dtype`, 16-byte aligned: fp32(code * s), or
  *               fp32(z + code * s) of the 4-bit cache, rounded to `dtype`.  Rows
  *               whose position holds no token become zeros, rows of no sequence
- *               are left.  k and v may not overlap (BL_ERR_ALIGN).
+ *               are left.  k and v may not overlap (BL_ERR_ALIGN), nor the cache.
  * Limits and no-ops as for the append.
  */
 bl_status bitlinear_kv8_read(const bl_kv8 *cache, const int32_t *q_start, const int32_t *lengths,

@@ -741,16 +741,18 @@ BL_EXPORT bl_status bitlinear_kv8_append(const void *k, const void *v, bl_dtype 
                     name);
 }
 
-// Whether two buffers of `bytes` each share a byte.
-static bool overlap(const void *p, const void *q, size_t bytes) {
+// Whether two buffers share a byte.
+static bool overlap(const void *p, size_t p_bytes, const void *q, size_t q_bytes) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + bytes && b < a + bytes;
+    return a < b + q_bytes && b < a + p_bytes;
 }
+static bool overlap(const void *p, const void *q, size_t bytes) { return overlap(p, bytes, q, bytes); }
 
 // A rotation of D-value heads for positions below `room`, and the queries that
-// are rotated with the keys (checked also where there is no row).
-static bl_status check_rope(const char *name, const bl_rope *r, int64_t D, int64_t room, const void *q,
-                            const void *q_out, bl_dtype dtype, int64_t n_tok, int64_t QH) {
+// are rotated with the KVH heads of k and v (checked also where there is no row).
+static bl_status check_rope(const char *name, const bl_rope *r, int64_t D, int64_t room, const void *k,
+                            const void *v, int64_t KVH, const void *q, const void *q_out, bl_dtype dtype,
+                            int64_t n_tok, int64_t QH) {
     if (r->rot < 16 || r->rot > D || r->rot % 16 != 0 || r->rows < room)
         return fail(BL_ERR_SHAPE, "%s: need rot a multiple of 16 in [16, %lld], rows >= max_blocks * T = "
                     "%lld (rot=%lld rows=%lld)", name, (long long)D, (long long)room, (long long)r->rot,
@@ -769,6 +771,9 @@ static bl_status check_rope(const char *name, const bl_rope *r, int64_t D, int64
     if (q != q_out && overlap(q, q_out, bytes))
         return fail(BL_ERR_ALIGN, "%s: q_out overlaps q (%p, %p, %zu bytes each)", name, q_out, q,
                     bytes);
+    const size_t new_bytes = (size_t)n_tok * (size_t)(KVH * D) * (dtype == BL_BF16 ? 2 : 4);
+    if (QH > 0 && (overlap(q_out, bytes, k, new_bytes) || overlap(q_out, bytes, v, new_bytes)))
+        return fail(BL_ERR_ALIGN, "%s: q_out overlaps k or v (%p, %p, %p)", name, q_out, k, v);
     return BL_OK;
 }
 
@@ -786,7 +791,8 @@ BL_EXPORT bl_status bitlinear_kv8_append_rope(const void *k, const void *v, cons
                              cache, &noop);
     if (st != BL_OK)
         return st;
-    st = check_rope(name, rope, cache->D, max_blocks * cache->T, q, q_out, dtype, noop ? 0 : n_tok, QH);
+    st = check_rope(name, rope, cache->D, max_blocks * cache->T, k, v, cache->KVH, q, q_out, dtype,
+                        noop ? 0 : n_tok, QH);
     if (st != BL_OK || noop)
         return st;
     st = check_arch();
@@ -810,7 +816,8 @@ BL_EXPORT bl_status bitlinear_kv4_append(const void *k, const void *v, const voi
     if (st != BL_OK)
         return st;
     if (rope)
-        st = check_rope(name, rope, cache->D, max_blocks * cache->T, q, q_out, dtype, noop ? 0 : n_tok, QH);
+        st = check_rope(name, rope, cache->D, max_blocks * cache->T, k, v, cache->KVH, q, q_out, dtype,
+                        noop ? 0 : n_tok, QH);
     if (st != BL_OK || noop)
         return st;
     st = check_arch();
@@ -1137,7 +1144,8 @@ static bl_status decode_stack_cached(const char *name, const bl_layer *layers, c
     }
     if (rope) {
         // q and where it goes are the workspace's own
-        st = check_rope(name, rope, dims->D, max_blocks * caches[0].T, nullptr, nullptr, BL_F32, 1, 0);
+        st = check_rope(name, rope, dims->D, max_blocks * caches[0].T, nullptr, nullptr, 0, nullptr, nullptr, BL_F32, 1,
+                        0);
         if (st != BL_OK)
             return st;
     }

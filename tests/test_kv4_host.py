@@ -204,3 +204,14 @@ def test_oracle_packing():
     assert V[1, 2, 1, 9, 3] == u[1, 1, 2, 22, 9] | u[1, 1, 2, 23, 9] << 4
     k, v = ref.unpack(K, V)
     assert np.array_equal(k, u[0]) and np.array_equal(v, u[1])
+
+
+def test_turned_queries_apart_from_the_new_rows(lib):
+    """3 query rows of 8 heads beside key and value rows of 2, of 128 values each."""
+    far = 1 << 40
+    for dt, es in ((0, 4), (1, 2)):
+        q_size, size = 3 * 8 * 128 * es, 3 * 2 * 128 * es
+        for by in (0, 16 - q_size, size - 16):
+            for q in (far, B16 + by):                       # from elsewhere and in place
+                assert each(lib, dt=dt, k=B16, v=2 * far, q=q, o=B16 + by)[:2] == (ALIGN,) * 2
+                assert each(lib, dt=dt, k=2 * far, v=B16, q=q, o=B16 + by)[:2] == (ALIGN,) * 2
