@@ -468,3 +468,37 @@ def test_a_failed_launch_is_not_made_again(gpu):
                 assert torch.equal(a, b)
     finally:
         native._calls.bind(*entries)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_captured_append_and_read(gpu, bits):
+    """An append with queries turned in place and the read of the new tokens, captured once and
+    replayed as the sequences grow out of their table's room."""
+    bl = gpu
+    s = cuda(make(21, [1, 5, 1], [15, 40, 62], 16, 128, 2, BF16, 4, bits, 64))
+    room = s["table"].shape[1] * 16
+    start, eager = copied(s), copied(s)
+    k, v = torch.zeros_like(s["k"]), torch.zeros_like(s["k"])
+
+    def step(x, **kw):
+        append(bl, x, q_out=x["q"])
+        return read(bl, x, 7, dtype=BF16, **kw)
+    step(s, k=k, v=v)
+    for a, b in zip(s["cache"] + [s["q"]], start["cache"] + [start["q"]]):
+        a.copy_(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(s, k=k, v=v)
+    for i in range(8):
+        for x in ("q", "k", "v"):
+            rows = torch.randn(s[x].shape, generator=torch.Generator().manual_seed(i)).to(BF16).cuda()
+            s[x].copy_(rows), eager[x].copy_(rows)
+        graph.replay()
+        want = step(eager)
+        torch.cuda.synchronize()
+        for a, b in zip([s["q"], k, v] + s["cache"], [eager["q"], *want] + eager["cache"]):
+            assert torch.equal(a, b)
+        s["lengths"] += 7
+        eager["lengths"] += 7
+    assert int(s["lengths"].max()) > room
