@@ -343,11 +343,26 @@ struct Parts {
     const float2 *ml;
     int64_t pitch;
 };
+// The pieces of a row that the few-rows kernel has cut, within the workspace whatever
+// it holds.
+template <int D, class C>
+__device__ __forceinline__ bool find_cut(const KvArgs<C> &a, int64_t row, Parts &p) {
+    const int2 info = cut_info(a, D)[row];
+    p.row = row;
+    p.n = info.y;
+    if (p.n < 2 || p.n > kMaxParts || info.x < 0 || info.x / kRows > a.slots - p.n)
+        return false;                                           // written directly
+    p.pitch = kRows;
+    p.lines = reinterpret_cast<const float4 *>(a.cut) + (int64_t)info.x * (D / 4);
+    p.ml = reinterpret_cast<const float2 *>(a.cut + (int64_t)a.slots * kRows * D) + info.x;
+    return true;
+}
 template <int D, bool FEW, class C>
 __device__ __forceinline__ bool find_parts(const KvArgs<C> &a, int64_t row, Parts &p) {
     const Kv8Seqs &sq = a.seqs;
     int b, t;
-    if (FEW && a.mixed) {
+    if (FEW && !a.mixed) return find_cut<D>(a, row, p);
+    if (FEW) {
         const int each = kFewRows * a.c.KVH;
         b = (int)(row / each);
         const int r = (int)(row - (int64_t)b * each), h = r / kFewRows;
@@ -360,27 +375,29 @@ __device__ __forceinline__ bool find_parts(const KvArgs<C> &a, int64_t row, Part
     const int q0 = q_at(sq, b), q1 = q_at(sq, b + 1);
     if (t < q0 || t >= q1) return false;
     const int64_t rows = (int64_t)(q1 - q0) * a.G;
+    if (FEW) return rows <= a.max_rows && find_cut<D>(a, row, p);
+    if (rows <= a.min_rows) return false;
+    const int64_t keys = min((int64_t)sq.lengths[b] - (q1 - t) + 1, key_capacity(a));
+    const int64_t chunk = keys_of_part(a, sq.lengths[b]);
+    if (keys <= chunk) return false;                            // written directly
     p.row = row;
-    if (FEW) {
-        if (rows > a.max_rows) return false;
-        const int2 info = cut_info(a, D)[row];
-        p.n = info.y;
-        if (p.n < 2 || p.n > kMaxParts || info.x < 0 || info.x / kRows > a.slots - p.n)
-            return false;                                       // written directly
-        p.pitch = kRows;
-        p.lines = reinterpret_cast<const float4 *>(a.cut) + (int64_t)info.x * (D / 4);
-        p.ml = reinterpret_cast<const float2 *>(a.cut + (int64_t)a.slots * kRows * D) + info.x;
-    } else {
-        if (rows <= a.min_rows) return false;
-        const int64_t keys = min((int64_t)sq.lengths[b] - (q1 - t) + 1, key_capacity(a));
-        const int64_t chunk = keys_of_part(a, sq.lengths[b]);
-        if (keys <= chunk) return false;                        // written directly
-        p.n = (int)((keys + chunk - 1) / chunk);                // <= S
-        p.pitch = (int64_t)sq.n_tok * a.QH;
-        p.lines = reinterpret_cast<const float4 *>(a.part) + row * (D / 4);
-        p.ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.S * p.pitch * D) + row;
-    }
+    p.n = (int)((keys + chunk - 1) / chunk);                    // <= S
+    p.pitch = (int64_t)sq.n_tok * a.QH;
+    p.lines = reinterpret_cast<const float4 *>(a.part) + row * (D / 4);
+    p.ml = reinterpret_cast<const float2 *>(a.part + (int64_t)a.S * p.pitch * D) + row;
     return true;
+}
+// What find_parts leaves to be looked at beside the parts' loads where the
+// few-rows kernel takes all rows: whether row p.row is of a sequence (if it is not,
+// what find_cut has read is of no meaning).  As a step of loads in front of theirs it
+// took 1 us.
+template <bool FEW, class C>
+__device__ __forceinline__ bool of_sequence(const KvArgs<C> &a, const Parts &p) {
+    if (!FEW || a.mixed) return true;
+    const int t = (int)(p.row / a.QH);
+    if (a.seqs.B == 1) return t >= q_at(a.seqs, 0) && t < q_at(a.seqs, 1);
+    const SeqPlace in = find_place(a.seqs, t, [](int q, int) { return (int64_t)q; });
+    return t >= in.q0 && t < in.q1;
 }
 
 // Up to kWaveParts parts: a wave to a row, four rows to a workgroup, no barrier.
@@ -407,6 +424,7 @@ __global__ __launch_bounds__(kThreads) void kv_join_wave_kernel(KvArgs<C> a, int
     load(0, kFirst);
     if (p.n > kFirst) load(kFirst, kWaveParts);
     const float2 v = p.ml[min(lane, p.n - 1) * p.pitch];
+    if (!of_sequence<FEW>(a, p)) return;
     const float m = group_max(lane < p.n ? v.x : -INFINITY, 16);          // -inf in lanes 16 on
     const float f = lane < p.n ? exp2_fast(v.x - (m == -INFINITY ? 0.0f : m)) : 0.0f;
     float l = lane < p.n ? v.y * f : 0.0f;
@@ -470,6 +488,7 @@ __global__ __launch_bounds__(THREADS) void kv_join_kernel(KvArgs<C> a) {
         v[i] = s < parts ? ml[s * pitch] : make_float2(-INFINITY, 0.0f);
         mm = fmaxf(mm, v[i].x);
     }
+    if (!of_sequence<FEW>(a, p)) return;                        // uniform
     mm = group_max(mm, 64);
     if (lane == 0) red[0][wave] = mm;
     __syncthreads();
