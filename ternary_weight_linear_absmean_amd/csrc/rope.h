@@ -100,7 +100,8 @@ __device__ __forceinline__ void load_turned(const E *const *rows, const int *d, 
 // The same for 8 values of several heads at one position: d .. d + 7, in range.
 struct Turn8 {
     float4 c[2], s[2];
-    int other;                    // where the second half of the pairs stands; -1: among the values
+    int other = -1;               // where the second half of the pairs stands; -1: among the values
+    __device__ __forceinline__ Turn8() {}
     __device__ __forceinline__ Turn8(const Rope &rope, int64_t pos, int d) {
         const int half = rope.rot / 2;
         const float *line = rope.cos_sin + pos * rope.rot;
@@ -196,7 +197,8 @@ __device__ __forceinline__ void turn_queries(const E *q, E *out, int QH, int per
     const int per_shift = d_shift - 3, step = 64 >> per_shift;    // lanes of a head, heads at once
     const int d = 8 * (lane & ((1 << per_shift) - 1));
     const bool on = pos >= 0 && d < rope.rot;
-    const Turn8 turn(rope, on ? pos : 0, on ? d : 0);
+    Turn8 turn;
+    if (room > 0) turn = Turn8(rope, on ? pos : 0, on ? d : 0);   // uniform; a cache without room has no cos_sin
     if (h1 - first <= step)
         turn_heads<1>(q, out, row * QH, first + (lane >> per_shift), h1, step, d_shift, d, on, turn);
     else

@@ -502,3 +502,23 @@ def test_captured_append_and_read(gpu, bits):
         s["lengths"] += 7
         eager["lengths"] += 7
     assert int(s["lengths"].max()) > room
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("near", [False, True])
+@pytest.mark.parametrize("n", [1, 700])
+def test_no_room_at_all(gpu, n, near, bits):
+    """A table of no blocks, and so a rotation of no rows (its address is null): queries are
+    copied, nothing is appended, reads and attention give zeros."""
+    bl = gpu
+    s = cuda(make(22, [n], [n], 16, 64, 2, F32, 4, bits, 32, near))
+    s["table"], s["cos_sin"] = s["table"][:, :0].contiguous(), s["cos_sin"][:0].contiguous()
+    was = copied(s)
+    out = append(bl, s, q_out=torch.full_like(s["q"], 77.0))
+    assert torch.equal(out, s["q"])
+    for a, b in zip(s["cache"], was["cache"]):
+        assert torch.equal(a, b)
+    assert append(bl, s, q_out=s["q"]) is s["q"] and torch.equal(s["q"], was["q"])
+    assert all(not x.any() for x in read(bl, s, n))
+    attend = bl.bitlinear_kv8_attention if bits == 8 else bl.bitlinear_kv4_attention
+    assert not attend(s["q"], *meta(s), s["cache"]).any()
