@@ -26,6 +26,8 @@
 #include "kv4_common.h"
 #include "rope.h"
 
+#include <type_traits>
+
 namespace bl {
 namespace {
 
@@ -39,15 +41,10 @@ __device__ __forceinline__ _Float16 f16_below(float x) {
     return (float)h > x ? __builtin_bit_cast(_Float16, down) : h;
 }
 
-template <int D>
 struct Args {
     Kv8Seqs seqs;
     Kv4Cache c;
-    Rope rope;
-    const void *k, *v, *q;
-    void *q_out;
-    int QH;
-    int64_t slots;                // of 16 positions; then the queries' workgroups
+    const void *k, *v;
 };
 
 // Eight values of a row, and with those of the row's other threads its z and s and
@@ -77,16 +74,20 @@ __device__ __forceinline__ uint32_t quantised(const float4 *x, uint32_t *u) {
 }
 
 template <typename E, int D, bool ROPE>
-__global__ __launch_bounds__(2 * D) void kv4_append_kernel(Args<D> a) {
+__global__ __launch_bounds__(2 * D) void kv4_append_kernel(std::conditional_t<ROPE, TurnedArgs, Args> given) {
     constexpr int kPer = D / 8;                           // threads of a token
     __shared__ alignas(16) uint8_t codes[D][kTokens];
+    const auto &a = unpacked<Kv4Cache, D>(given);
     const Kv8Seqs &seqs = a.seqs;
     const Kv4Cache &c = a.c;
-    const int64_t appends = a.slots * c.KVH;
-    if (ROPE && blockIdx.x >= appends) {
-        turn_queries(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(seqs.n_tok, a.QH, D),
-                     D == 64 ? 6 : 7, seqs, (int64_t)seqs.max_blocks << c.t_shift, a.rope, blockIdx.x - appends);
-        return;
+    if constexpr (ROPE) {
+        const int64_t appends = ((seqs.n_tok >> 4) + 2 * (int64_t)seqs.B) * c.KVH;
+        if (blockIdx.x >= appends) {
+            turn_queries<2 * D>(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH,
+                                rope_heads(seqs.n_tok, a.QH, D), D == 64 ? 6 : 7, seqs,
+                                (int64_t)seqs.max_blocks << c.t_shift, a.rope, blockIdx.x - appends);
+            return;
+        }
     }
     const uint32_t slot = blockIdx.x / (uint32_t)c.KVH;
     const int h = (int)(blockIdx.x - slot * c.KVH);
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(2 * D) void kv4_append_kernel(Args<D> a) {
     x[1] = load_row4(k + 8 * td + 4);
     w[0] = load_row4(v + 8 * td);
     w[1] = load_row4(v + 8 * td + 4);
-    if (ROPE) {
+    if constexpr (ROPE) {
         const bool on = 8 * td < a.rope.rot;
         const Turn8 turn(a.rope, pos, on ? 8 * td : 0);
         turn.load_others(k, y);
@@ -160,17 +161,18 @@ __global__ __launch_bounds__(2 * D) void kv4_append_kernel(Args<D> a) {
 template <typename E, int D>
 hipError_t append(const void *k, const void *v, const void *q, void *q_out, int QH, const Kv8Seqs &seqs,
                   const Kv4Cache &c, const Rope *rope, hipStream_t s) {
-    Args<D> a = {seqs, c, {}, k, v, q, q_out, QH, (seqs.n_tok >> 4) + 2 * (int64_t)seqs.B};
-    int64_t groups = a.slots * c.KVH;
-    if (rope) {
-        a.rope = *rope;
-        groups += rope_groups(seqs.n_tok, QH, D, 2 * D);
-    }
+    // of 16 positions; then the queries' workgroups
+    int64_t groups = ((seqs.n_tok >> 4) + 2 * (int64_t)seqs.B) * c.KVH;
+    if (rope) groups += rope_groups(seqs.n_tok, QH, D, 2 * D);
     if (groups * 2 * D >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-    if (rope)
+    if (rope) {
+        const TurnedArgs a = packed(Turned<Kv4Cache>{seqs, c, *rope, k, v, q, q_out, QH});
         hipLaunchKernelGGL((kv4_append_kernel<E, D, true>), dim3((unsigned)groups), dim3(2 * D), 0, s, a);
-    else
+    } else {
+        const Args a = {seqs, c, k, v};
+        static_assert(sizeof a <= kFewArgs, "a launch's arguments");
         hipLaunchKernelGGL((kv4_append_kernel<E, D, false>), dim3((unsigned)groups), dim3(2 * D), 0, s, a);
+    }
     return hipGetLastError();
 }
 

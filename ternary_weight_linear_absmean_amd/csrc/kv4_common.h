@@ -15,6 +15,15 @@ struct Kv4Cache {
     int t_shift;                  // log2(T)
 };
 
+inline void *scales1(const Kv4Cache &c) { return c.zk; }
+inline void *scales2(const Kv4Cache &c) { return c.zv; }
+template <>
+__device__ __forceinline__ Kv4Cache cache_of<Kv4Cache>(void *K, void *V, void *s1, void *s2, int n_blocks, int KVH,
+                                                     int t_shift, int D) {
+    return {static_cast<uint8_t *>(K), static_cast<uint8_t *>(V), static_cast<uint32_t *>(s1), static_cast<uint32_t *>(s2), n_blocks, KVH,
+            1 << t_shift, D, t_shift};
+}
+
 inline Kv4Cache kv4_device(const bl_kv4 &c) {
     Kv4Cache d = {c.K, c.V, reinterpret_cast<uint32_t *>(c.zk), reinterpret_cast<uint32_t *>(c.zv),
                   (int)c.n_blocks, (int)c.KVH, (int)c.T, (int)c.D, 0};

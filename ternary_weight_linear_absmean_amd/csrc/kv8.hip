@@ -222,22 +222,14 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(const E *__restric
 
 // The same with the keys turned by their positions, and in the workgroups behind
 // the queries.
-struct RopeArgs {
-    Kv8Seqs seqs;
-    Kv8Cache c;
-    Rope rope;
-    const void *k, *v, *q;
-    void *q_out;
-    int QH;
-    int64_t slots;
-};
-template <typename E, int NC>
-__global__ __launch_bounds__(kThreads) void kv8_append_rope_kernel(RopeArgs a) {
+template <typename E, int NC, int D>
+__global__ __launch_bounds__(kThreads) void kv8_append_rope_kernel(TurnedArgs given) {
     __shared__ AppendLds<E, NC> lds;
-    const int64_t appends = a.slots * a.c.KVH * 2;
+    const Turned<Kv8Cache> a = unpacked<Kv8Cache, D>(given);
+    const int64_t appends = (((int64_t)a.seqs.n_tok >> a.c.t_shift) + 2 * (int64_t)a.seqs.B) * a.c.KVH * 2;
     if (blockIdx.x >= appends) {
-        turn_queries(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(a.seqs.n_tok, a.QH, a.c.D),
-                     a.c.D == 64 ? 6 : 7, a.seqs, (int64_t)a.seqs.max_blocks << a.c.t_shift, a.rope,
+        turn_queries<kThreads>(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(a.seqs.n_tok, a.QH, D), D == 64 ? 6 : 7, a.seqs,
+                     (int64_t)a.seqs.max_blocks << a.c.t_shift, a.rope,
                      blockIdx.x - appends);
         return;
     }
@@ -260,15 +252,15 @@ hipError_t append(const E *k, const E *v, const Kv8Seqs &seqs, const Kv8Cache &c
     return hipGetLastError();
 }
 
-template <typename E>
-hipError_t append_rope(const RopeArgs &a, int64_t groups, hipStream_t s) {
+template <typename E, int D>
+hipError_t append_rope(const TurnedArgs &a, int64_t groups, hipStream_t s) {
     const dim3 grid((unsigned)groups), block(kThreads);
-    switch (a.c.T * a.c.D / (4 * kThreads)) {
-    case 1: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 2>), grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 4>), grid, block, 0, s, a); break;
-    case 8: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 8>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 16>), grid, block, 0, s, a);
+    constexpr int kLeast = D / 64;                     // pieces of T = 16
+    switch (a.t_shift) {
+    case 4: hipLaunchKernelGGL((kv8_append_rope_kernel<E, kLeast, D>), grid, block, 0, s, a); break;
+    case 5: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 2 * kLeast, D>), grid, block, 0, s, a); break;
+    case 6: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 4 * kLeast, D>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((kv8_append_rope_kernel<E, 8 * kLeast, D>), grid, block, 0, s, a);
     }
     return hipGetLastError();
 }
@@ -286,10 +278,12 @@ hipError_t launch_kv8_append(const void *k, const void *v, int dtype, const Kv8S
 hipError_t launch_kv8_append_rope(const void *k, const void *v, const void *q, void *q_out, int dtype, int QH,
                                   const Kv8Seqs &seqs, const bl_kv8 &cache, const bl_rope &rope, hipStream_t s) {
     const Kv8Cache c = kv8_device(cache);
-    const RopeArgs a = {seqs, c, rope_device(rope), k, v, q, q_out, QH, (seqs.n_tok >> c.t_shift) + 2 * (int64_t)seqs.B};
-    const int64_t groups = a.slots * c.KVH * 2 + rope_groups(seqs.n_tok, QH, c.D, kThreads);
+    const int64_t groups = (((int64_t)seqs.n_tok >> c.t_shift) + 2 * (int64_t)seqs.B) * c.KVH * 2 +
+                           rope_groups(seqs.n_tok, QH, c.D, kThreads);
     if (groups * kThreads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-    return dtype ? append_rope<uint16_t>(a, groups, s) : append_rope<float>(a, groups, s);
+    const TurnedArgs a = packed(Turned<Kv8Cache>{seqs, c, rope_device(rope), k, v, q, q_out, QH});
+    if (c.D == 64) return dtype ? append_rope<uint16_t, 64>(a, groups, s) : append_rope<float, 64>(a, groups, s);
+    return dtype ? append_rope<uint16_t, 128>(a, groups, s) : append_rope<float, 128>(a, groups, s);
 }
 
 }  // namespace bl

@@ -7,6 +7,14 @@
 
 namespace bl {
 
+// Bytes of a kernel's arguments up to which a launch takes the host 2.8 us; with a
+// few more it is 3.3 to 4.0 (as the hidden ones that blockDim and gridDim bring with them).
+constexpr size_t kFewArgs = 112;
+
+// A cache's device view of its parts (kv8_common.h, kv4_common.h).
+template <class C>
+__device__ __forceinline__ C cache_of(void *K, void *V, void *s1, void *s2, int n_blocks, int KVH, int t_shift, int D);
+
 // q_start[b] taken within the call's rows.
 __device__ __forceinline__ int q_at(const Kv8Seqs &s, int b) {
     return min(max(s.q_start[b], 0), s.n_tok);

@@ -26,7 +26,6 @@ struct Args {
     Kv8Seqs seqs;
     C c;
     void *k, *v;
-    int64_t slots;
 };
 
 template <typename E, int D, int HEADS, typename C>
@@ -138,9 +137,11 @@ constexpr int64_t kAtOnce = 4 * 256 * 2048;
 
 template <typename E, int D, typename C>
 hipError_t read(const Kv8Seqs &seqs, const C &c, void *k, void *v, hipStream_t s) {
-    const Args<C> a = {seqs, c, k, v, (seqs.n_tok >> 4) + 2 * (int64_t)seqs.B};
-    const bool four = a.slots * c.KVH * 2 * D > kAtOnce;
-    const int64_t groups = a.slots * (four ? (c.KVH + 3) / 4 : c.KVH);
+    const Args<C> a = {seqs, c, k, v};
+    static_assert(sizeof a <= kFewArgs, "a launch's arguments");
+    const int64_t slots = (seqs.n_tok >> 4) + 2 * (int64_t)seqs.B;
+    const bool four = slots * c.KVH * 2 * D > kAtOnce;
+    const int64_t groups = slots * (four ? (c.KVH + 3) / 4 : c.KVH);
     if (groups * 2 * D >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     if (four)
         hipLaunchKernelGGL((kv_read_kernel<E, D, 4, C>), dim3((unsigned)groups), dim3(2 * D), 0, s, a);

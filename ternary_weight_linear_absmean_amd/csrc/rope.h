@@ -28,6 +28,73 @@ inline Rope rope_device(const bl_rope &r) {
     return {r.cos_sin, (int)r.rot, r.interleaved};
 }
 
+// What an append with a rotation takes, on a cache C.
+template <class C>
+struct Turned {
+    Kv8Seqs seqs;
+    C c;
+    Rope rope;
+    const void *k, *v, *q;
+    void *q_out;
+    int QH;                       // 0: no queries
+};
+// The same in kFewArgs bytes: what the limits leave free in the counts, and the low
+// four bits of the pointers to what is 16-byte aligned, hold the smaller numbers.
+struct TurnedArgs {
+    const int32_t *q_start, *lengths, *table;
+    void *s1, *s2;
+    uintptr_t K, V, cos_sin;      // with 12 bits of KVH
+    uintptr_t k, v, q, q_out;     // with QH
+    int32_t n_tok, n_blocks;
+    uint32_t max_blocks : 27, t_shift : 3, neighbours : 1;       // max_blocks T < 2^31, T >= 16
+    uint32_t B : 24, rot16 : 4, kvh_top : 4;
+};
+static_assert(sizeof(TurnedArgs) <= kFewArgs, "a launch's arguments");
+
+template <class C>
+inline TurnedArgs packed(const Turned<C> &t) {
+    auto with = [](const void *p, int bits) { return reinterpret_cast<uintptr_t>(p) | (uintptr_t)(bits & 15); };
+    TurnedArgs a = {t.seqs.q_start, t.seqs.lengths, t.seqs.table, scales1(t.c), scales2(t.c)};
+    const int KVH = t.c.KVH, QH = t.QH;
+    a.K = with(t.c.K, KVH);
+    a.V = with(t.c.V, KVH >> 4);
+    a.cos_sin = with(t.rope.cos_sin, KVH >> 8);
+    a.kvh_top = (uint32_t)KVH >> 12;
+    a.k = with(t.k, QH);
+    a.v = with(t.v, QH >> 4);
+    a.q = with(QH > 0 ? t.q : nullptr, QH >> 8);
+    a.q_out = with(QH > 0 ? t.q_out : nullptr, QH >> 12);
+    a.n_tok = t.seqs.n_tok;
+    a.n_blocks = t.c.n_blocks;
+    a.max_blocks = (uint32_t)t.seqs.max_blocks;
+    a.t_shift = (uint32_t)t.c.t_shift;
+    a.neighbours = t.rope.neighbours != 0;
+    a.B = (uint32_t)t.seqs.B;
+    a.rot16 = (uint32_t)t.rope.rot / 16;
+    return a;
+}
+// On the device; an argument that is not packed is as it should be.
+template <class C, int D>
+__device__ __forceinline__ Turned<C> unpacked(const TurnedArgs &a) {
+    // told that it is global memory, as the compiler infers of an argument that is a pointer
+    typedef __attribute__((address_space(1))) void global;
+    auto address = [](uintptr_t p) { return (void *)(global *)(p & ~(uintptr_t)15); };
+    auto bits = [](uintptr_t p) { return (int)(p & 15); };
+    Turned<C> t;
+    t.seqs = {a.q_start, a.lengths, a.table, a.n_tok, (int)a.B, (int)a.max_blocks};
+    const int KVH = bits(a.K) | bits(a.V) << 4 | bits(a.cos_sin) << 8 | (int)a.kvh_top << 12;
+    t.c = cache_of<C>(address(a.K), address(a.V), a.s1, a.s2, a.n_blocks, KVH, (int)a.t_shift, D);
+    t.rope = {static_cast<const float *>(address(a.cos_sin)), (int)a.rot16 * 16, (int)a.neighbours};
+    t.k = address(a.k);
+    t.v = address(a.v);
+    t.q = address(a.q);
+    t.q_out = address(a.q_out);
+    t.QH = bits(a.k) | bits(a.v) << 4 | bits(a.q) << 8 | bits(a.q_out) << 12;
+    return t;
+}
+template <class C, int D, class A>
+__device__ __forceinline__ const A &unpacked(const A &a) { return a; }
+
 // Rows that this kernel does not read again: past the caches.
 __device__ __forceinline__ void store_row4(float *p, float4 v) {
     __builtin_nontemporal_store(float4v{v.x, v.y, v.z, v.w}, reinterpret_cast<float4v *>(p));
@@ -181,11 +248,11 @@ __device__ __forceinline__ void turn_heads(const E *q, E *out, int64_t row0, int
         }
     }
 }
-template <typename E>
+template <int THREADS, typename E>
 __device__ __forceinline__ void turn_queries(const E *q, E *out, int QH, int per, int d_shift, const Kv8Seqs &seqs,
                                              int64_t room, const Rope &rope, int64_t group) {
     const int lane = threadIdx.x & 63;
-    const int64_t unit = group * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t unit = group * (THREADS >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int chunks = (QH + per - 1) / per;
     const int64_t row = unit / chunks;
     const int first = (int)(unit - row * chunks) * per, h1 = min(first + per, QH);
