@@ -522,3 +522,40 @@ def test_no_room_at_all(gpu, n, near, bits):
     assert all(not x.any() for x in read(bl, s, n))
     attend = bl.bitlinear_kv8_attention if bits == 8 else bl.bitlinear_kv4_attention
     assert not attend(s["q"], *meta(s), s["cache"]).any()
+
+
+def test_fresh_tensors_under_torch_modes(gpu):
+    """Tensors that a call makes: filled where torch is asked to fill them, seen by a
+    dispatch mode, of another device's or inference mode's kind like torch.empty's."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Seen(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            seen.append(str(func))
+            return func(*args, **(kwargs or {}))
+
+    bl = gpu
+    s = cuda(make(23, [2], [40], 16, 64, 2, F32, 4, rot=32, behind=1))
+    plain = append(bl, s)
+    was, fill = torch.are_deterministic_algorithms_enabled(), torch.utils.deterministic.fill_uninitialized_memory
+    try:
+        torch.use_deterministic_algorithms(True)
+        torch.utils.deterministic.fill_uninitialized_memory = True
+        q = append(bl, s)
+        k, v = read(bl, s, 3)
+        out = bl.bitlinear_kv4_attention(s["q"], *meta(s), s["cache"])
+    finally:
+        torch.use_deterministic_algorithms(was)
+        torch.utils.deterministic.fill_uninitialized_memory = fill
+    assert torch.equal(q[:2], plain[:2]) and all(bool(x[2:].isnan().all()) for x in (q, k, v, out))
+    assert not any(bool(x[:2].isnan().any()) for x in (q, k, v, out))
+    seen = []
+    with Seen():
+        assert torch.equal(append(bl, s)[:2], plain[:2])
+    assert any("empty" in x for x in seen)
+    with torch.inference_mode():
+        q = append(bl, s)
+        assert q.is_inference() and torch.equal(q[:2], plain[:2])
+    assert not append(bl, s).is_inference()
+    g = s["q"].clone().requires_grad_()
+    assert not append(bl, dict(s, q=g)).requires_grad
