@@ -218,7 +218,7 @@ def load():
     lib.bl_abi_version.restype = ctypes.c_int
     lib.bl_abi_version.argtypes = []
     calls = importlib.import_module("._calls", __package__)
-    calls.bind(*(ctypes.cast(getattr(lib, name), _p).value for name in _ENTRIES))
+    calls.bind(_check, *(ctypes.cast(getattr(lib, name), _p).value for name in _ENTRIES))
     _lib, _calls = lib, calls
     return lib
 
@@ -226,13 +226,6 @@ def load():
 def _check(call, status):
     if status != 0:
         raise BitLinearError(call, status, load().bl_last_error().decode())
-
-
-def _made(call, r):
-    """Whether _calls made a call; raises for a launch that failed."""
-    if type(r) is int:
-        _check(call, r)
-    return r is not NotImplemented
 
 
 def _stream(stream):
@@ -712,7 +705,7 @@ def bitlinear_kv8_append(k, v, q_start, lengths, table, cache, stream=None):
     (Kv8Cache, updated in place).  int32 on the GPU: q_start [B + 1], lengths
     [B] (with the new tokens), table [B, max_blocks]."""
     if stream is None and _calls is not None:
-        if _made("bitlinear_kv8_append", _calls.append(8, k, v, q_start, lengths, table, cache, None, None, None)):
+        if _calls.append(8, k, v, q_start, lengths, table, cache, None, None, None) is not NotImplemented:
             return
     dev, dt, kp, shape = _rows(k, 3, "k")
     c = _kv8(cache, dev)
@@ -769,7 +762,7 @@ def bitlinear_kv8_append_rope(k, v, q_start, lengths, table, cache, rope, q=None
         raise ValueError("bitlinear_kv8_append_rope without rope")
     if stream is None and _calls is not None:
         r = _calls.append(8, k, v, q_start, lengths, table, cache, rope, q, q_out)
-        if _made("bitlinear_kv8_append_rope", r):
+        if r is not NotImplemented:
             return r
     return _append_turned("bitlinear_kv8_append_rope", _kv8, k, v, q_start, lengths, table, cache, rope, q,
                           q_out, stream)
@@ -781,18 +774,13 @@ def bitlinear_kv4_append(k, v, q_start, lengths, table, cache, rope=None, q=None
     by bitlinear_kv8_append_rope (which see for q and what is returned)."""
     if stream is None and _calls is not None:
         r = _calls.append(4, k, v, q_start, lengths, table, cache, rope, q, q_out)
-        if _made("bitlinear_kv4_append", r):
+        if r is not NotImplemented:
             return r
     return _append_turned("bitlinear_kv4_append", _kv4, k, v, q_start, lengths, table, cache, rope, q, q_out,
                           stream)
 
 
-def _read(call, bits, q_start, lengths, table, cache, n_tok, dtype, k, v, stream):
-    if stream is None and _calls is not None and dtype in _DTYPES:
-        r = _calls.read(bits, q_start, lengths, table, cache, n_tok, dtype is torch.bfloat16, k, v)
-        if _made(call, r):
-            return r
-    device_cache = _kv8 if bits == 8 else _kv4
+def _read(call, device_cache, q_start, lengths, table, cache, n_tok, dtype, k, v, stream):
     K = cache[0]
     if not isinstance(K, torch.Tensor) or not K.is_cuda:
         raise TypeError("the cache's K must be a CUDA (HIP) tensor")
@@ -823,12 +811,20 @@ def bitlinear_kv8_read(q_start, lengths, table, cache, n_tok, dtype=torch.float3
     """The cached tokens of rows 0 .. n_tok - 1 of a call as values, k and v
     [n_tok, KVH, D] of dtype (fp32 or bf16): the n_b rows of sequence b are its
     last n_b tokens.  q_start, lengths, table as for bitlinear_kv8_append."""
-    return _read("bitlinear_kv8_read", 8, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
+    if stream is None and _calls is not None:
+        r = _calls.read(8, q_start, lengths, table, cache, n_tok, dtype, k, v)
+        if r is not NotImplemented:
+            return r
+    return _read("bitlinear_kv8_read", _kv8, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
 
 
 def bitlinear_kv4_read(q_start, lengths, table, cache, n_tok, dtype=torch.float32, k=None, v=None, stream=None):
     """bitlinear_kv8_read of a 4-bit cache."""
-    return _read("bitlinear_kv4_read", 4, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
+    if stream is None and _calls is not None:
+        r = _calls.read(4, q_start, lengths, table, cache, n_tok, dtype, k, v)
+        if r is not NotImplemented:
+            return r
+    return _read("bitlinear_kv4_read", _kv4, q_start, lengths, table, cache, n_tok, dtype, k, v, stream)
 
 
 def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=None, ws=None,
@@ -839,7 +835,7 @@ def bitlinear_kv8_attention(q, q_start, lengths, table, cache, scale=None, out=N
     out may not overlap q."""
     if stream is None and _calls is not None:
         r = _calls.attention(8, q, q_start, lengths, table, cache, scale, out, ws)
-        if _made("bitlinear_kv8_attention", r):
+        if r is not NotImplemented:
             return r
     dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
     c = _kv8(cache, dev)
@@ -875,7 +871,7 @@ def bitlinear_kv4_attention(q, q_start, lengths, table, cache, scale=None, out=N
     """bitlinear_kv8_attention over a 4-bit cache (Kv4Cache)."""
     if stream is None and _calls is not None:
         r = _calls.attention(4, q, q_start, lengths, table, cache, scale, out, ws)
-        if _made("bitlinear_kv4_attention", r):
+        if r is not NotImplemented:
             return r
     dev, dt, qp, (n, QH, D) = _rows(q, 3, "q")
     c = _kv4(cache, dev)

@@ -9,8 +9,8 @@
 // and return NotImplemented, with nothing done, for anything else and for whatever the library
 // refuses: the Python of _native.py then makes the call, or says what is wrong with it.
 // A launch that the runtime reports as failed may be under way all the same (the
-// runtime gives an earlier call's error too), so that status is returned as a number and the
-// call is not made again: queries rotated in place would turn twice.
+// runtime gives an earlier call's error too), so that status is raised here and the
+// call not made again: queries rotated in place would turn twice.
 //
 // The library's entry points come in by address (bind), so this module is not
 // linked against it.
@@ -23,6 +23,7 @@
 #include <c10/hip/HIPFunctions.h>
 #include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "bitlinear.h"
@@ -126,7 +127,14 @@ at::Tensor fresh(at::IntArrayRef shape, const at::Tensor &like, at::ScalarType t
 }
 
 PyObject *left() { Py_RETURN_NOTIMPLEMENTED; }
-PyObject *failed(bl_status st) { return st == BL_ERR_HIP ? PyLong_FromLong(st) : left(); }
+// The binding's own way of raising, raises(call, status).
+PyObject *raises = nullptr;
+PyObject *failed(const char *call, bl_status st) {
+    if (st != BL_ERR_HIP) return left();
+    PyObject *none = PyObject_CallFunction(raises, "si", call, (int)st);
+    Py_XDECREF(none);
+    return none ? left() : nullptr;
+}
 
 template <typename F>
 bl_status without_gil(F f) {
@@ -204,14 +212,17 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
             return lib.kv8_append_rope(kp, vp, qp, op, dt, rows, QH, s.q_start, s.lengths, s.table, s.B, s.max_blocks,
                                        &c.c8, &rope, stream);
         });
-        if (st != BL_OK) return failed(st);
+        if (st != BL_OK) return failed(bits == 4      ? "bitlinear_kv4_append"
+                                       : is_none(a[7]) ? "bitlinear_kv8_append"
+                                                       : "bitlinear_kv8_append_rope",
+                                       st);
         if (made.defined()) return THPVariable_Wrap(made);
         Py_INCREF(a[9]);
         return a[9];
     });
 }
 
-// read(bits, q_start, lengths, table, cache, n_tok, bf16, k, v)
+// read(bits, q_start, lengths, table, cache, n_tok, dtype, k, v)
 PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 9) return left();
     return guarded([&]() -> PyObject * {
@@ -224,8 +235,9 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!PyLong_CheckExact(a[5])) throw Unusual();
         const int64_t rows = PyLong_AsLongLong(a[5]);
         if (rows < 0) throw Unusual();
-        const bool bf16 = a[6] == Py_True;
-        const at::ScalarType type = bf16 ? at::kBFloat16 : at::kFloat;
+        if (!THPDtype_Check(a[6])) throw Unusual();
+        const at::ScalarType type = reinterpret_cast<THPDtype *>(a[6])->scalar_type;
+        const bl_dtype dt = rows_type(type);
         at::Tensor out[2];
         void *p[2];
         for (int i = 0; i < 2; ++i) {
@@ -233,14 +245,13 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n) {
             p[i] = at_address(out[i], gpu, type, {rows, c.KVH, c.D});
         }
         void *stream = stream_of(gpu);
-        const bl_dtype dt = bf16 ? BL_BF16 : BL_F32;
         const bl_status st = without_gil([&] {
             return bits == 4 ? lib.kv4_read(&c.c4, s.q_start, s.lengths, s.table, s.B, s.max_blocks, rows, p[0], p[1], dt,
                                             stream)
                              : lib.kv8_read(&c.c8, s.q_start, s.lengths, s.table, s.B, s.max_blocks, rows, p[0], p[1], dt,
                                             stream);
         });
-        if (st != BL_OK) return failed(st);
+        if (st != BL_OK) return failed(bits == 4 ? "bitlinear_kv4_read" : "bitlinear_kv8_read", st);
         PyObject *both = PyTuple_New(2);
         if (!both) return nullptr;
         for (int i = 0; i < 2; ++i) {
@@ -303,22 +314,22 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
                              : lib.kv8_attention(qp, dt, rows, QH, s.q_start, s.lengths, s.table, s.B, s.max_blocks, &c.c8,
                                                  scale, op, wp, bytes, stream);
         });
-        if (st != BL_OK) return failed(st);
+        if (st != BL_OK) return failed(bits == 4 ? "bitlinear_kv4_attention" : "bitlinear_kv8_attention", st);
         if (made.defined()) return THPVariable_Wrap(made);
         Py_INCREF(a[7]);
         return a[7];
     });
 }
 
-// bind(addresses of the entry points in the order of Entries)
+// bind(raises, addresses of the entry points in the order of Entries)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *p[sizeof(Entries) / sizeof(void *)];
-    if (n != (Py_ssize_t)(sizeof p / sizeof *p)) {
-        PyErr_SetString(PyExc_TypeError, "bind: wrong number of addresses");
+    if (n != 1 + (Py_ssize_t)(sizeof p / sizeof *p)) {
+        PyErr_SetString(PyExc_TypeError, "bind: wrong number of arguments");
         return nullptr;
     }
-    for (Py_ssize_t i = 0; i < n; ++i) {
-        p[i] = PyLong_AsVoidPtr(a[i]);
+    for (Py_ssize_t i = 0; i < n - 1; ++i) {
+        p[i] = PyLong_AsVoidPtr(a[1 + i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null address");
             return nullptr;
@@ -326,6 +337,8 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     static_assert(sizeof p == sizeof lib, "entry points are addresses");
     memcpy(&lib, p, sizeof lib);
+    Py_INCREF(a[0]);
+    Py_XSETREF(raises, a[0]);
     Py_RETURN_NONE;
 }
 

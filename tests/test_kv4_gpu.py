@@ -426,7 +426,7 @@ def test_calls_from_python_and_from_c(gpu):
         # the short way took them
         rope = bl.Rope(one["cos_sin"])
         assert calls.append(bits, one["k"], one["v"], *meta(one), c, rope, one["q"], None) is not NotImplemented
-        assert calls.read(bits, *meta(one), tuple(c), 43, True, None, None) is not NotImplemented
+        assert calls.read(bits, *meta(one), tuple(c), 43, BF16, None, None) is not NotImplemented
         assert calls.attention(bits, q, *meta(one), c, None, None, None) is not NotImplemented
         # and leaves alone what is not as it should be
         for bad in (q.half(), q[:, :, :32], q.transpose(0, 1), q.cpu(), None, 3):
@@ -435,7 +435,9 @@ def test_calls_from_python_and_from_c(gpu):
         assert calls.attention(bits, q, *meta(one), c, "x", None, None) is NotImplemented
         assert calls.attention(bits, q, *meta(one), c, None, q[1:], None) is NotImplemented
         assert calls.attention(12 - bits, q, *meta(one), c, None, None, None) is NotImplemented
-        assert calls.read(bits, *meta(one), c, -1, True, None, None) is NotImplemented
+        assert calls.read(bits, *meta(one), c, -1, BF16, None, None) is NotImplemented
+        assert calls.read(bits, *meta(one), c, 43, torch.float16, None, None) is NotImplemented
+        assert calls.read(bits, *meta(one), c, 43, None, None, None) is NotImplemented
         assert calls.append(bits, one["k"], one["v"], *meta(one), c, rope, None, q) is NotImplemented
         assert calls.append(bits, one["k"], one["v"]) is NotImplemented
 
@@ -449,7 +451,7 @@ def test_a_failed_launch_is_not_made_again(gpu):
     failing = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: calls.append(1) or 7)
     address = ctypes.cast(failing, ctypes.c_void_p).value
     try:
-        native._calls.bind(*([address] * 7 + entries[7:]))
+        native._calls.bind(native._check, *([address] * 7 + entries[7:]))
         for bits in (4, 8):
             s = cuda(make(20, [2, 1], [40, 30], 16, 64, 2, F32, 4, bits, 32))
             was = copied(s)
@@ -467,7 +469,7 @@ def test_a_failed_launch_is_not_made_again(gpu):
             for a, b in zip(s["cache"], was["cache"]):
                 assert torch.equal(a, b)
     finally:
-        native._calls.bind(*entries)
+        native._calls.bind(native._check, *entries)
 
 
 @pytest.mark.parametrize("bits", [4, 8])
