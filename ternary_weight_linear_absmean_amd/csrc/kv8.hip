@@ -228,9 +228,9 @@ __global__ __launch_bounds__(kThreads) void kv8_append_rope_kernel(TurnedArgs gi
     const Turned<Kv8Cache> a = unpacked<Kv8Cache, D>(given);
     const int64_t appends = (((int64_t)a.seqs.n_tok >> a.c.t_shift) + 2 * (int64_t)a.seqs.B) * a.c.KVH * 2;
     if (blockIdx.x >= appends) {
-        turn_queries<kThreads>(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH, rope_heads(a.seqs.n_tok, a.QH, D), D == 64 ? 6 : 7, a.seqs,
-                     (int64_t)a.seqs.max_blocks << a.c.t_shift, a.rope,
-                     blockIdx.x - appends);
+        turn_queries<kThreads>(static_cast<const E *>(a.q), static_cast<E *>(a.q_out), a.QH,
+                               rope_heads(a.seqs.n_tok, a.QH, D), D == 64 ? 6 : 7, a.seqs,
+                               (int64_t)a.seqs.max_blocks << a.c.t_shift, a.rope, blockIdx.x - appends);
         return;
     }
     const uint32_t pair = blockIdx.x / 2, slot = pair / (uint32_t)a.c.KVH;
