@@ -801,9 +801,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_mixed_kernel(Args a) {
 //        17280  8 x 96 on 4000       69.2  88.3
 //        20320  128 on 32000         84.4   102
 //        21760  4 x 128 on 8000      96.5  84.3
-//        30720  64 x 96 on 500        112  70.3
+//       30.7 k  64 x 96 on 500        112  70.3
 //        46080  2048 on 4096          138   124
-// (8 heads of 2, D = 64: 30720 58 and 42, 46080 84 and 80, but 64 x 64 on 4000 178
+// (8 heads of 2, D = 64: 30.7 k 58 and 42, 46080 84 and 80, but 64 x 64 on 4000 178
 // and 209.)  A workgroup of many rows for half the CUs only: 1000 rows on 1777
 // keys 57.8 us, for two a CU 46.7.  One sequence of more than 32 units for 256
 // pieces: 128 rows on 32000 keys 133 us, for 512 84.
