@@ -561,3 +561,10 @@ def test_fresh_tensors_under_torch_modes(gpu):
     assert not append(bl, s).is_inference()
     g = s["q"].clone().requires_grad_()
     assert not append(bl, dict(s, q=g)).requires_grad
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("KVH,G", [(17, 1), (1, 257), (300, 3), (4111, 3), (5, 1009), (65535, 1)])
+def test_many_heads(gpu, KVH, G, bits):
+    """Numbers of heads of every size that a call takes, key heads and query heads apart."""
+    check_append(gpu, make(24, [1, 1], [1, 17], 16, 64, KVH, F32, G, bits, 16, True))
