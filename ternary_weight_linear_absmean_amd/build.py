@@ -65,7 +65,10 @@ def _build_calls(verbose):
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     rocm = os.path.dirname(os.path.dirname(HIPCC))
     tmp = CALLS + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    # NDEBUG: without it pybind11's headers bring a thread-local counter.  A library with
+    # thread-local storage that is loaded into a running program and never touches it makes
+    # every other library's access to its own take the slow way (glibc 2.35): 1 us a launch.
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DNDEBUG",
            "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(torch_dir, "include"),
            "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),

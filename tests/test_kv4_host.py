@@ -215,3 +215,17 @@ def test_turned_queries_apart_from_the_new_rows(lib):
             for q in (far, B16 + by):                       # from elsewhere and in place
                 assert each(lib, dt=dt, k=B16, v=2 * far, q=q, o=B16 + by)[:2] == (ALIGN,) * 2
                 assert each(lib, dt=dt, k=2 * far, v=B16, q=q, o=B16 + by)[:2] == (ALIGN,) * 2
+
+
+def test_binding_has_no_thread_local_storage():
+    """_calls.so has no PT_TLS (7) among its ELF program headers (see build.py)."""
+    import struct
+
+    from ternary_weight_linear_absmean_amd import build
+
+    with open(build.CALLS, "rb") as f:
+        elf = f.read()
+    assert elf[:5] == b"\x7fELF\x02"
+    offset, = struct.unpack_from("<Q", elf, 32)
+    size, count = struct.unpack_from("<HH", elf, 54)
+    assert 7 not in [struct.unpack_from("<I", elf, offset + i * size)[0] for i in range(count)]
