@@ -435,7 +435,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 // are on their way.  What goes to LDS are the keys and values themselves, fp16(z
 // + s u), an error of 2^-12 beside the result's 2^-9: no z or s is left in the
 // loop over scores.  (fp32 rows would need the codes and each token's z and s: 283 us
-// for 2048 rows on 4096 keys, 5 heads of 4 and D = 128, where 16-row units take 198.)
+// for 2048 rows on 4096 keys, 5 heads of 4 and D = 128, where 16-row units take 181.)
 //
 // Bound by vector and matrix instructions that hardly overlap: 2 x 2048 ragged rows
 // on 4096 keys, 5 heads of 4, 92 GFLOP: 133 us, 690 TFLOP/s (a large fp16 product
