@@ -807,7 +807,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_mixed_kernel(Args a) {
 // and 209.)  A workgroup of many rows for half the CUs only: 1000 rows on 1777
 // keys 57.8 us, for two a CU 46.7.  One sequence of more than 32 units for 256
 // pieces: 128 rows on 32000 keys 133 us, for 512 84.
-constexpr Rules kRules[2] = {{1e30, kCUs, 32}, {21000, 2 * kCUs, 32}};
+constexpr Rules kRules[2] = {{1e30, kCUs, 32, 8}, {21000, 2 * kCUs, 32, 8}};
 
 template <bool BF16, int D>
 Kernels<Kv4Cache> kernels() {

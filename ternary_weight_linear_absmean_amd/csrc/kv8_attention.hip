@@ -688,7 +688,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_mixed_kernel(Args a) {
     }
 }
 
-constexpr Rules kRules = {kManyWork, kCUs, INT32_MAX};
+// A single sequence is always cut where that may save steps: one token on 4000 keys in a
+// captured call of 128 rows takes 9.3 us, uncut 26.5 (128 tokens 32.2, without a join 29.8).
+constexpr Rules kRules = {kManyWork, kCUs, INT32_MAX, 0};
 
 template <bool BF16, int D>
 Kernels<Kv8Cache> kernels() {

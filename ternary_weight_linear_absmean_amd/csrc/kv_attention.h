@@ -600,6 +600,7 @@ struct Rules {
     double many_work;         // above which rows go to the kernel for many
     int many_groups;          // workgroups of that kernel to aim at with parts of the keys
     int one_seq_units;        // units of a single sequence above which pieces are for kGroups workgroups
+    int lone_steps;           // steps up to which a single sequence that can fill the GPU is not cut
 };
 Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t KVH, int64_t T, int64_t D,
               const Rules &rules) {
@@ -631,9 +632,13 @@ Plan plan_for(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks, int64_t 
         while (B <= kLineSeqs && line() >= (int64_t)1 << 30) ++p.step_shift;
         p.cuts = steps > 3 && B <= kLineSeqs &&
                  ((3 * KVH * seqs < 2 * p.most && (!p.many || p.S > 1)) || steps >= kLongSteps);
-        // units of one sequence for half the workgroups at least: steps_of_piece cuts none
-        // (1000 fp32 rows on 1777 4-bit keys 35.8 us with a join that finds nothing)
-        if (B == 1 && 2 * ((n_tok * G + kRows - 1) / kRows) * KVH >= p.most) p.cuts = false;
+        // A single sequence with a unit for every workgroup is not cut (steps_of_piece), and
+        // the join that finds nothing takes 3 us.  But q_start may name fewer rows than the
+        // call has, as in a captured one: a token in it then waits for its steps one after
+        // the other, so only where they are few.  4-bit cache, fp32, 1000 rows, joined and not:
+        // all of them on 1777 keys of 5 heads of 4 52.3 and 48.7 us, of 8 heads of 2, D = 64,
+        // 32.3 and 29.4; one token 9.0 and 15.1, 8.0 and 12.3 (on 4000 keys 9.4 and 28.1).
+        if (B == 1 && steps <= rules.lone_steps && (n_tok * G + kRows - 1) / kRows * KVH >= p.most) p.cuts = false;
         p.groups = units;
         if (B > kLineSeqs) p.groups = (p.many ? B * kFewTiles : n_tok * G / kRows + B) * KVH;
         if (p.cuts) {

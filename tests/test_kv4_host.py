@@ -229,3 +229,19 @@ def test_binding_has_no_thread_local_storage():
     offset, = struct.unpack_from("<Q", elf, 32)
     size, count = struct.unpack_from("<HH", elf, 54)
     assert 7 not in [struct.unpack_from("<I", elf, offset + i * size)[0] for i in range(count)]
+
+
+def test_a_lone_sequence_may_bring_fewer_rows_than_its_call(lib):
+    """A captured call holds rows for more tokens than a replay brings: one token on 4000
+    keys in it is read in parts all the same, which shows in the workspace (5 heads of 4, blocks
+    of 64)."""
+    for f, most in ((lib.bitlinear_kv8_attention_ws_bytes, 128), (lib.bitlinear_kv4_attention_ws_bytes, 512)):
+        for rows in (1, 32, 64, 100, 128, 206, 256, 400, 512):
+            if rows <= most:
+                assert f(rows, 20, 1, 63, 5, 64, 128) > 0, rows
+    # on the 8-bit cache also where the keys are few; on the 4-bit one while a full call's units
+    # do not fill the GPU
+    for rows in (52, 128, 200, 224):
+        assert lib.bitlinear_kv8_attention_ws_bytes(rows, 20, 1, 28, 5, 64, 128) > 0, rows
+    for rows in (52, 128, 256, 400):
+        assert lib.bitlinear_kv4_attention_ws_bytes(rows, 20, 1, 28, 5, 64, 128) > 0, rows
