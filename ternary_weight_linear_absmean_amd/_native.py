@@ -9,12 +9,15 @@ fallback: if the library is missing, ``load()`` raises.
 
 The calls on the paged caches are made by ``_calls`` (csrc/torch_calls.cpp) where
 nothing about their arguments is out of the ordinary, as a decode step waits for
-the host otherwise; what that leaves is made, or refused, here.
+the host otherwise; what that leaves is made, or refused, here, and so are all
+calls where ``_calls`` has not been built.
 """
 import collections
 import ctypes
 import importlib
 import os
+import sys
+import warnings
 
 import torch
 
@@ -122,9 +125,33 @@ class BitLinearError(RuntimeError):
         super().__init__(f"{call}: {STATUS.get(status, status)}: {detail}")
 
 
+def _bind(lib, calls):
+    calls.bind(_check, *(ctypes.cast(getattr(lib, name), _p).value for name in _ENTRIES))
+
+
+def _short_way(lib):
+    """_calls on the library's entry points, or None: it saves 5 us of host time a call
+    and nothing else, so where it was not built, or for another torch or Python, the calls are
+    made through ctypes."""
+    try:
+        calls = importlib.import_module("._calls", __package__)
+    except ImportError as e:
+        why = str(e)
+    else:
+        here = f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+        built_for = getattr(calls, "built_for", "another torch")
+        if built_for == here:
+            _bind(lib, calls)
+            return calls
+        why = f"it was built for {built_for}, this is {here}"
+    warnings.warn(f"_calls.so is not used, calls on the paged caches take 5 us more of host time ({why}); run "
+                  "`python -m ternary_weight_linear_absmean_amd.build`", RuntimeWarning, stacklevel=3)
+    return None
+
+
 def load():
-    """Load libbitlinear.so and _calls.so (built in-tree by build.py); raise if one is
-    missing."""
+    """Load libbitlinear.so (built in-tree by build.py), and _calls.so if it is there;
+    raise if the library is missing."""
     global _lib, _calls
     if _lib is not None:
         return _lib
@@ -217,9 +244,7 @@ def load():
     lib.bl_last_error.argtypes = []
     lib.bl_abi_version.restype = ctypes.c_int
     lib.bl_abi_version.argtypes = []
-    calls = importlib.import_module("._calls", __package__)
-    calls.bind(_check, *(ctypes.cast(getattr(lib, name), _p).value for name in _ENTRIES))
-    _lib, _calls = lib, calls
+    _lib, _calls = lib, _short_way(lib)
     return lib
 
 

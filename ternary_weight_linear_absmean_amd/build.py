@@ -7,11 +7,11 @@ Each source is compiled to an object (in parallel), then linked into
 with FMA contraction off (every fp32 step of the quantisers and the rescale
 is one IEEE rounding), without packed-fp32 instructions, and with the leading
 kernel arguments preloaded into SGPRs.  Beside it ``_calls.so``, the Python
-binding's short way into the calls on the paged caches (host code, with torch's
-headers).
+binding's short way into the calls on the paged caches (host code): it takes a C++
+compiler, Python's and torch's headers, and where it cannot be built the binding does
+without it.
 """
 import concurrent.futures as cf
-import importlib.util
 import os
 import subprocess
 import sys
@@ -61,16 +61,19 @@ def _compile(src, verbose):
     return obj
 
 
-def _build_calls(verbose):
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+def _compile_calls(verbose):
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
     rocm = os.path.dirname(os.path.dirname(HIPCC))
     tmp = CALLS + ".tmp"
+    built_for = f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
     # NDEBUG: without it pybind11's headers bring a thread-local counter.  A library with
     # thread-local storage that is loaded into a running program and never touches it makes
     # every other library's access to its own take the slow way (glibc 2.35): 1 us a launch.
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DNDEBUG",
-           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-           "-I", os.path.join(torch_dir, "include"),
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f'-DBUILT_FOR="{built_for}"', "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
            "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            "-I", os.path.join(rocm, "include"), os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp,
            "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
@@ -82,10 +85,23 @@ def _build_calls(verbose):
     os.replace(tmp, CALLS)
 
 
+def build_calls(verbose: bool = False):
+    """_calls.so's path, or None, with the reason on stderr and no file of an earlier
+    build left, where it cannot be built."""
+    try:
+        _compile_calls(verbose)
+        return CALLS
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(CALLS):
+            os.remove(CALLS)
+        print(f"_calls.so is not built, calls on the paged caches go through ctypes: {e}", file=sys.stderr, flush=True)
+        return None
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=max(1, min(jobs, len(SOURCES) + 1))) as ex:
-        calls = ex.submit(_build_calls, verbose)
+        calls = ex.submit(build_calls, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
         calls.result()
     tmp = LIB + ".tmp"

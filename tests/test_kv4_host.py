@@ -245,3 +245,55 @@ def test_a_lone_sequence_may_bring_fewer_rows_than_its_call(lib):
         assert lib.bitlinear_kv8_attention_ws_bytes(rows, 20, 1, 28, 5, 64, 128) > 0, rows
     for rows in (52, 128, 256, 400):
         assert lib.bitlinear_kv4_attention_ws_bytes(rows, 20, 1, 28, 5, 64, 128) > 0, rows
+
+
+@pytest.fixture
+def unloaded(lib):
+    """The binding before its first load(); as it was afterwards."""
+    native = bl._native
+    was = native._lib, native._calls
+    native._lib = native._calls = None
+    yield native
+    native._lib, native._calls = was
+    if was[1] is not None:
+        native._bind(was[0], was[1])
+
+
+def test_the_short_way_is_built_here(lib):
+    """Where the build has all it needs, the calls on the caches go through _calls.so."""
+    assert bl._native._calls is not None
+
+
+@pytest.mark.parametrize("error", [ImportError("No module named _calls"), ImportError("undefined symbol")])
+def test_the_library_loads_without_the_short_way(unloaded, monkeypatch, error):
+    """_calls.so saves host time and nothing else: where it cannot be imported, the calls
+    are made through ctypes."""
+    def fails(name, package=None):
+        raise error
+    monkeypatch.setattr(unloaded.importlib, "import_module", fails)
+    with pytest.warns(RuntimeWarning, match="_calls"):
+        loaded = unloaded.load()
+    assert loaded.bl_abi_version() and unloaded._calls is None
+
+
+def test_a_short_way_of_another_torch_is_not_taken(unloaded, monkeypatch):
+    calls = unloaded.importlib.import_module("._calls", bl.__name__)
+    monkeypatch.setattr(calls, "built_for", "torch 0.4.1, Python 3.6")
+    with pytest.warns(RuntimeWarning, match="0.4.1"):
+        unloaded.load()
+    assert unloaded._calls is None
+    with pytest.raises(TypeError):                     # refused by the long way
+        bl.bitlinear_kv4_attention(None, None, None, None, None)
+
+
+def test_the_library_builds_without_the_short_way(monkeypatch, tmp_path, capsys):
+    """A compiler that is missing or fails: the build says so, and leaves no _calls.so of an
+    earlier build behind."""
+    from ternary_weight_linear_absmean_amd import build
+    for compiler in ("false", str(tmp_path / "none")):
+        old = tmp_path / "_calls.so"
+        old.write_bytes(b"")
+        monkeypatch.setattr(build, "CALLS", str(old))
+        monkeypatch.setenv("CXX", compiler)
+        assert build.build_calls(False) is None
+        assert not old.exists() and "_calls.so" in capsys.readouterr().err
