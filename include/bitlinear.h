@@ -608,8 +608,9 @@ typedef struct {
  *               are as there.
  * Per token and head, for K and for V: z = the largest fp16 <= min x, s =
  * fp16(fp32(fp32(max x - z) / 15)), code = clamp(rne(fp32(fp32(x - z) / s)), 0,
- * 15), 0 where s = 0.  Bit-exact.  Slots without a new token keep their codes, z
- * and s.
+ * 15), 0 where s = 0.  Bit-exact.  A value is off by max(s / 2, 15 2^-25 = 4.5e-7):
+ * rows whose values span less than 15 2^-14 = 9.2e-4 get a step in fp16's subnormals.
+ * Slots without a new token keep their codes, z and s.
  * Blocks, limits and no-ops as for bitlinear_kv8_append.
  */
 bl_status bitlinear_kv4_append(const void *k, const void *v, const void *q, void *q_out,

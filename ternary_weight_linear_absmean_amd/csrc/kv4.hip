@@ -6,8 +6,10 @@
 //   z = the largest fp16 <= min x,  s = fp16(fl(fl(max x - z) / 15)),
 //   code = clamp(rne(fl(fl(x - z) / s)), 0, 15), 0 where s = 0;
 // the value is z + s code.  z is rounded down so that no value lies below the
-// first code; a step that is rounded down costs the largest value at most 15 /
-// 2048 of a step.  Scales of a token, not of a block: 4-bit codes do not survive
+// first code.  A step that is rounded down costs the largest value 15 times that: at
+// most 15 / 2048 of a step, or, where the spread is below 15 2^-14 = 9.2e-4 and fp16 holds
+// s in steps of 2^-24, at most 15 2^-25 = 4.5e-7, which can be several of its steps.  So
+// a value is off by max(s / 2, 4.5e-7).  Scales of a token, not of a block: 4-bit codes do not survive
 // being rescaled when a block's largest value grows.  Quotients are correctly
 // rounded, so the cache's bytes are defined to the bit.
 //

@@ -568,3 +568,21 @@ def test_fresh_tensors_under_torch_modes(gpu):
 def test_many_heads(gpu, KVH, G, bits):
     """Numbers of heads of every size that a call takes, key heads and query heads apart."""
     check_append(gpu, make(24, [1, 1], [1, 17], 16, 64, KVH, F32, G, bits, 16, True))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_rows_are_this_near(gpu, D):
+    """Rows that span 1e-9 to 1e-2, through the cache and back: off by max(s / 2, 15 2^-25),
+    a border between codes by 2^-22 of the spread, the value read by half a step of fp32."""
+    s = make(25, [90], [90], 32, D, 2, F32)
+    g = torch.Generator().manual_seed(25)
+    span = 10.0 ** (-9 + 7 * torch.arange(90) / 89.0)[:, None, None]
+    s["k"] = (torch.rand(90, 2, D, generator=g) - 0.5) * span
+    s["v"] = (torch.rand(90, 2, D, generator=g) + 0.3) * span
+    d = check_append(gpu, s)
+    for x, y, zs in zip((s["k"], s["v"]), gpu.bitlinear_kv4_read(*meta(d), d["cache"], 90), d["cache"][2:]):
+        zs = zs.cpu().double()[s["table"][0, torch.arange(90) // 32].long(), :, torch.arange(90) % 32]
+        x, y = x.double(), y.cpu().double()
+        wide = x.amax(-1) - zs[..., 0]
+        tol = torch.clamp(zs[..., 1] / 2, min=15 * 2.0 ** -25) + wide * 2.0 ** -22 + y.abs().amax(-1) * 2.0 ** -24
+        assert ((x - y).abs().amax(-1) <= tol).all()

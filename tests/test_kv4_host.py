@@ -297,3 +297,23 @@ def test_the_library_builds_without_the_short_way(monkeypatch, tmp_path, capsys)
         monkeypatch.setenv("CXX", compiler)
         assert build.build_calls(False) is None
         assert not old.exists() and "_calls.so" in capsys.readouterr().err
+
+
+def test_oracle_codes_are_this_near():
+    """|x - (z + s u)| <= max(s / 2, 15 2^-25).  Away from the last code a value is off by
+    half a step; at the last one by 15 times what s lost, 2^-25 where s is subnormal and
+    2^-11 of it (less than half a step) where not.  x - z and the quotient are rounded
+    to 24 bits, so a border between codes may move by 2^-22 of the spread."""
+    r = np.random.default_rng(5)
+    worst = 0.0
+    for spread in 10.0 ** np.arange(-10, 4.6, 0.25):
+        for middle in (0.0, 1.0, -0.37):
+            x = ((r.random((400, 64)) - 0.5 + middle) * spread).astype(np.float32).astype(np.float64)
+            z, s, u = ref.codes(x)
+            wide = x.max(-1) - z
+            off = np.abs(x - z[:, None] - s[:, None] * u).max(-1)
+            assert (off <= np.maximum(s / 2, 15 * 2.0 ** -25) + wide * 2.0 ** -22).all(), (spread, middle)
+            # for subnormal steps the second bound is needed, and met within a factor of two
+            if s.max() < 2.0 ** -14:
+                worst = max(worst, (off / (15 * 2.0 ** -25))[off > s].max(initial=0.0))
+    assert 0.5 < worst <= 1
