@@ -586,3 +586,47 @@ def test_small_rows_are_this_near(gpu, D):
         wide = x.amax(-1) - zs[..., 0]
         tol = torch.clamp(zs[..., 1] / 2, min=15 * 2.0 ** -25) + wide * 2.0 ** -22 + y.abs().amax(-1) * 2.0 ** -24
         assert ((x - y).abs().amax(-1) <= tol).all()
+
+
+# calls of more than kFewTurnedRows = 512 rows turn a row's heads by one wave, four times
+# 512 / D of them at once; heads that fill that not at all, once, and several times with a rest
+MANY_HEADS = [(128, 2, 10, 128, False), (128, 3, 2, 64, True), (128, 1, 33, 16, False), (64, 7, 10, 32, True),
+              (64, 3, 3, 64, False), (64, 1, 32, 48, False)]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,KVH,G,rot,near", MANY_HEADS)
+def test_queries_of_many_rows(gpu, D, KVH, G, rot, near, dtype, bits):
+    """Into another tensor and in place, rows of no sequence before and behind."""
+    s = make(26, [30, 1, 12], [90, 1, 333], 32, D, KVH, dtype, G, bits, rot, near, before=5, behind=480)
+    assert len(s["q"]) > 512
+    want = n64(check_append(gpu, s)["q"])                    # q itself is left
+    assert np.array_equal(want, n64(s["q"]))
+    d = cuda(s)
+    assert append(gpu, d, q_out=d["q"]) is d["q"]
+    q = want_append(s)[1]
+    of_none = ref.positions(*meta64(s)[:2], len(q), missing=-10 ** 12) == -10 ** 12
+    q[of_none] = n64(s["q"])[of_none]
+    assert np.array_equal(n64(d["q"]), q)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_queries_of_a_prompt(gpu, bits):
+    """600 rows of a sequence behind 50 tokens: every row's own position."""
+    s = make(27, [600, 3], [650, 40], 64, 64, 2, BF16, 10, bits, 16, False)
+    check_append(gpu, s)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,KVH,T", [(128, 1, 64), (128, 5, 32), (64, 6, 16), (64, 9, 128), (128, 4, 128)])
+def test_read_of_many_values(gpu, D, KVH, T, dtype, bits):
+    """Reads above kAtOnce = 2^21 threads take four heads a workgroup: numbers of heads that
+    are and are not their multiple, groups of 16 tokens that end early, blocks that hold nothing."""
+    behind = (1 << 21) // (KVH * 2 * D) * 16 + 40
+    s = make(28, [100, 37, 0, 1, 70], [100, 41, 9, 1, 333], T, D, KVH, F32, 1, bits, before=7, behind=behind)
+    assert (len(s["k"]) // 16 + 10) * KVH * 2 * D > 1 << 21
+    s["table"][0, 0] = -3
+    s["table"][4, 333 // T] = len(s["cache"][0])
+    check_read(gpu, s, dtype)
