@@ -640,7 +640,7 @@ bl_status bitlinear_kv4_attention(const void *q, bl_dtype dtype, int64_t n_tok, 
                                   const bl_kv4 *cache, float scale, void *out, void *ws,
                                   size_t ws_bytes, void *stream);
 
-/* Workspace bytes of bitlinear_kv4_attention; 0 also for sizes it refuses. */
+/* Workspace bytes of bitlinear_kv4_attention, of either dtype; 0 also for sizes it refuses. */
 size_t bitlinear_kv4_attention_ws_bytes(int64_t n_tok, int64_t QH, int64_t B, int64_t max_blocks,
                                         int64_t KVH, int64_t T, int64_t D);
 

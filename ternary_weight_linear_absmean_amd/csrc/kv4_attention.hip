@@ -124,15 +124,17 @@ struct Reference {
 // barrier in the loop: a cached byte has one reader.  The next tile's K is under way
 // from the moment this one's has been used, and so is V.
 //
-// Single tokens are bound by memory and, at the ends, by the chain starts -> entry
-// -> K -> scores -> V and by the join: 64 ragged sequences of up to 4096 keys, 5
-// heads of 4, bf16, 87 MB: 25.5 us, 3.4 TB/s and 4.1 of its middle, where a sum over
-// memory reads 4.0; the whole call 27.4.  About 370 vector instructions a wave and
+// Single tokens wait for the chain starts -> entry -> K -> scores -> V, for memory, and for
+// the join: 64 ragged sequences of up to 4096 keys, 5 heads of 4, bf16, 87 MB: 25.7 us, 3.4
+// TB/s (the 8-bit cache's kernel reads 4.65 where all lengths are equal), 53% of a SIMD's
+// time vector instructions, 37% of the waves' waiting, 1.4 waves of 2 on average; the whole
+// call 27.7.  About 370 vector instructions a wave and
 // tile (662 with one more add for each pair of codes, scores multiplied twice, and
 // loads behind a branch, which copied every loaded register: 36.2 us).  Loads of V
 // held in front of the loop's end: the same.  A third workgroup on a CU (168
 // registers, 768 pieces): 25.2.  Units of 32 rows, which turn a code once for two
-// products: 2048 bf16 rows on 4096 keys 135 us, of 16 rows 138.
+// products: 2048 bf16 rows on 4096 keys 135 us, of 16 rows 138 (124 with the tiles that see
+// most first).
 template <int D>
 struct FewLds {
     float join[kWaves][kRows][D + 4];
@@ -433,7 +435,7 @@ __device__ __forceinline__ void few_rows(const Args &a, uint32_t group, FewLds<D
 // a wave, 64 keys at a time, the tile turned into fp16 once, in LDS, for all rows.  While
 // tile t is used, t + 1 is turned into the other buffer and the codes of t + 2
 // are on their way.  What goes to LDS are the keys and values themselves, fp16(z
-// + s u), an error of 2^-12 beside the result's 2^-9: no z or s is left in the
+// + s u), an error of 2^-11 at most beside the result's 2^-8: no z or s is left in the
 // loop over scores.  (fp32 rows would need the codes and each token's z and s: 283 us
 // for 2048 rows on 4096 keys, 5 heads of 4 and D = 128, where 16-row units take 181.)
 //
@@ -795,18 +797,25 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_mixed_kernel(Args a) {
     }
 }
 
-// By type.  bf16 rows, few and many, 5 heads of 4 and D = 128, in us:
-//   work  7680  4 x 256 on 1000      35.0  37.8
-//        11520  512 on 4000          50.8  51.0
-//        17280  8 x 96 on 4000       69.2  88.3
-//        20320  128 on 32000         84.4   102
-//        21760  4 x 128 on 8000      96.5  84.3
-//       30.7 k  64 x 96 on 500        112  70.3
-//        46080  2048 on 4096          138   124
-// (8 heads of 2, D = 64: 30.7 k 58 and 42, 46080 84 and 80, but 64 x 64 on 4000 178
-// and 209.)  A workgroup of many rows for half the CUs only: 1000 rows on 1777
-// keys 57.8 us, for two a CU 46.7.  One sequence of more than 32 units for 256
-// pieces: 128 rows on 32000 keys 133 us, for 512 84.
+// By type.  bf16 rows, few and many, in us, tokens on keys of each sequence; 5 heads of 4
+// with D = 128, and 8 heads of 2 with D = 64:
+//   work  7680  4 x 256 on 1000      37.6  39.4     6144  22.7  34.5
+//        11250  1000 on 1777         35.3  45.3     9000  21.7  35.7
+//        15360  64 x 48 on 500       60.5  52.5    12288  34.6  32.2
+//        15360  16 x 128 on 1000     67.0  54.4
+//        17280  8 x 96 on 4000       69.6  89.0    13824  43.7  58.8
+//        20320  128 on 32000         85.6   104    16256  55.0  48.0
+//        21760  4 x 128 on 8000      95.3  86.1    17408  54.0  60.4
+//        22500  1500 on 2500         62.7  70.1
+//        25600  2048 on 2048         56.0  66.4
+//        30720  64 x 96 on 500        112  72.4    24576  58.0  43.0
+//        46080  2048 on 4096          124   124    36864  71.6  82.8
+//        46080  64 x 32 on 4000       203   174    36864  99.7   153
+//        92160  64 x 64 on 4000       344   296    73728   192   211
+// No one bound suits all: many short sequences want the 128-row form from 12000 on, lone
+// prompts and small heads on long keys not at 40000.  A workgroup of many rows for half
+// the CUs only: 1000 rows on 1777 keys 57.8 us, for two a CU 46.7.  One sequence of more
+// than 32 units for 256 pieces: 128 rows on 32000 keys 133 us, for 512 84.
 constexpr Rules kRules[2] = {{1e30, kCUs, 32, 8}, {21000, 2 * kCUs, 32, 8}};
 
 template <bool BF16, int D>

@@ -563,26 +563,34 @@ void join(const KvArgs<C> &a, int64_t rows, int64_t parts, hipStream_t s) {
 // rest, or else all.  A lone workgroup of many rows takes 2 us a tile of 64 keys,
 // so with little work the few-rows kernel, cut to fill the GPU, is done first
 // though it reads and converts a code 8 times as often.  In us, few and many
-// rows, 5 heads of 4, bf16 (not measured for other heads and fp32):
-//   work   120  128 rows on 500 keys      7.5  18.9
-//          720  128 on 4000                13    19
-//         1920  4 x 256 on 1000          22.9  29.5
-//         2880  512 on 4000 / 8 x 64     31.7  27.7 / 35.4 42.5
-//         3840  64 x 48 on 500           25.6    28
-//         4320  8 x 96 on 4000             37    46
-//         5080  128 on 32000             41.2  41.7
-//         5440  4 x 128 on 8000          58.6  45.6
-//         7680  64 x 96 on 500           44.5  29.8
-//        23000  64 x 64 on 4000           191   142
-// and with 32 rows a sequence, 64 on 4000 (work 11500) 110 and 140.
+// rows, 8-bit cache, tokens on keys of each sequence, 5 heads of 4 with D = 128, bf16 and
+// fp32, then 8 heads of 2 with D = 64, bf16, with its own work:
+//   work   640  128 on 500          8.5  20.9    9.7  28.8     512   5.9  15.7
+//         2880  128 on 4000        30.7  29.6   34.0  36.6    2304  19.5  22.5
+//         3840  8 x 64 on 1000     30.7  34.2   33.5  48.9
+//         4480  256 on 3000        39.4  33.0   41.8  42.2
+//         4800  16 x 48 on 700     28.9  26.7   31.9  37.6
+//         5760  16 x 16 on 4000    65.3  55.4   66.3  75.6
+//         7500  1000 on 1000       29.3  33.7   33.6  48.6
+//         7680  4 x 256 on 1000    48.2  35.8   50.2  51.1    6144  21.2  26.2
+//        11520  512 on 4000        68.6  54.2   74.7  76.1    9216  28.0  36.1
+//        15360  64 x 48 on 500     72.5  49.7   82.8  70.8   12288  31.6  34.9
+//        17280  8 x 96 on 4000      100  93.8    110   128   13824  44.8  69.8
+//        20320  128 on 32000        191   118    202   164   16256   127  68.8
+//        30720  64 x 96 on 500      132  68.8    154   101   24576  53.3  47.4
+//        92160  64 x 64 on 4000     491   281    578   440   73728   203   232
+// The bound is that of bf16 rows of D = 128.  For fp32 rows, and for two heads of
+// 64 on a key head, it is too low: calls above it may take up to 1.7 times as long as by the
+// few-rows kernel.
 //
 // Many rows: as many parts of the keys as keep a workgroup on every CU, if that
 // can save three steps; how many a sequence has, and of what keys, its length
 // says on the device (parts behind its end exit at once).
 //
 // The form and whether there is a join at all go by max_blocks, as a launch's grid
-// has to: with room for 8192 keys 128 rows on 500 take 22 us and not 8, and one
-// row on 200 takes 7.9 and not 5.8.
+// has to: with room for 8192 keys 128 bf16 rows on 500 take 22.7 us and not 8.4, and one
+// row on 200 takes 7.8 and not 6.0; on the 4-bit cache 512 rows on 512 25.3 and not 14.0,
+// one row on 200 7.4 and not 5.5.
 //
 // Few rows: units are cut where one sequence may be longer than three steps and
 // they are few, or where the longest could hold up the others or a prompt for
